@@ -1,0 +1,208 @@
+/* moe_layer.h -- C ABI of the decoder-layer operators around the fused MoE
+ * expert block (moe_fused.h), in the same library.
+ *
+ *   moe_layer_add_rmsnorm_quant  residual addition, RMS norm, per-token INT8
+ *                                quantisation (the block's own quant convention)
+ *   moe_layer_w4_linear          products with 4-bit weights and group scales for
+ *                                few tokens (projections, output head, router gate)
+ *   moe_layer_kv_append          quantised write of new keys and values into a
+ *                                paged INT8 cache, one scale a page and head
+ *   moe_layer_kv_attention       attention of new tokens over that cache
+ *
+ * Conventions are those of moe_fused.h: device pointers owned by the caller,
+ * no device memory allocated here, work enqueued asynchronously on `stream`
+ * (a cudaStream_t as void*) of the current device, MOE_OK or a negative
+ * MOE_ERR_* code, nothing launched by a call that returns an error.  There is
+ * no handle and no state: a call reads nothing that an earlier call left in
+ * the workspace.  Strides count elements, and the innermost dimension is
+ * contiguous.  Pointers need only the alignment that each call states.
+ */
+#ifndef MOE_LAYER_H
+#define MOE_LAYER_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_fused.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* element types */
+#define MOE_LAYER_BF16 0
+#define MOE_LAYER_FP16 1
+#define MOE_LAYER_FP32 2
+#define MOE_LAYER_INT8 3
+
+/* Residual addition, RMS norm and INT8 quant, row t of `rows`, in fp32:
+ *   s = x[t] + residual[t]          (x[t] without residual)
+ *   residual_out[t] = T(s)          T: rounding to `dtype`, to nearest even
+ *   y = s * (1 / sqrt(mean(s^2) + eps)) * weight
+ *   y_out[t] = T(y)
+ *   z = y * smooth                  (y without smooth)
+ *   a = max(max|z|, 1e-4), m = 127 / a
+ *   q[t] = clamp(rne(z * m), -127, 127), q_scale[t] = 1 / m
+ * The norm and the quant take the unrounded s and y.  A row that holds a NaN
+ * or an infinity gets a NaN scale, so that q * q_scale is NaN.
+ * x, residual, residual_out: [rows, hidden] of `dtype` (BF16 or FP16) with
+ * their own row strides (>= hidden); residual_out may be residual itself
+ * (same stride) and y_out may be x.  residual and residual_out are both
+ * given or both NULL.  weight: [hidden] of `weight_dtype` (`dtype` or FP32).
+ * smooth: [hidden] fp32 or NULL.  y_out: [rows, hidden] of `dtype` or NULL.
+ * q: [rows, hidden], q_scale: [rows].  1 <= hidden <= 16384 (any number),
+ * rows >= 0.  Every pointer aligned to its element. */
+typedef struct {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  const float* smooth;
+  void* residual_out;
+  void* y_out;
+  int8_t* q;
+  float* q_scale;
+  int64_t x_stride;
+  int64_t residual_stride;
+  int64_t residual_out_stride;
+  int32_t rows;
+  int32_t hidden;
+  int32_t dtype;
+  int32_t weight_dtype;
+  float eps;
+} moe_layer_norm_args_t;
+int moe_layer_add_rmsnorm_quant(const moe_layer_norm_args_t* args, void* stream);
+
+/* Products with 4-bit weights:
+ *   y[m, n] = x_scale[m] * sum over groups g of w_scale[n, g] *
+ *             sum over k in g of x[m, k] * (code[n, k] - zero[n, g])
+ * x: [m, k] of `x_dtype` (BF16, FP16, or INT8 codes with x_scale [m] fp32;
+ * x_scale is NULL for the other two), row stride x_stride (a multiple of 16
+ * bytes; 16-byte aligned base).  w: [n, k/2] uint8, 16-byte aligned, the code
+ * of an even k in the low four bits, of the next k in the high four.  w_scale:
+ * [n, k/group] of `scale_dtype` (BF16, FP16 or FP32).  w_zero: [n, k/group]
+ * uint8 in 0..15 (the low four bits count), NULL for 8 everywhere.  y: [m, n]
+ * of `out_dtype` (BF16, FP16 or FP32), dense.
+ * group: 32, 64 or a multiple of 128; k: a multiple of group, 32 <= k <=
+ * 65536; n >= 1; m >= 0.  Products of codes are exact, sums are fp32, y is
+ * rounded once.  The call is made for few rows (the weights are read once for
+ * every 32 rows of x); it is right for any m. */
+typedef struct {
+  const void* x;
+  const float* x_scale;
+  const uint8_t* w;
+  const void* w_scale;
+  const uint8_t* w_zero;
+  void* y;
+  int64_t x_stride;
+  int32_t m;
+  int32_t n;
+  int32_t k;
+  int32_t group;
+  int32_t x_dtype;
+  int32_t scale_dtype;
+  int32_t out_dtype;
+} moe_layer_w4_args_t;
+int moe_layer_w4_linear(const moe_layer_w4_args_t* args, void* stream);
+
+/* A paged INT8 cache of keys and values.  Page p holds page_size tokens of
+ * every kv head; the value of token slot s, channel d of head h is
+ *   k[p, h, s, d] * k_scale[p, h]         (v likewise)
+ * with k, v: int8, each head's [page_size, head_dim] contiguous, 16-byte
+ * aligned, page and head strides in elements (multiples of 16), and the scales
+ * fp32 [num_pages, kv_heads] with a page stride (heads contiguous).
+ * Row b of page_table ([batch, max_pages] int32, row stride table_stride)
+ * lists the pages of sequence b in order; entries past its length are not read.
+ * page_size: 16, 32, 64 or 128; head_dim: 64 or 128; 1 <= kv_heads <= 1024;
+ * 0 <= batch <= 4096. */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t scale_stride;
+  int32_t num_pages;
+  int32_t kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+} moe_layer_kv_cache_t;
+
+/* Write new keys and values.  Sequence b gets tokens cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 of k_new / v_new (token b alone when cu_tokens is
+ * NULL) at positions start[b], start[b] + 1, ...  For every touched page and
+ * head, K and V each by themselves:
+ *   a page that the call starts (its slot 0 is written): scale = max(amax,
+ *     1e-4) / 127 over the new tokens that it gets;
+ *   a page that already holds tokens: scale' = max(scale, amax / 127); if it
+ *     grew, the codes held below the first new slot become
+ *     clamp(rne(code * (scale / scale')), -127, 127);
+ *   new codes = clamp(rne(x * (1 / scale')), -127, 127).
+ * (Slots are filled in order: what a started page held before is forgotten.)
+ * k_new, v_new: [tokens, kv_heads, head_dim] of `dtype` (BF16 or FP16) with
+ * token strides (multiples of 8) and heads dense, 16-byte aligned.  A token whose page-table
+ * entry is outside [0, num_pages) or whose position is outside [0, max_pages *
+ * page_size) is not written.  No page may appear twice among those written. */
+typedef struct {
+  moe_layer_kv_cache_t cache;
+  const void* k_new;
+  const void* v_new;
+  const int32_t* page_table;
+  const int32_t* start;
+  const int32_t* cu_tokens;
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t table_stride;
+  int32_t tokens;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t dtype;
+} moe_layer_kv_append_args_t;
+int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
+
+/* Attention over the cache.  Sequence b has the query tokens cu_q[b] ..
+ * cu_q[b + 1] - 1 (token b alone when cu_q is NULL), qlen of them, and
+ * seq_lens[b] keys, its query tokens' own (already appended) among them.
+ * Query token j stands at position p = seq_lens[b] - qlen + j and sees the keys i with
+ * 0 <= i <= p, and i > p - window where window > 0.  Query head
+ * n uses kv head n / group_size:
+ *   out[t, n] = sum_i softmax_i(sm_scale * <q[t, n], key_i>) * value_i
+ * and zeros where no key is seen.  Keys on a page-table entry outside [0,
+ * num_pages) are not seen; lengths are held to [0, max_pages * page_size].
+ * q: [tokens, kv_heads * group_size, head_dim] of `dtype` (BF16 or FP16), token stride
+ * q_stride (a multiple of 8), heads dense, 16-byte aligned.  out: the same
+ * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the largest
+ * number of query tokens of a sequence (1 without cu_q); a larger one in cu_q
+ * leaves the tokens past max_q unwritten.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * rounded to fp16 (11 bits) for the product with the values.
+ * workspace: moe_layer_kv_attention_workspace_size bytes, 256-byte aligned,
+ * no initial content needed; calls that share one must be ordered. */
+typedef struct {
+  moe_layer_kv_cache_t cache;
+  const void* q;
+  void* out;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  int64_t q_stride;
+  int64_t table_stride;
+  int32_t tokens;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t max_q;
+  int32_t group_size;
+  int32_t window;
+  int32_t dtype;
+  float sm_scale;
+} moe_layer_kv_attention_args_t;
+/* Bytes for any call with this head_dim on the current device. */
+int moe_layer_kv_attention_workspace_size(int32_t head_dim, size_t* workspace_bytes);
+int moe_layer_kv_attention(const moe_layer_kv_attention_args_t* args, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_LAYER_H */

@@ -18,6 +18,8 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
+from .layer import LAYER_EXPORTS, KvCache, add_rmsnorm_quant, declare as declare_layer, w4_linear  # noqa: F401
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_moe_fused.so")
 
@@ -101,6 +103,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         for name in EXPORTS:
             getattr(L, name)  # raises AttributeError if a symbol is missing
+        declare_layer(L)
         L.moe_fused_create.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(P), ctypes.POINTER(ctypes.c_size_t)]
         L.moe_fused_workspace_size.argtypes = [ctypes.POINTER(Config), ctypes.POINTER(ctypes.c_size_t)]
         L.moe_fused_forward.argtypes = [P, ctypes.POINTER(Args), P, ctypes.c_size_t, P]

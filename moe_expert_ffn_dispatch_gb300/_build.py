@@ -15,8 +15,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(HERE, "_moe_fused.so")
-SOURCES = ["api.cu", "dispatch_quant.cu", "moe_gemm.cu", "tc_gemm.cu"]
-HEADERS = ["device_prims.cuh", "epilogue_ops.cuh", "moe_internal.h", "quant_ops.cuh"]
+SOURCES = ["api.cu", "dispatch_quant.cu", "moe_gemm.cu", "tc_gemm.cu",
+           "layer_api.cu", "norm_quant.cu", "w4_linear.cu", "kv_append.cu", "kv_attention.cu"]
+HEADERS = ["device_prims.cuh", "epilogue_ops.cuh", "moe_internal.h", "quant_ops.cuh", "layer_ops.cuh"]
+PUBLIC_HEADERS = ["moe_fused.h", "moe_layer.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -41,7 +43,7 @@ def _stale(target: str, deps) -> bool:
 
 def build(verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "moe_fused.h"), __file__]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS] + [__file__]
     flags = NVCC_FLAGS + list(extra_flags or [])
     procs, objs = [], []
     for src in SOURCES:

@@ -1,0 +1,146 @@
+// Quantised write of new keys and values into the paged INT8 cache.
+//
+// One CTA takes one page, one kv head and K or V: the new tokens that fall on
+// that page are at most page_size x head_dim elements, which stay in
+// registers between the maximum and the rounding.  Each page is touched by
+// one CTA alone, so nothing is atomic.  Bound by memory (2 bytes read and 1
+// written an element) for prompts, by latency for single tokens.
+//
+// The CTAs know only bounds of the ragged lengths.  Sequence b owns the unit
+// numbers from cu[b] / P + 2 b on, which leaves it floor(n / P) + 2, at least
+// the pages that n tokens can touch; spare units end at once.
+#include "layer_ops.cuh"
+
+namespace moe_layer {
+namespace {
+
+template <typename T, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_append_kernel(const moe_layer_kv_append_args_t a) {
+  constexpr int kRowChunks = D / 8;                       // chunks of 8 elements of a token
+  constexpr int kMaxChunks = 128 * kRowChunks / THREADS;  // of a thread, at the largest page
+  __shared__ uint32_t s_max[THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int P = a.cache.page_size;
+  const int u = blockIdx.x, head = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+
+  int b = u, tok0 = u, n = 1, unit = 0;
+  if (a.cu_tokens) {
+    // the last b with cu[b] / P + 2 b <= u: 33-ary search, one probe a lane
+    int lo = 0, hi = a.batch;  // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + lane * step;
+      const bool ok = at < hi && a.cu_tokens[at] / P + 2 * at <= u;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, ok) | 1u);
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    b = lo;
+    tok0 = max(a.cu_tokens[b], 0);
+    n = min(a.cu_tokens[b + 1], a.tokens) - tok0;
+    unit = u - (a.cu_tokens[b] / P + 2 * b);
+  }
+  const int start = a.start[b];
+  if (n <= 0 || start < 0) return;
+  const int64_t index = start / P + unit;  // page of the sequence
+  const int64_t first = index * P;
+  const int lo = static_cast<int>(max(static_cast<int64_t>(start) - first, static_cast<int64_t>(0)));
+  const int hi = static_cast<int>(min(static_cast<int64_t>(start) + n - first, static_cast<int64_t>(P)));
+  if (hi <= lo || index >= a.max_pages) return;
+  const int page = a.page_table[b * a.table_stride + index];
+  if (page < 0 || page >= a.cache.num_pages) return;
+
+  const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + head * D;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const int64_t t_lo = tok0 + (first + lo - start);  // the token at slot lo
+  int8_t* codes = (is_v ? a.cache.v : a.cache.k) + page * a.cache.page_stride + head * a.cache.head_stride;
+  float* scale = (is_v ? a.cache.v_scale : a.cache.k_scale) + page * a.cache.scale_stride + head;
+
+  const int chunks = (hi - lo) * kRowChunks;
+  const float old = lo > 0 ? *scale : 0.0f;
+  uint4 v[kMaxChunks];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {
+    const int i = c * THREADS + tid;
+    if (i < chunks) {
+      v[c] = *reinterpret_cast<const uint4*>(src + (t_lo + i / kRowChunks) * stride + (i % kRowChunks) * 8);
+      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(w[j]);
+        top = max(top, max(abs_bits(f.x), abs_bits(f.y)));
+      }
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_max[tid >> 5] = top;
+  __syncthreads();  // and every thread has read the old scale
+  top = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) top = max(top, s_max[w]);
+  float amax = __uint_as_float(top);
+  float to;
+  if (lo == 0) {
+    if (amax < kAmaxFloor) amax = kAmaxFloor;
+    to = __fdiv_rn(amax, 127.0f);
+  } else {
+    const float grown = __fdiv_rn(amax, 127.0f);
+    to = (grown > old || grown != grown) ? grown : old;
+  }
+  if (lo > 0 && to > old) {
+    // the page's scale grew: the codes that it holds move to the new one
+    const float f = __fdiv_rn(old, to);
+    for (int i = tid; i < lo * D / 16; i += THREADS) {
+      uint4 q = reinterpret_cast<uint4*>(codes)[i];
+      uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t o = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o |= code_of(__fmul_rn(static_cast<float>(static_cast<int8_t>((w[j] >> (8 * e)) & 0xFFu)), f)) << (8 * e);
+        w[j] = o;
+      }
+      reinterpret_cast<uint4*>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  const float inv = __fdiv_rn(1.0f, to);
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {
+    const int i = c * THREADS + tid;
+    if (i < chunks) {
+      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+      uint32_t o[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(w[j]);
+        o[j >> 1] |= (code_of(__fmul_rn(f.x, inv)) | (code_of(__fmul_rn(f.y, inv)) << 8)) << ((j & 1) * 16);
+      }
+      *reinterpret_cast<uint2*>(codes + (lo + i / kRowChunks) * D + (i % kRowChunks) * 8) = make_uint2(o[0], o[1]);
+    }
+  }
+  if (tid == 0) *scale = to;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const moe_layer_kv_append_args_t& a, cudaStream_t s) {
+  // single tokens: 128 threads requantise a whole page in a few steps; prompts fill 256
+  moe_layer_kv_append_args_t arg = a;
+  void* args[] = {&arg};
+  const int64_t most = a.cu_tokens ? static_cast<int64_t>(a.tokens) / a.cache.page_size + 2 * a.batch : a.batch;
+  const dim3 grid(static_cast<unsigned>(most), a.cache.kv_heads, 2);
+  if (!a.cu_tokens) return cudaLaunchKernel((const void*)kv_append_kernel<T, D, 128>, grid, dim3(128), args, 0, s);
+  return cudaLaunchKernel((const void*)kv_append_kernel<T, D, 256>, grid, dim3(256), args, 0, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const moe_layer_kv_append_args_t& a, cudaStream_t s) {
+  if (a.dtype == MOE_LAYER_BF16)
+    return a.cache.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(a, s) : launch_typed<__nv_bfloat16, 128>(a, s);
+  return a.cache.head_dim == 64 ? launch_typed<__half, 64>(a, s) : launch_typed<__half, 128>(a, s);
+}
+
+}  // namespace moe_layer

@@ -1,0 +1,528 @@
+// Attention of new tokens over the paged INT8 cache.
+//
+// The query rows of one kv head (query tokens x group_size) are cut into
+// tiles of 16.  A unit is (sequence, kv head, row tile); its keys are cut
+// into pieces of kTileTokens.  All pieces of all units form one sequence of
+// work that the CTAs share evenly, whatever the lengths are: a CTA takes
+// consecutive pieces, so only the first and the last unit that it meets can
+// be shared with other CTAs.  Those leave (row maximum, row sum, unnormalised
+// output) in the workspace, and a second kernel joins them in CTA order.
+//
+// Within a CTA each warp streams its own 16-token slices of keys and values
+// through a ring of asynchronous copies and keeps a running softmax of its
+// own (no barrier in the loop); the warps join in shared memory at the end of
+// a unit.
+//
+// Arithmetic (mma.sync m16n8k16, fp32 accumulators): the int8 codes become
+// exact fp16 (a byte set into the mantissa of 1024, minus 1152).  A query row
+// is scaled by a power of two to [1, 2) at its largest element, so bf16 rows
+// are exact in fp16 as far as an fp32 sum can tell.  With x the scores times
+// log2(e), the page scale of K and the row's power of two enter x in fp32;
+// the page scale of V enters the weight exp2(x - max) as its ratio to the
+// largest page scale so far (in [0, 1]), which is rounded to fp16.
+// Both matrix products let the k index run over channels (or tokens) in
+// whatever order makes shared-memory reads whole 16-byte chunks: a permuted
+// sum is the same sum.
+//
+// Bound by the cache's bytes while a row tile holds all rows of a kv head.
+#include "layer_ops.cuh"
+
+namespace moe_layer {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSlice = 16;                       // tokens of a warp's ring stage
+constexpr int kTileTokens = kSlice * kWarps;     // tokens of a piece of work
+constexpr int kStages = 5;
+constexpr int kMaxSlots = 1024;                  // CTAs of a launch
+
+struct Record {  // a unit that several CTAs share, left by the CTA that holds its last piece
+  int b, head, rt, c0;  // c0: its first CTA; b < 0: none
+};
+
+struct AttnParams {
+  moe_layer_kv_attention_args_t a;
+  float* part_o;      // [2 * grid][16][D]
+  float* part_ml;     // [2 * grid][16][2]
+  Record* records;    // [grid]
+  float scale_log2;   // sm_scale * log2(e)
+  int page_shift;
+};
+
+// What a sequence contributes, from its lengths.
+struct SeqShape {
+  int q0, qlen;     // query tokens
+  int len;          // keys
+  int row_tiles;
+  int tile0, tiles; // pieces of kTileTokens that its rows see; tiles >= 1
+};
+
+__device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_t& a, int b) {
+  SeqShape s;
+  if (a.cu_q) {
+    s.q0 = min(max(a.cu_q[b], 0), a.tokens);
+    s.qlen = min(max(min(a.cu_q[b + 1], a.tokens) - s.q0, 0), a.max_q);
+  } else {
+    s.q0 = b;
+    s.qlen = 1;
+  }
+  const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
+  s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
+  s.row_tiles = (s.qlen * a.group_size + 15) / 16;
+  int lo = 0;
+  if (a.window > 0) lo = max(0, static_cast<int>(static_cast<int64_t>(s.len) - s.qlen - a.window + 1));
+  s.tile0 = lo / kTileTokens;
+  s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.tile0);
+  return s;
+}
+
+// position of channel chunk `c` (16 bytes) of token row `r` in a slice of [16][D] bytes
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  else return r * 64 + ((c ^ (((r >> 2) & 1) << 1)) << 4);
+}
+// token (0..7) of score column n (0..7).  D = 64: two rows share a 128-byte
+// line, and this order puts the rows that are read together on other banks.
+template <int D>
+__device__ __forceinline__ int token_of(int n) {
+  if constexpr (D == 128) return n;
+  else return n ^ ((n >> 1) & 1);
+}
+
+// four int8 codes -> two pairs of fp16: (0, 1) and (2, 3)
+__device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t off = 0x64806480u;  // 1152
+  const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&off));
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&off));
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnParams p) {
+  constexpr int KS = D / 16;                   // k steps of the score product
+  constexpr int NT = D / 8;                    // column tiles of the output
+  constexpr int kSliceBytes = kSlice * D;      // of K; V follows
+  constexpr int kStageBytes = 2 * kSliceBytes;
+  constexpr int kRing = kStages * kStageBytes;
+  constexpr int kCopies = kSliceBytes / 16 / 32;  // 16-byte copies of a lane for K (and for V)
+  static_assert(kRing >= 16 * D * 4 + 256, "the join reuses the ring");
+  extern __shared__ __align__(128) uint8_t smem[];
+  const moe_layer_kv_attention_args_t& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kRing);  // [batch + 1]
+  __shared__ int64_t s_carry[kWarps + 1];
+
+  // ---- the work of every sequence, summed
+  if (tid == 0) prefix[0] = 0;
+  int64_t run = 0;
+  for (int base = 0; base < a.batch; base += kThreads) {
+    const int b = base + tid;
+    int64_t v = 0;
+    if (b < a.batch) {
+      const SeqShape s = seq_shape(a, b);
+      v = static_cast<int64_t>(a.cache.kv_heads) * s.row_tiles * s.tiles;
+    }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) s_carry[warp] = v;
+    __syncthreads();
+    int64_t before = run, all = run;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_carry[w];
+      all += s_carry[w];
+    }
+    if (b < a.batch) prefix[b + 1] = before + v;
+    run = all;
+    __syncthreads();
+  }
+  const int64_t total = run;
+  const int c = blockIdx.x;
+  if (tid == 0) p.records[c].b = -1;
+  // CTA c takes pieces [total * c / G, total * (c + 1) / G), at least one of them
+  const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  if (c >= G) return;
+  int64_t at = total * c / G;
+  const int64_t end = total * (c + 1) / G;
+
+  uint8_t* ring = smem + warp * kRing;
+  const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+
+  while (at < end) {
+    int lo = 0, hi = a.batch;  // the b with prefix[b] <= at < prefix[b + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    const int b = lo;
+    const SeqShape s = seq_shape(a, b);
+    const int64_t rel = at - prefix[b];
+    const int unit = static_cast<int>(rel / s.tiles);
+    const int ta = static_cast<int>(rel - static_cast<int64_t>(unit) * s.tiles);
+    const int tb = static_cast<int>(min(static_cast<int64_t>(s.tiles), ta + (end - at)));
+    const int head = unit / s.row_tiles, rt = unit - head * s.row_tiles;
+    const int64_t unit_begin = at - ta;
+    at += tb - ta;
+
+    // ---- rows of this tile: row r is query token r / group of the sequence
+    const int rows = min(16, s.qlen * a.group_size - rt * 16);
+    const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
+    int64_t row_pos[2];
+    uint32_t qf[KS][4];
+    float row_scale[2];
+#pragma unroll
+    for (int r2 = 0; r2 < 2; ++r2) {
+      const int r = g + 8 * r2, row = rt * 16 + r;
+      const int j = row / a.group_size, hq = row - j * a.group_size;
+      row_pos[r2] = r < rows ? pos0 + j : -1;
+      // lane t holds channels [t D / 4, (t + 1) D / 4) of the row
+      uint32_t w[KS * 2];
+      if (r < rows) {
+        const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(s.q0 + j) * a.q_stride +
+                       static_cast<int64_t>(head * a.group_size + hq) * D + t * (D / 4);
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 u = reinterpret_cast<const uint4*>(src)[i];
+          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS * 2; ++i) w[i] = 0u;
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) {
+        const float2 f = unpack2<T>(w[i]);
+        top = max(top, max(abs_bits(f.x), abs_bits(f.y)));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // exponent of the largest element, inside what 2^-e can hold
+      const int e = min(max(static_cast<int>(top >> 23), 1), 253);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
+      row_scale[r2] = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const float2 f0 = unpack2<T>(w[2 * i]), f1 = unpack2<T>(w[2 * i + 1]);
+        qf[i][r2] = pack2<__half>(__fmul_rn(f0.x, down), __fmul_rn(f0.y, down));
+        qf[i][2 + r2] = pack2<__half>(__fmul_rn(f1.x, down), __fmul_rn(f1.y, down));
+      }
+    }
+    // keys that any row of the tile sees, cut to this CTA's pieces
+    const int64_t last = pos0 + (rt * 16 + rows - 1) / a.group_size;
+    int64_t k_lo = static_cast<int64_t>(s.tile0 + ta) * kTileTokens;
+    int64_t k_hi = min(static_cast<int64_t>(s.tile0 + tb) * kTileTokens, last + 1);
+    if (a.window > 0) k_lo = max(k_lo, (pos0 + rt * 16 / a.group_size - a.window + 1) & ~static_cast<int64_t>(kSlice - 1));
+    // this warp's slices: first + 8 i, from the slice of k_lo on
+    const int first = static_cast<int>(k_lo / kSlice) + warp;
+    const int n = k_hi > static_cast<int64_t>(first) * kSlice
+                      ? static_cast<int>(((k_hi + kSlice - 1) / kSlice - first + kWarps - 1) / kWarps)
+                      : 0;
+
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 0.0f;
+
+    // page, and scales, of the slices 32 at a time: lane i holds slice base + i
+    auto look_up = [&](int base, int& page, float& ks, float& vs) {
+      page = -1;
+      ks = vs = 0.0f;
+      const int i = base + lane;
+      if (i < n) {
+        const int64_t tok = static_cast<int64_t>(first + i * kWarps) * kSlice;
+        const int pg = a.page_table[b * a.table_stride + (tok >> p.page_shift)];
+        if (pg >= 0 && pg < a.cache.num_pages) {
+          page = pg;
+          ks = a.cache.k_scale[pg * a.cache.scale_stride + head];
+          vs = a.cache.v_scale[pg * a.cache.scale_stride + head];
+        }
+      }
+    };
+    int page0, page1;
+    float ks0, vs0, ks1, vs1;
+    look_up(0, page0, ks0, vs0);
+    look_up(32, page1, ks1, vs1);
+    const int in_page = a.cache.page_size - 1;
+    auto issue = [&](int i, int rel_i) {  // slice i of this warp, rel_i from the base of page0
+      const int page = rel_i < 32 ? __shfl_sync(0xffffffffu, page0, rel_i & 31) : __shfl_sync(0xffffffffu, page1, rel_i & 31);
+      if (i < n) {
+        const int64_t tok = static_cast<int64_t>(first + i * kWarps) * kSlice;
+        const int64_t off = max(page, 0) * a.cache.page_stride + head * a.cache.head_stride +
+                            (static_cast<int>(tok) & in_page) * D;
+        const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) {
+          const int ch = x * 32 + lane, r = ch / (D / 16), cc = ch % (D / 16);
+          cp_async16(dst + chunk_at<D>(r, cc), a.cache.k + off + ch * 16, page >= 0);
+          cp_async16(dst + kSliceBytes + chunk_at<D>(r, cc), a.cache.v + off + ch * 16, page >= 0);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+
+    for (int i = 0; i < n; ++i) {
+      const int ri = i & 31;
+      if (ri == 0 && i > 0) {
+        page0 = page1, ks0 = ks1, vs0 = vs1;
+        look_up(i + 32, page1, ks1, vs1);
+      }
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      const uint32_t kb = ring_u + (i % kStages) * kStageBytes, vb = kb + kSliceBytes;
+      const int page = __shfl_sync(0xffffffffu, page0, ri);
+      const float ks = __shfl_sync(0xffffffffu, ks0, ri), vs = __shfl_sync(0xffffffffu, vs0, ri);
+      const int64_t tok0 = static_cast<int64_t>(first + i * kWarps) * kSlice;
+
+      // scores of 16 rows x 16 tokens
+      float sc[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.0f;
+        const int r = h * 8 + token_of<D>(g);
+        uint32_t w[KS];
+        if constexpr (D == 128) {
+          const uint4 x = lds128(kb + chunk_at<D>(r, 2 * t)), y = lds128(kb + chunk_at<D>(r, 2 * t + 1));
+          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+        } else {
+          const uint4 x = lds128(kb + chunk_at<D>(r, t));
+          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        }
+#pragma unroll
+        for (int q = 0; q < KS; ++q) {
+          uint32_t b0, b1;
+          half_pairs(w[q], b0, b1);
+          mma16816<__half>(sc[h], qf[q][0], qf[q][1], qf[q][2], qf[q][3], b0, b1);
+        }
+      }
+      // x = score * scales * log2(e), masked
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r2 = e >> 1;
+          const int64_t key = tok0 + h * 8 + token_of<D>(2 * t + (e & 1));
+          const bool seen = page >= 0 && key <= row_pos[r2] && (a.window <= 0 || key > row_pos[r2] - a.window);
+          const float x = seen ? __fmul_rn(sc[h][e], __fmul_rn(ks, row_scale[r2])) : -INFINITY;
+          sc[h][e] = x;
+          top[r2] = fmaxf(top[r2], x);
+        }
+      // largest page scale of V so far; the weights carry the ratio to it
+      const float vnew = fmaxf(vref, fabsf(vs));
+      const float vcorr = vnew > vref ? __fdiv_rn(vref, vnew) : 1.0f;
+      const float vw = vnew > 0.0f ? __fdiv_rn(vs, vnew) : vs;
+      vref = vnew;
+      float corr[2];
+#pragma unroll
+      for (int r2 = 0; r2 < 2; ++r2) {
+        top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 1));
+        top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 2));
+        const float mn = fmaxf(m[r2], top[r2]);
+        const float base = mn == -INFINITY ? 0.0f : mn;
+        corr[r2] = exp2_fast(__fsub_rn(m[r2], base));
+        m[r2] = mn;
+        float sum = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w = exp2_fast(__fsub_rn(sc[h][2 * r2 + e], base));
+            sum = __fadd_rn(sum, w);
+            sc[h][2 * r2 + e] = __fmul_rn(w, vw);
+          }
+        l[r2] = __fmaf_rn(l[r2], corr[r2], sum);
+        corr[r2] = __fmul_rn(corr[r2], vcorr);
+      }
+      if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          o[q][0] = __fmul_rn(o[q][0], corr[0]);
+          o[q][1] = __fmul_rn(o[q][1], corr[0]);
+          o[q][2] = __fmul_rn(o[q][2], corr[1]);
+          o[q][3] = __fmul_rn(o[q][3], corr[1]);
+        }
+      }
+      const uint32_t a0 = pack2<__half>(sc[0][0], sc[0][1]), a1 = pack2<__half>(sc[0][2], sc[0][3]);
+      const uint32_t a2 = pack2<__half>(sc[1][0], sc[1][1]), a3 = pack2<__half>(sc[1][2], sc[1][3]);
+      // values: lane column g holds channels [g D / 8, (g + 1) D / 8), one a column tile
+      uint32_t w[4][NT / 4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = (q >> 1) * 8 + token_of<D>(2 * t + (q & 1));
+        if constexpr (D == 128) {
+          const uint4 x = lds128(vb + chunk_at<D>(r, g));
+          w[q][0] = x.x, w[q][1] = x.y, w[q][2] = x.z, w[q][3] = x.w;
+        } else {
+          const uint2 x = lds64(vb + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
+          w[q][0] = x.x, w[q][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < NT / 4; ++q) {
+        // bytes of tokens (2t, 2t + 1) side by side, then (2t + 8, 2t + 9)
+        uint32_t lo0, lo1, lo2, lo3, hi0, hi1, hi2, hi3;
+        half_pairs(__byte_perm(w[0][q], w[1][q], 0x5140), lo0, lo1);
+        half_pairs(__byte_perm(w[0][q], w[1][q], 0x7362), lo2, lo3);
+        half_pairs(__byte_perm(w[2][q], w[3][q], 0x5140), hi0, hi1);
+        half_pairs(__byte_perm(w[2][q], w[3][q], 0x7362), hi2, hi3);
+        mma16816<__half>(o[4 * q], a0, a1, a2, a3, lo0, hi0);
+        mma16816<__half>(o[4 * q + 1], a0, a1, a2, a3, lo1, hi1);
+        mma16816<__half>(o[4 * q + 2], a0, a1, a2, a3, lo2, hi2);
+        mma16816<__half>(o[4 * q + 3], a0, a1, a2, a3, lo3, hi3);
+      }
+      __syncwarp();  // the stage is read before it is filled again
+      issue(i + kStages - 1, ri + kStages - 1);
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r2 = 0; r2 < 2; ++r2) {
+      l[r2] += __shfl_xor_sync(0xffffffffu, l[r2], 1);
+      l[r2] += __shfl_xor_sync(0xffffffffu, l[r2], 2);
+    }
+    __syncwarp();
+
+    // ---- join the warps: O [16][D], then m [16], l [16] in each warp's ring
+    float* wo = reinterpret_cast<float*>(ring);
+    float* wm = wo + 16 * D;
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        wo[(g + 8 * (e >> 1)) * D + (2 * t + (e & 1)) * NT + q] = __fmul_rn(o[q][e], vref);
+    if (t == 0) {
+      wm[g] = m[0], wm[g + 8] = m[1];
+      wm[16 + g] = l[0], wm[24 + g] = l[1];
+    }
+    __syncthreads();
+    const int r = tid >> 4;  // 16 threads a row
+    constexpr int kEach = D / 16;
+    float top = -INFINITY;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, reinterpret_cast<float*>(smem + w * kRing)[16 * D + r]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc[kEach] = {};
+    const int d0 = (tid & 15) * kEach;
+    for (int w = 0; w < kWarps; ++w) {
+      const float* from = reinterpret_cast<float*>(smem + w * kRing);
+      const float f = exp2_fast(__fsub_rn(from[16 * D + r], base));
+      sum = __fmaf_rn(from[16 * D + 16 + r], f, sum);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) acc[i] = __fmaf_rn(from[r * D + d0 + i], f, acc[i]);
+    }
+    if (ta == 0 && tb == s.tiles) {
+      if (r < rows) {
+        const int row = rt * 16 + r, j = row / a.group_size, hq = row - j * a.group_size;
+        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
+        T* out = static_cast<T*>(a.out) +
+                 (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + head * a.group_size + hq) * D + d0;
+#pragma unroll
+        for (int i = 0; i < kEach; i += 2)
+          *reinterpret_cast<uint32_t*>(out + i) = pack2<T>(__fmul_rn(acc[i], inv), __fmul_rn(acc[i + 1], inv));
+      }
+    } else {
+      const int64_t slot = 2 * static_cast<int64_t>(c) + (ta > 0 ? 0 : 1);
+      float* po = p.part_o + (slot * 16 + r) * D + d0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) po[i] = acc[i];
+      if ((tid & 15) == 0) {
+        p.part_ml[(slot * 16 + r) * 2] = top;
+        p.part_ml[(slot * 16 + r) * 2 + 1] = sum;
+      }
+      if (tb == s.tiles && tid == 0) {
+        // the CTA of a piece x is the last c with total * c / G <= x
+        int64_t c0 = unit_begin * G / total;
+        while (c0 + 1 < G && total * (c0 + 1) / G <= unit_begin) ++c0;
+        while (c0 > 0 && total * c0 / G > unit_begin) --c0;
+        p.records[c] = Record{b, head, rt, static_cast<int>(c0)};
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the parts of a unit that several CTAs shared, in CTA order.  CTA
+// (c, y) takes rows 2 y and 2 y + 1 of the unit that CTA c finished.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams p) {
+  const int c = blockIdx.x;
+  const Record rec = p.records[c];
+  if (rec.b < 0) return;
+  const moe_layer_kv_attention_args_t& a = p.a;
+  const SeqShape s = seq_shape(a, rec.b);
+  const int rows = min(16, s.qlen * a.group_size - rec.rt * 16);
+  constexpr int kEach = D / 64;  // 64 threads a row
+  const int r = blockIdx.y * 2 + threadIdx.x / 64, d0 = (threadIdx.x % 64) * kEach;
+  if (r >= rows) return;
+  float top = -INFINITY, sum = 0.0f, acc[kEach] = {};
+  for (int x = rec.c0; x <= c; ++x) {
+    const int64_t slot = 2 * static_cast<int64_t>(x) + (x == rec.c0 ? 1 : 0);
+    const float m = p.part_ml[(slot * 16 + r) * 2], l = p.part_ml[(slot * 16 + r) * 2 + 1];
+    const float mn = fmaxf(top, m), base = mn == -INFINITY ? 0.0f : mn;
+    const float f0 = exp2_fast(__fsub_rn(top, base)), f1 = exp2_fast(__fsub_rn(m, base));
+    top = mn;
+    sum = __fmaf_rn(l, f1, __fmul_rn(sum, f0));
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      acc[i] = __fmaf_rn(p.part_o[(slot * 16 + r) * D + d0 + i], f1, __fmul_rn(acc[i], f0));
+  }
+  const int row = rec.rt * 16 + r, j = row / a.group_size, hq = row - j * a.group_size;
+  const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
+  T* out = static_cast<T*>(a.out) +
+           (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + rec.head * a.group_size + hq) * D + d0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) out[i] = from_f32<T>(__fmul_rn(acc[i], inv));
+}
+
+int grid_max(int num_sms) { return num_sms < kMaxSlots ? num_sms : kMaxSlots; }
+
+template <typename T, int D>
+cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
+  const moe_layer_kv_attention_args_t& a = p.a;
+  const int smem = kWarps * kStages * 2 * kSlice * D + (a.batch + 1) * 8;
+  cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_kernel<T, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than pieces of work there can be
+  const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.cache.page_size + kTileTokens - 1) / kTileTokens;
+  const int64_t row_tiles = (static_cast<int64_t>(a.max_q) * a.group_size + 15) / 16;
+  const double most = static_cast<double>(a.batch) * a.cache.kv_heads * row_tiles * (tiles > 0 ? tiles : 1);
+  const int grid = most < grid_max(num_sms) ? static_cast<int>(most) : grid_max(num_sms);
+  AttnParams arg = p;
+  void* args[] = {&arg};
+  e = cudaLaunchKernel((const void*)kv_attention_kernel<T, D>, dim3(grid), dim3(kThreads), args, smem, s);
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernel((const void*)kv_attention_join_kernel<T, D>, dim3(grid, 8), dim3(128), args, 0, s);
+}
+
+}  // namespace
+
+size_t attention_workspace(int head_dim, int num_sms) {
+  const size_t g = grid_max(num_sms);
+  return 2 * g * 16 * (head_dim + 2) * sizeof(float) + g * sizeof(Record) + 256;
+}
+
+cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s) {
+  AttnParams p;
+  p.a = a;
+  const size_t g = grid_max(num_sms);
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = p.part_o + 2 * g * 16 * a.cache.head_dim;
+  p.records = reinterpret_cast<Record*>(p.part_ml + 2 * g * 16 * 2);
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.page_shift = 31 - __builtin_clz(static_cast<unsigned>(a.cache.page_size));
+  if (a.dtype == MOE_LAYER_BF16)
+    return a.cache.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(p, num_sms, s)
+                                  : launch_typed<__nv_bfloat16, 128>(p, num_sms, s);
+  return a.cache.head_dim == 64 ? launch_typed<__half, 64>(p, num_sms, s) : launch_typed<__half, 128>(p, num_sms, s);
+}
+
+}  // namespace moe_layer
