@@ -18,8 +18,8 @@
 // is scaled by a power of two to [1, 2) at its largest element, so bf16 rows
 // are exact in fp16 as far as an fp32 sum can tell.  With x the scores times
 // log2(e), the page scale of K and the row's power of two enter x in fp32;
-// the page scale of V enters the weight exp2(x - max) as its ratio to the
-// largest page scale so far (in [0, 1]), which is rounded to fp16.
+// the page scale of V enters the weight exp2(x - max) as its ratio to a
+// reference page scale, and that product is rounded to fp16.
 // Both matrix products let the k index run over channels (or tokens) in
 // whatever order makes shared-memory reads whole 16-byte chunks: a permuted
 // sum is the same sum.
@@ -30,12 +30,15 @@
 namespace moe_layer {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 3;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSlice = 16;                       // tokens of a warp's ring stage
 constexpr int kTileTokens = kSlice * kWarps;     // tokens of a piece of work
-constexpr int kStages = 5;
-constexpr int kMaxSlots = 1024;                  // CTAs of a launch
+constexpr int kStages = 4;
+constexpr int kMaxSlots = 4096;                  // CTAs of a launch
+// what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces
+constexpr int kUnitCost = 4;
 
 struct Record {  // a unit that several CTAs share, left by the CTA that holds its last piece
   int b, head, rt, c0;  // c0: its first CTA; b < 0: none
@@ -103,7 +106,7 @@ __device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& h
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(const AttnParams p) {
   constexpr int KS = D / 16;                   // k steps of the score product
   constexpr int NT = D / 8;                    // column tiles of the output
   constexpr int kSliceBytes = kSlice * D;      // of K; V follows
@@ -115,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
   const moe_layer_kv_attention_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kRing);  // [batch + 1]
+  int4* shapes = reinterpret_cast<int4*>(smem + kWarps * kRing + (a.batch + 2) / 2 * 16);  // [batch]: q0, qlen, len, tile0
   __shared__ int64_t s_carry[kWarps + 1];
 
   // ---- the work of every sequence, summed
@@ -125,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
     int64_t v = 0;
     if (b < a.batch) {
       const SeqShape s = seq_shape(a, b);
-      v = static_cast<int64_t>(a.cache.kv_heads) * s.row_tiles * s.tiles;
+      v = static_cast<int64_t>(a.cache.kv_heads) * s.row_tiles * (s.tiles + kUnitCost);
+      shapes[b] = make_int4(s.q0, s.qlen, s.len, s.tile0);
     }
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
   const int64_t total = run;
   const int c = blockIdx.x;
   if (tid == 0) p.records[c].b = -1;
-  // CTA c takes pieces [total * c / G, total * (c + 1) / G), at least one of them
+  // CTA c takes costs [total * c / G, total * (c + 1) / G), at least one of them
   const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
   if (c >= G) return;
   int64_t at = total * c / G;
@@ -162,18 +167,85 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
       else hi = mid;
     }
     const int b = lo;
-    const SeqShape s = seq_shape(a, b);
+    SeqShape s;
+    const int4 sh = shapes[b];
+    s.q0 = sh.x, s.qlen = sh.y, s.len = sh.z, s.tile0 = sh.w;
+    s.row_tiles = (s.qlen * a.group_size + 15) / 16;
+    s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.tile0);
+    const int cost = s.tiles + kUnitCost;
     const int64_t rel = at - prefix[b];
-    const int unit = static_cast<int>(rel / s.tiles);
-    const int ta = static_cast<int>(rel - static_cast<int64_t>(unit) * s.tiles);
-    const int tb = static_cast<int>(min(static_cast<int64_t>(s.tiles), ta + (end - at)));
+    const int unit = static_cast<int>(rel / cost);
+    const int xa = static_cast<int>(rel - static_cast<int64_t>(unit) * cost);
+    const int xb = static_cast<int>(min(static_cast<int64_t>(cost), xa + (end - at)));
+    const int ta = max(0, xa - kUnitCost), tb = max(0, xb - kUnitCost);
     const int head = unit / s.row_tiles, rt = unit - head * s.row_tiles;
-    const int64_t unit_begin = at - ta;
-    at += tb - ta;
+    const int64_t first_piece = at - xa + kUnitCost;  // where the unit's first piece lies
+    at += xb - xa;
+    if (tb == ta) continue;
 
-    // ---- rows of this tile: row r is query token r / group of the sequence
     const int rows = min(16, s.qlen * a.group_size - rt * 16);
     const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
+    // keys that any row of the tile sees, cut to this CTA's pieces
+    const int64_t last = pos0 + (rt * 16 + rows - 1) / a.group_size;
+    int64_t k_lo = static_cast<int64_t>(s.tile0 + ta) * kTileTokens;
+    int64_t k_hi = min(static_cast<int64_t>(s.tile0 + tb) * kTileTokens, last + 1);
+    if (a.window > 0) k_lo = max(k_lo, (pos0 + rt * 16 / a.group_size - a.window + 1) & ~static_cast<int64_t>(kSlice - 1));
+    // this warp's slices: first + 8 i, from the slice of k_lo on
+    const int first = static_cast<int>(k_lo / kSlice) + warp;
+    const int n = k_hi > static_cast<int64_t>(first) * kSlice
+                      ? static_cast<int>(((k_hi + kSlice - 1) / kSlice - first + kWarps - 1) / kWarps)
+                      : 0;
+
+    // keys [all_lo, all_hi) are seen by every row of the tile; n_all: slices of
+    // this warp that end there need no mask (rows past the last take part
+    // with zero queries and are not stored)
+    const int64_t all_hi = pos0 + rt * 16 / a.group_size + 1;
+    const int64_t all_lo = a.window > 0 ? last - a.window + 1 : 0;
+
+    // page, and scales, of the slices 32 at a time: lane i holds slice base + i
+    auto look_up = [&](int base, int& page, float& ks, float& vs) {
+      page = -1;
+      ks = vs = 0.0f;
+      const int i = base + lane;
+      if (i < n) {
+        const int64_t tok = static_cast<int64_t>(first + i * kWarps) * kSlice;
+        const int pg = a.page_table[b * a.table_stride + (tok >> p.page_shift)];
+        if (pg >= 0 && pg < a.cache.num_pages) {
+          page = pg;
+          ks = a.cache.k_scale[pg * a.cache.scale_stride + head];
+          vs = a.cache.v_scale[pg * a.cache.scale_stride + head];
+        }
+      }
+    };
+    int page0, page1;
+    float ks0, vs0, ks1, vs1;
+    look_up(0, page0, ks0, vs0);
+    look_up(32, page1, ks1, vs1);
+    const int in_page = a.cache.page_size - 1;
+    // lane offsets of the copies of a slice
+    const int8_t* k_head = a.cache.k + head * a.cache.head_stride + lane * 16;
+    const int8_t* v_head = a.cache.v + head * a.cache.head_stride + lane * 16;
+    uint32_t to[kCopies];
+#pragma unroll
+    for (int x = 0; x < kCopies; ++x) to[x] = chunk_at<D>((x * 32 + lane) / (D / 16), (x * 32 + lane) % (D / 16));
+    auto issue = [&](int i, int rel_i) {  // slice i of this warp, rel_i from the base of page0
+      const int page = rel_i < 32 ? __shfl_sync(0xffffffffu, page0, rel_i & 31) : __shfl_sync(0xffffffffu, page1, rel_i & 31);
+      if (i < n) {
+        const int64_t off = max(page, 0) * a.cache.page_stride + (((first + i * kWarps) * kSlice) & in_page) * D;
+        const int8_t *kp = k_head + off, *vp = v_head + off;
+        const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) {
+          cp_async16(dst + to[x], kp + x * 512, page >= 0);
+          cp_async16(dst + kSliceBytes + to[x], vp + x * 512, page >= 0);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+
+    // ---- rows of this tile: row r is query token r / group of the sequence
     int64_t row_pos[2];
     uint32_t qf[KS][4];
     float row_scale[2];
@@ -215,60 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
         qf[i][2 + r2] = pack2<__half>(__fmul_rn(f1.x, down), __fmul_rn(f1.y, down));
       }
     }
-    // keys that any row of the tile sees, cut to this CTA's pieces
-    const int64_t last = pos0 + (rt * 16 + rows - 1) / a.group_size;
-    int64_t k_lo = static_cast<int64_t>(s.tile0 + ta) * kTileTokens;
-    int64_t k_hi = min(static_cast<int64_t>(s.tile0 + tb) * kTileTokens, last + 1);
-    if (a.window > 0) k_lo = max(k_lo, (pos0 + rt * 16 / a.group_size - a.window + 1) & ~static_cast<int64_t>(kSlice - 1));
-    // this warp's slices: first + 8 i, from the slice of k_lo on
-    const int first = static_cast<int>(k_lo / kSlice) + warp;
-    const int n = k_hi > static_cast<int64_t>(first) * kSlice
-                      ? static_cast<int>(((k_hi + kSlice - 1) / kSlice - first + kWarps - 1) / kWarps)
-                      : 0;
-
     float o[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 0.0f;
-
-    // page, and scales, of the slices 32 at a time: lane i holds slice base + i
-    auto look_up = [&](int base, int& page, float& ks, float& vs) {
-      page = -1;
-      ks = vs = 0.0f;
-      const int i = base + lane;
-      if (i < n) {
-        const int64_t tok = static_cast<int64_t>(first + i * kWarps) * kSlice;
-        const int pg = a.page_table[b * a.table_stride + (tok >> p.page_shift)];
-        if (pg >= 0 && pg < a.cache.num_pages) {
-          page = pg;
-          ks = a.cache.k_scale[pg * a.cache.scale_stride + head];
-          vs = a.cache.v_scale[pg * a.cache.scale_stride + head];
-        }
-      }
-    };
-    int page0, page1;
-    float ks0, vs0, ks1, vs1;
-    look_up(0, page0, ks0, vs0);
-    look_up(32, page1, ks1, vs1);
-    const int in_page = a.cache.page_size - 1;
-    auto issue = [&](int i, int rel_i) {  // slice i of this warp, rel_i from the base of page0
-      const int page = rel_i < 32 ? __shfl_sync(0xffffffffu, page0, rel_i & 31) : __shfl_sync(0xffffffffu, page1, rel_i & 31);
-      if (i < n) {
-        const int64_t tok = static_cast<int64_t>(first + i * kWarps) * kSlice;
-        const int64_t off = max(page, 0) * a.cache.page_stride + head * a.cache.head_stride +
-                            (static_cast<int>(tok) & in_page) * D;
-        const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
-#pragma unroll
-        for (int x = 0; x < kCopies; ++x) {
-          const int ch = x * 32 + lane, r = ch / (D / 16), cc = ch % (D / 16);
-          cp_async16(dst + chunk_at<D>(r, cc), a.cache.k + off + ch * 16, page >= 0);
-          cp_async16(dst + kSliceBytes + chunk_at<D>(r, cc), a.cache.v + off + ch * 16, page >= 0);
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 0.0f, vinv = 1.0f;
 
     for (int i = 0; i < n; ++i) {
       const int ri = i & 31;
@@ -304,46 +326,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
           mma16816<__half>(sc[h], qf[q][0], qf[q][1], qf[q][2], qf[q][3], b0, b1);
         }
       }
-      // x = score * scales * log2(e), masked
+      // x = score * scales * log2(e), masked where a row does not see the whole slice
+      const float f0 = __fmul_rn(ks, row_scale[0]), f1 = __fmul_rn(ks, row_scale[1]);
       float top[2] = {-INFINITY, -INFINITY};
+      const bool whole = page >= 0 && tok0 >= all_lo && tok0 + kSlice <= all_hi;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r2 = e >> 1;
-          const int64_t key = tok0 + h * 8 + token_of<D>(2 * t + (e & 1));
-          const bool seen = page >= 0 && key <= row_pos[r2] && (a.window <= 0 || key > row_pos[r2] - a.window);
-          const float x = seen ? __fmul_rn(sc[h][e], __fmul_rn(ks, row_scale[r2])) : -INFINITY;
-          sc[h][e] = x;
-          top[r2] = fmaxf(top[r2], x);
-        }
-      // largest page scale of V so far; the weights carry the ratio to it
-      const float vnew = fmaxf(vref, fabsf(vs));
-      const float vcorr = vnew > vref ? __fdiv_rn(vref, vnew) : 1.0f;
-      const float vw = vnew > 0.0f ? __fdiv_rn(vs, vnew) : vs;
-      vref = vnew;
-      float corr[2];
-#pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2) {
-        top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 1));
-        top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 2));
-        const float mn = fmaxf(m[r2], top[r2]);
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        corr[r2] = exp2_fast(__fsub_rn(m[r2], base));
-        m[r2] = mn;
-        float sum = 0.0f;
+        for (int e = 0; e < 4; ++e) sc[h][e] = __fmul_rn(sc[h][e], e < 2 ? f0 : f1);
+      if (!whole) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float w = exp2_fast(__fsub_rn(sc[h][2 * r2 + e], base));
-            sum = __fadd_rn(sum, w);
-            sc[h][2 * r2 + e] = __fmul_rn(w, vw);
+          for (int e = 0; e < 4; ++e) {
+            const int64_t key = tok0 + h * 8 + token_of<D>(2 * t + (e & 1)), pos = row_pos[e >> 1];
+            if (page < 0 || key > pos || (a.window > 0 && key <= pos - a.window)) sc[h][e] = -INFINITY;
           }
-        l[r2] = __fmaf_rn(l[r2], corr[r2], sum);
-        corr[r2] = __fmul_rn(corr[r2], vcorr);
       }
-      if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+      for (int r2 = 0; r2 < 2; ++r2)
+        top[r2] = fmaxf(fmaxf(sc[0][2 * r2], sc[0][2 * r2 + 1]), fmaxf(sc[1][2 * r2], sc[1][2 * r2 + 1]));
+      // The references of the weights move only when a weight would pass 2^8
+      // (a page scale of V 8 times its reference): weights of up to 2^11 are
+      // as exact in fp16 as weights up to 1, and most slices rescale nothing.
+      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f || !(fabsf(vs) <= 8.0f * vref))) {
+        const float vnew = fmaxf(vref, fabsf(vs));
+        const float vcorr = vnew > vref ? __fdiv_rn(vref, vnew) : 1.0f;
+        vref = vnew;
+        vinv = vnew > 0.0f ? __fdiv_rn(1.0f, vnew) : 1.0f;
+        float corr[2];
+#pragma unroll
+        for (int r2 = 0; r2 < 2; ++r2) {
+          top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 1));
+          top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 2));
+          const float mn = fmaxf(m[r2], top[r2]);
+          corr[r2] = mn == m[r2] ? 1.0f : exp2_fast(__fsub_rn(m[r2], mn));
+          m[r2] = mn;
+          l[r2] = __fmul_rn(l[r2], corr[r2]);
+          corr[r2] = __fmul_rn(corr[r2], vcorr);
+        }
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
           o[q][0] = __fmul_rn(o[q][0], corr[0]);
@@ -351,6 +372,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
           o[q][2] = __fmul_rn(o[q][2], corr[1]);
           o[q][3] = __fmul_rn(o[q][3], corr[1]);
         }
+      }
+      const float vw = __fmul_rn(vs, vinv);
+#pragma unroll
+      for (int r2 = 0; r2 < 2; ++r2) {
+        const float base = m[r2] == -INFINITY ? 0.0f : m[r2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w = exp2_fast(__fsub_rn(sc[h][2 * r2 + e], base));
+            l[r2] = __fadd_rn(l[r2], w);
+            sc[h][2 * r2 + e] = __fmul_rn(w, vw);
+          }
       }
       const uint32_t a0 = pack2<__half>(sc[0][0], sc[0][1]), a1 = pack2<__half>(sc[0][2], sc[0][3]);
       const uint32_t a2 = pack2<__half>(sc[1][0], sc[1][1]), a3 = pack2<__half>(sc[1][2], sc[1][3]);
@@ -404,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
       wm[16 + g] = l[0], wm[24 + g] = l[1];
     }
     __syncthreads();
-    const int r = tid >> 4;  // 16 threads a row
-    constexpr int kEach = D / 16;
+    constexpr int kPerRow = kThreads / 16, kEach = D / kPerRow;
+    const int r = tid / kPerRow;
     float top = -INFINITY;
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, reinterpret_cast<float*>(smem + w * kRing)[16 * D + r]);
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, acc[kEach] = {};
-    const int d0 = (tid & 15) * kEach;
+    const int d0 = (tid % kPerRow) * kEach;
     for (int w = 0; w < kWarps; ++w) {
       const float* from = reinterpret_cast<float*>(smem + w * kRing);
       const float f = exp2_fast(__fsub_rn(from[16 * D + r], base));
@@ -433,15 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
       float* po = p.part_o + (slot * 16 + r) * D + d0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) po[i] = acc[i];
-      if ((tid & 15) == 0) {
+      if (tid % kPerRow == 0) {
         p.part_ml[(slot * 16 + r) * 2] = top;
         p.part_ml[(slot * 16 + r) * 2 + 1] = sum;
       }
       if (tb == s.tiles && tid == 0) {
-        // the CTA of a piece x is the last c with total * c / G <= x
-        int64_t c0 = unit_begin * G / total;
-        while (c0 + 1 < G && total * (c0 + 1) / G <= unit_begin) ++c0;
-        while (c0 > 0 && total * c0 / G > unit_begin) --c0;
+        // the CTA of x is the last c with total * c / G <= x
+        int64_t c0 = first_piece * G / total;
+        while (c0 + 1 < G && total * (c0 + 1) / G <= first_piece) ++c0;
+        while (c0 > 0 && total * c0 / G > first_piece) --c0;
         p.records[c] = Record{b, head, rt, static_cast<int>(c0)};
       }
     }
@@ -449,58 +483,87 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const AttnPar
   }
 }
 
-// Joins the parts of a unit that several CTAs shared, in CTA order.  CTA
-// (c, y) takes rows 2 y and 2 y + 1 of the unit that CTA c finished.
+// Joins the parts of a unit that several CTAs shared.  CTA (c, y) takes rows
+// 4 y .. 4 y + 3 of the unit that CTA c finished, four warps a row: warp i
+// sums every fourth part, a lane D / 32 channels, and the four sums are added
+// in a fixed order.  The maxima are read first, so that the parts' loads
+// depend on nothing but their addresses.
+constexpr int kJoinWarps = 4;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv_attention_join_kernel(const AttnParams p) {
-  const int c = blockIdx.x;
+__global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(const AttnParams p) {
+  constexpr int kEach = D / 32;
+  __shared__ float s_acc[4][kJoinWarps][D];
+  __shared__ float s_sum[4][kJoinWarps];
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r4 = warp / kJoinWarps, part = warp % kJoinWarps, r = blockIdx.y * 4 + r4;
   const Record rec = p.records[c];
   if (rec.b < 0) return;
   const moe_layer_kv_attention_args_t& a = p.a;
-  const SeqShape s = seq_shape(a, rec.b);
-  const int rows = min(16, s.qlen * a.group_size - rec.rt * 16);
-  constexpr int kEach = D / 64;  // 64 threads a row
-  const int r = blockIdx.y * 2 + threadIdx.x / 64, d0 = (threadIdx.x % 64) * kEach;
-  if (r >= rows) return;
-  float top = -INFINITY, sum = 0.0f, acc[kEach] = {};
-  for (int x = rec.c0; x <= c; ++x) {
-    const int64_t slot = 2 * static_cast<int64_t>(x) + (x == rec.c0 ? 1 : 0);
-    const float m = p.part_ml[(slot * 16 + r) * 2], l = p.part_ml[(slot * 16 + r) * 2 + 1];
-    const float mn = fmaxf(top, m), base = mn == -INFINITY ? 0.0f : mn;
-    const float f0 = exp2_fast(__fsub_rn(top, base)), f1 = exp2_fast(__fsub_rn(m, base));
-    top = mn;
-    sum = __fmaf_rn(l, f1, __fmul_rn(sum, f0));
+  const int np = c - rec.c0 + 1;
+  // the first CTA left its part in slot 1, the others in slot 0
+  auto slot_row = [&](int i) { return (2 * static_cast<int64_t>(rec.c0 + i) + (i == 0 ? 1 : 0)) * 16 + r; };
+  float top = -INFINITY;
+  for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_ml[slot_row(i) * 2]);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      acc[i] = __fmaf_rn(p.part_o[(slot * 16 + r) * D + d0 + i], f1, __fmul_rn(acc[i], f0));
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, acc[kEach] = {};
+#pragma unroll 4
+  for (int i = part; i < np; i += kJoinWarps) {
+    const int64_t at = slot_row(i);
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+    const float f = exp2_fast(__fsub_rn(ml.x, base));
+    sum = __fmaf_rn(ml.y, f, sum);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] = __fmaf_rn(p.part_o[at * D + lane * kEach + e], f, acc[e]);
   }
-  const int row = rec.rt * 16 + r, j = row / a.group_size, hq = row - j * a.group_size;
-  const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
-  T* out = static_cast<T*>(a.out) +
-           (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + rec.head * a.group_size + hq) * D + d0;
+  if (lane == 0) s_sum[r4][part] = sum;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) out[i] = from_f32<T>(__fmul_rn(acc[i], inv));
+  for (int e = 0; e < kEach; ++e) s_acc[r4][part][lane * kEach + e] = acc[e];
+  __syncthreads();
+  const SeqShape s = seq_shape(a, rec.b);
+  if (part != 0 || r >= min(16, s.qlen * a.group_size - rec.rt * 16)) return;
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum = __fadd_rn(sum, s_sum[r4][w]);
+  const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
+  const int row = rec.rt * 16 + r, j = row / a.group_size, hq = row - j * a.group_size;
+  T* out = static_cast<T*>(a.out) +
+           (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + rec.head * a.group_size + hq) * D;
+#pragma unroll
+  for (int e = 0; e < kEach; e += 2) {
+    float v[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      v[z] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) v[z] = __fadd_rn(v[z], s_acc[r4][w][lane * kEach + e + z]);
+    }
+    *reinterpret_cast<uint32_t*>(out + lane * kEach + e) = pack2<T>(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv));
+  }
 }
 
-int grid_max(int num_sms) { return num_sms < kMaxSlots ? num_sms : kMaxSlots; }
+int grid_max(int num_sms) { return num_sms * kCtasPerSm < kMaxSlots ? num_sms * kCtasPerSm : kMaxSlots; }
 
 template <typename T, int D>
 cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
   const moe_layer_kv_attention_args_t& a = p.a;
-  const int smem = kWarps * kStages * 2 * kSlice * D + (a.batch + 1) * 8;
+  const int smem = kWarps * kStages * 2 * kSlice * D + (a.batch + 2) / 2 * 16 + a.batch * 16;
   cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // no more CTAs than pieces of work there can be
   const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.cache.page_size + kTileTokens - 1) / kTileTokens;
   const int64_t row_tiles = (static_cast<int64_t>(a.max_q) * a.group_size + 15) / 16;
-  const double most = static_cast<double>(a.batch) * a.cache.kv_heads * row_tiles * (tiles > 0 ? tiles : 1);
+  const double most = static_cast<double>(a.batch) * a.cache.kv_heads * row_tiles * ((tiles > 0 ? tiles : 1) + kUnitCost);
   const int grid = most < grid_max(num_sms) ? static_cast<int>(most) : grid_max(num_sms);
   AttnParams arg = p;
   void* args[] = {&arg};
   e = cudaLaunchKernel((const void*)kv_attention_kernel<T, D>, dim3(grid), dim3(kThreads), args, smem, s);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernel((const void*)kv_attention_join_kernel<T, D>, dim3(grid, 8), dim3(128), args, 0, s);
+  const int rows = static_cast<int64_t>(a.max_q) * a.group_size < 16 ? a.max_q * a.group_size : 16;
+  return cudaLaunchKernel((const void*)kv_attention_join_kernel<T, D>, dim3(grid, (rows + 3) / 4),
+                          dim3(kJoinWarps * 4 * 32), args, 0, s);
 }
 
 }  // namespace
