@@ -31,12 +31,15 @@ namespace moe_layer {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 3;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSlice = 16;                       // tokens of a warp's ring stage
 constexpr int kTileTokens = kSlice * kWarps;     // tokens of a piece of work
-constexpr int kStages = 4;
-constexpr int kMaxSlots = 4096;                  // CTAs of a launch
+// NR: blocks of 8 query rows that a unit holds.  One block leaves registers for 16 warps on an SM, two for 12.
+template <int NR>
+constexpr int kCtasPerSm = NR == 1 ? 4 : 3;
+template <int NR>
+constexpr int kStagesOf = NR == 1 ? 3 : 4;
+constexpr int kMaxSlots = 4096;                  // CTAs of a launch (at most 4 an SM)
 // what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces
 constexpr int kUnitCost = 4;
 
@@ -61,6 +64,7 @@ struct SeqShape {
   int tile0, tiles; // pieces of kTileTokens that its rows see; tiles >= 1
 };
 
+template <int NR>
 __device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_t& a, int b) {
   SeqShape s;
   if (a.cu_q) {
@@ -72,7 +76,7 @@ __device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_
   }
   const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
   s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
-  s.row_tiles = (s.qlen * a.group_size + 15) / 16;
+  s.row_tiles = (s.qlen * a.group_size + 8 * NR - 1) / (8 * NR);
   int lo = 0;
   if (a.window > 0) lo = max(0, static_cast<int>(static_cast<int64_t>(s.len) - s.qlen - a.window + 1));
   s.tile0 = lo / kTileTokens;
@@ -105,15 +109,24 @@ __device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& h
   hi = *reinterpret_cast<const uint32_t*>(&b);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(const AttnParams p) {
+// 8x8 matrix of 16-bit elements, transposed: lane 4 g + t gives (g, 2t..2t+1) and gets (2t..2t+1, g)
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(const AttnParams p) {
   constexpr int KS = D / 16;                   // k steps of the score product
-  constexpr int NT = D / 8;                    // column tiles of the output
+  constexpr int NT = D / 16;                   // channel tiles of the output
+  constexpr int R = 8 * NR;                    // rows of a unit
+  constexpr int kStages = kStagesOf<NR>;
   constexpr int kSliceBytes = kSlice * D;      // of K; V follows
   constexpr int kStageBytes = 2 * kSliceBytes;
   constexpr int kRing = kStages * kStageBytes;
   constexpr int kCopies = kSliceBytes / 16 / 32;  // 16-byte copies of a lane for K (and for V)
-  static_assert(kRing >= 16 * D * 4 + 256, "the join reuses the ring");
+  static_assert(kRing >= R * D * 4 + 8 * R, "the join reuses the ring");
   extern __shared__ __align__(128) uint8_t smem[];
   const moe_layer_kv_attention_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -128,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
     const int b = base + tid;
     int64_t v = 0;
     if (b < a.batch) {
-      const SeqShape s = seq_shape(a, b);
+      const SeqShape s = seq_shape<NR>(a, b);
       v = static_cast<int64_t>(a.cache.kv_heads) * s.row_tiles * (s.tiles + kUnitCost);
       shapes[b] = make_int4(s.q0, s.qlen, s.len, s.tile0);
     }
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
     SeqShape s;
     const int4 sh = shapes[b];
     s.q0 = sh.x, s.qlen = sh.y, s.len = sh.z, s.tile0 = sh.w;
-    s.row_tiles = (s.qlen * a.group_size + 15) / 16;
+    s.row_tiles = (s.qlen * a.group_size + 8 * NR - 1) / (8 * NR);
     s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.tile0);
     const int cost = s.tiles + kUnitCost;
     const int64_t rel = at - prefix[b];
@@ -183,13 +196,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
     at += xb - xa;
     if (tb == ta) continue;
 
-    const int rows = min(16, s.qlen * a.group_size - rt * 16);
+    const int rows = min(R, s.qlen * a.group_size - rt * R);
     const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
     // keys that any row of the tile sees, cut to this CTA's pieces
-    const int64_t last = pos0 + (rt * 16 + rows - 1) / a.group_size;
+    const int64_t last = pos0 + (rt * R + rows - 1) / a.group_size;
     int64_t k_lo = static_cast<int64_t>(s.tile0 + ta) * kTileTokens;
     int64_t k_hi = min(static_cast<int64_t>(s.tile0 + tb) * kTileTokens, last + 1);
-    if (a.window > 0) k_lo = max(k_lo, (pos0 + rt * 16 / a.group_size - a.window + 1) & ~static_cast<int64_t>(kSlice - 1));
+    if (a.window > 0) k_lo = max(k_lo, (pos0 + rt * R / a.group_size - a.window + 1) & ~static_cast<int64_t>(kSlice - 1));
     // this warp's slices: first + 8 i, from the slice of k_lo on
     const int first = static_cast<int>(k_lo / kSlice) + warp;
     const int n = k_hi > static_cast<int64_t>(first) * kSlice
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
     // keys [all_lo, all_hi) are seen by every row of the tile; n_all: slices of
     // this warp that end there need no mask (rows past the last take part
     // with zero queries and are not stored)
-    const int64_t all_hi = pos0 + rt * 16 / a.group_size + 1;
+    const int64_t all_hi = pos0 + rt * R / a.group_size + 1;
     const int64_t all_lo = a.window > 0 ? last - a.window + 1 : 0;
 
     // page, and scales, of the slices 32 at a time: lane i holds slice base + i
@@ -246,15 +259,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
     for (int i = 0; i < kStages - 1; ++i) issue(i, i);
 
     // ---- rows of this tile: row r is query token r / group of the sequence
-    int64_t row_pos[2];
-    uint32_t qf[KS][4];
-    float row_scale[2];
+    int row_pos[NR][2];          // positions of rows 2t and 2t + 1 of each block, -1 past the last row
+    float row_scale[NR][2];
+    uint32_t qf[NR][KS][2];
 #pragma unroll
-    for (int r2 = 0; r2 < 2; ++r2) {
-      const int r = g + 8 * r2, row = rt * 16 + r;
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = g + 8 * nr, row = rt * R + r;
       const int j = row / a.group_size, hq = row - j * a.group_size;
-      row_pos[r2] = r < rows ? pos0 + j : -1;
-      // lane t holds channels [t D / 4, (t + 1) D / 4) of the row
+      // lane t holds channels [t D / 4, (t + 1) D / 4) of row g of the block
       uint32_t w[KS * 2];
       if (r < rows) {
         const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(s.q0 + j) * a.q_stride +
@@ -279,18 +291,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
       // exponent of the largest element, inside what 2^-e can hold
       const int e = min(max(static_cast<int>(top >> 23), 1), 253);
       const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
-      row_scale[r2] = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
+      const float up = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const float2 f0 = unpack2<T>(w[2 * i]), f1 = unpack2<T>(w[2 * i + 1]);
-        qf[i][r2] = pack2<__half>(__fmul_rn(f0.x, down), __fmul_rn(f0.y, down));
-        qf[i][2 + r2] = pack2<__half>(__fmul_rn(f1.x, down), __fmul_rn(f1.y, down));
+        qf[nr][i][0] = pack2<__half>(__fmul_rn(f0.x, down), __fmul_rn(f0.y, down));
+        qf[nr][i][1] = pack2<__half>(__fmul_rn(f1.x, down), __fmul_rn(f1.y, down));
+      }
+      const int pos = r < rows ? static_cast<int>(max(pos0 + j, static_cast<int64_t>(-1))) : -1;
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        row_scale[nr][e2] = __shfl_sync(0xffffffffu, up, (2 * t + e2) * 4);
+        row_pos[nr][e2] = __shfl_sync(0xffffffffu, pos, (2 * t + e2) * 4);
       }
     }
-    float o[NT][4];
+    float o[NR][NT][4];  // transposed: channels g D / 8 + 2 i and + 1 of column tile i, rows 2t and 2t + 1
+    float m[NR][2], l[NR][2], vref = 0.0f, vinv = 1.0f;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 0.0f, vinv = 1.0f;
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.0f;
+      m[nr][0] = m[nr][1] = -INFINITY;
+      l[nr][0] = l[nr][1] = 0.0f;
+    }
 
     for (int i = 0; i < n; ++i) {
       const int ri = i & 31;
@@ -305,91 +328,104 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
       const float ks = __shfl_sync(0xffffffffu, ks0, ri), vs = __shfl_sync(0xffffffffu, vs0, ri);
       const int64_t tok0 = static_cast<int64_t>(first + i * kWarps) * kSlice;
 
-      // scores of 16 rows x 16 tokens
-      float sc[2][4];
+      // scores, transposed: 16 tokens x 8 NR rows, in two chains of products
+      float sc[NR][4], s2[NR][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.0f;
-        const int r = h * 8 + token_of<D>(g);
-        uint32_t w[KS];
-        if constexpr (D == 128) {
-          const uint4 x = lds128(kb + chunk_at<D>(r, 2 * t)), y = lds128(kb + chunk_at<D>(r, 2 * t + 1));
-          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-        } else {
-          const uint4 x = lds128(kb + chunk_at<D>(r, t));
-          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nr][e] = s2[nr][e] = 0.0f;
+      {
+        uint32_t w[2][KS];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = h * 8 + token_of<D>(g);
+          if constexpr (D == 128) {
+            const uint4 x = lds128(kb + chunk_at<D>(r, 2 * t)), y = lds128(kb + chunk_at<D>(r, 2 * t + 1));
+            w[h][0] = x.x, w[h][1] = x.y, w[h][2] = x.z, w[h][3] = x.w;
+            w[h][4] = y.x, w[h][5] = y.y, w[h][6] = y.z, w[h][7] = y.w;
+          } else {
+            const uint4 x = lds128(kb + chunk_at<D>(r, t));
+            w[h][0] = x.x, w[h][1] = x.y, w[h][2] = x.z, w[h][3] = x.w;
+          }
         }
 #pragma unroll
         for (int q = 0; q < KS; ++q) {
-          uint32_t b0, b1;
-          half_pairs(w[q], b0, b1);
-          mma16816<__half>(sc[h], qf[q][0], qf[q][1], qf[q][2], qf[q][3], b0, b1);
+          uint32_t a0, a1, a2, a3;
+          half_pairs(w[0][q], a0, a2);
+          half_pairs(w[1][q], a1, a3);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+            mma16816<__half>(q & 1 ? s2[nr] : sc[nr], a0, a1, a2, a3, qf[nr][q][0], qf[nr][q][1]);
         }
       }
       // x = score * scales * log2(e), masked where a row does not see the whole slice
-      const float f0 = __fmul_rn(ks, row_scale[0]), f1 = __fmul_rn(ks, row_scale[1]);
-      float top[2] = {-INFINITY, -INFINITY};
       const bool whole = page >= 0 && tok0 >= all_lo && tok0 + kSlice <= all_hi;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[h][e] = __fmul_rn(sc[h][e], e < 2 ? f0 : f1);
+        for (int e = 0; e < 4; ++e)
+          sc[nr][e] = __fmul_rn(__fadd_rn(sc[nr][e], s2[nr][e]), __fmul_rn(ks, row_scale[nr][e & 1]));
       if (!whole) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int64_t key = tok0 + h * 8 + token_of<D>(2 * t + (e & 1)), pos = row_pos[e >> 1];
-            if (page < 0 || key > pos || (a.window > 0 && key <= pos - a.window)) sc[h][e] = -INFINITY;
+            const int64_t key = tok0 + (e >> 1) * 8 + token_of<D>(g), pos = row_pos[nr][e & 1];
+            if (page < 0 || key > pos || (a.window > 0 && key <= pos - a.window)) sc[nr][e] = -INFINITY;
           }
       }
-#pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2)
-        top[r2] = fmaxf(fmaxf(sc[0][2 * r2], sc[0][2 * r2 + 1]), fmaxf(sc[1][2 * r2], sc[1][2 * r2 + 1]));
       // The references of the weights move only when a weight would pass 2^8
       // (a page scale of V 8 times its reference): weights of up to 2^11 are
       // as exact in fp16 as weights up to 1, and most slices rescale nothing.
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f || !(fabsf(vs) <= 8.0f * vref))) {
+      float top[NR][2];
+      bool move = !(fabsf(vs) <= 8.0f * vref);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nr][e] = fmaxf(sc[nr][e], sc[nr][2 + e]);
+          move |= top[nr][e] > m[nr][e] + 8.0f;
+        }
+      if (__any_sync(0xffffffffu, move)) {
         const float vnew = fmaxf(vref, fabsf(vs));
         const float vcorr = vnew > vref ? __fdiv_rn(vref, vnew) : 1.0f;
         vref = vnew;
         vinv = vnew > 0.0f ? __fdiv_rn(1.0f, vnew) : 1.0f;
-        float corr[2];
 #pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2) {
-          top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 1));
-          top[r2] = fmaxf(top[r2], __shfl_xor_sync(0xffffffffu, top[r2], 2));
-          const float mn = fmaxf(m[r2], top[r2]);
-          corr[r2] = mn == m[r2] ? 1.0f : exp2_fast(__fsub_rn(m[r2], mn));
-          m[r2] = mn;
-          l[r2] = __fmul_rn(l[r2], corr[r2]);
-          corr[r2] = __fmul_rn(corr[r2], vcorr);
-        }
+        for (int nr = 0; nr < NR; ++nr) {
+          float corr[2];
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          o[q][0] = __fmul_rn(o[q][0], corr[0]);
-          o[q][1] = __fmul_rn(o[q][1], corr[0]);
-          o[q][2] = __fmul_rn(o[q][2], corr[1]);
-          o[q][3] = __fmul_rn(o[q][3], corr[1]);
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top[nr][e] = fmaxf(top[nr][e], __shfl_xor_sync(0xffffffffu, top[nr][e], x));
+            const float mn = fmaxf(m[nr][e], top[nr][e]);
+            corr[e] = mn == m[nr][e] ? 1.0f : exp2_fast(__fsub_rn(m[nr][e], mn));
+            m[nr][e] = mn;
+            l[nr][e] = __fmul_rn(l[nr][e], corr[e]);
+            corr[e] = __fmul_rn(corr[e], vcorr);
+          }
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nr][q][e] = __fmul_rn(o[nr][q][e], corr[e & 1]);
         }
       }
       const float vw = __fmul_rn(vs, vinv);
+      uint32_t pb[NR][2];  // weights: tokens 2t.. (and 2t + 8..) of row g
 #pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2) {
-        const float base = m[r2] == -INFINITY ? 0.0f : m[r2];
+      for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float w = exp2_fast(__fsub_rn(sc[h][2 * r2 + e], base));
-            l[r2] = __fadd_rn(l[r2], w);
-            sc[h][2 * r2 + e] = __fmul_rn(w, vw);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[nr][e & 1];
+          const float w = exp2_fast(__fsub_rn(sc[nr][e], ref == -INFINITY ? 0.0f : ref));
+          l[nr][e & 1] = __fadd_rn(l[nr][e & 1], w);
+          sc[nr][e] = __fmul_rn(w, vw);
+        }
+        pb[nr][0] = transpose8x8(pack2<__half>(sc[nr][0], sc[nr][1]));
+        pb[nr][1] = transpose8x8(pack2<__half>(sc[nr][2], sc[nr][3]));
       }
-      const uint32_t a0 = pack2<__half>(sc[0][0], sc[0][1]), a1 = pack2<__half>(sc[0][2], sc[0][3]);
-      const uint32_t a2 = pack2<__half>(sc[1][0], sc[1][1]), a3 = pack2<__half>(sc[1][2], sc[1][3]);
-      // values: lane column g holds channels [g D / 8, (g + 1) D / 8), one a column tile
-      uint32_t w[4][NT / 4];
+      // values: lane row g holds channels [g D / 8, (g + 1) D / 8), two a channel tile
+      uint32_t w[4][NT / 2];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = (q >> 1) * 8 + token_of<D>(2 * t + (q & 1));
@@ -402,59 +438,63 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
         }
       }
 #pragma unroll
-      for (int q = 0; q < NT / 4; ++q) {
+      for (int q = 0; q < NT / 2; ++q) {
         // bytes of tokens (2t, 2t + 1) side by side, then (2t + 8, 2t + 9)
         uint32_t lo0, lo1, lo2, lo3, hi0, hi1, hi2, hi3;
         half_pairs(__byte_perm(w[0][q], w[1][q], 0x5140), lo0, lo1);
         half_pairs(__byte_perm(w[0][q], w[1][q], 0x7362), lo2, lo3);
         half_pairs(__byte_perm(w[2][q], w[3][q], 0x5140), hi0, hi1);
         half_pairs(__byte_perm(w[2][q], w[3][q], 0x7362), hi2, hi3);
-        mma16816<__half>(o[4 * q], a0, a1, a2, a3, lo0, hi0);
-        mma16816<__half>(o[4 * q + 1], a0, a1, a2, a3, lo1, hi1);
-        mma16816<__half>(o[4 * q + 2], a0, a1, a2, a3, lo2, hi2);
-        mma16816<__half>(o[4 * q + 3], a0, a1, a2, a3, lo3, hi3);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          mma16816<__half>(o[nr][2 * q], lo0, lo1, hi0, hi1, pb[nr][0], pb[nr][1]);
+          mma16816<__half>(o[nr][2 * q + 1], lo2, lo3, hi2, hi3, pb[nr][0], pb[nr][1]);
+        }
       }
       __syncwarp();  // the stage is read before it is filled again
       issue(i + kStages - 1, ri + kStages - 1);
     }
     cp_async_wait<0>();
 #pragma unroll
-    for (int r2 = 0; r2 < 2; ++r2) {
-      l[r2] += __shfl_xor_sync(0xffffffffu, l[r2], 1);
-      l[r2] += __shfl_xor_sync(0xffffffffu, l[r2], 2);
-    }
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], x);
     __syncwarp();
 
-    // ---- join the warps: O [16][D], then m [16], l [16] in each warp's ring
+    // ---- join the warps: O [R][D], then m [R], l [R] in each warp's ring
     float* wo = reinterpret_cast<float*>(ring);
-    float* wm = wo + 16 * D;
+    float* wm = wo + R * D;
 #pragma unroll
-    for (int q = 0; q < NT; ++q)
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        wo[(g + 8 * (e >> 1)) * D + (2 * t + (e & 1)) * NT + q] = __fmul_rn(o[q][e], vref);
-    if (t == 0) {
-      wm[g] = m[0], wm[g + 8] = m[1];
-      wm[16 + g] = l[0], wm[24 + g] = l[1];
-    }
+      for (int e = 0; e < 2; ++e) {
+        const int r = nr * 8 + 2 * t + e;
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+          *reinterpret_cast<float2*>(wo + r * D + g * (D / 8) + 2 * q) =
+              make_float2(__fmul_rn(o[nr][q][e], vref), __fmul_rn(o[nr][q][2 + e], vref));
+        if (g == 0) wm[r] = m[nr][e], wm[R + r] = l[nr][e];
+      }
     __syncthreads();
-    constexpr int kPerRow = kThreads / 16, kEach = D / kPerRow;
+    constexpr int kPerRow = kThreads / R, kEach = D / kPerRow;
     const int r = tid / kPerRow;
     float top = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, reinterpret_cast<float*>(smem + w * kRing)[16 * D + r]);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, reinterpret_cast<float*>(smem + w * kRing)[R * D + r]);
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, acc[kEach] = {};
     const int d0 = (tid % kPerRow) * kEach;
     for (int w = 0; w < kWarps; ++w) {
       const float* from = reinterpret_cast<float*>(smem + w * kRing);
-      const float f = exp2_fast(__fsub_rn(from[16 * D + r], base));
-      sum = __fmaf_rn(from[16 * D + 16 + r], f, sum);
+      const float f = exp2_fast(__fsub_rn(from[R * D + r], base));
+      sum = __fmaf_rn(from[R * D + R + r], f, sum);
 #pragma unroll
       for (int i = 0; i < kEach; ++i) acc[i] = __fmaf_rn(from[r * D + d0 + i], f, acc[i]);
     }
     if (ta == 0 && tb == s.tiles) {
       if (r < rows) {
-        const int row = rt * 16 + r, j = row / a.group_size, hq = row - j * a.group_size;
+        const int row = rt * R + r, j = row / a.group_size, hq = row - j * a.group_size;
         const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
         T* out = static_cast<T*>(a.out) +
                  (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + head * a.group_size + hq) * D + d0;
@@ -489,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attention_kernel(cons
 // in a fixed order.  The maxima are read first, so that the parts' loads
 // depend on nothing but their addresses.
 constexpr int kJoinWarps = 4;
-template <typename T, int D>
+template <typename T, int D, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(const AttnParams p) {
   constexpr int kEach = D / 32;
   __shared__ float s_acc[4][kJoinWarps][D];
@@ -521,13 +561,13 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
 #pragma unroll
   for (int e = 0; e < kEach; ++e) s_acc[r4][part][lane * kEach + e] = acc[e];
   __syncthreads();
-  const SeqShape s = seq_shape(a, rec.b);
-  if (part != 0 || r >= min(16, s.qlen * a.group_size - rec.rt * 16)) return;
+  const SeqShape s = seq_shape<NR>(a, rec.b);
+  if (part != 0 || r >= min(8 * NR, s.qlen * a.group_size - rec.rt * 8 * NR)) return;
   sum = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) sum = __fadd_rn(sum, s_sum[r4][w]);
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
-  const int row = rec.rt * 16 + r, j = row / a.group_size, hq = row - j * a.group_size;
+  const int row = rec.rt * 8 * NR + r, j = row / a.group_size, hq = row - j * a.group_size;
   T* out = static_cast<T*>(a.out) +
            (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + rec.head * a.group_size + hq) * D;
 #pragma unroll
@@ -543,40 +583,48 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
   }
 }
 
-int grid_max(int num_sms) { return num_sms * kCtasPerSm < kMaxSlots ? num_sms * kCtasPerSm : kMaxSlots; }
+int grid_max(int num_sms, int per_sm) { return num_sms * per_sm < kMaxSlots ? num_sms * per_sm : kMaxSlots; }
 
-template <typename T, int D>
-cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
+template <typename T, int D, int NR>
+cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   const moe_layer_kv_attention_args_t& a = p.a;
-  const int smem = kWarps * kStages * 2 * kSlice * D + (a.batch + 2) / 2 * 16 + a.batch * 16;
-  cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_kernel<T, D>,
+  const int smem = kWarps * kStagesOf<NR> * 2 * kSlice * D + (a.batch + 2) / 2 * 16 + a.batch * 16;
+  cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_kernel<T, D, NR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // no more CTAs than pieces of work there can be
   const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.cache.page_size + kTileTokens - 1) / kTileTokens;
-  const int64_t row_tiles = (static_cast<int64_t>(a.max_q) * a.group_size + 15) / 16;
-  const double most = static_cast<double>(a.batch) * a.cache.kv_heads * row_tiles * ((tiles > 0 ? tiles : 1) + kUnitCost);
-  const int grid = most < grid_max(num_sms) ? static_cast<int>(most) : grid_max(num_sms);
+  const int64_t rows = static_cast<int64_t>(a.max_q) * a.group_size;
+  const double most = static_cast<double>(a.batch) * a.cache.kv_heads * ((rows + 8 * NR - 1) / (8 * NR)) *
+                      ((tiles > 0 ? tiles : 1) + kUnitCost);
+  const int full = grid_max(num_sms, kCtasPerSm<NR>);
+  const int grid = most < full ? static_cast<int>(most) : full;
   AttnParams arg = p;
   void* args[] = {&arg};
-  e = cudaLaunchKernel((const void*)kv_attention_kernel<T, D>, dim3(grid), dim3(kThreads), args, smem, s);
+  e = cudaLaunchKernel((const void*)kv_attention_kernel<T, D, NR>, dim3(grid), dim3(kThreads), args, smem, s);
   if (e != cudaSuccess) return e;
-  const int rows = static_cast<int64_t>(a.max_q) * a.group_size < 16 ? a.max_q * a.group_size : 16;
-  return cudaLaunchKernel((const void*)kv_attention_join_kernel<T, D>, dim3(grid, (rows + 3) / 4),
+  const int join_rows = rows < 8 * NR ? static_cast<int>(rows) : 8 * NR;
+  return cudaLaunchKernel((const void*)kv_attention_join_kernel<T, D, NR>, dim3(grid, (join_rows + 3) / 4),
                           dim3(kJoinWarps * 4 * 32), args, 0, s);
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
+  return static_cast<int64_t>(p.a.max_q) * p.a.group_size <= 8 ? launch_rows<T, D, 1>(p, num_sms, s)
+                                                              : launch_rows<T, D, 2>(p, num_sms, s);
 }
 
 }  // namespace
 
 size_t attention_workspace(int head_dim, int num_sms) {
-  const size_t g = grid_max(num_sms);
+  const size_t g = grid_max(num_sms, 4);
   return 2 * g * 16 * (head_dim + 2) * sizeof(float) + g * sizeof(Record) + 256;
 }
 
 cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s) {
   AttnParams p;
   p.a = a;
-  const size_t g = grid_max(num_sms);
+  const size_t g = grid_max(num_sms, 4);
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + 2 * g * 16 * a.cache.head_dim;
   p.records = reinterpret_cast<Record*>(p.part_ml + 2 * g * 16 * 2);
