@@ -19,6 +19,8 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const moe_layer_kv_a
   constexpr int kRowChunks = D / 8;                       // chunks of 8 elements of a token
   constexpr int kMaxChunks = 128 * kRowChunks / THREADS;  // of a thread, at the largest page
   __shared__ uint32_t s_max[THREADS / 32];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int P = a.cache.page_size;
   const int u = blockIdx.x, head = blockIdx.y;
@@ -131,8 +133,8 @@ cudaError_t launch_typed(const moe_layer_kv_append_args_t& a, cudaStream_t s) {
   void* args[] = {&arg};
   const int64_t most = a.cu_tokens ? static_cast<int64_t>(a.tokens) / a.cache.page_size + 2 * a.batch : a.batch;
   const dim3 grid(static_cast<unsigned>(most), a.cache.kv_heads, 2);
-  if (!a.cu_tokens) return cudaLaunchKernel((const void*)kv_append_kernel<T, D, 128>, grid, dim3(128), args, 0, s);
-  return cudaLaunchKernel((const void*)kv_append_kernel<T, D, 256>, grid, dim3(256), args, 0, s);
+  if (!a.cu_tokens) return launch_after((const void*)kv_append_kernel<T, D, 128>, grid, dim3(128), args, 0, s);
+  return launch_after((const void*)kv_append_kernel<T, D, 256>, grid, dim3(256), args, 0, s);
 }
 
 }  // namespace

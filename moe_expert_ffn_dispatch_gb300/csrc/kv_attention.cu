@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
   constexpr int kCopies = kSliceBytes / 16 / 32;  // 16-byte copies of a lane for K (and for V)
   static_assert(kRing >= R * D * 4 + 8 * R, "the join reuses the ring");
   extern __shared__ __align__(128) uint8_t smem[];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const moe_layer_kv_attention_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kRing);  // [batch + 1]
@@ -534,6 +536,8 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
   constexpr int kEach = D / 32;
   __shared__ float s_acc[4][kJoinWarps][D];
   __shared__ float s_sum[4][kJoinWarps];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r4 = warp / kJoinWarps, part = warp % kJoinWarps, r = blockIdx.y * 4 + r4;
   const Record rec = p.records[c];
@@ -601,10 +605,10 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   const int grid = most < full ? static_cast<int>(most) : full;
   AttnParams arg = p;
   void* args[] = {&arg};
-  e = cudaLaunchKernel((const void*)kv_attention_kernel<T, D, NR>, dim3(grid), dim3(kThreads), args, smem, s);
+  e = launch_after((const void*)kv_attention_kernel<T, D, NR>, dim3(grid), dim3(kThreads), args, smem, s);
   if (e != cudaSuccess) return e;
   const int join_rows = rows < 8 * NR ? static_cast<int>(rows) : 8 * NR;
-  return cudaLaunchKernel((const void*)kv_attention_join_kernel<T, D, NR>, dim3(grid, (join_rows + 3) / 4),
+  return launch_after((const void*)kv_attention_join_kernel<T, D, NR>, dim3(grid, (join_rows + 3) / 4),
                           dim3(kJoinWarps * 4 * 32), args, 0, s);
 }
 

@@ -19,6 +19,27 @@ cudaError_t launch_append(const moe_layer_kv_append_args_t& a, cudaStream_t s);
 size_t attention_workspace(int head_dim, int num_sms);
 cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s);
 
+// Launch that may begin while the stream's previous kernel still runs: every
+// kernel here starts with grid_dependency_wait, before it touches memory.
+inline cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args, size_t smem, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+// Wait until the preceding grid of the stream has completed and its memory is
+// visible; let the next grid be placed.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
+
 constexpr float kAmaxFloor = 1e-4f;  // floor of an amax before 127 / amax, as in the block's quant
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

@@ -18,6 +18,8 @@ template <typename T, typename W, int C, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer_norm_args_t a) {
   __shared__ float s_sum[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   const int h = a.hidden;
   const int64_t row = blockIdx.x;
@@ -184,7 +186,7 @@ cudaError_t launch_typed(const moe_layer_norm_args_t& a, cudaStream_t s) {
                                   : (const void*)add_rmsnorm_quant_kernel<T, W, 2, false>);
   moe_layer_norm_args_t arg = a;
   void* args[] = {&arg};
-  return cudaLaunchKernel(k, dim3(a.rows), dim3(nt), args, 0, s);
+  return launch_after(k, dim3(a.rows), dim3(nt), args, 0, s);
 }
 
 }  // namespace
