@@ -593,8 +593,8 @@ template <typename T, int D, int NR>
 cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   const moe_layer_kv_attention_args_t& a = p.a;
   const int smem = kWarps * kStagesOf<NR> * 2 * kSlice * D + (a.batch + 2) / 2 * 16 + a.batch * 16;
-  cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_kernel<T, D, NR>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem((const void*)kv_attention_kernel<T, D, NR>, kMaxSmem - 1024, allowed);
   if (e != cudaSuccess) return e;
   // no more CTAs than pieces of work there can be
   const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.cache.page_size + kTileTokens - 1) / kTileTokens;

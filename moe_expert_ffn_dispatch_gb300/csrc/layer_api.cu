@@ -11,11 +11,14 @@ bool act(int32_t dt) { return dt == MOE_LAYER_BF16 || dt == MOE_LAYER_FP16; }
 
 int done(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-// SM count of the current device; 0 if it cannot be asked
+// SM count of the current device, asked once a device; 0 if it cannot be asked
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -3,6 +3,8 @@
 // kv_append.cu and kv_attention.cu hold the kernels).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
@@ -18,6 +20,20 @@ cudaError_t launch_w4(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
 cudaError_t launch_append(const moe_layer_kv_append_args_t& a, cudaStream_t s);
 size_t attention_workspace(int head_dim, int num_sms);
 cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s);
+
+// Lets `kernel` have `most` bytes of dynamic shared memory on the current
+// device, asking the runtime once a device and kernel (`done`: one bit a device).
+inline cudaError_t allow_smem(const void* kernel, int most, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+constexpr int kMaxSmem = 227 * 1024;  // dynamic shared memory that a block can have, less what a kernel has of its own
 
 // Launch that may begin while the stream's previous kernel still runs: every
 // kernel here starts with grid_dependency_wait, before it touches memory.

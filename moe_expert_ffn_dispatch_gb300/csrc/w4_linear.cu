@@ -331,10 +331,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   cp_async_wait<0>();
 }
 
+template <typename T, int NT, int GPS, int kStages>
+cudaError_t launch_stages(const W4Params& p, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  const void* k = (const void*)w4_linear_kernel<T, NT, GPS, kStages>;
+  if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
+  const int red = p.wr == kWarps ? 0 : (NT == 1 ? 2 : 1) * kWarps * NT * 8 * 16 * 4;
+  const int smem = 8 * NT * p.xpitch + kWarps * kStages * kStageBytes + red;
+  W4Params arg = p;
+  void* args[] = {&arg};
+  const int groups = (p.tiles + p.wr - 1) / p.wr;
+  return launch_after(k, dim3(groups < num_sms ? groups : num_sms, (p.a.m + 8 * NT - 1) / (8 * NT)), dim3(kWarps * 32),
+                      args, smem, s);
+}
+
 template <typename T, int NT, int GPS>
-const void* kernel_of(bool many) {
-  if constexpr (NT == 4) return (const void*)w4_linear_kernel<T, NT, GPS, 4>;
-  else return many ? (const void*)w4_linear_kernel<T, NT, GPS, 8> : (const void*)w4_linear_kernel<T, NT, GPS, 4>;
+cudaError_t launch_gps(const W4Params& p, int num_sms, cudaStream_t s) {
+  if constexpr (NT < 4)
+    if (8 * NT * p.xpitch <= kXSmall) return launch_stages<T, NT, GPS, 8>(p, num_sms, s);
+  return launch_stages<T, NT, GPS, 4>(p, num_sms, s);
 }
 
 template <typename T, int NT>
@@ -353,17 +368,9 @@ cudaError_t launch_nt(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
   // but no more than a piece has steps
   p.wr = kWarps;
   while (p.wr > 1 && p.tiles < 2 * p.wr * num_sms && 2 * (kWarps / p.wr) <= p.kc / kStepK) p.wr /= 2;
-  const bool many = NT < 4 && 8 * NT * p.xpitch <= kXSmall;
-  const int red = p.wr == kWarps ? 0 : (NT == 1 ? 2 : 1) * kWarps * NT * 8 * 16 * 4;
-  const int smem = 8 * NT * p.xpitch + kWarps * (many ? 8 : 4) * kStageBytes + red;
-  const int gps = a.group == 32 ? 4 : (a.group == 64 ? 2 : 1);
-  const void* k = gps == 4 ? kernel_of<T, NT, 4>(many) : (gps == 2 ? kernel_of<T, NT, 2>(many) : kernel_of<T, NT, 1>(many));
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  void* args[] = {&p};
-  const int groups = (p.tiles + p.wr - 1) / p.wr;
-  return launch_after(k, dim3(groups < num_sms ? groups : num_sms, (a.m + 8 * NT - 1) / (8 * NT)), dim3(kWarps * 32), args,
-                      smem, s);
+  if (a.group == 32) return launch_gps<T, NT, 4>(p, num_sms, s);
+  if (a.group == 64) return launch_gps<T, NT, 2>(p, num_sms, s);
+  return launch_gps<T, NT, 1>(p, num_sms, s);
 }
 
 template <typename T>

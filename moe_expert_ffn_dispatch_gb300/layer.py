@@ -65,84 +65,80 @@ def declare(L: ctypes.CDLL) -> None:
 
 
 _lib = None
+# the current device's index, and the raw handle of a device's current stream: plain
+# integers, without the objects of torch.cuda (which cost as much as a launch)
+_device_index = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(name, args, stream: int, *more) -> None:
+def _entry(name: str):
     global _lib
     if _lib is None:
         from . import lib
         _lib = lib()
-    rc = getattr(_lib, name)(ctypes.byref(args), *more, stream)
-    if rc:
-        from . import MoeError
-        raise MoeError(rc, name)
+    return getattr(_lib, name)
+
+
+def _raise(rc: int, name: str):
+    from . import MoeError
+    raise MoeError(rc, name)
 
 
 class _On:
-    """The stream that a call runs on, as a context in which its device is
-    current and its outputs are allocated."""
-
-    __slots__ = ("raw", "ctx")
+    """Context in which a tensor's device is current, and `stream` its stream."""
 
     def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
         if device.type != "cuda":
             raise ValueError("the decoder-layer operators run on a CUDA device only")
-        now = torch.cuda.current_stream(device)
-        self.ctx = None
-        if stream is not None and stream != now:
-            if stream.device != device:
-                raise ValueError("stream: on %s, expected %s" % (stream.device, device))
-            self.ctx, now = torch.cuda.stream(stream), stream
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-        self.raw = now.cuda_stream
+        if stream is not None and stream.device != device:
+            raise ValueError("stream: on %s, expected %s" % (stream.device, device))
+        self.ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
 def _act(t: torch.Tensor, name: str) -> int:
-    if t.dtype != torch.bfloat16 and t.dtype != torch.float16:
+    code = DTYPE_CODES.get(t.dtype, 9)
+    if code > 1:
         raise TypeError("%s: dtype %s, expected bfloat16 or float16" % (name, t.dtype))
-    return DTYPE_CODES[t.dtype]
+    return code
 
 
-def _dense(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> int:
+def _dense(t: Optional[torch.Tensor], name: str, dtype, shape, index: int) -> int:
     """Pointer of a contiguous tensor; 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.device != device:
-        raise ValueError("%s: on %s, expected %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s: on %s, expected cuda:%d" % (name, t.device, index))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, dtype, shape, device) -> Tuple[int, int]:
+def _rows(t: torch.Tensor, name: str, dtype, shape, index: int) -> Tuple[int, int]:
     """Pointer and row stride of a tensor whose inner dimensions are dense."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.device != device:
-        raise ValueError("%s: on %s, expected %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s: on %s, expected cuda:%d" % (name, t.device, index))
+    strides = t.stride()
     inner = 1
-    for d in range(t.dim() - 1, 0, -1):
-        if t.stride(d) != inner and shape[d] != 1:
+    for d in range(len(shape) - 1, 0, -1):
+        if strides[d] != inner and shape[d] != 1:
             raise ValueError("%s: every dimension but the first must be dense" % name)
         inner *= shape[d]
     # a single row has no stride that matters
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else -(-inner // 16) * 16
+    return t.data_ptr(), strides[0] if shape[0] > 1 else -(-inner // 16) * 16
 
 
 def add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -158,35 +154,41 @@ def add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     in x's dtype (None without residual; pass residual itself to add in
     place); y is the norm in x's dtype (None unless `want_y` or a tensor for
     it is given)."""
-    code, device, shape = _act(x, "x"), x.device, x.shape
+    code, shape, index = _act(x, "x"), x.shape, x.get_device()
     if len(shape) != 2:
         raise ValueError("x: %d dimensions, expected 2" % len(shape))
+    if stream is not None or index != _device_index():
+        with _On(x.device, stream):
+            return add_rmsnorm_quant(x, weight, eps, residual, smooth, want_y, q, q_scale, residual_out, y)
     rows, hidden = shape
+    dtype, wdtype = x.dtype, weight.dtype
+    if wdtype is not dtype and wdtype is not torch.float32:
+        raise TypeError("weight: dtype %s, expected %s or float32" % (wdtype, dtype))
     a = NormArgs()
-    a.x, a.x_stride = _rows(x, "x", x.dtype, shape, device)
-    if weight.dtype != x.dtype and weight.dtype != torch.float32:
-        raise TypeError("weight: dtype %s, expected %s or float32" % (weight.dtype, x.dtype))
-    a.weight = _dense(weight, "weight", weight.dtype, (hidden,), device)
-    a.smooth = _dense(smooth, "smooth", torch.float32, (hidden,), device)
-    a.rows, a.hidden, a.dtype, a.weight_dtype, a.eps = rows, hidden, code, DTYPE_CODES[weight.dtype], eps
-    with _On(device, stream) as raw:
-        if q is None:
-            q = torch.empty(shape, dtype=torch.int8, device=device)
-        if q_scale is None:
-            q_scale = torch.empty(rows, dtype=torch.float32, device=device)
-        if residual is not None:
-            a.residual, a.residual_stride = _rows(residual, "residual", x.dtype, shape, device)
-            if residual_out is None:
-                residual_out = torch.empty(shape, dtype=x.dtype, device=device)
-            a.residual_out, a.residual_out_stride = _rows(residual_out, "residual_out", x.dtype, shape, device)
-        elif residual_out is not None:
-            raise ValueError("residual_out without residual")
-        if y is None and want_y:
-            y = torch.empty(shape, dtype=x.dtype, device=device)
-        a.y_out = _dense(y, "y", x.dtype, shape, device)
-        a.q = _dense(q, "q", torch.int8, shape, device)
-        a.q_scale = _dense(q_scale, "q_scale", torch.float32, (rows,), device)
-        _call("moe_layer_add_rmsnorm_quant", a, raw)
+    a.x, a.x_stride = _rows(x, "x", dtype, shape, index)
+    a.weight = _dense(weight, "weight", wdtype, (hidden,), index)
+    a.smooth = _dense(smooth, "smooth", torch.float32, (hidden,), index)
+    a.rows, a.hidden, a.dtype, a.weight_dtype, a.eps = rows, hidden, code, DTYPE_CODES[wdtype], eps
+    device = x.device
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=device)
+    if q_scale is None:
+        q_scale = torch.empty(rows, dtype=torch.float32, device=device)
+    if residual is not None:
+        a.residual, a.residual_stride = _rows(residual, "residual", dtype, shape, index)
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=dtype, device=device)
+        a.residual_out, a.residual_out_stride = _rows(residual_out, "residual_out", dtype, shape, index)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    if y is None and want_y:
+        y = torch.empty(shape, dtype=dtype, device=device)
+    a.y_out = _dense(y, "y", dtype, shape, index)
+    a.q = _dense(q, "q", torch.int8, shape, index)
+    a.q_scale = _dense(q_scale, "q_scale", torch.float32, (rows,), index)
+    rc = _entry("moe_layer_add_rmsnorm_quant")(ctypes.byref(a), _raw_stream(index))
+    if rc:
+        _raise(rc, "moe_layer_add_rmsnorm_quant")
     return q, q_scale, residual_out, y
 
 
@@ -201,39 +203,49 @@ def w4_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, zero: Opt
     fp32, zero [n, k / group] uint8 or None (8 everywhere).  The group is what
     w_scale's shape says.  out_dtype: bf16, fp16 or fp32; x's dtype without
     it (bf16 for int8 x)."""
-    device = x.device
-    if x.dim() != 2 or w.dim() != 2 or w_scale.dim() != 2:
-        raise ValueError("x, w and w_scale have 2 dimensions")
-    m, k = x.shape
-    n, groups = w_scale.shape
-    if x.dtype == torch.int8:
-        if x_scale is None:
-            raise ValueError("x_scale is required with int8 x")
-    else:
-        _act(x, "x")
-        if x_scale is not None:
-            raise ValueError("x_scale is for int8 x only")
+    index, shape, xdtype = x.get_device(), x.shape, x.dtype
+    if stream is not None or index != _device_index():
+        with _On(x.device, stream):
+            return w4_linear(x, w, w_scale, zero, x_scale, out_dtype, out)
+    gshape = w_scale.shape
+    if len(shape) != 2 or len(gshape) != 2:
+        raise ValueError("x and w_scale have 2 dimensions")
+    m, k = shape
+    n, groups = gshape
+    xcode = DTYPE_CODES.get(xdtype, 2)
+    if xcode == 2:
+        raise TypeError("x: dtype %s, expected bfloat16, float16 or int8" % xdtype)
+    if (xcode == 3) != (x_scale is not None):
+        raise ValueError("x_scale is required with int8 x, and for int8 x only")
     if groups < 1 or k % groups:
         raise ValueError("w_scale: %d groups do not divide k = %d" % (groups, k))
-    if w_scale.dtype not in DTYPE_CODES or w_scale.dtype == torch.int8:
-        raise TypeError("w_scale: dtype %s, expected bfloat16, float16 or float32" % w_scale.dtype)
+    sdtype = w_scale.dtype
+    scode = DTYPE_CODES.get(sdtype, 3)
+    if scode == 3:
+        raise TypeError("w_scale: dtype %s, expected bfloat16, float16 or float32" % sdtype)
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else (torch.bfloat16 if x.dtype == torch.int8 else x.dtype)
-    if out_dtype not in DTYPE_CODES or out_dtype == torch.int8:
+        out_dtype = out.dtype if out is not None else (torch.bfloat16 if xcode == 3 else xdtype)
+    ocode = DTYPE_CODES.get(out_dtype, 3)
+    if ocode == 3:
         raise TypeError("out_dtype: %s, expected bfloat16, float16 or float32" % out_dtype)
     a = W4Args()
-    a.x, a.x_stride = _rows(x, "x", x.dtype, x.shape, device)
-    a.x_scale = _dense(x_scale, "x_scale", torch.float32, (m,), device)
-    a.w = _dense(w, "w", torch.uint8, (n, k // 2), device)
-    a.w_scale = _dense(w_scale, "w_scale", w_scale.dtype, (n, groups), device)
-    a.w_zero = _dense(zero, "zero", torch.uint8, (n, groups), device)
+    a.x, a.x_stride = _rows(x, "x", xdtype, shape, index)
+    if x_scale is not None:
+        a.x_scale = _dense(x_scale, "x_scale", torch.float32, (m,), index)
+    a.w = _dense(w, "w", torch.uint8, (n, k // 2), index)
+    a.w_scale = _dense(w_scale, "w_scale", sdtype, gshape, index)
+    if zero is not None:
+        a.w_zero = _dense(zero, "zero", torch.uint8, gshape, index)
     a.m, a.n, a.k, a.group = m, n, k, k // groups
-    a.x_dtype, a.scale_dtype, a.out_dtype = DTYPE_CODES[x.dtype], DTYPE_CODES[w_scale.dtype], DTYPE_CODES[out_dtype]
-    with _On(device, stream) as raw:
-        if out is None:
-            out = torch.empty(m, n, dtype=out_dtype, device=device)
-        a.y = _dense(out, "out", out_dtype, (m, n), device)
-        _call("moe_layer_w4_linear", a, raw)
+    a.x_dtype, a.scale_dtype, a.out_dtype = xcode, scode, ocode
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        a.y = out.data_ptr()
+    else:
+        a.y = _dense(out, "out", out_dtype, (m, n), index)
+    rc = _entry("moe_layer_w4_linear")(ctypes.byref(a), _raw_stream(index))
+    if rc:
+        _raise(rc, "moe_layer_w4_linear")
     return out
 
 
@@ -282,6 +294,7 @@ class KvCache:
         c.page_stride, c.head_stride, c.scale_stride = k.stride(0), k.stride(1), k_scale.stride(0)
         c.num_pages, c.kv_heads, c.page_size, c.head_dim = pages, heads, page_size, dim
         self._args = c
+        self._index = k.get_device()
         self._ws = None
 
     @classmethod
@@ -304,17 +317,22 @@ class KvCache:
             self._ws = buf[(-buf.data_ptr()) % 256:]
         return self._ws
 
-    def _table(self, page_table: torch.Tensor) -> Tuple[int, int, int, int]:
-        if page_table.dtype != torch.int32:
+    def _table(self, a, page_table: torch.Tensor) -> int:
+        """Sets the page table's fields of `a`; returns the batch."""
+        if page_table.dtype is not torch.int32:
             raise TypeError("page_table: dtype %s, expected int32" % page_table.dtype)
-        if page_table.dim() != 2:
-            raise ValueError("page_table: %d dimensions, expected 2" % page_table.dim())
-        if page_table.device != self.device:
+        shape, strides = page_table.shape, page_table.stride()
+        if len(shape) != 2:
+            raise ValueError("page_table: %d dimensions, expected 2" % len(shape))
+        if page_table.get_device() != self._index:
             raise ValueError("page_table: on %s, expected %s" % (page_table.device, self.device))
-        batch, pages = page_table.shape
-        if pages > 1 and page_table.stride(1) != 1:
+        batch, pages = shape
+        if pages > 1 and strides[1] != 1:
             raise ValueError("page_table: the pages of a sequence must be dense")
-        return page_table.data_ptr(), batch, pages, page_table.stride(0) if batch > 1 else pages
+        a.cache = self._args
+        a.page_table, a.batch, a.max_pages = page_table.data_ptr(), batch, pages
+        a.table_stride = strides[0] if batch > 1 else pages
+        return batch
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
                cu_tokens: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -322,23 +340,25 @@ class KvCache:
         kv_heads, head_dim] bf16 or fp16 (tokens may be strided); page_table
         [batch, max_pages] and start [batch] int32; cu_tokens [batch + 1]
         int32 where sequences get more or fewer tokens than one."""
-        code, dev = _act(k_new, "k_new"), self.device
-        if k_new.dim() != 3:
-            raise ValueError("k_new: %d dimensions, expected 3" % k_new.dim())
+        code, index, shape, dtype = _act(k_new, "k_new"), self._index, k_new.shape, k_new.dtype
+        if stream is not None or index != _device_index():
+            with _On(self.device, stream):
+                return self.append(k_new, v_new, page_table, start, cu_tokens)
+        if len(shape) != 3 or shape[1] != self.kv_heads or shape[2] != self.head_dim:
+            raise ValueError("k_new: shape %s, expected [tokens, %d, %d]" % (tuple(shape), self.kv_heads, self.head_dim))
         a = KvAppendArgs()
-        a.cache = self._args
-        a.page_table, a.batch, a.max_pages, a.table_stride = self._table(page_table)
-        tokens = k_new.shape[0]
-        shape = (tokens, self.kv_heads, self.head_dim)
-        a.k_new, a.k_stride = _rows(k_new, "k_new", k_new.dtype, shape, dev)
-        a.v_new, a.v_stride = _rows(v_new, "v_new", k_new.dtype, shape, dev)
-        a.start = _dense(start, "start", torch.int32, (a.batch,), dev)
-        a.cu_tokens = _dense(cu_tokens, "cu_tokens", torch.int32, (a.batch + 1,), dev)
-        if cu_tokens is None and tokens != a.batch:
-            raise ValueError("k_new: %d tokens for %d sequences without cu_tokens" % (tokens, a.batch))
-        a.tokens, a.dtype = tokens, code
-        with _On(dev, stream) as raw:
-            _call("moe_layer_kv_append", a, raw)
+        batch = self._table(a, page_table)
+        a.k_new, a.k_stride = _rows(k_new, "k_new", dtype, shape, index)
+        a.v_new, a.v_stride = _rows(v_new, "v_new", dtype, shape, index)
+        a.start = _dense(start, "start", torch.int32, (batch,), index)
+        if cu_tokens is not None:
+            a.cu_tokens = _dense(cu_tokens, "cu_tokens", torch.int32, (batch + 1,), index)
+        elif shape[0] != batch:
+            raise ValueError("k_new: %d tokens for %d sequences without cu_tokens" % (shape[0], batch))
+        a.tokens, a.dtype = shape[0], code
+        rc = _entry("moe_layer_kv_append")(ctypes.byref(a), _raw_stream(index))
+        if rc:
+            _raise(rc, "moe_layer_kv_append")
 
     def attention(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                   cu_q: Optional[torch.Tensor] = None, max_q: int = 1, scale: Optional[float] = None, window: int = 0,
@@ -352,27 +372,33 @@ class KvCache:
         not one each; scale: head_dim ** -0.5 without it; window: keys that a
         token sees at most, itself among them (0: no limit).  Returns out
         [tokens, heads, head_dim]."""
-        code, dev = _act(q, "q"), self.device
-        if q.dim() != 3:
-            raise ValueError("q: %d dimensions, expected 3" % q.dim())
-        tokens, heads, dim = q.shape
+        code, index, shape, dtype = _act(q, "q"), self._index, q.shape, q.dtype
+        if stream is not None or index != _device_index():
+            with _On(self.device, stream):
+                return self.attention(q, page_table, seq_lens, cu_q, max_q, scale, window, out, workspace)
+        if len(shape) != 3:
+            raise ValueError("q: %d dimensions, expected 3" % len(shape))
+        tokens, heads, dim = shape
         if dim != self.head_dim or heads % self.kv_heads:
             raise ValueError("q: %d heads of %d do not fit %d kv heads of %d" %
                              (heads, dim, self.kv_heads, self.head_dim))
         a = KvAttentionArgs()
-        a.cache = self._args
-        a.page_table, a.batch, a.max_pages, a.table_stride = self._table(page_table)
-        a.q, a.q_stride = _rows(q, "q", q.dtype, q.shape, dev)
-        a.seq_lens = _dense(seq_lens, "seq_lens", torch.int32, (a.batch,), dev)
-        a.cu_q = _dense(cu_q, "cu_q", torch.int32, (a.batch + 1,), dev)
-        if cu_q is None and (tokens != a.batch or max_q != 1):
-            raise ValueError("q: %d tokens (max_q %d) for %d sequences without cu_q" % (tokens, max_q, a.batch))
+        batch = self._table(a, page_table)
+        a.q, a.q_stride = _rows(q, "q", dtype, shape, index)
+        a.seq_lens = _dense(seq_lens, "seq_lens", torch.int32, (batch,), index)
+        if cu_q is not None:
+            a.cu_q = _dense(cu_q, "cu_q", torch.int32, (batch + 1,), index)
+        elif tokens != batch or max_q != 1:
+            raise ValueError("q: %d tokens (max_q %d) for %d sequences without cu_q" % (tokens, max_q, batch))
         a.tokens, a.max_q, a.group_size, a.window, a.dtype = tokens, max_q, heads // self.kv_heads, window, code
         a.sm_scale = dim ** -0.5 if scale is None else scale
-        with _On(dev, stream) as raw:
-            ws = self.workspace() if workspace is None else workspace
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            a.out = _dense(out, "out", q.dtype, q.shape, dev)
-            _call("moe_layer_kv_attention", a, raw, ws.data_ptr(), ws.numel())
+        ws = workspace if workspace is not None else self._ws if self._ws is not None else self.workspace()
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+            a.out = out.data_ptr()
+        else:
+            a.out = _dense(out, "out", dtype, shape, index)
+        rc = _entry("moe_layer_kv_attention")(ctypes.byref(a), ws.data_ptr(), ws.numel(), _raw_stream(index))
+        if rc:
+            _raise(rc, "moe_layer_kv_attention")
         return out
