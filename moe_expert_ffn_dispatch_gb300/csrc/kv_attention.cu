@@ -77,9 +77,9 @@ __device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_
   const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
   s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
   s.row_tiles = (s.qlen * a.group_size + 8 * NR - 1) / (8 * NR);
-  int lo = 0;
-  if (a.window > 0) lo = max(0, static_cast<int>(static_cast<int64_t>(s.len) - s.qlen - a.window + 1));
-  s.tile0 = lo / kTileTokens;
+  int64_t lo = 0;
+  if (a.window > 0) lo = max(lo, static_cast<int64_t>(s.len) - s.qlen - a.window + 1);
+  s.tile0 = static_cast<int>(lo / kTileTokens);
   s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.tile0);
   return s;
 }

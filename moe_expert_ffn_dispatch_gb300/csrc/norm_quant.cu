@@ -10,17 +10,77 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-// C chunks of 8 elements a thread.  VEC: a chunk is 8 neighbours, moved by
-// 16-byte accesses (needs hidden % 8 == 0, aligned rows); otherwise the 8
-// elements of a chunk lie a block apart and move one by one, for any hidden
-// and alignment.
+// A thread holds C chunks of 8 neighbouring elements; a warp's 32 chunks are
+// 256 neighbours.  VEC: a chunk moves by 16-byte accesses (needs hidden % 8 ==
+// 0 and aligned rows).  Otherwise the warp moves its 256 elements one by one,
+// neighbours by neighbouring lanes, and hands them round in shared memory, so
+// that every thread holds the same elements in either form and the sums, and
+// with them every result, do not depend on alignment.
+template <typename E, bool VEC>
+__device__ __forceinline__ void load8(const E* p, int i, int h, float* buf, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (i < h) {
+      if constexpr (sizeof(E) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = unpack2<E>(w[j]);
+          v[2 * j] = f.x;
+          v[2 * j + 1] = f.y;
+        }
+      } else {
+        const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+  } else {
+    const int lane = threadIdx.x & 31, first = i - lane * 8;
+    float e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = first + j * 32 + lane < h ? to_f32(p[first + j * 32 + lane]) : 0.0f;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) buf[(j * 32 + lane) + (j * 32 + lane) / 8] = e[j];  // 9 words a chunk: no bank twice
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = buf[lane * 9 + j];
+  }
+}
+
+template <typename E, bool VEC>
+__device__ __forceinline__ void store8(E* p, int i, int h, float* buf, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (i < h) {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = pack2<E>(v[2 * j], v[2 * j + 1]);
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+    const int lane = threadIdx.x & 31, first = i - lane * 8;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) buf[lane * 9 + j] = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (first + j * 32 + lane < h) p[first + j * 32 + lane] = from_f32<E>(buf[(j * 32 + lane) + (j * 32 + lane) / 8]);
+  }
+}
+
 template <typename T, typename W, int C, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer_norm_args_t a) {
   __shared__ float s_sum[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
+  __shared__ float s_buf[VEC ? 1 : kMaxWarps * 32 * 9];
   grid_dependency_wait();
   grid_launch_dependents();
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  float* buf = s_buf + (VEC ? 0 : warp * 32 * 9);
   const int h = a.hidden;
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
@@ -33,48 +93,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if constexpr (VEC) {
-      const int i = (c * nt + tid) * 8;
-      if (i < h) {
-        const uint4 u = *reinterpret_cast<const uint4*>(x + i);
-        const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+    const int i = (c * nt + tid) * 8;
+    load8<T, VEC>(x, i, h, buf, v[c]);
+    if (res) {
+      float r[8];
+      load8<T, VEC>(res, i, h, buf, r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<T>(uw[j]);
-          v[c][2 * j] = f.x;
-          v[c][2 * j + 1] = f.y;
-        }
-        if (res) {
-          const uint4 r = *reinterpret_cast<const uint4*>(res + i);
-          const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack2<T>(rw[j]);
-            v[c][2 * j] = __fadd_rn(v[c][2 * j], f.x);
-            v[c][2 * j + 1] = __fadd_rn(v[c][2 * j + 1], f.y);
-            o[j] = pack2<T>(v[c][2 * j], v[c][2 * j + 1]);
-          }
-          *reinterpret_cast<uint4*>(res_out + i) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = (c * 8 + j) * nt + tid;
-        float f = 0.0f;
-        if (i < h) {
-          f = to_f32(x[i]);
-          if (res) {
-            f = __fadd_rn(f, to_f32(res[i]));
-            res_out[i] = from_f32<T>(f);
-          }
-        }
-        v[c][j] = f;
-      }
+      for (int j = 0; j < 8; ++j) v[c][j] = __fadd_rn(v[c][j], r[j]);
+      store8<T, VEC>(res_out, i, h, buf, v[c]);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = __fmaf_rn(v[c][j], v[c][j], sum);
@@ -91,50 +117,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
   uint32_t top = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if constexpr (VEC) {
-      const int i = (c * nt + tid) * 8;
-      if (i < h) {
-        float wv[8];
-        if constexpr (sizeof(W) == 2) {
-          const uint4 u = *reinterpret_cast<const uint4*>(w + i);
-          const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+    const int i = (c * nt + tid) * 8;
+    float f[8];
+    load8<W, VEC>(w, i, h, buf, f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack2<W>(uw[j]);
-            wv[2 * j] = f.x;
-            wv[2 * j + 1] = f.y;
-          }
-        } else {
-          const float4 p0 = *reinterpret_cast<const float4*>(w + i), p1 = *reinterpret_cast<const float4*>(w + i + 4);
-          wv[0] = p0.x, wv[1] = p0.y, wv[2] = p0.z, wv[3] = p0.w;
-          wv[4] = p1.x, wv[5] = p1.y, wv[6] = p1.z, wv[7] = p1.w;
-        }
+    for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(__fmul_rn(v[c][j], r), f[j]) : 0.0f;
+    if (y_out) store8<T, VEC>(y_out, i, h, buf, v[c]);
+    if (a.smooth) {
+      load8<float, VEC>(a.smooth, i, h, buf, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(__fmul_rn(v[c][j], r), wv[j]);
-        if (y_out) {
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = pack2<T>(v[c][2 * j], v[c][2 * j + 1]);
-          *reinterpret_cast<uint4*>(y_out + i) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        if (a.smooth) {
-          const float4 p0 = *reinterpret_cast<const float4*>(a.smooth + i),
-                       p1 = *reinterpret_cast<const float4*>(a.smooth + i + 4);
-          const float sv[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(v[c][j], sv[j]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = (c * 8 + j) * nt + tid;
-        if (i < h) {
-          v[c][j] = __fmul_rn(__fmul_rn(v[c][j], r), to_f32(w[i]));
-          if (y_out) y_out[i] = from_f32<T>(v[c][j]);
-          if (a.smooth) v[c][j] = __fmul_rn(v[c][j], a.smooth[i]);
-        }
-      }
+      for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(v[c][j], f[j]) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[c][j]));
@@ -151,20 +143,21 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
   int8_t* q = a.q + row * h;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
+    const int i = (c * nt + tid) * 8;
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j >> 2] |= code_of(__fmul_rn(v[c][j], m)) << ((j & 3) * 8);
     if constexpr (VEC) {
-      const int i = (c * nt + tid) * 8;
-      if (i < h) {
-        uint32_t o[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j >> 2] |= code_of(__fmul_rn(v[c][j], m)) << ((j & 3) * 8);
-        *reinterpret_cast<uint2*>(q + i) = make_uint2(o[0], o[1]);
-      }
+      if (i < h) *reinterpret_cast<uint2*>(q + i) = make_uint2(o[0], o[1]);
     } else {
+      uint8_t* b = reinterpret_cast<uint8_t*>(buf);
+      __syncwarp();
+      *reinterpret_cast<uint2*>(b + lane * 8) = make_uint2(o[0], o[1]);
+      __syncwarp();
+      const int first = i - lane * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = (c * 8 + j) * nt + tid;
-        if (i < h) q[i] = static_cast<int8_t>(code_of(__fmul_rn(v[c][j], m)));
-      }
+      for (int j = 0; j < 8; ++j)
+        if (first + j * 32 + lane < h) q[first + j * 32 + lane] = static_cast<int8_t>(b[j * 32 + lane]);
     }
   }
   if (tid == 0) a.q_scale[row] = __fdiv_rn(1.0f, m);

@@ -157,7 +157,7 @@ def add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     code, shape, index = _act(x, "x"), x.shape, x.get_device()
     if len(shape) != 2:
         raise ValueError("x: %d dimensions, expected 2" % len(shape))
-    if stream is not None or index != _device_index():
+    if stream is not None or index < 0 or index != _device_index():
         with _On(x.device, stream):
             return add_rmsnorm_quant(x, weight, eps, residual, smooth, want_y, q, q_scale, residual_out, y)
     rows, hidden = shape
@@ -204,7 +204,7 @@ def w4_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, zero: Opt
     w_scale's shape says.  out_dtype: bf16, fp16 or fp32; x's dtype without
     it (bf16 for int8 x)."""
     index, shape, xdtype = x.get_device(), x.shape, x.dtype
-    if stream is not None or index != _device_index():
+    if stream is not None or index < 0 or index != _device_index():
         with _On(x.device, stream):
             return w4_linear(x, w, w_scale, zero, x_scale, out_dtype, out)
     gshape = w_scale.shape
@@ -341,7 +341,7 @@ class KvCache:
         [batch, max_pages] and start [batch] int32; cu_tokens [batch + 1]
         int32 where sequences get more or fewer tokens than one."""
         code, index, shape, dtype = _act(k_new, "k_new"), self._index, k_new.shape, k_new.dtype
-        if stream is not None or index != _device_index():
+        if stream is not None or index < 0 or index != _device_index():
             with _On(self.device, stream):
                 return self.append(k_new, v_new, page_table, start, cu_tokens)
         if len(shape) != 3 or shape[1] != self.kv_heads or shape[2] != self.head_dim:
@@ -373,7 +373,7 @@ class KvCache:
         token sees at most, itself among them (0: no limit).  Returns out
         [tokens, heads, head_dim]."""
         code, index, shape, dtype = _act(q, "q"), self._index, q.shape, q.dtype
-        if stream is not None or index != _device_index():
+        if stream is not None or index < 0 or index != _device_index():
             with _On(self.device, stream):
                 return self.attention(q, page_table, seq_lens, cu_q, max_q, scale, window, out, workspace)
         if len(shape) != 3:
