@@ -8,7 +8,8 @@
 namespace moe_layer {
 namespace {
 
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 16;
+constexpr int kRowWarps = 4;
 
 // A thread holds C chunks of 8 neighbouring elements; a warp's 32 chunks are
 // 256 neighbours.  VEC: a chunk moves by 16-byte accesses (needs hidden % 8 ==
@@ -16,40 +17,48 @@ constexpr int kMaxWarps = 32;
 // neighbours by neighbouring lanes, and hands them round in shared memory, so
 // that every thread holds the same elements in either form and the sums, and
 // with them every result, do not depend on alignment.
+// Raw holds a chunk's bits between the load, which a kernel issues early, and take.
 template <typename E, bool VEC>
-__device__ __forceinline__ void load8(const E* p, int i, int h, float* buf, float (&v)[8]) {
-  if constexpr (VEC) {
-    if (i < h) {
-      if constexpr (sizeof(E) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+  uint32_t w[VEC ? sizeof(E) * 2 : 8];
+  __device__ __forceinline__ void load(const E* p, int i, int h) {
+    if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+      for (int k = 0; k < static_cast<int>(sizeof(E) / 2); ++k) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < h) u = reinterpret_cast<const uint4*>(p + i)[k];
+        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+      }
+    } else {
+      const int lane = threadIdx.x & 31, first = i - lane * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = first + j * 32 + lane < h ? __float_as_uint(to_f32(p[first + j * 32 + lane])) : 0u;
+    }
+  }
+  __device__ __forceinline__ void take(float* buf, float (&v)[8]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(E) == 2) {
           const float2 f = unpack2<E>(w[j]);
           v[2 * j] = f.x;
           v[2 * j + 1] = f.y;
+        } else {
+          v[2 * j] = __uint_as_float(w[2 * j]);
+          v[2 * j + 1] = __uint_as_float(w[2 * j + 1]);
         }
-      } else {
-        const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
       }
     } else {
+      const int lane = threadIdx.x & 31;
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      for (int j = 0; j < 8; ++j) buf[(j * 32 + lane) + (j * 32 + lane) / 8] = __uint_as_float(w[j]);  // 9 words a chunk: no bank twice
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = buf[lane * 9 + j];
     }
-  } else {
-    const int lane = threadIdx.x & 31, first = i - lane * 8;
-    float e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = first + j * 32 + lane < h ? to_f32(p[first + j * 32 + lane]) : 0.0f;
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) buf[(j * 32 + lane) + (j * 32 + lane) / 8] = e[j];  // 9 words a chunk: no bank twice
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = buf[lane * 9 + j];
   }
-}
+};
 
 template <typename E, bool VEC>
 __device__ __forceinline__ void store8(E* p, int i, int h, float* buf, const float (&v)[8]) {
@@ -72,32 +81,45 @@ __device__ __forceinline__ void store8(E* p, int i, int h, float* buf, const flo
   }
 }
 
-template <typename T, typename W, int C, bool VEC>
-__global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer_norm_args_t a) {
+// ROW_WARP: a warp takes a row by itself, kRowWarps rows a CTA
+template <typename T, typename W, int C, bool VEC, bool ROW_WARP>
+__global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : 512, ROW_WARP ? 6 : 2) add_rmsnorm_quant_kernel(const moe_layer_norm_args_t a) {
   __shared__ float s_sum[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
-  __shared__ float s_buf[VEC ? 1 : kMaxWarps * 32 * 9];
+  __shared__ float s_buf[VEC ? 1 : (ROW_WARP ? kRowWarps : kMaxWarps) * 32 * 9];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int nt = ROW_WARP ? 32 : blockDim.x, tid = ROW_WARP ? lane : threadIdx.x;
   float* buf = s_buf + (VEC ? 0 : warp * 32 * 9);
   const int h = a.hidden;
-  const int64_t row = blockIdx.x;
+  const int64_t row = ROW_WARP ? static_cast<int64_t>(blockIdx.x) * kRowWarps + warp : blockIdx.x;
+  if (ROW_WARP && row >= a.rows) return;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
   T* res_out = a.residual ? static_cast<T*>(a.residual_out) + row * a.residual_out_stride : nullptr;
   T* y_out = a.y_out ? static_cast<T*>(a.y_out) + row * h : nullptr;
   const W* w = static_cast<const W*>(a.weight);
 
+  // every load of the row before the first use or store
+  Raw<T, VEC> xr[C], rr[C];
+  Raw<W, VEC> wr[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    xr[c].load(x, (c * nt + tid) * 8, h);
+    if (res) rr[c].load(res, (c * nt + tid) * 8, h);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) wr[c].load(w, (c * nt + tid) * 8, h);
   float v[C][8];
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (c * nt + tid) * 8;
-    load8<T, VEC>(x, i, h, buf, v[c]);
+    xr[c].take(buf, v[c]);
     if (res) {
       float r[8];
-      load8<T, VEC>(res, i, h, buf, r);
+      rr[c].take(buf, r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] = __fadd_rn(v[c][j], r[j]);
       store8<T, VEC>(res_out, i, h, buf, v[c]);
@@ -107,11 +129,13 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  sum = lane < nw ? s_sum[lane] : 0.0f;
+  if constexpr (!ROW_WARP) {
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    sum = lane < nw ? s_sum[lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
   const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps));
 
   uint32_t top = 0;
@@ -119,12 +143,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
   for (int c = 0; c < C; ++c) {
     const int i = (c * nt + tid) * 8;
     float f[8];
-    load8<W, VEC>(w, i, h, buf, f);
+    wr[c].take(buf, f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(__fmul_rn(v[c][j], r), f[j]) : 0.0f;
     if (y_out) store8<T, VEC>(y_out, i, h, buf, v[c]);
     if (a.smooth) {
-      load8<float, VEC>(a.smooth, i, h, buf, f);
+      Raw<float, VEC> sr;
+      sr.load(a.smooth, i, h);
+      sr.take(buf, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(v[c][j], f[j]) : 0.0f;
     }
@@ -132,9 +158,11 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
     for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[c][j]));
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_max[warp] = top;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+  if constexpr (!ROW_WARP) {
+    if (lane == 0) s_max[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+  }
   // a NaN or an infinity in the row is a NaN here (infinity times r = 0), and so in the scale
   float amax = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : top);
   if (amax < kAmaxFloor) amax = kAmaxFloor;
@@ -163,6 +191,17 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_quant_kernel(const moe_layer
   if (tid == 0) a.q_scale[row] = __fdiv_rn(1.0f, m);
 }
 
+template <typename T, typename W, int C, bool ROW_WARP>
+cudaError_t launch_shape(const moe_layer_norm_args_t& a, bool vec, cudaStream_t s) {
+  const int chunks = (a.hidden + 7) / 8;
+  const int nt = ROW_WARP ? kRowWarps * 32 : ((chunks + C - 1) / C + 31) / 32 * 32;
+  const void* k = vec ? (const void*)add_rmsnorm_quant_kernel<T, W, C, true, ROW_WARP>
+                      : (const void*)add_rmsnorm_quant_kernel<T, W, C, false, ROW_WARP>;
+  moe_layer_norm_args_t arg = a;
+  void* args[] = {&arg};
+  return launch_after(k, dim3(ROW_WARP ? (a.rows + kRowWarps - 1) / kRowWarps : a.rows), dim3(nt), args, 0, s);
+}
+
 template <typename T, typename W>
 cudaError_t launch_typed(const moe_layer_norm_args_t& a, cudaStream_t s) {
   auto at = [](const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
@@ -170,16 +209,12 @@ cudaError_t launch_typed(const moe_layer_norm_args_t& a, cudaStream_t s) {
                    (!a.residual || (at(a.residual, 16) && at(a.residual_out, 16) && a.residual_stride % 8 == 0 &&
                                     a.residual_out_stride % 8 == 0)) &&
                    (!a.y_out || at(a.y_out, 16)) && (!a.smooth || at(a.smooth, 16));
-  const int chunks = (a.hidden + 7) / 8;
-  const int per = chunks <= 512 ? 1 : 2;
-  const int nt = ((chunks + per - 1) / per + 31) / 32 * 32;
-  const void* k = per == 1 ? (vec ? (const void*)add_rmsnorm_quant_kernel<T, W, 1, true>
-                                  : (const void*)add_rmsnorm_quant_kernel<T, W, 1, false>)
-                           : (vec ? (const void*)add_rmsnorm_quant_kernel<T, W, 2, true>
-                                  : (const void*)add_rmsnorm_quant_kernel<T, W, 2, false>);
-  moe_layer_norm_args_t arg = a;
-  void* args[] = {&arg};
-  return launch_after(k, dim3(a.rows), dim3(nt), args, 0, s);
+  // The form goes by hidden alone, so that a row's results do not depend on
+  // the rows beside it.
+  if (a.hidden <= 512) return launch_shape<T, W, 2, true>(a, vec, s);
+  if (a.hidden <= 1024) return launch_shape<T, W, 4, true>(a, vec, s);
+  if (a.hidden <= 4096) return launch_shape<T, W, 2, false>(a, vec, s);
+  return launch_shape<T, W, 4, false>(a, vec, s);
 }
 
 }  // namespace
