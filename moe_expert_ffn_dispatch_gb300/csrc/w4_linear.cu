@@ -1,24 +1,35 @@
 // Products of a few rows of x with 4-bit weights and group scales.
 //
-// y^T = W x^T as mma.sync m16n8k16: 16 weight rows are the M side, 8 rows of
-// x the N side, so that one row of x costs what eight do and the weights pass
-// through registers once.  Codes become exact 16-bit floats (a code set into
-// the mantissa of 1024 or 128, minus that and the zero point), products are
-// exact, each group's sum is one fp32 accumulator chain and enters the row's
-// sum through an fp32 fma with the group's scale.
+// y^T = W x^T as mma.sync m16n8k16 in fp16: weight rows are the M side, 8 rows
+// of x the N side, so that one row of x costs what eight do and the weights
+// pass through registers once.
 //
-// Bound by the weights' bytes.  A CTA has 16 warps in WR groups of rows x
-// (16 / WR) parts of K; a warp streams its own 16-row tiles through a ring of
-// 128-k steps by asynchronous copies, which needs no barrier.  One part of K
-// is written straight from the accumulators; several are summed in shared
-// memory, in a fixed order.  x lies in shared memory, its elements in the
-// order in which the codes leave a 32-bit word.
+// Codes.  A code masked out of its word is, as fp16 bits, the subnormal code x
+// 2^-24 (or, four bits higher, code x 2^-20), which the matrix unit multiplies
+// exactly: five operations turn a word into four pairs.  The elements of x
+// that meet the higher position are stored as x / 16.  With X the sum of a
+// group's x, sum x (code - zero) = sum x code - zero X: the second term is one
+// fp32 fma a group.
+//
+// x.  Each 128 k of a row are scaled by a power of two to [2^8, 2^9) at their
+// largest element, so x and x / 16 are exact in fp16 but for elements 2^18
+// below the largest, which keep a step of 2^-28 of it: nothing that an fp32
+// sum over them can tell.  Products are exact, a group's sum is one fp32
+// accumulator chain and enters the row's sum through an fp32 fma with the
+// group's scale and the power of two.
+//
+// Bound by the weights' bytes, and close behind by instructions.  A CTA has 16
+// warps in WR groups of rows x (16 / WR) parts of K; a warp streams its own
+// 16-row tiles through a ring of 128-k steps by asynchronous copies, which
+// needs no barrier.  One part of K is written straight from the accumulators;
+// several are summed in shared memory, in a fixed order.
 //
 // k order.  Both operands may take the k of a group in any common order.  A
 // lane takes neighbouring words of a weight row, as many as the group allows
 // the four lanes of a row to take (4 words at groups of 128 and more, 2 at
 // 64, 1 at 32), so that each product of 16 k stays inside one group.
-#include <type_traits>
+#include <climits>
+#include <cstdint>
 
 #include "layer_ops.cuh"
 
@@ -26,67 +37,39 @@ namespace moe_layer {
 namespace {
 
 constexpr int kWarps = 16;
+constexpr int kRows = 16;                      // weight rows of a tile
 constexpr int kStepK = 128;                    // k of one ring stage
-constexpr int kStageBytes = 16 * kStepK / 2;   // 16 weight rows
+constexpr int kStageBytes = kRows * kStepK / 2;
 constexpr int kXSmall = 66 * 1024;             // bytes of x that leave room for 8 stages of a warp
 constexpr int kXMost = 130 * 1024;             // and for 4
 
+// bytes of a warp's own: the scales and scale x zero of 8 groups, or its partial sums
+template <int NT>
+constexpr int kPrivateOf = NT * 8 * kRows * 4 > 2 * 8 * kRows * 4 ? NT * 8 * kRows * 4 : 2 * 8 * kRows * 4;
+
 struct W4Params {
   moe_layer_w4_args_t a;
-  int kc;         // k of one piece of x that fits shared memory (multiple of 128)
+  int kc;         // k of one piece of x that fits shared memory (whole steps of every part of K)
   int pieces;     // pieces of kc that cover k
-  int wr;         // row groups of a CTA: 1, 2, 4, 8 or 16
-  int tiles;      // tiles of 16 weight rows
+  int wr;         // row groups of a CTA: 1, 2, 4 or 8
+  int tiles;      // tiles of kRows weight rows
   int xpitch;     // bytes of a row of x in shared memory
   int ngroups;    // k / group
+  int gsteps;     // steps of a group (1 for groups of 128 and less)
 };
 
-__device__ __forceinline__ float scale_at(const void* p, int64_t i, int dt) {
-  if (dt == MOE_LAYER_FP32) return __ldg(static_cast<const float*>(p) + i);
-  const uint16_t b = __ldg(static_cast<const uint16_t*>(p) + i);
-  return dt == MOE_LAYER_BF16 ? __uint_as_float(static_cast<uint32_t>(b) << 16) : __half2float(__ushort_as_half(b));
+// bits of a scale, loaded early; its value
+__device__ __forceinline__ uint32_t scale_bits(const void* p, int64_t i, int dt) {
+  if (dt == MOE_LAYER_FP32) return __ldg(static_cast<const uint32_t*>(p) + i);
+  return __ldg(static_cast<const uint16_t*>(p) + i);
+}
+__device__ __forceinline__ float scale_value(uint32_t b, int dt) {
+  if (dt == MOE_LAYER_FP16) return __half2float(__ushort_as_half(static_cast<uint16_t>(b)));
+  return __uint_as_float(dt == MOE_LAYER_BF16 ? b << 16 : b);
 }
 
-// The 8 codes of a word as 4 pairs (0,4) (1,5) (2,6) (3,7), minus the zero
-// point.  fp16: a code in the low bits of the mantissa of 1024 is 1024 + code,
-// four bits higher 1024 + 16 code, which one exact fma turns into code - zero.
-// bf16's mantissa holds the low position only.  zp: zero_words.
-template <typename T>
-__device__ __forceinline__ void expand8(uint32_t w, const uint32_t (&zp)[2], uint32_t (&o)[4]) {
-  if constexpr (std::is_same_v<T, __half>) {
-    const uint32_t sixteenth = 0x2C002C00u;  // 1 / 16
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t v = i ? w >> 8 : w;
-      const uint32_t lo = (v & 0x000F000Fu) | 0x64006400u, hi = (v & 0x00F000F0u) | 0x64006400u;
-      const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&zp[0]));
-      const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), *reinterpret_cast<const __half2*>(&sixteenth),
-                                *reinterpret_cast<const __half2*>(&zp[1]));
-      o[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
-      o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-      const __nv_bfloat162 r =
-          __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&zp[0]));
-      o[i] = *reinterpret_cast<const uint32_t*>(&r);
-    }
-  }
-}
-
-// fp16: 1024 + zero, and -(64 + zero); bf16: 128 + zero
-template <typename T>
-__device__ __forceinline__ void zero_words(uint32_t z, uint32_t (&zp)[2]) {
-  if constexpr (std::is_same_v<T, __half>) {
-    zp[0] = (0x6400u | z) * 0x10001u;
-    zp[1] = (0xD400u | (z << 4)) * 0x10001u;
-  } else {
-    zp[0] = (0x4300u | z) * 0x10001u;
-    zp[1] = 0u;
-  }
-}
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // where 16-byte chunk c of row r of a stage lies: reads of 16, 8 and 4 bytes
 // a lane (8 rows x 4 lanes) all fall on different banks
@@ -95,116 +78,192 @@ __device__ __forceinline__ uint32_t stage_at(int r, int c) {
   return r * 64 + ((c ^ s) << 4);
 }
 
-// 8 neighbouring elements of x as pairs (0,4) (1,5) (2,6) (3,7)
-__device__ __forceinline__ uint4 pair04(uint4 v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                    __byte_perm(v.y, v.w, 0x7632));
-}
-
 // NT: tiles of 8 rows of x.  GPS: groups of a 128-k step (1, 2 or 4)
-template <typename T, int NT, int GPS, int kStages>
+template <int NT, int GPS, int kStages>
 __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int M = 8 * NT;                            // rows of x of a CTA
+  constexpr int kBlock = 8 / GPS;                      // steps whose scales come together: 8 groups
+  constexpr int kPrivate = kPrivateOf<NT>;  // of a warp: scales and scale x zero of a block; its partial sums
   grid_dependency_wait();
   grid_launch_dependents();
   const moe_layer_w4_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int wr = p.wr, wk = kWarps / wr;
   const int row_group = warp / wk, kpart = warp - row_group * wk;
-  const int m0 = blockIdx.y * (8 * NT);
-  const int mrows = min(a.m - m0, 8 * NT);
-  // x | rings | partial sums
+  const int m0 = blockIdx.y * M;
+  const int mrows = min(a.m - m0, M);
+  const int steps = (a.k + kStepK - 1) / kStepK, steps_pp = p.kc / kStepK;
+  // x | of each group of a step and pair of rows, the sums and the powers of two [steps_pp * GPS][M / 2] | private | rings
   uint8_t* xs = smem;
-  uint8_t* ring = smem + 8 * NT * p.xpitch + warp * (kStages * kStageBytes);
-  float* red = reinterpret_cast<float*>(smem + 8 * NT * p.xpitch + kWarps * kStages * kStageBytes);
-  const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  float4* xsum = reinterpret_cast<float4*>(smem + M * p.xpitch);
+  float* priv = reinterpret_cast<float*>(xsum + steps_pp * GPS * (M / 2));
+  float* mine = priv + warp * (kPrivate / 4);
+  const uint32_t ring_u =
+      static_cast<uint32_t>(__cvta_generic_to_shared(priv + kWarps * (kPrivate / 4))) + warp * (kStages * kStageBytes);
   const uint32_t xs_u = static_cast<uint32_t>(__cvta_generic_to_shared(xs));
+  const uint32_t xsum_u = static_cast<uint32_t>(__cvta_generic_to_shared(xsum));
 
   // row group r of CTA c takes tiles (r + wr i) grid + c: every SM gets as many, to one
   const int first_tile = row_group * gridDim.x + blockIdx.x, next_tile = wr * gridDim.x;
   const int rounds = (p.tiles + next_tile - 1) / next_tile;  // the same for every warp
-  const int steps_pp = p.kc / kStepK;                        // steps of a piece, all parts
-  const int64_t row_bytes = a.k / 2;
+  const int run = steps_pp / wk;                             // steps of a part of K in a piece
+  const int row_bytes = a.k / 2;
+  // steps of this warp's part in a piece: [piece * steps_pp + kpart * run, ...)
+  auto run_of = [&](int piece) { return min(run, steps - piece * steps_pp - kpart * run); };
 
-  // position of the copies: tile, piece, step of this warp, ahead of the products
-  int c_tile = first_tile, c_piece = 0, c_step = kpart, c_slot = 0;
-  const int cr = lane >> 2, cc = lane & 3;  // this lane copies chunk cc of rows cr and cr + 8
+  // the copies run ahead of the products: this lane copies chunk cc of rows cr and cr + 8
+  const int cr = lane >> 2, cc = lane & 3;
+  const int tail = (row_bytes & (kStepK / 2 - 1)) ? row_bytes & (kStepK / 2 - 1) : kStepK / 2;  // bytes of the last step
+  int c_tile = first_tile, c_piece = 0, c_left = run_of(0);
+  uint32_t c_slot = 0;
+  const uint8_t *c_row0 = a.w, *c_row1 = a.w;
+  bool c_last = false;  // the run ends with K, whose last step this lane may be past
+  auto copy_run = [&]() {  // the start of a run
+    const int step = c_piece * steps_pp + kpart * run, kb = step * (kStepK / 2) + cc * 16;
+    c_row0 = a.w + static_cast<int64_t>(min(c_tile * kRows + cr, a.n - 1)) * row_bytes + kb;
+    c_row1 = a.w + static_cast<int64_t>(min(c_tile * kRows + cr + 8, a.n - 1)) * row_bytes + kb;
+    c_last = step + c_left == steps && cc * 16 >= tail;
+  };
+  if (c_left <= 0) c_tile = p.tiles;  // no part of K for this warp
+  if (c_tile < p.tiles) copy_run();
+  const uint32_t c_dst = ring_u + stage_at(cr, cc);  // row cr + 8 lies 512 bytes on
   auto issue = [&]() {
     if (c_tile < p.tiles) {
-      const int kb = (c_piece * p.kc + c_step * kStepK) / 2 + cc * 16;
-      const bool ok = kb < row_bytes;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = cr + hh * 8, n = min(c_tile * 16 + r, a.n - 1);
-        cp_async16(ring_u + c_slot * kStageBytes + stage_at(r, cc), a.w + n * row_bytes + (ok ? kb : 0), ok);
-      }
-      c_step += wk;
-      if (c_step >= steps_pp || c_piece * p.kc + c_step * kStepK >= a.k) {
-        c_step = kpart;
-        if (++c_piece == p.pieces || c_piece * p.kc + c_step * kStepK >= a.k) {
+      const bool ok = !(c_last && c_left == 1);  // past the end of K: zeros
+      cp_async16(c_dst + c_slot, ok ? c_row0 : a.w, ok);
+      cp_async16(c_dst + c_slot + 8 * 64, ok ? c_row1 : a.w, ok);
+      c_row0 += kStepK / 2;
+      c_row1 += kStepK / 2;
+      if (--c_left == 0) {
+        if (++c_piece == p.pieces || run_of(c_piece) <= 0) {
           c_piece = 0;
           c_tile += next_tile;
         }
+        c_left = run_of(c_piece);
+        if (c_tile < p.tiles) copy_run();
       }
     }
-    c_slot = c_slot + 1 == kStages ? 0 : c_slot + 1;
+    c_slot = (c_slot + kStageBytes) & (kStages * kStageBytes - 1);
     cp_async_commit();
   };
-  // a warp whose part of K is empty issues nothing
-  if (kpart * kStepK >= min(p.kc, a.k)) c_tile = p.tiles;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue();
 
-  // x of one piece, 8 elements at a time, four loads in flight
-  auto load_x = [&](int piece) {
-    const int k0 = piece * p.kc, n8 = p.kc / 8, all = 8 * NT * n8;
-    for (int base = tid; base < all; base += 4 * kWarps * 32) {
-      uint4 v[4];
+  // Scales and zeros come 8 groups at a time: lane t of a quad loads groups 2t
+  // and 2t + 1 of rows g and g + 8, one block ahead, and lays scale x 2^16 and
+  // -scale x zero out as [group][g][row] for one 16-byte read a group.
+  uint32_t sraw[2][2], zraw[2][2] = {{8u, 8u}, {8u, 8u}};
+  int64_t s_row0 = 0, s_row1 = 0;
+  auto scale_tile = [&](int tile) {
+    s_row0 = static_cast<int64_t>(min(tile * kRows + g, a.n - 1)) * p.ngroups;
+    s_row1 = static_cast<int64_t>(min(tile * kRows + g + 8, a.n - 1)) * p.ngroups;
+  };
+  auto load_scales = [&](int first_step) {
+    const int v = first_step * GPS + 2 * t;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = base + u * kWarps * 32, m = i / n8, k = k0 + (i - m * n8) * 8;
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (m < mrows && k < a.k) {
-          const int64_t at = (m0 + m) * a.x_stride + k;
-          if (a.x_dtype == MOE_LAYER_INT8) {
-            const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.x) + at);
-            v[u].x = q.x, v[u].y = q.y;
-          } else {
-            v[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at);
-          }
-        }
+    for (int i = 0; i < 2; ++i) {
+      const int gi = min(GPS == 1 && p.gsteps > 1 ? (v + i) / p.gsteps : v + i, p.ngroups - 1);
+      sraw[0][i] = scale_bits(a.w_scale, s_row0 + gi, a.scale_dtype);
+      sraw[1][i] = scale_bits(a.w_scale, s_row1 + gi, a.scale_dtype);
+      if (a.w_zero) {
+        zraw[0][i] = __ldg(a.w_zero + s_row0 + gi) & 15u;
+        zraw[1][i] = __ldg(a.w_zero + s_row1 + gi) & 15u;
+      }
+    }
+  };
+  if (kpart * run < steps) {
+    scale_tile(min(first_tile, p.tiles - 1));
+    load_scales(kpart * run);
+  }
+  const uint32_t mine_u = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+
+  // 8 elements of x as they lie in memory
+  auto x_at8 = [&](int64_t at) {
+    if (a.x_dtype == MOE_LAYER_INT8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.x) + at);
+      return make_uint4(q.x, q.y, 0u, 0u);
+    }
+    return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at);
+  };
+  // x of one piece: 16 / (rows, as a power of two) warps a row, 8 elements a
+  // lane, so 16 lanes hold the 128 k that share a power of two.  Rows past the
+  // last are not written: a column of the products meets no other.
+  const int row_shift = 31 - __clz(2 * mrows - 1);
+  auto load_x = [&](int piece) {
+    const int k0 = piece * p.kc, n8 = p.kc / 8;
+    const int m = warp & ((1 << row_shift) - 1), part = warp >> row_shift, parts = kWarps >> row_shift;
+    if (m >= mrows) return;
+    const int64_t row = static_cast<int64_t>(m0 + m) * a.x_stride + k0;
+    uint8_t* to = xs + m * p.xpitch;
+    float* sums = reinterpret_cast<float*>(xsum) + (m >> 1) * 4 + (m & 1);
+    for (int first = part * 32; first < n8; first += 8 * 32 * parts) {  // the same for every lane: sums cross lanes
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k8 = first + u * 32 * parts + lane;
+        v[u] = k8 < n8 && k0 + k8 * 8 < a.k ? x_at8(row + k8 * 8) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = base + u * kWarps * 32;
-        if (i >= all) break;
-        const int m = i / n8, k8 = i - m * n8;
-        uint4 x = v[u];
-        if (a.x_dtype == MOE_LAYER_INT8) {
-          uint32_t o[4];
+      for (int u = 0; u < 8; ++u) {
+        const int k8 = first + u * 32 * parts + lane;
+        if (k8 - lane >= n8) break;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        float f[8];
+        uint32_t top = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t b = (j < 2 ? v[u].x : v[u].y) >> ((j & 1) * 16);
-            o[j] = pack2<T>(static_cast<float>(static_cast<int8_t>(b & 0xFF)),
-                            static_cast<float>(static_cast<int8_t>((b >> 8) & 0xFF)));
+        for (int j = 0; j < 8; ++j) {
+          if (a.x_dtype == MOE_LAYER_INT8) {
+            f[j] = static_cast<float>(static_cast<int8_t>((w[j >> 2] >> ((j & 3) * 8)) & 0xFFu));
+          } else {
+            const float2 h = a.x_dtype == MOE_LAYER_BF16 ? unpack2<__nv_bfloat16>(w[j >> 1]) : unpack2<__half>(w[j >> 1]);
+            f[j] = j & 1 ? h.y : h.x;
           }
-          x = make_uint4(o[0], o[1], o[2], o[3]);
+          top = max(top, abs_bits(f[j]));
         }
-        // block k8 of a step belongs to lane xt, word xj: it is read as block 4 xj + xt
-        const int kk = k8 & 15;
-        int xt, xj;
-        if constexpr (GPS == 1) xt = kk >> 2, xj = kk & 3;
-        else if constexpr (GPS == 2) xt = (kk & 7) >> 1, xj = (kk >> 3) * 2 + (kk & 1);
-        else xt = kk & 3, xj = kk >> 2;
-        *reinterpret_cast<uint4*>(xs + m * p.xpitch + ((k8 & ~15) + xj * 4 + xt) * 16) = pair04(x);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // an infinity or a NaN stays one; a row of zeros may have any exponent
+        const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127;
+        const float up0 = pow2(4 - e / 2), up1 = pow2(4 - (e - e / 2));  // 2^(8 - e)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], up0), up1);
+        // pairs (0,4) (1,5) (2,6) (3,7); the second and the last meet codes four bits higher
+        uint4 x;
+        x.x = pack2<__half>(f[0], f[4]);
+        x.y = pack2<__half>(f[1] * 0.0625f, f[5] * 0.0625f);
+        x.z = pack2<__half>(f[2], f[6]);
+        x.w = pack2<__half>(f[3] * 0.0625f, f[7] * 0.0625f);
+        // the sums of what is stored
+        const float2 s0 = unpack2<__half>(x.x), s1 = unpack2<__half>(x.y), s2 = unpack2<__half>(x.z),
+                     s3 = unpack2<__half>(x.w);
+        float sum = __fadd_rn(__fadd_rn(__fadd_rn(s0.x, s0.y), __fadd_rn(s2.x, s2.y)),
+                              16.0f * __fadd_rn(__fadd_rn(s1.x, s1.y), __fadd_rn(s3.x, s3.y)));
+#pragma unroll
+        for (int o = 1; o < 16 / GPS; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+        if (k8 < n8) {
+          if (lane % (16 / GPS) == 0) {
+            float* at = sums + (k8 / (16 / GPS)) * (M * 2);
+            at[0] = __fmul_rn(sum * 0x1p-8f, pow2(e));
+            at[2] = pow2(e);
+          }
+          // block k8 of a step belongs to lane xt, word xj: it is read as block 4 xj + xt
+          const int kk = k8 & 15;
+          int xt, xj;
+          if constexpr (GPS == 1) xt = kk >> 2, xj = kk & 3;
+          else if constexpr (GPS == 2) xt = (kk & 7) >> 1, xj = (kk >> 3) * 2 + (kk & 1);
+          else xt = kk & 3, xj = kk >> 2;
+          *reinterpret_cast<uint4*>(to + ((k8 & ~15) + xj * 4 + xt) * 16) = x;
+        }
       }
     }
   };
 
-  int slot = 0, buf = 0;
+  const uint32_t w_at = ring_u + (GPS == 1 ? stage_at(g, t) : 0);
+  const int wr_shift = 31 - __clz(wr);
+  uint32_t slot = 0;
   for (int it = 0; it < rounds; ++it) {
     const int tile = first_tile + it * next_tile;
-    const int64_t na = min(tile * 16 + g, a.n - 1), nb = min(tile * 16 + g + 8, a.n - 1);
     float acc[NT][4] = {};
     for (int piece = 0; piece < p.pieces; ++piece) {
       if (it == 0 || p.pieces > 1) {
@@ -212,81 +271,96 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         load_x(piece);
         __syncthreads();
       }
-      const int k0 = piece * p.kc;
-      if (tile < p.tiles) {
-        for (int step = kpart; step < steps_pp && k0 + step * kStepK < a.k; step += wk) {
-          // scales and zeros of this step's groups, asked for before the wait
-          const int kk = k0 + step * kStepK;
-          float sa[GPS], sb[GPS];
-          uint32_t za[GPS][2], zb[GPS][2];
+      const int todo = tile < p.tiles ? run_of(piece) : 0;
+      const int s0 = piece * steps_pp + kpart * run;
+      uint32_t xa = xs_u + g * p.xpitch + t * 16 + kpart * run * kStepK * 2;
+      uint32_t xg = xsum_u + (kpart * run * GPS * (M / 2) + t) * 16;
+      for (int base = 0; base < todo; base += kBlock) {
 #pragma unroll
-          for (int i = 0; i < GPS; ++i) {
-            const int gi = min(GPS == 1 ? kk / a.group : kk / (kStepK / GPS) + i, p.ngroups - 1);
-            sa[i] = scale_at(a.w_scale, na * p.ngroups + gi, a.scale_dtype);
-            sb[i] = scale_at(a.w_scale, nb * p.ngroups + gi, a.scale_dtype);
-            zero_words<T>(a.w_zero ? __ldg(a.w_zero + na * p.ngroups + gi) & 15u : 8u, za[i]);
-            zero_words<T>(a.w_zero ? __ldg(a.w_zero + nb * p.ngroups + gi) & 15u : 8u, zb[i]);
-          }
+        for (int i = 0; i < 2; ++i) {
+          const float v0 = scale_value(sraw[0][i], a.scale_dtype), v1 = scale_value(sraw[1][i], a.scale_dtype);
+          *reinterpret_cast<float4*>(mine + ((2 * t + i) * 8 + g) * 4) =
+              make_float4(v0 * 0x1p16f, v1 * 0x1p16f, -__fmul_rn(v0, static_cast<float>(zraw[0][i])),
+                          -__fmul_rn(v1, static_cast<float>(zraw[1][i])));
+        }
+        // the next block: of this run, of the next piece, or of the next tile
+        if (base + kBlock < todo) {
+          load_scales(s0 + base + kBlock);
+        } else if (piece + 1 < p.pieces && run_of(piece + 1) > 0) {
+          load_scales(s0 + steps_pp);
+        } else if (tile + next_tile < p.tiles) {
+          scale_tile(tile + next_tile);
+          load_scales(kpart * run);
+        }
+        uint32_t sa = mine_u + g * 16;
+        const int here = min(kBlock, todo - base);
+        for (int b = 0; b < here; ++b) {
           cp_async_wait<kStages - 2>();
-          __syncwarp();
-          const uint32_t st = ring_u + slot * kStageBytes;
-          uint32_t wa[4], wb[4];
-          if constexpr (GPS == 1) {
-            const uint4 u = lds128(st + stage_at(g, t)), v = lds128(st + stage_at(g + 8, t));
-            wa[0] = u.x, wa[1] = u.y, wa[2] = u.z, wa[3] = u.w;
-            wb[0] = v.x, wb[1] = v.y, wb[2] = v.z, wb[3] = v.w;
-          } else if constexpr (GPS == 2) {
+          __syncwarp();  // every lane's copies, and the block's scales
+          const uint32_t st = w_at + slot;
+          uint32_t w[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint2 u = lds64(st + stage_at(g, 2 * i + (t >> 1)) + (t & 1) * 8);
-              const uint2 v = lds64(st + stage_at(g + 8, 2 * i + (t >> 1)) + (t & 1) * 8);
-              wa[2 * i] = u.x, wa[2 * i + 1] = u.y;
-              wb[2 * i] = v.x, wb[2 * i + 1] = v.y;
-            }
-          } else {
+          for (int r = 0; r < 2; ++r) {
+            if constexpr (GPS == 1) {
+              const uint4 u = lds128(st + r * 8 * 64);
+              w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
+            } else if constexpr (GPS == 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              wa[i] = lds32(st + stage_at(g, i) + t * 4);
-              wb[i] = lds32(st + stage_at(g + 8, i) + t * 4);
+              for (int i = 0; i < 2; ++i) {
+                const uint2 u = lds64(st + stage_at(g, 2 * i + (t >> 1)) + (t & 1) * 8 + r * 8 * 64);
+                w[r][2 * i] = u.x, w[r][2 * i + 1] = u.y;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[r][i] = lds32(st + stage_at(g, i) + t * 4 + r * 8 * 64);
             }
           }
-          const uint32_t xa = xs_u + g * p.xpitch + step * kStepK * 2 + t * 16;
-          float part[NT][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            constexpr int jpg = 4 / GPS;  // words of a lane in a group
-            const int gi = j / jpg;
-            if (j % jpg == 0) {
+          for (int q = 0; q < GPS; ++q) {  // groups of the step
+            constexpr int kWords = 4 / GPS;
+            float part[NT][4];
 #pragma unroll
-              for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.0f;
-            }
-            uint32_t ea[4], eb[4];
-            expand8<T>(wa[j], za[gi], ea);
-            expand8<T>(wb[j], zb[gi], eb);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 xv = lds128(xa + n * 8 * p.xpitch + j * 64);
-              mma16816<T>(part[n], ea[0], eb[0], ea[1], eb[1], xv.x, xv.y);
-              mma16816<T>(part[n], ea[2], eb[2], ea[3], eb[3], xv.z, xv.w);
-            }
-            if (j % jpg == jpg - 1) {
+            for (int i = 0; i < kWords; ++i) {
+              const int j = q * kWords + i;
+              const uint32_t wa = w[0][j], wb = w[1][j], va = wa >> 8, vb = wb >> 8;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                acc[n][0] = __fmaf_rn(sa[gi], part[n][0], acc[n][0]);
-                acc[n][1] = __fmaf_rn(sa[gi], part[n][1], acc[n][1]);
-                acc[n][2] = __fmaf_rn(sb[gi], part[n][2], acc[n][2]);
-                acc[n][3] = __fmaf_rn(sb[gi], part[n][3], acc[n][3]);
+                const uint4 xv = lds128(xa + n * 8 * p.xpitch + j * 64);
+                if (i == 0)
+                  mma16816_first<__half>(part[n], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u,
+                                         xv.x, xv.y);
+                else
+                  mma16816<__half>(part[n], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, xv.x,
+                                   xv.y);
+                mma16816<__half>(part[n], va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, xv.z,
+                                 xv.w);
               }
             }
+            const uint4 su = lds128(sa);
+            sa += kRows * 8;
+            const float sv[2] = {__uint_as_float(su.x), __uint_as_float(su.y)};
+            const float zv[2] = {__uint_as_float(su.z), __uint_as_float(su.w)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 xu = lds128(xg + n * 64);
+              const float x2[2] = {__uint_as_float(xu.x), __uint_as_float(xu.y)};
+              const float p2[2] = {__uint_as_float(xu.z), __uint_as_float(xu.w)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[n][e] = __fmaf_rn(zv[e >> 1], x2[e & 1],
+                                      __fmaf_rn(__fmul_rn(sv[e >> 1], p2[e & 1]), part[n][e], acc[n][e]));
+            }
+            xg += M * 8;
           }
+          xa += kStepK * 2;
           __syncwarp();  // the stage is read before it is filled again
           issue();
-          slot = slot + 1 == kStages ? 0 : slot + 1;
+          slot = (slot + kStageBytes) & (kStages * kStageBytes - 1);
         }
       }
     }
     auto store = [&](int m, int n, float y) {
-      if (a.x_scale) y = __fmul_rn(y, a.x_scale[m0 + m]);
+      if (a.x_scale) y = __fmul_rn(y, __ldg(a.x_scale + m0 + m));
       const int64_t at = static_cast<int64_t>(m0 + m) * a.n + n;
       if (a.out_dtype == MOE_LAYER_FP32) static_cast<float*>(a.y)[at] = y;
       else if (a.out_dtype == MOE_LAYER_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(y);
@@ -298,46 +372,40 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int m = n * 8 + 2 * t + (e & 1), row = tile * 16 + g + 8 * (e >> 1);
+            const int m = n * 8 + 2 * t + (e & 1), row = tile * kRows + g + 8 * (e >> 1);
             if (m < mrows && row < a.n) store(m, row, acc[n][e]);
           }
       }
       continue;
     }
-    // parts of K: red[buf][warp][x row][16 weight rows]
-    float* mine = red + (buf * kWarps + warp) * (NT * 8 * 16);
+    // parts of K, in each warp's private memory: [x row][16 weight rows]
+    __syncwarp();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mine[(n * 8 + 2 * t) * 16 + g] = acc[n][0];
-      mine[(n * 8 + 2 * t + 1) * 16 + g] = acc[n][1];
-      mine[(n * 8 + 2 * t) * 16 + g + 8] = acc[n][2];
-      mine[(n * 8 + 2 * t + 1) * 16 + g + 8] = acc[n][3];
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mine[(n * 8 + 2 * t + (e & 1)) * kRows + g + 8 * (e >> 1)] = acc[n][e];
     __syncthreads();
-    const int cols = 16 * wr;
-    for (int i = tid; i < mrows * cols; i += kWarps * 32) {
-      const int m = i / cols, c = i - m * cols, rg = c >> 4;
-      const int n = (rg * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + it * next_tile) * 16 + (c & 15);
-      if (n >= a.n) continue;
-      const float* from = red + (buf * kWarps + rg * wk) * (NT * 8 * 16) + m * 16 + (c & 15);
+    const int cshift = wr_shift + 4;  // columns: 16 x wr
+    for (int i = tid; i < mrows << cshift; i += kWarps * 32) {
+      const int m = i >> cshift, c = i & ((1 << cshift) - 1), rg = c >> 4;
+      const int n = (rg * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + it * next_tile) * kRows + (c & 15);
+      const float* from = priv + rg * wk * (kPrivate / 4) + m * kRows + (c & 15);
       float y = 0.0f;
-      for (int q = 0; q < wk; ++q) y = __fadd_rn(y, from[q * (NT * 8 * 16)]);
-      store(m, n, y);
+      for (int q = 0; q < wk; ++q) y = __fadd_rn(y, from[q * (kPrivate / 4)]);
+      if (n < a.n) store(m, n, y);
     }
-    // with two halves the other one is written while this one may still be read
-    if constexpr (NT == 1) buf ^= 1;
-    else __syncthreads();
+    __syncthreads();  // the sums are read before the next block's scales take their place
   }
   cp_async_wait<0>();
 }
 
-template <typename T, int NT, int GPS, int kStages>
+template <int NT, int GPS, int kStages>
 cudaError_t launch_stages(const W4Params& p, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  const void* k = (const void*)w4_linear_kernel<T, NT, GPS, kStages>;
+  const void* k = (const void*)w4_linear_kernel<NT, GPS, kStages>;
   if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
-  const int red = p.wr == kWarps ? 0 : (NT == 1 ? 2 : 1) * kWarps * NT * 8 * 16 * 4;
-  const int smem = 8 * NT * p.xpitch + kWarps * kStages * kStageBytes + red;
+  const int smem = 8 * NT * (p.xpitch + p.kc / kStepK * GPS * 8) + kWarps * kPrivateOf<NT> +
+                   kWarps * kStages * kStageBytes;
   W4Params arg = p;
   void* args[] = {&arg};
   const int groups = (p.tiles + p.wr - 1) / p.wr;
@@ -345,46 +413,53 @@ cudaError_t launch_stages(const W4Params& p, int num_sms, cudaStream_t s) {
                       args, smem, s);
 }
 
-template <typename T, int NT, int GPS>
+template <int NT, int GPS>
 cudaError_t launch_gps(const W4Params& p, int num_sms, cudaStream_t s) {
-  if constexpr (NT < 4)
-    if (8 * NT * p.xpitch <= kXSmall) return launch_stages<T, NT, GPS, 8>(p, num_sms, s);
-  return launch_stages<T, NT, GPS, 4>(p, num_sms, s);
+  if (8 * NT * p.xpitch <= kXSmall) return launch_stages<NT, GPS, 8>(p, num_sms, s);
+  return launch_stages<NT, GPS, 4>(p, num_sms, s);
 }
 
-template <typename T, int NT>
+template <int NT>
 cudaError_t launch_nt(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s) {
   W4Params p;
   p.a = a;
-  const int kpad = (a.k + kStepK - 1) / kStepK * kStepK;
-  const int fit = (kXMost / (8 * NT) - 64) / 2 / kStepK * kStepK;
-  p.pieces = (kpad + fit - 1) / fit;
-  p.kc = (kpad / kStepK + p.pieces - 1) / p.pieces * kStepK;
-  p.pieces = (kpad + p.kc - 1) / p.kc;
-  p.xpitch = p.kc * 2 + 64;  // a multiple of 128 plus 64: rows 2i and 2i + 1 of a 16-byte read fall on other banks
   p.ngroups = a.k / a.group;
-  p.tiles = (a.n + 15) / 16;
-  // one part of K where every warp gets two tiles or more; else more parts,
-  // but no more than a piece has steps
-  p.wr = kWarps;
-  while (p.wr > 1 && p.tiles < 2 * p.wr * num_sms && 2 * (kWarps / p.wr) <= p.kc / kStepK) p.wr /= 2;
-  if (a.group == 32) return launch_gps<T, NT, 4>(p, num_sms, s);
-  if (a.group == 64) return launch_gps<T, NT, 2>(p, num_sms, s);
-  return launch_gps<T, NT, 1>(p, num_sms, s);
-}
-
-template <typename T>
-cudaError_t launch_t(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s) {
-  if (a.m <= 8) return launch_nt<T, 1>(a, num_sms, s);
-  if (a.m <= 16) return launch_nt<T, 2>(a, num_sms, s);
-  return launch_nt<T, 4>(a, num_sms, s);
+  p.gsteps = a.group > kStepK ? a.group / kStepK : 1;
+  p.tiles = (a.n + kRows - 1) / kRows;
+  const int steps = (a.k + kStepK - 1) / kStepK;
+  const int fit = (kXMost / (8 * NT) - 64) / (2 * kStepK);  // steps of x that shared memory takes
+  // Row groups: the split with the least work in the longest warp, in steps.
+  // A tile costs about one step beside its own, about six where parts of K
+  // are summed (measured: 130001 x 4096 took 58 us in one part, 83 us in eight).
+  int64_t best = INT64_MAX;
+  p.wr = 1;
+  for (int wr = kWarps; wr >= 1; wr /= 2) {
+    const int wk = kWarps / wr;
+    if (wk > steps || wk > fit) break;
+    const int64_t rounds = (p.tiles + static_cast<int64_t>(wr) * num_sms - 1) / (static_cast<int64_t>(wr) * num_sms);
+    const int64_t cost = rounds * ((steps + wk - 1) / wk + (wk > 1 ? 6 : 1));
+    if (cost < best) best = cost, p.wr = wr;
+  }
+  const int wk = kWarps / p.wr;
+  // pieces of whole rounds of the parts of K
+  p.kc = (steps + wk - 1) / wk * wk;
+  if (p.kc > fit) {
+    const int most = fit / wk * wk;
+    p.pieces = (steps + most - 1) / most;
+    p.kc = ((steps + p.pieces - 1) / p.pieces + wk - 1) / wk * wk;
+  }
+  p.pieces = (steps + p.kc - 1) / p.kc;
+  p.kc *= kStepK;
+  p.xpitch = p.kc * 2 + 64;  // a multiple of 128 plus 64: rows 2i and 2i + 1 of a 16-byte read fall on other banks
+  if (a.group == 32) return launch_gps<NT, 4>(p, num_sms, s);
+  if (a.group == 64) return launch_gps<NT, 2>(p, num_sms, s);
+  return launch_gps<NT, 1>(p, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_w4(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s) {
-  // int8 codes are exact in fp16 and bf16; fp16 needs fewer operations a weight
-  return a.x_dtype == MOE_LAYER_BF16 ? launch_t<__nv_bfloat16>(a, num_sms, s) : launch_t<__half>(a, num_sms, s);
+  return a.m <= 8 ? launch_nt<1>(a, num_sms, s) : launch_nt<2>(a, num_sms, s);
 }
 
 }  // namespace moe_layer
