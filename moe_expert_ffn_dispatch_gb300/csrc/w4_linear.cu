@@ -178,23 +178,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   }
   const uint32_t mine_u = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
 
-  // 8 elements of x as they lie in memory
-  auto x_at8 = [&](int64_t at) {
-    if (a.x_dtype == MOE_LAYER_INT8) {
-      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.x) + at);
-      return make_uint4(q.x, q.y, 0u, 0u);
-    }
-    return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at);
-  };
   // x of one piece: 16 / (rows, as a power of two) warps a row, 8 elements a
   // lane, so 16 lanes hold the 128 k that share a power of two.  Rows past the
   // last are not written: a column of the products meets no other.
   const int row_shift = 31 - __clz(2 * mrows - 1);
-  auto load_x = [&](int piece) {
+  auto load_x_as = [&](auto type, int piece) {
+    using X = decltype(type);
+    constexpr bool kInt8 = sizeof(X) == 1;
     const int k0 = piece * p.kc, n8 = p.kc / 8;
     const int m = warp & ((1 << row_shift) - 1), part = warp >> row_shift, parts = kWarps >> row_shift;
     if (m >= mrows) return;
-    const int64_t row = static_cast<int64_t>(m0 + m) * a.x_stride + k0;
+    const X* row = static_cast<const X*>(a.x) + static_cast<int64_t>(m0 + m) * a.x_stride + k0;
     uint8_t* to = xs + m * p.xpitch;
     float* sums = reinterpret_cast<float*>(xsum) + (m >> 1) * 4 + (m & 1);
     for (int first = part * 32; first < n8; first += 8 * 32 * parts) {  // the same for every lane: sums cross lanes
@@ -202,7 +196,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int k8 = first + u * 32 * parts + lane;
-        v[u] = k8 < n8 && k0 + k8 * 8 < a.k ? x_at8(row + k8 * 8) : make_uint4(0, 0, 0, 0);
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (k8 < n8 && k0 + k8 * 8 < a.k) {
+          if constexpr (kInt8) {
+            const uint2 q = *reinterpret_cast<const uint2*>(row + k8 * 8);
+            v[u].x = q.x, v[u].y = q.y;
+          } else {
+            v[u] = *reinterpret_cast<const uint4*>(row + k8 * 8);
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
@@ -210,41 +212,41 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         if (k8 - lane >= n8) break;
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
         float f[8];
-        uint32_t top = 0;
+        int e = 7;  // codes of up to 127: [2^6, 2^7)
+        if constexpr (kInt8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (a.x_dtype == MOE_LAYER_INT8) {
-            f[j] = static_cast<float>(static_cast<int8_t>((w[j >> 2] >> ((j & 3) * 8)) & 0xFFu));
-          } else {
-            const float2 h = a.x_dtype == MOE_LAYER_BF16 ? unpack2<__nv_bfloat16>(w[j >> 1]) : unpack2<__half>(w[j >> 1]);
-            f[j] = j & 1 ? h.y : h.x;
+          for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int8_t>((w[j >> 2] >> ((j & 3) * 8)) & 0xFFu));
+        } else {
+          // magnitudes are ordered as 16-bit integers
+          uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                  __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          top = max(top >> 16, top & 0xFFFFu);
+          const float2 big = unpack2<X>(top);
+          // an infinity or a NaN stays one; elements of 2^-110 and less may vanish
+          e = min(max(static_cast<int>(__float_as_uint(big.x) >> 23), 17), 254) - 127;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 h = unpack2<X>(w[j]);
+            f[2 * j] = h.x, f[2 * j + 1] = h.y;
           }
-          top = max(top, abs_bits(f[j]));
         }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // an infinity or a NaN stays one; a row of zeros may have any exponent
-        const int e = min(max(static_cast<int>(top >> 23), 1), 254) - 127;
-        const float up0 = pow2(4 - e / 2), up1 = pow2(4 - (e - e / 2));  // 2^(8 - e)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], up0), up1);
-        // pairs (0,4) (1,5) (2,6) (3,7); the second and the last meet codes four bits higher
+        float sum = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                              __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
+        // pairs (0,4) (1,5) (2,6) (3,7) x 2^(8 - e); the second and the last meet codes four bits higher
+        const float up = pow2(8 - e), up16 = pow2(4 - e);
         uint4 x;
-        x.x = pack2<__half>(f[0], f[4]);
-        x.y = pack2<__half>(f[1] * 0.0625f, f[5] * 0.0625f);
-        x.z = pack2<__half>(f[2], f[6]);
-        x.w = pack2<__half>(f[3] * 0.0625f, f[7] * 0.0625f);
-        // the sums of what is stored
-        const float2 s0 = unpack2<__half>(x.x), s1 = unpack2<__half>(x.y), s2 = unpack2<__half>(x.z),
-                     s3 = unpack2<__half>(x.w);
-        float sum = __fadd_rn(__fadd_rn(__fadd_rn(s0.x, s0.y), __fadd_rn(s2.x, s2.y)),
-                              16.0f * __fadd_rn(__fadd_rn(s1.x, s1.y), __fadd_rn(s3.x, s3.y)));
+        x.x = pack2<__half>(__fmul_rn(f[0], up), __fmul_rn(f[4], up));
+        x.y = pack2<__half>(__fmul_rn(f[1], up16), __fmul_rn(f[5], up16));
+        x.z = pack2<__half>(__fmul_rn(f[2], up), __fmul_rn(f[6], up));
+        x.w = pack2<__half>(__fmul_rn(f[3], up16), __fmul_rn(f[7], up16));
 #pragma unroll
         for (int o = 1; o < 16 / GPS; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
         if (k8 < n8) {
           if (lane % (16 / GPS) == 0) {
             float* at = sums + (k8 / (16 / GPS)) * (M * 2);
-            at[0] = __fmul_rn(sum * 0x1p-8f, pow2(e));
+            at[0] = sum;
             at[2] = pow2(e);
           }
           // block k8 of a step belongs to lane xt, word xj: it is read as block 4 xj + xt
@@ -257,6 +259,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         }
       }
     }
+  };
+  auto load_x = [&](int piece) {
+    if (a.x_dtype == MOE_LAYER_INT8) load_x_as(int8_t(), piece);
+    else if (a.x_dtype == MOE_LAYER_BF16) load_x_as(__nv_bfloat16(), piece);
+    else load_x_as(__half(), piece);
   };
 
   const uint32_t w_at = ring_u + (GPS == 1 ? stage_at(g, t) : 0);
