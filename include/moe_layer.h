@@ -200,6 +200,10 @@ typedef struct {
 int moe_layer_kv_attention_workspace_size(int32_t head_dim, size_t* workspace_bytes);
 int moe_layer_kv_attention(const moe_layer_kv_attention_args_t* args, void* workspace, size_t workspace_bytes,
                            void* stream);
+/* Synchronise `stream` and say whether a wait inside the last call that used
+ * `workspace` gave up (MOE_ERR_DEVICE_TIMEOUT; its output is then not to be
+ * used).  Every wait inside a kernel is bounded. */
+int moe_layer_kv_attention_status(const void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,8 +16,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(HERE, "_moe_fused.so")
 SOURCES = ["api.cu", "dispatch_quant.cu", "moe_gemm.cu", "tc_gemm.cu",
-           "layer_api.cu", "norm_quant.cu", "w4_linear.cu", "kv_append.cu", "kv_attention.cu"]
-HEADERS = ["device_prims.cuh", "epilogue_ops.cuh", "moe_internal.h", "quant_ops.cuh", "layer_ops.cuh"]
+           "layer_api.cu", "norm_quant.cu", "w4_linear.cu", "kv_append.cu", "kv_attention.cu",
+           "kv_attention_chunk.cu"]
+HEADERS = ["device_prims.cuh", "epilogue_ops.cuh", "moe_internal.h", "quant_ops.cuh", "layer_ops.cuh", "kv_attention.cuh"]
 PUBLIC_HEADERS = ["moe_fused.h", "moe_layer.h"]
 
 NVCC_FLAGS = [

@@ -25,7 +25,7 @@
 // sum is the same sum.
 //
 // Bound by the cache's bytes while a row tile holds all rows of a kv head.
-#include "layer_ops.cuh"
+#include "kv_attention.cuh"
 
 namespace moe_layer {
 namespace {
@@ -42,47 +42,8 @@ constexpr int kStagesOf = NR == 1 ? 3 : 4;
 constexpr int kMaxSlots = 4096;                  // CTAs of a launch (at most 4 an SM)
 // what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces
 constexpr int kUnitCost = 4;
-
-struct Record {  // a unit that several CTAs share, left by the CTA that holds its last piece
-  int b, head, rt, c0;  // c0: its first CTA; b < 0: none
-};
-
-struct AttnParams {
-  moe_layer_kv_attention_args_t a;
-  float* part_o;      // [2 * grid][16][D]
-  float* part_ml;     // [2 * grid][16][2]
-  Record* records;    // [grid]
-  float scale_log2;   // sm_scale * log2(e)
-  int page_shift;
-};
-
-// What a sequence contributes, from its lengths.
-struct SeqShape {
-  int q0, qlen;     // query tokens
-  int len;          // keys
-  int row_tiles;
-  int tile0, tiles; // pieces of kTileTokens that its rows see; tiles >= 1
-};
-
-template <int NR>
-__device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_t& a, int b) {
-  SeqShape s;
-  if (a.cu_q) {
-    s.q0 = min(max(a.cu_q[b], 0), a.tokens);
-    s.qlen = min(max(min(a.cu_q[b + 1], a.tokens) - s.q0, 0), a.max_q);
-  } else {
-    s.q0 = b;
-    s.qlen = 1;
-  }
-  const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
-  s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
-  s.row_tiles = (s.qlen * a.group_size + 8 * NR - 1) / (8 * NR);
-  int64_t lo = 0;
-  if (a.window > 0) lo = max(lo, static_cast<int64_t>(s.len) - s.qlen - a.window + 1);
-  s.tile0 = static_cast<int>(lo / kTileTokens);
-  s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.tile0);
-  return s;
-}
+// query rows of a kv head (the longest sequence's) from which the tensor-memory kernel takes over
+constexpr int kChunkFrom = 64;
 
 // position of channel chunk `c` (16 bytes) of token row `r` in a slice of [16][D] bytes
 template <int D>
@@ -96,17 +57,6 @@ template <int D>
 __device__ __forceinline__ int token_of(int n) {
   if constexpr (D == 128) return n;
   else return n ^ ((n >> 1) & 1);
-}
-
-// four int8 codes -> two pairs of fp16: (0, 1) and (2, 3)
-__device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t off = 0x64806480u;  // 1152
-  const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&off));
-  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&off));
-  lo = *reinterpret_cast<const uint32_t*>(&a);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // 8x8 matrix of 16-bit elements, transposed: lane 4 g + t gives (g, 2t..2t+1) and gets (2t..2t+1, g)
@@ -132,73 +82,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
   grid_launch_dependents();
   const moe_layer_kv_attention_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kRing);  // [batch + 1]
-  int4* shapes = reinterpret_cast<int4*>(smem + kWarps * kRing + (a.batch + 2) / 2 * 16);  // [batch]: q0, qlen, len, tile0
-  __shared__ int64_t s_carry[kWarps + 1];
-
-  // ---- the work of every sequence, summed
-  if (tid == 0) prefix[0] = 0;
-  int64_t run = 0;
-  for (int base = 0; base < a.batch; base += kThreads) {
-    const int b = base + tid;
-    int64_t v = 0;
-    if (b < a.batch) {
-      const SeqShape s = seq_shape<NR>(a, b);
-      v = static_cast<int64_t>(a.cache.kv_heads) * s.row_tiles * (s.tiles + kUnitCost);
-      shapes[b] = make_int4(s.q0, s.qlen, s.len, s.tile0);
-    }
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) s_carry[warp] = v;
-    __syncthreads();
-    int64_t before = run, all = run;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_carry[w];
-      all += s_carry[w];
-    }
-    if (b < a.batch) prefix[b + 1] = before + v;
-    run = all;
-    __syncthreads();
-  }
-  const int64_t total = run;
+  __shared__ int64_t s_carry[kWarps];
+  Schedule<R, kTileTokens, kUnitCost> work;
+  work.template build<kThreads>(a, smem + kWarps * kRing, s_carry);
   const int c = blockIdx.x;
-  if (tid == 0) p.records[c].b = -1;
-  // CTA c takes costs [total * c / G, total * (c + 1) / G), at least one of them
-  const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  if (c >= G) return;
-  int64_t at = total * c / G;
-  const int64_t end = total * (c + 1) / G;
+  if (tid == 0) {
+    p.records[c].b = -1;
+    if (c == 0) p.status[1] = p.status[2] = 0;  // no wait of this kernel can give up
+  }
 
   uint8_t* ring = smem + warp * kRing;
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
-  while (at < end) {
-    int lo = 0, hi = a.batch;  // the b with prefix[b] <= at < prefix[b + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= at) lo = mid;
-      else hi = mid;
-    }
-    const int b = lo;
-    SeqShape s;
-    const int4 sh = shapes[b];
-    s.q0 = sh.x, s.qlen = sh.y, s.len = sh.z, s.tile0 = sh.w;
-    s.row_tiles = (s.qlen * a.group_size + 8 * NR - 1) / (8 * NR);
-    s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.tile0);
-    const int cost = s.tiles + kUnitCost;
-    const int64_t rel = at - prefix[b];
-    const int unit = static_cast<int>(rel / cost);
-    const int xa = static_cast<int>(rel - static_cast<int64_t>(unit) * cost);
-    const int xb = static_cast<int>(min(static_cast<int64_t>(cost), xa + (end - at)));
-    const int ta = max(0, xa - kUnitCost), tb = max(0, xb - kUnitCost);
-    const int head = unit / s.row_tiles, rt = unit - head * s.row_tiles;
-    const int64_t first_piece = at - xa + kUnitCost;  // where the unit's first piece lies
-    at += xb - xa;
-    if (tb == ta) continue;
-
-    const int rows = min(R, s.qlen * a.group_size - rt * R);
+  Segment seg;
+  while (work.next(a, seg)) {
+    const SeqShape& s = seg.s;
+    const int b = seg.b, head = seg.head, rt = seg.rt, rows = seg.rows, ta = seg.ta, tb = seg.tb;
     const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
     // keys that any row of the tile sees, cut to this CTA's pieces
     const int64_t last = pos0 + (rt * R + rows - 1) / a.group_size;
@@ -506,24 +405,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
       }
     } else {
       const int64_t slot = 2 * static_cast<int64_t>(c) + (ta > 0 ? 0 : 1);
-      float* po = p.part_o + (slot * 16 + r) * D + d0;
+      float* po = p.part_o + (slot * R + r) * D + d0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) po[i] = acc[i];
       if (tid % kPerRow == 0) {
-        p.part_ml[(slot * 16 + r) * 2] = top;
-        p.part_ml[(slot * 16 + r) * 2 + 1] = sum;
+        p.part_ml[(slot * R + r) * 2] = top;
+        p.part_ml[(slot * R + r) * 2 + 1] = sum;
       }
       if (tb == s.tiles && tid == 0) {
-        // the CTA of x is the last c with total * c / G <= x
-        int64_t c0 = first_piece * G / total;
-        while (c0 + 1 < G && total * (c0 + 1) / G <= first_piece) ++c0;
-        while (c0 > 0 && total * c0 / G > first_piece) --c0;
-        p.records[c] = Record{b, head, rt, static_cast<int>(c0)};
+        p.records[c] = Record{b, head, rt, work.cta_of(seg.first_piece)};
       }
     }
     __syncthreads();
   }
 }
+
+}  // namespace
+
+namespace {
 
 // Joins the parts of a unit that several CTAs shared.  CTA (c, y) takes rows
 // 4 y .. 4 y + 3 of the unit that CTA c finished, four warps a row: warp i
@@ -531,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
 // in a fixed order.  The maxima are read first, so that the parts' loads
 // depend on nothing but their addresses.
 constexpr int kJoinWarps = 4;
-template <typename T, int D, int NR>
+template <typename T, int D, int R, int TILE>
 __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(const AttnParams p) {
   constexpr int kEach = D / 32;
   __shared__ float s_acc[4][kJoinWarps][D];
@@ -545,7 +444,7 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
   const moe_layer_kv_attention_args_t& a = p.a;
   const int np = c - rec.c0 + 1;
   // the first CTA left its part in slot 1, the others in slot 0
-  auto slot_row = [&](int i) { return (2 * static_cast<int64_t>(rec.c0 + i) + (i == 0 ? 1 : 0)) * 16 + r; };
+  auto slot_row = [&](int i) { return (2 * static_cast<int64_t>(rec.c0 + i) + (i == 0 ? 1 : 0)) * R + r; };
   float top = -INFINITY;
   for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_ml[slot_row(i) * 2]);
 #pragma unroll
@@ -565,13 +464,13 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
 #pragma unroll
   for (int e = 0; e < kEach; ++e) s_acc[r4][part][lane * kEach + e] = acc[e];
   __syncthreads();
-  const SeqShape s = seq_shape<NR>(a, rec.b);
-  if (part != 0 || r >= min(8 * NR, s.qlen * a.group_size - rec.rt * 8 * NR)) return;
+  const SeqShape s = seq_shape<TILE>(a, rec.b);
+  if (part != 0 || r >= min(R, s.qlen * a.group_size - rec.rt * R)) return;
   sum = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) sum = __fadd_rn(sum, s_sum[r4][w]);
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
-  const int row = rec.rt * 8 * NR + r, j = row / a.group_size, hq = row - j * a.group_size;
+  const int row = rec.rt * R + r, j = row / a.group_size, hq = row - j * a.group_size;
   T* out = static_cast<T*>(a.out) +
            (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + rec.head * a.group_size + hq) * D;
 #pragma unroll
@@ -592,7 +491,8 @@ int grid_max(int num_sms, int per_sm) { return num_sms * per_sm < kMaxSlots ? nu
 template <typename T, int D, int NR>
 cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   const moe_layer_kv_attention_args_t& a = p.a;
-  const int smem = kWarps * kStagesOf<NR> * 2 * kSlice * D + (a.batch + 2) / 2 * 16 + a.batch * 16;
+  using Work = Schedule<8 * NR, kTileTokens, kUnitCost>;
+  const size_t smem = kWarps * kStagesOf<NR> * 2 * kSlice * D + Work::bytes(a.batch);
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem((const void*)kv_attention_kernel<T, D, NR>, kMaxSmem - 1024, allowed);
   if (e != cudaSuccess) return e;
@@ -607,31 +507,49 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   void* args[] = {&arg};
   e = launch_after((const void*)kv_attention_kernel<T, D, NR>, dim3(grid), dim3(kThreads), args, smem, s);
   if (e != cudaSuccess) return e;
-  const int join_rows = rows < 8 * NR ? static_cast<int>(rows) : 8 * NR;
-  return launch_after((const void*)kv_attention_join_kernel<T, D, NR>, dim3(grid, (join_rows + 3) / 4),
-                          dim3(kJoinWarps * 4 * 32), args, 0, s);
+  return launch_join<T, D, 8 * NR, kTileTokens>(p, grid, rows < 8 * NR ? static_cast<int>(rows) : 8 * NR, s);
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
-  return static_cast<int64_t>(p.a.max_q) * p.a.group_size <= 8 ? launch_rows<T, D, 1>(p, num_sms, s)
-                                                              : launch_rows<T, D, 2>(p, num_sms, s);
+  const int64_t rows = static_cast<int64_t>(p.a.max_q) * p.a.group_size;
+  if (rows <= 8) return launch_rows<T, D, 1>(p, num_sms, s);
+  if (rows < kChunkFrom || !chunk_fits(D, p.a.batch)) return launch_rows<T, D, 2>(p, num_sms, s);
+  return launch_chunk<T, D>(p, num_sms, s);
 }
 
 }  // namespace
 
+template <typename T, int D, int R, int TILE>
+cudaError_t launch_join(const AttnParams& p, int grid, int rows, cudaStream_t s) {
+  AttnParams arg = p;
+  void* args[] = {&arg};
+  return launch_after((const void*)kv_attention_join_kernel<T, D, R, TILE>, dim3(grid, (rows + 3) / 4),
+                      dim3(kJoinWarps * 4 * 32), args, 0, s);
+}
+template cudaError_t launch_join<__nv_bfloat16, 64, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__nv_bfloat16, 128, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__half, 64, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__half, 128, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
+
+namespace {
+// rows of all parts: 4 CTAs an SM of 8 or 3 of 16, or one of kChunkRows
+constexpr size_t kStatusBytes = 256;
+size_t part_rows(int num_sms) { return 2 * static_cast<size_t>(num_sms) * kChunkRows; }
+static_assert(kChunkRows >= 3 * 16 && kChunkRows >= 4 * 8, "the parts of every kernel fit");
+}  // namespace
+
 size_t attention_workspace(int head_dim, int num_sms) {
-  const size_t g = grid_max(num_sms, 4);
-  return 2 * g * 16 * (head_dim + 2) * sizeof(float) + g * sizeof(Record) + 256;
+  return kStatusBytes + part_rows(num_sms) * (head_dim + 2) * sizeof(float) + grid_max(num_sms, 4) * sizeof(Record);
 }
 
 cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s) {
   AttnParams p;
   p.a = a;
-  const size_t g = grid_max(num_sms, 4);
-  p.part_o = static_cast<float*>(ws);
-  p.part_ml = p.part_o + 2 * g * 16 * a.cache.head_dim;
-  p.records = reinterpret_cast<Record*>(p.part_ml + 2 * g * 16 * 2);
+  p.status = static_cast<int32_t*>(ws);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  p.part_ml = p.part_o + part_rows(num_sms) * a.cache.head_dim;
+  p.records = reinterpret_cast<Record*>(p.part_ml + part_rows(num_sms) * 2);
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   p.page_shift = 31 - __builtin_clz(static_cast<unsigned>(a.cache.page_size));
   if (a.dtype == MOE_LAYER_BF16)

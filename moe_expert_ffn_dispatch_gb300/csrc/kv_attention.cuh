@@ -1,0 +1,167 @@
+// What the two attention kernels share: the division of the work over the
+// CTAs, and the records of units that several CTAs hold.
+#pragma once
+
+#include "layer_ops.cuh"
+
+namespace moe_layer {
+
+struct Record {  // a unit that several CTAs share, left by the CTA that holds its last piece
+  int b, head, rt, c0;  // c0: its first CTA; b < 0: none
+};
+
+struct AttnParams {
+  moe_layer_kv_attention_args_t a;
+  float* part_o;      // [2 * grid][rows of a unit][D]
+  float* part_ml;     // [2 * grid][rows of a unit][2]
+  Record* records;    // [grid]
+  int32_t* status;    // [4] words of the workspace: a wait that gave up is noted here
+  float scale_log2;   // sm_scale * log2(e)
+  int page_shift;
+};
+
+// What a sequence contributes, from its lengths.
+struct SeqShape {
+  int q0, qlen;     // query tokens
+  int len;          // keys
+  int tile0, tiles; // pieces of TILE keys that its rows see; tiles >= 1
+};
+
+template <int TILE>
+__device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_t& a, int b) {
+  SeqShape s;
+  if (a.cu_q) {
+    s.q0 = min(max(a.cu_q[b], 0), a.tokens);
+    s.qlen = min(max(min(a.cu_q[b + 1], a.tokens) - s.q0, 0), a.max_q);
+  } else {
+    s.q0 = b;
+    s.qlen = 1;
+  }
+  const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
+  s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
+  int64_t lo = 0;
+  if (a.window > 0) lo = max(lo, static_cast<int64_t>(s.len) - s.qlen - a.window + 1);
+  s.tile0 = static_cast<int>(lo / TILE);
+  s.tiles = max(1, (s.len + TILE - 1) / TILE - s.tile0);
+  return s;
+}
+
+// A stretch of a unit's pieces that one CTA takes.
+struct Segment {
+  int b, head, rt, rows;  // rows: query rows of the unit
+  int ta, tb;             // its pieces, counted from the sequence's first
+  SeqShape s;
+  int64_t first_piece;    // where the unit's first piece lies in the sequence of work
+};
+
+// The work of all units (sequence, kv head, tile of R rows) in a row: each
+// costs its pieces of TILE keys and COST more (its queries, a cold pipeline,
+// the join).  CTA c of G takes [total c / G, total (c + 1) / G) of it.
+template <int R, int TILE, int COST>
+struct Schedule {
+  int64_t* prefix;  // shared memory: [batch + 1]
+  int4* shapes;     // shared memory: [batch], q0, qlen, len, tile0
+  int64_t total, at, end;
+  int G;
+
+  static __host__ __device__ size_t bytes(int batch) { return static_cast<size_t>(batch + 2) / 2 * 16 + batch * 16; }
+
+  // by every thread of the CTA; carry: shared, one entry a warp
+  template <int THREADS>
+  __device__ __forceinline__ void build(const moe_layer_kv_attention_args_t& a, uint8_t* mem, int64_t* carry) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    prefix = reinterpret_cast<int64_t*>(mem);
+    shapes = reinterpret_cast<int4*>(mem + (a.batch + 2) / 2 * 16);
+    if (tid == 0) prefix[0] = 0;
+    int64_t run = 0;
+    for (int base = 0; base < a.batch; base += THREADS) {
+      const int b = base + tid;
+      int64_t v = 0;
+      if (b < a.batch) {
+        const SeqShape s = seq_shape<TILE>(a, b);
+        v = static_cast<int64_t>(a.cache.kv_heads) * ((s.qlen * a.group_size + R - 1) / R) * (s.tiles + COST);
+        shapes[b] = make_int4(s.q0, s.qlen, s.len, s.tile0);
+      }
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane == 31) carry[warp] = v;
+      __syncthreads();
+      int64_t before = run, all = run;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += carry[w];
+        all += carry[w];
+      }
+      if (b < a.batch) prefix[b + 1] = before + v;
+      run = all;
+      __syncthreads();
+    }
+    total = run;
+    G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int c = blockIdx.x;
+    at = c < G ? total * c / G : 0;
+    end = c < G ? total * (c + 1) / G : 0;
+  }
+
+  // the CTA's next stretch; false at the end
+  __device__ __forceinline__ bool next(const moe_layer_kv_attention_args_t& a, Segment& g) {
+    while (at < end) {
+      int lo = 0, hi = a.batch;  // the b with prefix[b] <= at < prefix[b + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= at) lo = mid;
+        else hi = mid;
+      }
+      const int4 sh = shapes[lo];
+      g.b = lo;
+      g.s.q0 = sh.x, g.s.qlen = sh.y, g.s.len = sh.z, g.s.tile0 = sh.w;
+      g.s.tiles = max(1, (g.s.len + TILE - 1) / TILE - g.s.tile0);
+      const int row_tiles = (g.s.qlen * a.group_size + R - 1) / R, cost = g.s.tiles + COST;
+      const int64_t rel = at - prefix[lo];
+      const int unit = static_cast<int>(rel / cost);
+      const int xa = static_cast<int>(rel - static_cast<int64_t>(unit) * cost);
+      const int xb = static_cast<int>(min(static_cast<int64_t>(cost), xa + (end - at)));
+      g.ta = max(0, xa - COST);
+      g.tb = max(0, xb - COST);
+      g.head = unit / row_tiles;
+      g.rt = unit - g.head * row_tiles;
+      g.rows = min(R, g.s.qlen * a.group_size - g.rt * R);
+      g.first_piece = at - xa + COST;
+      at += xb - xa;
+      if (g.tb > g.ta) return true;
+    }
+    return false;
+  }
+
+  // the CTA that holds piece x: the last c with total c / G <= x
+  __device__ __forceinline__ int cta_of(int64_t x) const {
+    int64_t c = x * G / total;
+    while (c + 1 < G && total * (c + 1) / G <= x) ++c;
+    while (c > 0 && total * c / G > x) --c;
+    return static_cast<int>(c);
+  }
+};
+
+// four int8 codes -> two pairs of fp16: (0, 1) and (2, 3)
+__device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t off = 0x64806480u;  // 1152
+  const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&off));
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&off));
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Joins the parts of units that several CTAs shared (kv_attention.cu); rows: the most that a unit has.
+template <typename T, int D, int R, int TILE>
+cudaError_t launch_join(const AttnParams& p, int grid, int rows, cudaStream_t s);
+
+// kv_attention_chunk.cu: tensor-memory kernel for many query rows a kv head.
+constexpr int kChunkRows = 256;
+template <typename T, int D>
+cudaError_t launch_chunk(const AttnParams& p, int num_sms, cudaStream_t s);
+bool chunk_fits(int head_dim, int batch);  // its shared memory, which the batch's lengths share
+
+}  // namespace moe_layer

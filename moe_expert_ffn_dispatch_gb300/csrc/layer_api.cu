@@ -123,4 +123,15 @@ int moe_layer_kv_attention(const moe_layer_kv_attention_args_t* a, void* workspa
   return done(moe_layer::launch_attention(*a, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int moe_layer_kv_attention_status(const void* workspace, void* stream) {
+  if (!workspace) return MOE_ERR_INVALID_ARG;
+  if (!at(workspace, 256)) return MOE_ERR_ALIGNMENT;
+  int32_t words[4] = {0, 0, 0, 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyAsync(words, workspace, sizeof(words), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return words[1] ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+}
+
 }  // extern "C"

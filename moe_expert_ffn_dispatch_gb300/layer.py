@@ -20,7 +20,7 @@ I32 = ctypes.c_int32
 I64 = ctypes.c_int64
 
 LAYER_EXPORTS = ["moe_layer_add_rmsnorm_quant", "moe_layer_w4_linear", "moe_layer_kv_append",
-                 "moe_layer_kv_attention_workspace_size", "moe_layer_kv_attention"]
+                 "moe_layer_kv_attention_workspace_size", "moe_layer_kv_attention", "moe_layer_kv_attention_status"]
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3}
 
 
@@ -59,6 +59,7 @@ def declare(L: ctypes.CDLL) -> None:
                        ("moe_layer_kv_append", KvAppendArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), P]
     L.moe_layer_kv_attention.argtypes = [ctypes.POINTER(KvAttentionArgs), P, ctypes.c_size_t, P]
+    L.moe_layer_kv_attention_status.argtypes = [P, P]
     L.moe_layer_kv_attention_workspace_size.argtypes = [I32, ctypes.POINTER(ctypes.c_size_t)]
     for name in LAYER_EXPORTS:
         getattr(L, name).restype = ctypes.c_int
@@ -402,3 +403,10 @@ class KvCache:
         if rc:
             _raise(rc, "moe_layer_kv_attention")
         return out
+
+    def status(self, workspace: Optional[torch.Tensor] = None) -> int:
+        """Synchronises the current stream; the code of the last attention on
+        this workspace: 0, or MOE_ERR_DEVICE_TIMEOUT where a wait inside it
+        gave up."""
+        ws = self.workspace() if workspace is None else workspace
+        return _entry("moe_layer_kv_attention_status")(ws.data_ptr(), torch.cuda.current_stream(self.device).cuda_stream)
