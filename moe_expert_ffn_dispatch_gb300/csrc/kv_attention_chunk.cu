@@ -107,6 +107,33 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float log2_fast(float v) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const AttnParams p) {
   using L = Layout<D>;
@@ -240,19 +267,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           const uint32_t s_col = s_at(q) + lanes;
           auto seen = [&](int c) { return c >= c_lo && c <= c_hi && !((gone >> (c >> 4)) & 1u); };
           float top = -INFINITY;
+          if (whole) {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+              float v[32];
+              tmem_ld32(s_col + c, v);
 #pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
-            float v[32];
-            tmem_ld32(s_col + c, v);
+              for (int h = 0; h < 2; ++h) {
+                const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
+                float big = v[h * 16];
+                if (f >= 0.0f) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-              if (whole) {
-                float big = v[h * 16], small = v[h * 16];
+                  for (int e = 1; e < 16; ++e) big = fmaxf(big, v[h * 16 + e]);
+                } else {
 #pragma unroll
-                for (int e = 1; e < 16; ++e) big = fmaxf(big, v[h * 16 + e]), small = fminf(small, v[h * 16 + e]);
-                top = fmaxf(top, fmaxf(__fmul_rn(big, f), __fmul_rn(small, f)));
-              } else {
+                  for (int e = 1; e < 16; ++e) big = fminf(big, v[h * 16 + e]);
+                }
+                top = fmaxf(top, __fmul_rn(big, f));
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+              float v[32];
+              tmem_ld32(s_col + c, v);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                   top = fmaxf(top, seen(c + h * 16 + e) ? __fmul_rn(v[h * 16 + e], f) : -INFINITY);
@@ -281,32 +322,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
             }
           }
           const float ref = m == -INFINITY ? 0.0f : m;
+          // Where every scale of V is an ordinary positive number, its ratio to
+          // the reference joins the exponent, and the sum of a block's weights
+          // is divided by it.
+          const float vw = __fmul_rn(vs, vinv);
+          if (whole && __all_sync(0xffffffffu, lane >= 8 || (vw >= 0x1p-60f && vw <= 16.0f))) {
+            const float lv = log2_fast(vw), rv = __fdiv_rn(1.0f, vw);
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+              float v[32];
+              tmem_ld32(s_col + c, v);
+              uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
-            float v[32];
-            tmem_ld32(s_col + c, v);
-            uint32_t w[16];
+              for (int h = 0; h < 2; ++h) {
+                const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
+                const float b = __fsub_rn(__shfl_sync(0xffffffffu, lv, (c >> 4) + h), ref);
+                const float r1 = __shfl_sync(0xffffffffu, rv, (c >> 4) + h);
+                const uint64_t ff = pair_of(f, f), bb = pair_of(b, b);
+                uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-              const float vw = __fmul_rn(__shfl_sync(0xffffffffu, vs, (c >> 4) + h), vinv);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float w0 = exp2_fast(__fmaf_rn(v[h * 16 + e], f, -ref)), w1 = exp2_fast(__fmaf_rn(v[h * 16 + e + 1], f, -ref));
-                if (!whole) {
-                  w0 = seen(c + h * 16 + e) ? w0 : 0.0f;
-                  w1 = seen(c + h * 16 + e + 1) ? w1 : 0.0f;
+                for (int e = 0; e < 16; e += 4) {
+                  const float2 x0 = of_pair(fma_pair(pair_of(v[h * 16 + e], v[h * 16 + e + 1]), ff, bb));
+                  const float2 x1 = of_pair(fma_pair(pair_of(v[h * 16 + e + 2], v[h * 16 + e + 3]), ff, bb));
+                  const float p0 = exp2_fast(x0.x), p1 = exp2_fast(x0.y), p2 = exp2_fast(x1.x), p3 = exp2_fast(x1.y);
+                  sum0 = add_pair(sum0, pair_of(p0, p1));
+                  sum1 = add_pair(sum1, pair_of(p2, p3));
+                  w[h * 8 + e / 2] = pack2<__half>(p0, p1);
+                  w[h * 8 + e / 2 + 1] = pack2<__half>(p2, p3);
                 }
-                l = __fadd_rn(l, __fadd_rn(w0, w1));
-                float p0 = __fmul_rn(w0, vw), p1 = __fmul_rn(w1, vw);
-                if (!whole) {  // a scale that is not finite stays out of what is not seen
-                  p0 = seen(c + h * 16 + e) ? p0 : 0.0f;
-                  p1 = seen(c + h * 16 + e + 1) ? p1 : 0.0f;
-                }
-                w[h * 8 + e / 2] = pack2<__half>(p0, p1);
+                const float2 s2 = of_pair(add_pair(sum0, sum1));
+                l = __fmaf_rn(__fadd_rn(s2.x, s2.y), r1, l);
               }
+              tmem_st16(s_col + c / 2, w);  // columns that have been read
             }
-            tmem_st16(s_col + c / 2, w);  // columns that have been read
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+              float v[32];
+              tmem_ld32(s_col + c, v);
+              uint32_t w[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
+                const float vb = __shfl_sync(0xffffffffu, vw, (c >> 4) + h);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  float p2[2];
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    // a scale that is not finite stays out of what is not seen
+                    const bool on = seen(c + h * 16 + e + z);
+                    const float w1 = on ? exp2_fast(__fmaf_rn(v[h * 16 + e + z], f, -ref)) : 0.0f;
+                    l = __fadd_rn(l, w1);
+                    p2[z] = on ? __fmul_rn(w1, vb) : 0.0f;
+                  }
+                  w[h * 8 + e / 2] = pack2<__half>(p2[0], p2[1]);
+                }
+              }
+              tmem_st16(s_col + c / 2, w);
+            }
           }
           moe::tmem_st_wait();
           moe::tc_fence_before();
@@ -364,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
     const int ct = tid - kSoftWarps * 32;
     const int cc = ct % kRowChunks, r0 = ct / kRowChunks;
     constexpr int kRowStep = kConvThreads / kRowChunks;
-    // a piece ahead of the conversion: the codes; two ahead: the pages
+    // the codes come a piece ahead of the conversion, into the registers that it
+    // has just emptied; their pages a piece ahead of that
     Pieces pc;
     pc.n = 0;
     int at = 0;
@@ -385,16 +460,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       ++at;
       return true;
     };
-    uint4 nk[kIt], nv[kIt], ck[kIt], cv[kIt];
-    auto fetch = [&]() {
+    uint4 ck[kIt], cv[kIt];
+    auto fetch = [&](const int8_t* base, uint4 (&u)[kIt]) {
 #pragma unroll
       for (int i = 0; i < kIt; ++i) {
-        nk[i] = nv[i] = make_uint4(0, 0, 0, 0);
-        if (page[i] >= 0 && page[i] < a.cache.num_pages) {
-          const int64_t off = page[i] * a.cache.page_stride + head * a.cache.head_stride + slot[i] * D + cc * 16;
-          nk[i] = __ldg(reinterpret_cast<const uint4*>(a.cache.k + off));
-          nv[i] = __ldg(reinterpret_cast<const uint4*>(a.cache.v + off));
-        }
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (page[i] >= 0 && page[i] < a.cache.num_pages)
+          u[i] = __ldg(reinterpret_cast<const uint4*>(base + page[i] * a.cache.page_stride + head * a.cache.head_stride +
+                                                      slot[i] * D + cc * 16));
       }
     };
     auto convert = [&](uint8_t* to, const uint4 (&u)[kIt]) {
@@ -415,30 +488,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       moe::fence_proxy_async_smem();
     };
     uint32_t t = 0;
-    bool more = pages_of_next(), ok = true;
-    if (more) {
-      fetch();
-      bool next = pages_of_next();
-      while (ok) {
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) ck[i] = nk[i], cv[i] = nv[i];
-        const bool have = next;
-        if (have) {
-          fetch();
-          next = pages_of_next();
-        }
+    bool ok = true;
+    if (pages_of_next()) {
+      fetch(a.cache.k, ck);
+      fetch(a.cache.v, cv);
+      bool more = pages_of_next();
+      while (true) {
         const int st = t & 1;
         const uint32_t ph = (t >> 1) & 1;
         if (t >= 2) ok = moe::mbar_wait_bounded(&bar.k_empty[st], ph ^ 1, abort, p.status, kSite + 3);
         if (!ok) break;
         convert(smem + L::kK + st * L::kOperand, ck);
         moe::mbar_arrive(&bar.k_full[st]);
+        if (more) fetch(a.cache.k, ck);
         if (t >= 2) ok = moe::mbar_wait_bounded(&bar.v_empty[st], ph ^ 1, abort, p.status, kSite + 4);
         if (!ok) break;
         convert(smem + L::kV + st * L::kOperand, cv);
         moe::mbar_arrive(&bar.v_full[st]);
         ++t;
-        if (!have) break;
+        if (!more) break;
+        fetch(a.cache.v, cv);
+        more = pages_of_next();
       }
     }
   } else {
