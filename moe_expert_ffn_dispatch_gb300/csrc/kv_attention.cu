@@ -95,15 +95,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
   Segment seg;
-  while (work.next(a, seg)) {
+  int64_t at = work.begin;
+  while (work.next(a, at, seg)) {
     const SeqShape& s = seg.s;
     const int b = seg.b, head = seg.head, rt = seg.rt, rows = seg.rows, ta = seg.ta, tb = seg.tb;
     const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
     // keys that any row of the tile sees, cut to this CTA's pieces
     const int64_t last = pos0 + (rt * R + rows - 1) / a.group_size;
-    int64_t k_lo = static_cast<int64_t>(s.tile0 + ta) * kTileTokens;
-    int64_t k_hi = min(static_cast<int64_t>(s.tile0 + tb) * kTileTokens, last + 1);
-    if (a.window > 0) k_lo = max(k_lo, (pos0 + rt * R / a.group_size - a.window + 1) & ~static_cast<int64_t>(kSlice - 1));
+    int64_t k_lo = static_cast<int64_t>(seg.tile0 + ta) * kTileTokens;
+    const int64_t k_hi = min(static_cast<int64_t>(seg.tile0 + tb) * kTileTokens, static_cast<int64_t>(seg.keys.hi));
+    k_lo = max(k_lo, static_cast<int64_t>(seg.keys.lo & ~(kSlice - 1)));
     // this warp's slices: first + 8 i, from the slice of k_lo on
     const int first = static_cast<int>(k_lo / kSlice) + warp;
     const int n = k_hi > static_cast<int64_t>(first) * kSlice
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
 #pragma unroll
       for (int i = 0; i < kEach; ++i) acc[i] = __fmaf_rn(from[r * D + d0 + i], f, acc[i]);
     }
-    if (ta == 0 && tb == s.tiles) {
+    if (ta == 0 && tb == seg.tiles) {
       if (r < rows) {
         const int row = rt * R + r, j = row / a.group_size, hq = row - j * a.group_size;
         const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         p.part_ml[(slot * R + r) * 2] = top;
         p.part_ml[(slot * R + r) * 2 + 1] = sum;
       }
-      if (tb == s.tiles && tid == 0) {
+      if (tb == seg.tiles && tid == 0) {
         p.records[c] = Record{b, head, rt, work.cta_of(seg.first_piece)};
       }
     }
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
 #pragma unroll
   for (int e = 0; e < kEach; ++e) s_acc[r4][part][lane * kEach + e] = acc[e];
   __syncthreads();
-  const SeqShape s = seq_shape<TILE>(a, rec.b);
+  const SeqShape s = seq_shape(a, rec.b);
   if (part != 0 || r >= min(R, s.qlen * a.group_size - rec.rt * R)) return;
   sum = 0.0f;
 #pragma unroll

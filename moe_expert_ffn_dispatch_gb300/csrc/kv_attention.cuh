@@ -24,10 +24,8 @@ struct AttnParams {
 struct SeqShape {
   int q0, qlen;     // query tokens
   int len;          // keys
-  int tile0, tiles; // pieces of TILE keys that its rows see; tiles >= 1
 };
 
-template <int TILE>
 __device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_t& a, int b) {
   SeqShape s;
   if (a.cu_q) {
@@ -39,18 +37,33 @@ __device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_
   }
   const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
   s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
-  int64_t lo = 0;
-  if (a.window > 0) lo = max(lo, static_cast<int64_t>(s.len) - s.qlen - a.window + 1);
-  s.tile0 = static_cast<int>(lo / TILE);
-  s.tiles = max(1, (s.len + TILE - 1) / TILE - s.tile0);
   return s;
+}
+
+// Keys that the rows of tile rt (R rows) of a sequence see: [lo, hi)
+struct KeyRange {
+  int lo, hi;
+};
+template <int R>
+__device__ __forceinline__ KeyRange keys_of(const moe_layer_kv_attention_args_t& a, const SeqShape& s, int rt) {
+  const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;
+  const int last_row = min((rt + 1) * R, s.qlen * a.group_size) - 1;
+  KeyRange k;
+  k.hi = static_cast<int>(max(static_cast<int64_t>(0), pos0 + last_row / a.group_size + 1));
+  k.lo = 0;
+  if (a.window > 0)
+    k.lo = static_cast<int>(min(max(static_cast<int64_t>(0), pos0 + rt * R / a.group_size - a.window + 1),
+                                static_cast<int64_t>(k.hi)));
+  return k;
 }
 
 // A stretch of a unit's pieces that one CTA takes.
 struct Segment {
   int b, head, rt, rows;  // rows: query rows of the unit
-  int ta, tb;             // its pieces, counted from the sequence's first
+  int tile0, tiles;       // the unit's pieces of TILE keys: the first, how many (1 at least)
+  int ta, tb;             // of them, this stretch
   SeqShape s;
+  KeyRange keys;          // that any row sees
   int64_t first_piece;    // where the unit's first piece lies in the sequence of work
 };
 
@@ -60,9 +73,13 @@ struct Segment {
 template <int R, int TILE, int COST>
 struct Schedule {
   int64_t* prefix;  // shared memory: [batch + 1]
-  int4* shapes;     // shared memory: [batch], q0, qlen, len, tile0
-  int64_t total, at, end;
+  int4* shapes;     // shared memory: [batch], q0, qlen, len, work of one head
+  int64_t total, begin, end;  // of all the work; this CTA's
   int G;
+
+  static __device__ __forceinline__ int pieces(const KeyRange& k) {
+    return max(1, (k.hi + TILE - 1) / TILE - k.lo / TILE);
+  }
 
   static __host__ __device__ size_t bytes(int batch) { return static_cast<size_t>(batch + 2) / 2 * 16 + batch * 16; }
 
@@ -78,9 +95,12 @@ struct Schedule {
       const int b = base + tid;
       int64_t v = 0;
       if (b < a.batch) {
-        const SeqShape s = seq_shape<TILE>(a, b);
-        v = static_cast<int64_t>(a.cache.kv_heads) * ((s.qlen * a.group_size + R - 1) / R) * (s.tiles + COST);
-        shapes[b] = make_int4(s.q0, s.qlen, s.len, s.tile0);
+        const SeqShape s = seq_shape(a, b);
+        const int row_tiles = (s.qlen * a.group_size + R - 1) / R;
+        int one = 0;
+        for (int rt = 0; rt < row_tiles; ++rt) one += pieces(keys_of<R>(a, s, rt)) + COST;
+        v = static_cast<int64_t>(a.cache.kv_heads) * one;
+        shapes[b] = make_int4(s.q0, s.qlen, s.len, one);
       }
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -100,12 +120,12 @@ struct Schedule {
     total = run;
     G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
     const int c = blockIdx.x;
-    at = c < G ? total * c / G : 0;
+    begin = c < G ? total * c / G : 0;
     end = c < G ? total * (c + 1) / G : 0;
   }
 
-  // the CTA's next stretch; false at the end
-  __device__ __forceinline__ bool next(const moe_layer_kv_attention_args_t& a, Segment& g) {
+  // the stretch at `at`, which starts at `begin` and is moved on; false at the end
+  __device__ __forceinline__ bool next(const moe_layer_kv_attention_args_t& a, int64_t& at, Segment& g) const {
     while (at < end) {
       int lo = 0, hi = a.batch;  // the b with prefix[b] <= at < prefix[b + 1]
       while (hi - lo > 1) {
@@ -115,17 +135,22 @@ struct Schedule {
       }
       const int4 sh = shapes[lo];
       g.b = lo;
-      g.s.q0 = sh.x, g.s.qlen = sh.y, g.s.len = sh.z, g.s.tile0 = sh.w;
-      g.s.tiles = max(1, (g.s.len + TILE - 1) / TILE - g.s.tile0);
-      const int row_tiles = (g.s.qlen * a.group_size + R - 1) / R, cost = g.s.tiles + COST;
+      g.s.q0 = sh.x, g.s.qlen = sh.y, g.s.len = sh.z;
       const int64_t rel = at - prefix[lo];
-      const int unit = static_cast<int>(rel / cost);
-      const int xa = static_cast<int>(rel - static_cast<int64_t>(unit) * cost);
-      const int xb = static_cast<int>(min(static_cast<int64_t>(cost), xa + (end - at)));
+      g.head = static_cast<int>(rel / sh.w);
+      int rem = static_cast<int>(rel - static_cast<int64_t>(g.head) * sh.w);
+      g.rt = 0;
+      while (true) {  // the unit of this head that holds `rem`
+        g.keys = keys_of<R>(a, g.s, g.rt);
+        g.tiles = pieces(g.keys);
+        if (rem < g.tiles + COST) break;
+        rem -= g.tiles + COST;
+        ++g.rt;
+      }
+      g.tile0 = g.keys.lo / TILE;
+      const int xa = rem, xb = static_cast<int>(min(static_cast<int64_t>(g.tiles + COST), xa + (end - at)));
       g.ta = max(0, xa - COST);
       g.tb = max(0, xb - COST);
-      g.head = unit / row_tiles;
-      g.rt = unit - g.head * row_tiles;
       g.rows = min(R, g.s.qlen * a.group_size - g.rt * R);
       g.first_piece = at - xa + COST;
       at += xb - xa;

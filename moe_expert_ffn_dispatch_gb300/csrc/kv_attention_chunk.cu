@@ -59,14 +59,12 @@ struct Pieces {
   int lo, hi;       // keys that any row sees
   int64_t pos0;     // position of query token 0
 };
-__device__ __forceinline__ Pieces pieces_of(const moe_layer_kv_attention_args_t& a, const Segment& g) {
+__device__ __forceinline__ Pieces pieces_of(const Segment& g) {
   Pieces r;
   r.pos0 = static_cast<int64_t>(g.s.len) - g.s.qlen;
-  const int64_t last = r.pos0 + (g.rt * kChunkRows + g.rows - 1) / a.group_size;
-  r.hi = static_cast<int>(max(static_cast<int64_t>(0), last + 1));
-  r.lo = a.window > 0 ? static_cast<int>(max(static_cast<int64_t>(0), r.pos0 + g.rt * kChunkRows / a.group_size - a.window + 1)) : 0;
-  r.first = max(g.s.tile0 + g.ta, r.lo / kTile);
-  r.n = max(0, min(g.s.tile0 + g.tb, (r.hi + kTile - 1) / kTile) - r.first);
+  r.lo = g.keys.lo, r.hi = g.keys.hi;
+  r.first = g.tile0 + g.ta;
+  r.n = max(0, min(g.tile0 + g.tb, (r.hi + kTile - 1) / kTile) - r.first);
   return r;
 }
 
@@ -163,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
   }
   if (warp == kWarpMma) moe::tmem_alloc(&bar.tmem, 512);
   Work work;
-  work.template build<kThreads>(a, smem + L::kWork, bar.carry);  // ends with a CTA barrier when there is a sequence
+  work.template build<kThreads>(a, smem + L::kWork, bar.carry);
   __syncthreads();
   moe::tc_fence_after();
   const uint32_t tmem = bar.tmem;
@@ -176,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
   auto s_at = [&](int q) { return tmem + q * kTile; };
   auto o_at = [&](int q) { return tmem + 2 * kTile + q * D; };
   Segment seg;
+  int64_t at = work.begin;
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------ weights: a row a thread
@@ -183,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
-    while (ok && work.next(a, seg)) {
-      const Pieces pc = pieces_of(a, seg);
+    while (ok && work.next(a, at, seg)) {
+      const Pieces pc = pieces_of(seg);
       const int row = q * 128 + r;
       const bool mine = row < seg.rows, active = q * 128 < seg.rows;  // active: uniform over the tile
       const int grow = seg.rt * kChunkRows + row, j = grow / a.group_size, hq = grow - j * a.group_size;
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       }
       if (!active) continue;
       // ---- the rows' results
-      const bool done = seg.ta == 0 && seg.tb == seg.s.tiles;
+      const bool whole_unit = seg.ta == 0 && seg.tb == seg.tiles;
       const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
       const int64_t slot_row = (2 * static_cast<int64_t>(blockIdx.x) + (seg.ta > 0 ? 0 : 1)) * kChunkRows + row;
       T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(seg.s.q0 + j) * a.cache.kv_heads * a.group_size +
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(v[e], vref);
-        if (done) {
+        if (whole_unit) {
           if (mine) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -425,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
             *reinterpret_cast<float4*>(p.part_o + slot_row * D + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
-      if (!done) {
+      if (!whole_unit) {
         p.part_ml[slot_row * 2] = m;
         p.part_ml[slot_row * 2 + 1] = l;
-        if (seg.tb == seg.s.tiles && row == 0)
+        if (seg.tb == seg.tiles && row == 0)
           p.records[blockIdx.x] = Record{seg.b, seg.head, seg.rt, work.cta_of(seg.first_piece)};
       }
     }
@@ -442,22 +441,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
     // has just emptied; their pages a piece ahead of that
     Pieces pc;
     pc.n = 0;
-    int at = 0;
+    int done = 0;  // pieces of the segment
     int page[kIt], head = 0, slot[kIt];
     auto pages_of_next = [&]() {  // false: no piece left
-      while (at >= pc.n) {
-        if (!work.next(a, seg)) return false;
-        pc = pieces_of(a, seg);
-        at = 0;
+      while (done >= pc.n) {
+        if (!work.next(a, at, seg)) return false;
+        pc = pieces_of(seg);
+        done = 0;
       }
       head = seg.head;
 #pragma unroll
       for (int i = 0; i < kIt; ++i) {
-        const int tok = (pc.first + at) * kTile + r0 + i * kRowStep;
+        const int tok = (pc.first + done) * kTile + r0 + i * kRowStep;
         page[i] = tok < pc.hi ? a.page_table[seg.b * a.table_stride + (tok >> p.page_shift)] : -1;
         slot[i] = tok & (a.cache.page_size - 1);
       }
-      ++at;
+      ++done;
       return true;
     };
     uint4 ck[kIt], cv[kIt];
@@ -470,20 +469,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
                                                       slot[i] * D + cc * 16));
       }
     };
+    // rows of a thread lie a multiple of 8 apart: one swizzle for all of them.
+    // Lanes of the other half of the channels store in the other order: no bank twice
+    static_assert(kRowStep % 8 == 0, "");
+    const bool swap = cc & 4;
+    const uint32_t first_at = operand_at(r0, 2 * cc + (swap ? 1 : 0)), second_at = operand_at(r0, 2 * cc + (swap ? 0 : 1));
     auto convert = [&](uint8_t* to, const uint4 (&u)[kIt]) {
 #pragma unroll
       for (int i = 0; i < kIt; ++i) {
-        const int r = r0 + i * kRowStep;
         uint32_t h[8];
-        half_pairs(u[i].x, h[0], h[1]);
-        half_pairs(u[i].y, h[2], h[3]);
-        half_pairs(u[i].z, h[4], h[5]);
-        half_pairs(u[i].w, h[6], h[7]);
-        const uint4 first = make_uint4(h[0], h[1], h[2], h[3]), second = make_uint4(h[4], h[5], h[6], h[7]);
-        // lanes of the other half of the channels store in the other order: no bank twice
-        const bool swap = cc & 4;
-        *reinterpret_cast<uint4*>(to + operand_at(r, 2 * cc + (swap ? 1 : 0))) = swap ? second : first;
-        *reinterpret_cast<uint4*>(to + operand_at(r, 2 * cc + (swap ? 0 : 1))) = swap ? first : second;
+        half_pairs(swap ? u[i].z : u[i].x, h[0], h[1]);
+        half_pairs(swap ? u[i].w : u[i].y, h[2], h[3]);
+        half_pairs(swap ? u[i].x : u[i].z, h[4], h[5]);
+        half_pairs(swap ? u[i].y : u[i].w, h[6], h[7]);
+        *reinterpret_cast<uint4*>(to + first_at + i * kRowStep * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(to + second_at + i * kRowStep * 128) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       moe::fence_proxy_async_smem();
     };
@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       if (moe::elect_one()) moe::umma_commit(b);
       __syncwarp();
     };
-    while (ok && work.next(a, seg)) {
-      const Pieces pc = pieces_of(a, seg);
+    while (ok && work.next(a, at, seg)) {
+      const Pieces pc = pieces_of(seg);
       if (pc.n == 0) continue;
       const bool two = seg.rows > 128;
       ok = wait(&bar.q_full, u & 1, kSite + 8);
