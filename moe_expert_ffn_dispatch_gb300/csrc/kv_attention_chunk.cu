@@ -29,7 +29,7 @@ namespace moe_layer {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 4;
 constexpr int kSoftWarps = 8, kConvWarps = 8, kWarpMma = kSoftWarps + kConvWarps;
 constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
 constexpr int kConvThreads = kConvWarps * 32;
@@ -189,35 +189,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       const int grow = seg.rt * kChunkRows + row, j = grow / a.group_size, hq = grow - j * a.group_size;
       float m = -INFINITY, l = 0.0f, vref = 0.0f, vinv = 1.0f, up = 0.0f;
       if (pc.n > 0) {
-        // the row of Q, scaled by a power of two to [1, 2) at its largest element
+        // The rows of Q, each scaled by a power of two to [1, 2) at its largest
+        // element: D / 8 lanes a row, 16 bytes a lane, 4 loads in flight.
         if (active) {
-          const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(seg.s.q0 + j) * a.q_stride +
-                         static_cast<int64_t>(seg.head * a.group_size + hq) * D;
-          uint32_t top = 0;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 u = mine ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<T>(w[e]);
-              top = max(top, max(abs_bits(f.x), abs_bits(f.y)));
-            }
-          }
-          const int e = min(max(static_cast<int>(top >> 23), 1), 253);
-          const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-          up = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 u = mine ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            uint32_t o[4];
+          constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
+          const int rl = lane / kLanes, ch = lane % kLanes;
+#pragma unroll 1
+          for (int r4 = 0; r4 < 32; r4 += 4 * kRowsAt) {
+            uint4 u[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float2 f = unpack2<T>(w[x]);
-              o[x] = pack2<__half>(__fmul_rn(f.x, down), __fmul_rn(f.y, down));
+              const int rr = q * 128 + (warp & 3) * 32 + r4 + x * kRowsAt + rl;
+              const int gr = seg.rt * kChunkRows + rr, jj = gr / a.group_size;
+              u[x] = make_uint4(0, 0, 0, 0);
+              if (rr < seg.rows)
+                u[x] = *reinterpret_cast<const uint4*>(
+                    static_cast<const T*>(a.q) + static_cast<int64_t>(seg.s.q0 + jj) * a.q_stride +
+                    static_cast<int64_t>(seg.head * a.group_size + gr - jj * a.group_size) * D + ch * 8);
             }
-            *reinterpret_cast<uint4*>(smem + L::kQ + q * L::kOperand + operand_at(r, i)) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2<T>(w[e]);
+                top = max(top, max(abs_bits(f.x), abs_bits(f.y)));
+              }
+#pragma unroll
+              for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int e = min(max(static_cast<int>(top >> 23), 1), 253);
+              const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+              uint32_t o[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float2 f = unpack2<T>(w[z]);
+                o[z] = pack2<__half>(__fmul_rn(f.x, down), __fmul_rn(f.y, down));
+              }
+              const int rr = (warp & 3) * 32 + r4 + x * kRowsAt + rl;
+              *reinterpret_cast<uint4*>(smem + L::kQ + q * L::kOperand + operand_at(rr, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
+              // to the thread that has the row
+              const float up1 = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
+              const float mine_up = __shfl_sync(0xffffffffu, up1, ((lane - r4 - x * kRowsAt) & (kRowsAt - 1)) * kLanes);
+              if (lane >= r4 + x * kRowsAt && lane < r4 + (x + 1) * kRowsAt) up = mine_up;
+            }
           }
           moe::fence_proxy_async_smem();
         }
@@ -264,7 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           ++s_phase;
           moe::tc_fence_after();
           const uint32_t s_col = s_at(q) + lanes;
-          auto seen = [&](int c) { return c >= c_lo && c <= c_hi && !((gone >> (c >> 4)) & 1u); };
+          // columns c .. c + 31 that this row sees, as bits
+          auto bits_of = [&](int c) {
+            const int lo = max(c_lo - c, 0), hi = min(c_hi - c, 31);
+            uint32_t b = hi < lo ? 0u : (0xFFFFFFFFu >> (31 - hi)) & (0xFFFFFFFFu << lo);
+            if ((gone >> (c >> 4)) & 1u) b &= 0xFFFF0000u;
+            if ((gone >> (c >> 4)) & 2u) b &= 0x0000FFFFu;
+            return b;
+          };
           float top = -INFINITY;
           if (whole) {
 #pragma unroll 1
@@ -288,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           } else {
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
+              const uint32_t bits = bits_of(c);
+              if (__all_sync(0xffffffffu, bits == 0)) continue;
               float v[32];
               tmem_ld32(s_col + c, v);
 #pragma unroll
@@ -295,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
                 const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                  top = fmaxf(top, seen(c + h * 16 + e) ? __fmul_rn(v[h * 16 + e], f) : -INFINITY);
+                  top = fmaxf(top, bits & (1u << (h * 16 + e)) ? __fmul_rn(v[h * 16 + e], f) : -INFINITY);
               }
             }
           }
@@ -357,25 +381,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           } else {
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
-              float v[32];
-              tmem_ld32(s_col + c, v);
+              const uint32_t bits = whole ? 0xFFFFFFFFu : bits_of(c);
               uint32_t w[16];
+              if (__all_sync(0xffffffffu, bits == 0)) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-                const float vb = __shfl_sync(0xffffffffu, vw, (c >> 4) + h);
+                for (int e = 0; e < 16; ++e) w[e] = 0u;
+              } else {
+                float v[32];
+                tmem_ld32(s_col + c, v);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  float p2[2];
+                for (int h = 0; h < 2; ++h) {
+                  const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
+                  const float vb = __shfl_sync(0xffffffffu, vw, (c >> 4) + h);
 #pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    // a scale that is not finite stays out of what is not seen
-                    const bool on = seen(c + h * 16 + e + z);
-                    const float w1 = on ? exp2_fast(__fmaf_rn(v[h * 16 + e + z], f, -ref)) : 0.0f;
-                    l = __fadd_rn(l, w1);
-                    p2[z] = on ? __fmul_rn(w1, vb) : 0.0f;
+                  for (int e = 0; e < 16; e += 2) {
+                    float p2[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                      // a scale that is not finite stays out of what is not seen
+                      const bool on = bits & (1u << (h * 16 + e + z));
+                      const float w1 = on ? exp2_fast(__fmaf_rn(v[h * 16 + e + z], f, -ref)) : 0.0f;
+                      l = __fadd_rn(l, w1);
+                      p2[z] = on ? __fmul_rn(w1, vb) : 0.0f;
+                    }
+                    w[h * 8 + e / 2] = pack2<__half>(p2[0], p2[1]);
                   }
-                  w[h * 8 + e / 2] = pack2<__half>(p2[0], p2[1]);
                 }
               }
               tmem_st16(s_col + c / 2, w);
