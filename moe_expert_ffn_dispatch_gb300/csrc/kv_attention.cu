@@ -425,21 +425,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
 
 namespace {
 
-// Joins the parts of a unit that several CTAs shared.  CTA (c, y) takes rows
-// 4 y .. 4 y + 3 of the unit that CTA c finished, four warps a row: warp i
-// sums every fourth part, a lane D / 32 channels, and the four sums are added
-// in a fixed order.  The maxima are read first, so that the parts' loads
-// depend on nothing but their addresses.
-constexpr int kJoinWarps = 4;
-template <typename T, int D, int R, int TILE>
-__global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(const AttnParams p) {
-  constexpr int kEach = D / 32;
-  __shared__ float s_acc[4][kJoinWarps][D];
-  __shared__ float s_sum[4][kJoinWarps];
+// Joins the parts of a unit that several CTAs shared.  CTA (c, y) takes 16 /
+// JW rows of the unit that CTA c finished, JW warps a row: warp i sums every
+// JW-th part, a lane D / 32 channels, and the JW sums are added in a fixed
+// order.  The maxima are read first, so that the parts' loads depend on
+// nothing but their addresses.  Units of few rows have many parts (JW = 4),
+// units of 256 rows two or three (JW = 1).
+constexpr int kJoinThreads = 512;
+template <typename T, int D, int R, int TILE, int JW>
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttnParams p) {
+  constexpr int kEach = D / 32, kRowsHere = 16 / JW;
+  __shared__ float s_acc[kRowsHere][JW][D];
+  __shared__ float s_sum[kRowsHere][JW];
   grid_dependency_wait();
   grid_launch_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r4 = warp / kJoinWarps, part = warp % kJoinWarps, r = blockIdx.y * 4 + r4;
+  const int r4 = warp / JW, part = warp % JW, r = blockIdx.y * kRowsHere + r4;
   const Record rec = p.records[c];
   if (rec.b < 0) return;
   const moe_layer_kv_attention_args_t& a = p.a;
@@ -452,8 +453,8 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float base = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f, acc[kEach] = {};
-#pragma unroll 4
-  for (int i = part; i < np; i += kJoinWarps) {
+#pragma unroll (JW == 1 ? 8 : 4)
+  for (int i = part; i < np; i += JW) {
     const int64_t at = slot_row(i);
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
     const float f = exp2_fast(__fsub_rn(ml.x, base));
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
   if (part != 0 || r >= min(R, s.qlen * a.group_size - rec.rt * R)) return;
   sum = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) sum = __fadd_rn(sum, s_sum[r4][w]);
+  for (int w = 0; w < JW; ++w) sum = __fadd_rn(sum, s_sum[r4][w]);
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
   const int row = rec.rt * R + r, j = row / a.group_size, hq = row - j * a.group_size;
   T* out = static_cast<T*>(a.out) +
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kJoinWarps * 4 * 32) kv_attention_join_kernel(
     for (int z = 0; z < 2; ++z) {
       v[z] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) v[z] = __fadd_rn(v[z], s_acc[r4][w][lane * kEach + e + z]);
+      for (int w = 0; w < JW; ++w) v[z] = __fadd_rn(v[z], s_acc[r4][w][lane * kEach + e + z]);
     }
     *reinterpret_cast<uint32_t*>(out + lane * kEach + e) = pack2<T>(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv));
   }
@@ -523,10 +524,11 @@ cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
 
 template <typename T, int D, int R, int TILE>
 cudaError_t launch_join(const AttnParams& p, int grid, int rows, cudaStream_t s) {
+  constexpr int JW = R > 16 ? 1 : 4;
   AttnParams arg = p;
   void* args[] = {&arg};
-  return launch_after((const void*)kv_attention_join_kernel<T, D, R, TILE>, dim3(grid, (rows + 3) / 4),
-                      dim3(kJoinWarps * 4 * 32), args, 0, s);
+  return launch_after((const void*)kv_attention_join_kernel<T, D, R, TILE, JW>,
+                      dim3(grid, (rows + 16 / JW - 1) / (16 / JW)), dim3(kJoinThreads), args, 0, s);
 }
 template cudaError_t launch_join<__nv_bfloat16, 64, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
 template cudaError_t launch_join<__nv_bfloat16, 128, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);

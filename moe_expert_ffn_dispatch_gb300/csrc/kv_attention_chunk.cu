@@ -16,11 +16,15 @@
 // each.  Keys lie [key][channel] in both operands; V's is the transposed
 // (channel-contiguous) form.  The arithmetic of the weights is that of the
 // kernel for few rows: row scaled by a power of two, page scale of K in the
-// score, page scale of V in the weight as its ratio to a reference, references
-// moved only when a weight would pass 2^8.
+// score, page scale of V in the weight as its ratio to a reference.  The rows'
+// references move by whole powers of two, and only when a weight would pass
+// 2^11, so that S is read once: weights of the same piece that are already
+// written move with the reference, exactly.
 //
-// Bound by the weights' exponentials and the conversion of the codes, which
-// the 256 rows share; the products take about half of the time.
+// Bound by a tile's chain (S, weights, O: about 5000 cycles a piece, of which the
+// products are 1100) at 42 % of the issue slots; two tiles overlap, a third has
+// no room in tensor memory.  8 chunks of 512 tokens over 8192 keys (32 heads on
+// 8, channels 128): 633 us, 841 TFLOP/s.
 #include "kv_attention.cuh"
 
 #include "device_prims.cuh"
@@ -31,7 +35,13 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kUnitCost = 4;
 constexpr int kSoftWarps = 8, kConvWarps = 8, kWarpMma = kSoftWarps + kConvWarps;
-constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
+constexpr int kThreads = (kSoftWarps + kConvWarps + 4) * 32;  // warps in fours, which share a register limit
+// Registers a thread: 96 at launch (640 x 96 = 61440 of the SM's 65536); the
+// weights' warps take 120 once the others have gone down to 80 (256 x 120 + 256
+// x 80 + 128 x 80 = 61440).  With 96 for all the weights' warps spill: 864 us in
+// place of 633 (8 chunks of 512 tokens at 8192 keys, 32 heads on 8).
+constexpr int kSoftRegs = 120, kConvRegs = 80, kMmaRegs = 80;
+static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "the split fits what the launch has");
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kSite = 1 << 8;  // of the waits, in the status
 
@@ -42,7 +52,7 @@ template <int D>
 struct Layout {
   static constexpr int kOperand = kTile * D * 2;  // one tile of Q, K or V: halves of 64 channels, [128][128 bytes] each
   static constexpr int kQ = 0, kK = 2 * kOperand, kV = 4 * kOperand, kMisc = 6 * kOperand;
-  static constexpr int kWork = kMisc + 512;
+  static constexpr int kWork = kMisc + 2560;
 };
 
 struct Barriers {
@@ -50,8 +60,10 @@ struct Barriers {
   uint32_t tmem;
   int abort;
   int64_t carry[kThreads / 32];
+  Work work;
+  Segment seg[kThreads / 32];
 };
-static_assert(sizeof(Barriers) <= 512, "");
+static_assert(sizeof(Barriers) <= 2560, "");
 
 // keys of a segment in pieces: the first, and how many
 struct Pieces {
@@ -94,6 +106,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
         "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
         "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr)
       : "memory");
 }
@@ -160,8 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
     moe::fence_barrier_init();
   }
   if (warp == kWarpMma) moe::tmem_alloc(&bar.tmem, 512);
-  Work work;
-  work.template build<kThreads>(a, smem + L::kWork, bar.carry);
+  {
+    Work built;
+    built.template build<kThreads>(a, smem + L::kWork, bar.carry);
+    if (tid == 0) bar.work = built;
+  }
   __syncthreads();
   moe::tc_fence_after();
   const uint32_t tmem = bar.tmem;
@@ -173,16 +197,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
   // columns: S of A and B, then O of A and B
   auto s_at = [&](int q) { return tmem + q * kTile; };
   auto o_at = [&](int q) { return tmem + 2 * kTile + q * D; };
-  Segment seg;
+  // what a warp works on lies in shared memory: registers are for the tiles
+  const Work& work = bar.work;
+  Segment& seg = bar.seg[warp];
   int64_t at = work.begin;
+  auto next_segment = [&]() {
+    Segment s;
+    const bool more = work.next(a, at, s);
+    __syncwarp();
+    if (more && lane == 0) seg = s;
+    __syncwarp();
+    return more;
+  };
 
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ------------------------------------------------ weights: a row a thread
     const int q = warp >> 2, r = (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
-    while (ok && work.next(a, at, seg)) {
+    while (ok && next_segment()) {
       const Pieces pc = pieces_of(seg);
       const int row = q * 128 + r;
       const bool mine = row < seg.rows, active = q * 128 < seg.rows;  // active: uniform over the tile
@@ -270,7 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           }
           const uint32_t gone = __ballot_sync(0xffffffffu, page < 0);  // blocks on pages that do not exist
           const bool whole = gone == 0 && __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kTile - 1);
-          const uint32_t vtop = __reduce_max_sync(0xffffffffu, abs_bits(vs));
+          // blocks that no row of the warp sees (lane i: block i); their scales do not count
+          const int low = __reduce_min_sync(0xffffffffu, mine ? c_lo : kTile - 1);
+          const int high = __reduce_max_sync(0xffffffffu, mine ? c_hi : -1);
+          const bool hidden = page < 0 || 16 * lane > high || 16 * lane + 15 < low;
+          const uint32_t vtop = __reduce_max_sync(0xffffffffu, hidden || lane >= 8 ? 0u : abs_bits(vs));
           const float vbig = vtop > 0x7F800000u ? 0.0f : __uint_as_float(vtop);
           if (!wait(&bar.s_full[q], s_phase & 1, kSite + q)) {
             ok = false;
@@ -287,31 +326,111 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
             if ((gone >> (c >> 4)) & 2u) b &= 0x0000FFFFu;
             return b;
           };
-          float top = -INFINITY;
-          if (whole) {
+          auto scale_o = [&](float corr) {  // S(i) is there, so the products of earlier pieces are done
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              tmem_ld32(o_at(q) + lanes + c, v);
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__fmul_rn(v[e], corr));
+              moe::tmem_st32(o_at(q) + lanes + c, w);
+            }
+          };
+          if (!(vbig <= 8.0f * vref)) {  // the same for the whole warp
+            const float vnew = fmaxf(vref, vbig);
+            if (i > 0) scale_o(__fdiv_rn(vref, vnew));
+            vref = vnew;
+            vinv = __fdiv_rn(1.0f, vnew);
+          }
+          // Where every scale of V is an ordinary positive number (or no row
+          // sees its keys), its ratio to the reference joins the exponent, and the
+          // sum of a block's weights is divided by it.
+          const float vw = __fmul_rn(vs, vinv);
+          if (__all_sync(0xffffffffu, lane >= 8 || hidden || (vw >= 0x1p-60f && vw <= 16.0f))) {
+            const float lv = hidden ? 0.0f : log2_fast(vw), rv = hidden ? 0.0f : __fdiv_rn(1.0f, vw);
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
+              const uint32_t bits = whole ? 0xFFFFFFFFu : bits_of(c);
+              uint32_t w[16];
+              if (!whole && __all_sync(0xffffffffu, bits == 0)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = 0u;
+                tmem_st16(s_col + c / 2, w);
+                continue;
+              }
+              const float ref = m == -INFINITY ? 0.0f : m;
               float v[32];
               tmem_ld32(s_col + c, v);
+              float top = -INFINITY;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-                float big = v[h * 16];
-                if (f >= 0.0f) {
+                const float b = __fsub_rn(__shfl_sync(0xffffffffu, lv, (c >> 4) + h), ref);
+                const uint64_t ff = pair_of(f, f), bb = pair_of(b, b);
 #pragma unroll
-                  for (int e = 1; e < 16; ++e) big = fmaxf(big, v[h * 16 + e]);
-                } else {
-#pragma unroll
-                  for (int e = 1; e < 16; ++e) big = fminf(big, v[h * 16 + e]);
+                for (int e = h * 16; e < h * 16 + 16; e += 2) {
+                  const float2 x = of_pair(fma_pair(pair_of(v[e], v[e + 1]), ff, bb));
+                  v[e] = x.x, v[e + 1] = x.y;
                 }
-                top = fmaxf(top, __fmul_rn(big, f));
               }
+              if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = bits & (1u << e) ? v[e] : -INFINITY;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+              // The reference moves, by whole powers of two, when a weight would
+              // pass 2^11 (or is a row's first): what the row has so far moves
+              // exactly with it, this piece's weights among it.
+              const bool fresh = m == -INFINITY && top > -INFINITY;
+              if (__any_sync(0xffffffffu, top > 11.0f || fresh)) {
+                const float d = top > 11.0f || fresh ? ceilf(top) : 0.0f;
+                const float corr = fresh ? 1.0f : exp2_fast(-d);  // a fresh row has nothing yet
+                m = __fadd_rn(ref, d) + (m == -INFINITY && !fresh ? -INFINITY : 0.0f);
+                l = __fmul_rn(l, corr);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __fsub_rn(v[e], d);
+                const __half2 ch = __float2half2_rn(corr);
+                moe::tmem_st_wait();
+#pragma unroll 1
+                for (int x = 0; x < c; x += 32) {
+                  float pv[16];
+                  tmem_ld16(s_col + x / 2, pv);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const uint32_t u = __float_as_uint(pv[e]);
+                    const __half2 s = __hmul2(*reinterpret_cast<const __half2*>(&u), ch);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&s);
+                  }
+                  tmem_st16(s_col + x / 2, w);
+                  moe::tmem_st_wait();
+                }
+                if (i > 0) scale_o(corr);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float r1 = __shfl_sync(0xffffffffu, rv, (c >> 4) + h);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int e = h * 16; e < h * 16 + 16; e += 4) {
+                  const float p0 = exp2_fast(v[e]), p1 = exp2_fast(v[e + 1]), p2 = exp2_fast(v[e + 2]), p3 = exp2_fast(v[e + 3]);
+                  sum0 = add_pair(sum0, pair_of(p0, p1));
+                  sum1 = add_pair(sum1, pair_of(p2, p3));
+                  w[e / 2] = pack2<__half>(p0, p1);
+                  w[e / 2 + 1] = pack2<__half>(p2, p3);
+                }
+                const float2 s2 = of_pair(add_pair(sum0, sum1));
+                l = __fmaf_rn(__fadd_rn(s2.x, s2.y), r1, l);
+              }
+              tmem_st16(s_col + c / 2, w);  // columns that have been read
             }
           } else {
+            // any scales: the maximum first, then the weights
+            float top = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
               const uint32_t bits = bits_of(c);
-              if (__all_sync(0xffffffffu, bits == 0)) continue;
               float v[32];
               tmem_ld32(s_col + c, v);
 #pragma unroll
@@ -322,93 +441,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
                   top = fmaxf(top, bits & (1u << (h * 16 + e)) ? __fmul_rn(v[h * 16 + e], f) : -INFINITY);
               }
             }
-          }
-          if (__any_sync(0xffffffffu, top > m + 8.0f || !(vbig <= 8.0f * vref))) {
-            const float vnew = fmaxf(vref, vbig), vcorr = vnew > vref ? __fdiv_rn(vref, vnew) : 1.0f;
-            vref = vnew;
-            vinv = vnew > 0.0f ? __fdiv_rn(1.0f, vnew) : 1.0f;
-            const float mn = fmaxf(m, top);
-            float corr = mn == m ? 1.0f : exp2_fast(__fsub_rn(m, mn));
-            m = mn;
-            l = __fmul_rn(l, corr);
-            corr = __fmul_rn(corr, vcorr);
-            if (i > 0) {
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float v[32];
-                tmem_ld32(o_at(q) + lanes + c, v);
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__fmul_rn(v[e], corr));
-                moe::tmem_st32(o_at(q) + lanes + c, w);
-              }
+            if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+              const float mn = fmaxf(m, top), corr = mn == m ? 1.0f : exp2_fast(__fsub_rn(m, mn));
+              m = mn;
+              l = __fmul_rn(l, corr);
+              if (i > 0) scale_o(corr);
             }
-          }
-          const float ref = m == -INFINITY ? 0.0f : m;
-          // Where every scale of V is an ordinary positive number, its ratio to
-          // the reference joins the exponent, and the sum of a block's weights
-          // is divided by it.
-          const float vw = __fmul_rn(vs, vinv);
-          if (whole && __all_sync(0xffffffffu, lane >= 8 || (vw >= 0x1p-60f && vw <= 16.0f))) {
-            const float lv = log2_fast(vw), rv = __fdiv_rn(1.0f, vw);
+            const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
+              const uint32_t bits = bits_of(c);
+              uint32_t w[16];
               float v[32];
               tmem_ld32(s_col + c, v);
-              uint32_t w[16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-                const float b = __fsub_rn(__shfl_sync(0xffffffffu, lv, (c >> 4) + h), ref);
-                const float r1 = __shfl_sync(0xffffffffu, rv, (c >> 4) + h);
-                const uint64_t ff = pair_of(f, f), bb = pair_of(b, b);
-                uint64_t sum0 = 0, sum1 = 0;
+                const float vb = __shfl_sync(0xffffffffu, vw, (c >> 4) + h);
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                  const float2 x0 = of_pair(fma_pair(pair_of(v[h * 16 + e], v[h * 16 + e + 1]), ff, bb));
-                  const float2 x1 = of_pair(fma_pair(pair_of(v[h * 16 + e + 2], v[h * 16 + e + 3]), ff, bb));
-                  const float p0 = exp2_fast(x0.x), p1 = exp2_fast(x0.y), p2 = exp2_fast(x1.x), p3 = exp2_fast(x1.y);
-                  sum0 = add_pair(sum0, pair_of(p0, p1));
-                  sum1 = add_pair(sum1, pair_of(p2, p3));
-                  w[h * 8 + e / 2] = pack2<__half>(p0, p1);
-                  w[h * 8 + e / 2 + 1] = pack2<__half>(p2, p3);
+                for (int e = 0; e < 16; e += 2) {
+                  float p2[2];
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    // a scale that is not finite stays out of what is not seen
+                    const bool on = bits & (1u << (h * 16 + e + z));
+                    const float w1 = on ? exp2_fast(__fmaf_rn(v[h * 16 + e + z], f, -ref)) : 0.0f;
+                    l = __fadd_rn(l, w1);
+                    p2[z] = on ? __fmul_rn(w1, vb) : 0.0f;
+                  }
+                  w[h * 8 + e / 2] = pack2<__half>(p2[0], p2[1]);
                 }
-                const float2 s2 = of_pair(add_pair(sum0, sum1));
-                l = __fmaf_rn(__fadd_rn(s2.x, s2.y), r1, l);
               }
               tmem_st16(s_col + c / 2, w);  // columns that have been read
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-              const uint32_t bits = whole ? 0xFFFFFFFFu : bits_of(c);
-              uint32_t w[16];
-              if (__all_sync(0xffffffffu, bits == 0)) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = 0u;
-              } else {
-                float v[32];
-                tmem_ld32(s_col + c, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-                  const float vb = __shfl_sync(0xffffffffu, vw, (c >> 4) + h);
-#pragma unroll
-                  for (int e = 0; e < 16; e += 2) {
-                    float p2[2];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                      // a scale that is not finite stays out of what is not seen
-                      const bool on = bits & (1u << (h * 16 + e + z));
-                      const float w1 = on ? exp2_fast(__fmaf_rn(v[h * 16 + e + z], f, -ref)) : 0.0f;
-                      l = __fadd_rn(l, w1);
-                      p2[z] = on ? __fmul_rn(w1, vb) : 0.0f;
-                    }
-                    w[h * 8 + e / 2] = pack2<__half>(p2[0], p2[1]);
-                  }
-                }
-              }
-              tmem_st16(s_col + c / 2, w);
             }
           }
           moe::tmem_st_wait();
@@ -462,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       }
     }
   } else if (warp < kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // ------------------------------------------------ int8 codes to fp16 operands
     constexpr int kRowChunks = D / 16, kIt = kTile * kRowChunks / kConvThreads;  // 16-byte copies of a thread
     const int ct = tid - kSoftWarps * 32;
@@ -475,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
     int page[kIt], head = 0, slot[kIt];
     auto pages_of_next = [&]() {  // false: no piece left
       while (done >= pc.n) {
-        if (!work.next(a, at, seg)) return false;
+        if (!next_segment()) return false;
         pc = pieces_of(seg);
         done = 0;
       }
@@ -542,6 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       }
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kWarpMma) {
     // ------------------------------------------------ the products, by one lane
     const uint32_t idesc_s = moe::umma_idesc_f16(kTile, kTile);
     const uint32_t idesc_o = moe::umma_idesc_f16(kTile, D) | (1u << 16);  // V's contiguous dimension is N
@@ -581,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       if (moe::elect_one()) moe::umma_commit(b);
       __syncwarp();
     };
-    while (ok && work.next(a, at, seg)) {
+    while (ok && next_segment()) {
       const Pieces pc = pieces_of(seg);
       if (pc.n == 0) continue;
       const bool two = seg.rows > 128;
@@ -614,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
     commit(&bar.drain);
     moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 10);
     __syncwarp();
+    }
   }
   moe::tc_fence_before();
   __syncthreads();
