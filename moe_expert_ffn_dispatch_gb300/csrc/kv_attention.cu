@@ -1,30 +1,44 @@
-// Attention of new tokens over the paged INT8 cache.
+// Attention of new tokens over the paged INT8 cache: the kernel for few query
+// rows, the join of shared units, and the choice between the kernels.
 //
 // The query rows of one kv head (query tokens x group_size) are cut into
-// tiles of 16.  A unit is (sequence, kv head, row tile); its keys are cut
+// tiles of 8 or 16.  A unit is (sequence, kv head, row tile); its keys are cut
 // into pieces of kTileTokens.  All pieces of all units form one sequence of
 // work that the CTAs share evenly, whatever the lengths are: a CTA takes
 // consecutive pieces, so only the first and the last unit that it meets can
-// be shared with other CTAs.  Those leave (row maximum, row sum, unnormalised
-// output) in the workspace, and a second kernel joins them in CTA order.
+// be shared with other CTAs.  Those leave (row reference, row sum,
+// unnormalised output) in the workspace, and a second kernel joins them in
+// CTA order.  (One CTA a unit, or a fixed split of every sequence, leaves most
+// of the GPU idle behind the longest context.)
 //
-// Within a CTA each warp streams its own 16-token slices of keys and values
-// through a ring of asynchronous copies and keeps a running softmax of its
-// own (no barrier in the loop); the warps join in shared memory at the end of
-// a unit.
+// Within a CTA each of 4 warps streams its own 16-token slices of keys and
+// values through a ring of asynchronous copies and keeps a running softmax of
+// its own (no barrier in the loop); the warps join in shared memory at the end
+// of a unit.  Several small CTAs an SM hide one another's cold starts: 4 of
+// them at 8 rows, 3 at 16 (8-warp CTAs, one an SM: 71 us where these take 52).
 //
-// Arithmetic (mma.sync m16n8k16, fp32 accumulators): the int8 codes become
-// exact fp16 (a byte set into the mantissa of 1024, minus 1152).  A query row
-// is scaled by a power of two to [1, 2) at its largest element, so bf16 rows
-// are exact in fp16 as far as an fp32 sum can tell.  With x the scores times
-// log2(e), the page scale of K and the row's power of two enter x in fp32;
-// the page scale of V enters the weight exp2(x - max) as its ratio to a
-// reference page scale, and that product is rounded to fp16.
-// Both matrix products let the k index run over channels (or tokens) in
-// whatever order makes shared-memory reads whole 16-byte chunks: a permuted
-// sum is the same sum.
+// Both products are transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync
+// m16n8k16, fp32 accumulators): tokens and channels are the 16-wide M side, 8
+// query rows the N side, so 8 rows fill what they occupy (with rows on the M
+// side the same kernel took 84 us where this one takes 68).  The weights turn
+// from one layout into the other by movmatrix.  The tensor-memory product would
+// pad 8 rows to 128 and stage every operand through shared memory as fp16.
 //
-// Bound by the cache's bytes while a row tile holds all rows of a kv head.
+// Arithmetic: the int8 codes become exact fp16 (a byte set into the mantissa
+// of 1024, minus 1152).  A query row is scaled by a power of two to [1, 2) at
+// its largest element, so bf16 rows are exact in fp16 as far as an fp32 sum
+// can tell.  With x the scores times log2(e), the page scale of K and the
+// row's power of two enter x in fp32; the page scale of V enters the weight
+// exp2(x - reference) as its ratio to a reference page scale, and that product
+// is rounded to fp16: 11 bits, where the output has 8 or 11.  Sums of weights
+// are taken before that rounding, in fp32.
+// Both products let the k index run over channels (or tokens) in whatever
+// order makes shared-memory reads whole 16-byte chunks: a permuted sum is the
+// same sum.
+//
+// Bound by the cache's bytes at 8 rows (two contexts of 200003 and 100000
+// tokens, 8 kv heads of 128, 4 rows each: 104 us, 5.9 TB/s of 6.8), by
+// instructions at 16 (64 contexts of 2000 tokens: 76 us, 3.5 TB/s).
 #include "kv_attention.cuh"
 
 namespace moe_layer {

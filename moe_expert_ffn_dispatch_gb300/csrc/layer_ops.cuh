@@ -96,11 +96,14 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return r;
 }
 
-// fp32 -> int8 code, round half to even, clamped to [-127, 127]; NaN gives 0
-__device__ __forceinline__ uint32_t code_of(float v) {
-  int r = __float2int_rn(v);
-  r = r > 127 ? 127 : (r < -127 ? -127 : r);
-  return static_cast<uint32_t>(r) & 0xFFu;
+// four fp32 -> int8 codes of one word, round half to even; NaN gives 0.  The
+// conversion saturates at -128 and 127; the callers' values are quotients by
+// amax / 127 and stay within 127.0001 of zero, so -128 does not occur.
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d) {
+  uint32_t hi, r;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(__float2int_rn(d)), "r"(__float2int_rn(c)), "r"(0));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(__float2int_rn(b)), "r"(__float2int_rn(a)), "r"(hi));
+  return r;
 }
 
 // |v| as ordered bits: the unsigned maximum of these is the maximum |v|, and
