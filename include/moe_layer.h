@@ -83,9 +83,12 @@ int moe_layer_add_rmsnorm_quant(const moe_layer_norm_args_t* args, void* stream)
  * uint8 in 0..15 (the low four bits count), NULL for 8 everywhere.  y: [m, n]
  * of `out_dtype` (BF16, FP16 or FP32), dense.
  * group: 32, 64 or a multiple of 128; k: a multiple of group, 32 <= k <=
- * 65536; n >= 1; m >= 0.  Products of codes are exact, sums are fp32, y is
- * rounded once.  The call is made for few rows (the weights are read once for
- * every 32 rows of x); it is right for any m. */
+ * 65536; n >= 1; 0 <= m <= 1000000.  x is held in fp16 with a power of two for
+ * every 128 k of a row: exact but for elements 2^18 below the largest of them,
+ * which keep a step of 2^-28 of it.  Products are exact, sums are fp32, y is
+ * rounded once.  A row of x that holds a NaN or an infinity gives no finite
+ * value in its own row of y and touches no other.  The call is made for few
+ * rows (the weights are read once for every 16 rows of x); it is right for any m. */
 typedef struct {
   const void* x;
   const float* x_scale;
@@ -175,7 +178,8 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
  * number of query tokens of a sequence (1 without cu_q); a larger one in cu_q
  * leaves the tokens past max_q unwritten.
  * Scores, softmax statistics and sums are fp32; the softmax weights are
- * rounded to fp16 (11 bits) for the product with the values.
+ * rounded to fp16 (11 bits) for the product with the values.  Where max_q *
+ * group_size is 64 or more the products run on the tensor memory units.
  * workspace: moe_layer_kv_attention_workspace_size bytes, 256-byte aligned,
  * no initial content needed; calls that share one must be ordered. */
 typedef struct {

@@ -73,7 +73,7 @@ struct Segment {
 template <int R, int TILE, int COST>
 struct Schedule {
   int64_t* prefix;  // shared memory: [batch + 1]
-  int4* shapes;     // shared memory: [batch], q0, qlen, len, work of one head
+  int4* shapes;     // shared memory: [batch], q0, qlen, len
   int64_t total, begin, end;  // of all the work; this CTA's
   int G;
 
@@ -97,10 +97,10 @@ struct Schedule {
       if (b < a.batch) {
         const SeqShape s = seq_shape(a, b);
         const int row_tiles = (s.qlen * a.group_size + R - 1) / R;
-        int one = 0;
+        int64_t one = 0;  // of one head
         for (int rt = 0; rt < row_tiles; ++rt) one += pieces(keys_of<R>(a, s, rt)) + COST;
-        v = static_cast<int64_t>(a.cache.kv_heads) * one;
-        shapes[b] = make_int4(s.q0, s.qlen, s.len, one);
+        v = a.cache.kv_heads * one;
+        shapes[b] = make_int4(s.q0, s.qlen, s.len, 0);
       }
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -136,9 +136,9 @@ struct Schedule {
       const int4 sh = shapes[lo];
       g.b = lo;
       g.s.q0 = sh.x, g.s.qlen = sh.y, g.s.len = sh.z;
-      const int64_t rel = at - prefix[lo];
-      g.head = static_cast<int>(rel / sh.w);
-      int rem = static_cast<int>(rel - static_cast<int64_t>(g.head) * sh.w);
+      const int64_t rel = at - prefix[lo], one = (prefix[lo + 1] - prefix[lo]) / a.cache.kv_heads;
+      g.head = static_cast<int>(rel / one);
+      int64_t rem = rel - g.head * one;
       g.rt = 0;
       while (true) {  // the unit of this head that holds `rem`
         g.keys = keys_of<R>(a, g.s, g.rt);
@@ -148,7 +148,7 @@ struct Schedule {
         ++g.rt;
       }
       g.tile0 = g.keys.lo / TILE;
-      const int xa = rem, xb = static_cast<int>(min(static_cast<int64_t>(g.tiles + COST), xa + (end - at)));
+      const int xa = static_cast<int>(rem), xb = static_cast<int>(min(static_cast<int64_t>(g.tiles + COST), xa + (end - at)));
       g.ta = max(0, xa - COST);
       g.tb = max(0, xb - COST);
       g.rows = min(R, g.s.qlen * a.group_size - g.rt * R);

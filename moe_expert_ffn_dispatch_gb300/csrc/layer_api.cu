@@ -60,7 +60,7 @@ int moe_layer_w4_linear(const moe_layer_w4_args_t* a, void* stream) {
   if (!a || (!act(a->x_dtype) && a->x_dtype != MOE_LAYER_INT8) || (!act(a->out_dtype) && a->out_dtype != MOE_LAYER_FP32) ||
       (!act(a->scale_dtype) && a->scale_dtype != MOE_LAYER_FP32))
     return MOE_ERR_INVALID_ARG;
-  if (a->m < 0 || a->m > 2000000 || a->n < 1 || a->k < 32 || a->k > 65536 || a->group < 32 ||
+  if (a->m < 0 || a->m > 1000000 || a->n < 1 || a->k < 32 || a->k > 65536 || a->group < 32 ||
       (a->group != 32 && a->group != 64 && a->group % 128) || a->k % a->group)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (a->m == 0) return MOE_OK;
