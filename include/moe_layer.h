@@ -142,6 +142,8 @@ typedef struct {
  *     clamp(rne(code * (scale / scale')), -127, 127);
  *   new codes = clamp(rne(x * (1 / scale')), -127, 127).
  * (Slots are filled in order: what a started page held before is forgotten.)
+ * A NaN or an infinity among a page's tokens becomes the scale of that page and
+ * head, and with it all that they hold.
  * k_new, v_new: [tokens, kv_heads, head_dim] of `dtype` (BF16 or FP16) with
  * token strides (multiples of 8) and heads dense, 16-byte aligned.  A token whose page-table
  * entry is outside [0, num_pages) or whose position is outside [0, max_pages *
@@ -171,7 +173,8 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
  * n uses kv head n / group_size:
  *   out[t, n] = sum_i softmax_i(sm_scale * <q[t, n], key_i>) * value_i
  * and zeros where no key is seen.  Keys on a page-table entry outside [0,
- * num_pages) are not seen; lengths are held to [0, max_pages * page_size].
+ * num_pages) are not seen; a scale that is not finite reaches only the query tokens
+ * that see a key of its page, whose outputs are then not finite; lengths are held to [0, max_pages * page_size].
  * q: [tokens, kv_heads * group_size, head_dim] of `dtype` (BF16 or FP16), token stride
  * q_stride (a multiple of 8), heads dense, 16-byte aligned.  out: the same
  * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the largest

@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
       __syncwarp();
       const uint32_t kb = ring_u + (i % kStages) * kStageBytes, vb = kb + kSliceBytes;
       const int page = __shfl_sync(0xffffffffu, page0, ri);
-      const float ks = __shfl_sync(0xffffffffu, ks0, ri), vs = __shfl_sync(0xffffffffu, vs0, ri);
+      const float ks = __shfl_sync(0xffffffffu, ks0, ri);
+      float vs = __shfl_sync(0xffffffffu, vs0, ri);
       const int64_t tok0 = static_cast<int64_t>(first + i * kWarps) * kSlice;
 
       // scores, transposed: 16 tokens x 8 NR rows, in two chains of products
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
           half_pairs(w[1][q], a1, a3);
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
-            mma16816<__half>(q & 1 ? s2[nr] : sc[nr], a0, a1, a2, a3, qf[nr][q][0], qf[nr][q][1]);
+            mma16816(q & 1 ? s2[nr] : sc[nr], a0, a1, a2, a3, qf[nr][q][0], qf[nr][q][1]);
         }
       }
       // x = score * scales * log2(e), masked where a row does not see the whole slice
@@ -290,11 +291,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
             if (page < 0 || key > pos || (a.window > 0 && key <= pos - a.window)) sc[nr][e] = -INFINITY;
           }
       }
+      // A page scale of V that is not finite makes the rows that see the page
+      // NaN, through their sums, and stays out of what the rows share.
+      if (!(fabsf(vs) < INFINITY)) {
+        vs = 0.0f;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (sc[nr][e] != -INFINITY) l[nr][e & 1] = NAN;
+      }
       // The references of the weights move only when a weight would pass 2^8
       // (a page scale of V 8 times its reference): weights of up to 2^11 are
       // as exact in fp16 as weights up to 1, and most slices rescale nothing.
       float top[NR][2];
-      bool move = !(fabsf(vs) <= 8.0f * vref);
+      bool move = fabsf(vs) > 8.0f * vref;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -363,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         half_pairs(__byte_perm(w[2][q], w[3][q], 0x7362), hi2, hi3);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          mma16816<__half>(o[nr][2 * q], lo0, lo1, hi0, hi1, pb[nr][0], pb[nr][1]);
-          mma16816<__half>(o[nr][2 * q + 1], lo2, lo3, hi2, hi3, pb[nr][0], pb[nr][1]);
+          mma16816(o[nr][2 * q], lo0, lo1, hi0, hi1, pb[nr][0], pb[nr][1]);
+          mma16816(o[nr][2 * q + 1], lo2, lo3, hi2, hi3, pb[nr][0], pb[nr][1]);
         }
       }
       __syncwarp();  // the stage is read before it is filled again

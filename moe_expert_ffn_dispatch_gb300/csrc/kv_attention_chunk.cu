@@ -24,7 +24,7 @@
 // Bound by a tile's chain (S, weights, O: about 5000 cycles a piece, of which the
 // products are 1100) at 42 % of the issue slots; two tiles overlap, a third has
 // no room in tensor memory.  8 chunks of 512 tokens over 8192 keys (32 heads on
-// 8, channels 128): 633 us, 841 TFLOP/s.
+// 8, channels 128): 630 us, 845 TFLOP/s.
 #include "kv_attention.cuh"
 
 #include "device_prims.cuh"
@@ -309,8 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           const int low = __reduce_min_sync(0xffffffffu, mine ? c_lo : kTile - 1);
           const int high = __reduce_max_sync(0xffffffffu, mine ? c_hi : -1);
           const bool hidden = page < 0 || 16 * lane > high || 16 * lane + 15 < low;
-          const uint32_t vtop = __reduce_max_sync(0xffffffffu, hidden || lane >= 8 ? 0u : abs_bits(vs));
-          const float vbig = vtop > 0x7F800000u ? 0.0f : __uint_as_float(vtop);
+          // (nor does one that is not finite: the rows that see it take it in their weights)
+          const bool counts = !hidden && lane < 8 && fabsf(vs) < INFINITY;
+          const float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, counts ? abs_bits(vs) : 0u));
           if (!wait(&bar.s_full[q], s_phase & 1, kSite + q)) {
             ok = false;
             break;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
               moe::tmem_st32(o_at(q) + lanes + c, w);
             }
           };
-          if (!(vbig <= 8.0f * vref)) {  // the same for the whole warp
+          if (vbig > 8.0f * vref) {  // the same for the whole warp
             const float vnew = fmaxf(vref, vbig);
             if (i > 0) scale_o(__fdiv_rn(vref, vnew));
             vref = vnew;

@@ -7,7 +7,9 @@
 // memory and two barriers.
 // Bound by memory: 2 bytes read (4 with a residual) and 1 to 5 written an
 // element.  4093 x 4096 with residual and y: 23.8 us, 6.3 TB/s of 6.8; 8 x 4096:
-// 2.2 us, latency.  Rows that are not 16-byte aligned: 2.1 to 2.8 TB/s.
+// 2.2 us, latency.  Rows that are not 16-byte aligned go one element
+// at a time, 1.4 to 2.9 TB/s (4093 x 4097: 84 us); 16-byte reads shifted into
+// place between lanes were no faster (91 us).
 #include "layer_ops.cuh"
 
 namespace moe_layer {

@@ -339,13 +339,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
               for (int n = 0; n < NT; ++n) {
                 const uint4 xv = lds128(xa + n * 8 * p.xpitch + j * 64);
                 if (i == 0)
-                  mma16816_first<__half>(part[n], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u,
-                                         xv.x, xv.y);
+                  mma16816_first(part[n], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u,
+                                 xv.x, xv.y);
                 else
-                  mma16816<__half>(part[n], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, xv.x,
-                                   xv.y);
-                mma16816<__half>(part[n], va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, xv.z,
-                                 xv.w);
+                  mma16816(part[n], wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, xv.x,
+                           xv.y);
+                mma16816(part[n], va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, xv.z,
+                         xv.w);
               }
             }
             const uint4 su = lds128(sa);

@@ -438,6 +438,30 @@ def test_attention_keeps_nan_to_its_sequence_and_head(qlen):
     assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], base[~hit])
 
 
+@pytest.mark.parametrize("what, value", [("v_scale", math.nan), ("v_scale", math.inf), ("v_scale", -math.inf),
+                                         ("k_scale", math.nan), ("k_scale", math.inf)])
+@pytest.mark.parametrize("kv, qlen, G, page, bad, window", [
+    (52, 8, 1, 16, 3, 0), (52, 8, 2, 16, 3, 0), (68, 8, 1, 16, 3, 3), (68, 8, 2, 16, 3, 3), (100, 100, 2, 16, 3, 20),
+    (700, 300, 2, 32, 15, 0), (700, 300, 2, 32, 15, 100), (300, 200, 4, 128, 1, 0), (40, 40, 5, 16, 0, 7)])
+def test_attention_keeps_a_scale_that_is_not_finite_to_the_tokens_that_see_it(kv, qlen, G, page, bad, window, what, value):
+    H, D, need = 2, 128, -(-kv // page)
+    cache, table = new_cache(need + 1, H, page, D, seed=kv), page_table([need], need + 1, seed=kv)
+    q = randn(qlen, G * H, D, g=gen(kv), std=2.0).to(BF16)
+    ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, [kv], [qlen], window, D ** -0.5)
+    getattr(cache, what)[table[0, bad], 1] = value
+    cu = torch.tensor([0, qlen], dtype=torch.int32, device=DEV)
+    got = cache.attention(q, table.to(DEV), torch.tensor([kv], dtype=torch.int32, device=DEV), cu_q=cu, max_q=qlen,
+                          window=window)
+    p = torch.arange(kv - qlen, kv, device=DEV)
+    sees = (p >= bad * page) & ((p - (window or kv + 1)) < (bad + 1) * page - 1)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[sees, G:] = True
+    assert hit.any()
+    close(got[~hit], ref[~hit], (tol + ref.abs() * U[BF16] + TINY[BF16])[~hit])
+    if what == "v_scale" or math.isnan(value):  # (an infinite scale of K makes a score of minus infinity a weight of 0)
+        assert not torch.isfinite(got[hit]).any()
+
+
 def test_attention_lengths_beyond_the_table_and_tokens_beyond_max_q():
     cache, table = new_cache(4, 1, 16, 64, seed=41), torch.tensor([[2, 0]], dtype=torch.int32, device=DEV)
     q = randn(1, 2, 64, g=gen(42)).to(BF16)
