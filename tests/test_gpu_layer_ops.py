@@ -71,6 +71,29 @@ def test_norm_sizes(dtype, wdtype, rows, h):
     check_norm(x, w, None, None, m.add_rmsnorm_quant(x, w, 1e-5), 1e-5)
 
 
+@pytest.mark.parametrize("h", [1, 5, 8, 15, 16, 250, 513, 1023, 1024, 1031, 4095, 4104])
+def test_norm_rows_at_any_offset(h):
+    """Rows, and what is written, at odd places of larger buffers whose other bytes stay."""
+    g = gen(h)
+    for rows, off in ((1, 1), (3, 3), (6, 0), (2, 6)):
+        wide_x, wide_r = randn(rows, h + 24, g=g).to(BF16), randn(rows, h + 9, g=g).to(BF16)
+        x, r = wide_x[:, off:off + h], wide_r[:, off:off + h]
+        w, sm = (torch.rand(h + off, device=DEV, generator=g) + 0.5)[off:], torch.rand(h + 1, device=DEV, generator=g)[1:] + 0.5
+        w = w.to(BF16)
+        q_all = torch.full((rows * h + 32,), 77, dtype=torch.int8, device=DEV)
+        y_all, r_all = torch.full((rows * h + 32,), 7.0, dtype=BF16, device=DEV), torch.full((rows, h + 24), 7.0, dtype=BF16, device=DEV)
+        q, y, ro = q_all[off:off + rows * h].view(rows, h), y_all[off:off + rows * h].view(rows, h), r_all[:, off + 1:off + 1 + h]
+        scale = torch.empty(rows, device=DEV)
+        want = m.add_rmsnorm_quant(x.contiguous(), w, 1e-6, residual=r.contiguous(), smooth=sm, want_y=True)
+        m.add_rmsnorm_quant(x, w, 1e-6, residual=r, smooth=sm, q=q, q_scale=scale, residual_out=ro, y=y)
+        check_norm(x, w, r, sm, (q, scale, ro, y), 1e-6)
+        for a, b in zip((q, scale, ro, y), want):
+            assert torch.equal(a, b)
+        assert (q_all[:off] == 77).all() and (q_all[off + rows * h:] == 77).all()
+        assert (y_all[:off] == 7).all() and (y_all[off + rows * h:] == 7).all()
+        assert (r_all[:, :off + 1] == 7).all() and (r_all[:, off + 1 + h:] == 7).all()
+
+
 def test_norm_strides_alignment_and_in_place():
     g = gen(1)
     wide = randn(6, 600, g=g).to(BF16)
