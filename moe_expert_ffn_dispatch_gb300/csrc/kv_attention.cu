@@ -2,14 +2,25 @@
 // rows, the join of shared units, and the choice between the kernels.
 //
 // The query rows of one kv head (query tokens x group_size) are cut into
-// tiles of 8 or 16.  A unit is (sequence, kv head, row tile); its keys are cut
-// into pieces of kTileTokens.  All pieces of all units form one sequence of
-// work that the CTAs share evenly, whatever the lengths are: a CTA takes
-// consecutive pieces, so only the first and the last unit that it meets can
-// be shared with other CTAs.  Those leave (row reference, row sum,
-// unnormalised output) in the workspace, and a second kernel joins them in
-// CTA order.  (One CTA a unit, or a fixed split of every sequence, leaves most
-// of the GPU idle behind the longest context.)
+// tiles of 8 or 16.  A unit is (sequence, kv head, row tile).  The host knows
+// how many there can be and how many keys a page table has room for, not the
+// lengths, and by these takes one of two forms:
+//
+// Whole units, where a table is short: a cluster of 8, 4, 2 or 1 CTAs, as many
+// as let all units run at once, takes a unit, deals its slices out to the
+// warps and joins them over distributed shared memory.  One launch: 1 context
+// of 1009 tokens 5.4 us (the other form 9.3), 64 of 500 15 (23), 256 of 100 21
+// (32).
+//
+// A schedule, where tables are long, for then one context may be far longer
+// than the others: a unit's keys are cut into pieces of kTileTokens, all pieces
+// of all units form one sequence of work, and the CTAs share it evenly, whatever
+// the lengths are.  A CTA takes consecutive pieces, so only the first and the
+// last unit that it meets can be shared with other CTAs.  Those leave (row
+// reference, row sum, unnormalised output) in the workspace, and a second
+// kernel joins them in CTA order.  64 contexts, one of 2000 tokens and the others
+// of 50: 13 us (whole units 28); from 768 keys a CTA on the whole form loses on
+// such lengths and wins on even ones (64 of 2000: 46 us for 53).
 //
 // Within a CTA each of 4 warps streams its own 16-token slices of keys and
 // values through a ring of asynchronous copies and keeps a running softmax of
@@ -37,7 +48,7 @@
 // same sum.
 //
 // Bound by the cache's bytes at 8 rows (two contexts of 200003 and 100000
-// tokens, 8 kv heads of 128, 4 rows each: 104 us, 5.9 TB/s of 6.8), by
+// tokens, 8 kv heads of 128, 4 rows each: 101 us, 6.1 TB/s of 6.8), by
 // instructions at 16 (64 contexts of 2000 tokens: 76 us, 3.5 TB/s).
 #include "kv_attention.cuh"
 
@@ -56,6 +67,9 @@ constexpr int kStagesOf = NR == 1 ? 3 : 4;
 constexpr int kMaxSlots = 4096;                  // CTAs of a launch (at most 4 an SM)
 // what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces
 constexpr int kUnitCost = 4;
+// A cluster of CTAs takes a whole unit where the table has no more keys than this for each of them
+constexpr int kWholeKeys = 768;
+constexpr int kWholeUnits = 1 << 20;  // a grid's size stays far below 2^31
 // query rows of a kv head (the longest sequence's) from which the tensor-memory kernel takes over
 constexpr int kChunkFrom = 64;
 
@@ -80,7 +94,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-template <typename T, int D, int NR>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the float at shared address `at` of CTA `rank` of the cluster
+__device__ __forceinline__ float cluster_read(uint32_t at, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// CS 0: the CTAs divide the work of all units by the schedule.  Otherwise a
+// cluster of CS CTAs takes a unit, all of its pieces, and joins its parts itself.
+template <typename T, int D, int NR, int CS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(const AttnParams p) {
   constexpr int KS = D / 16;                   // k steps of the score product
   constexpr int NT = D / 16;                   // channel tiles of the output
@@ -96,21 +124,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
   grid_launch_dependents();
   const moe_layer_kv_attention_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  __shared__ int64_t s_carry[kWarps];
-  Schedule<R, kTileTokens, kUnitCost> work;
-  work.template build<kThreads>(a, smem + kWarps * kRing, s_carry);
-  const int c = blockIdx.x;
-  if (tid == 0) {
-    p.records[c].b = -1;
-    if (c == 0) p.status[1] = p.status[2] = 0;  // no wait of this kernel can give up
+  using Work = Schedule<R, kTileTokens, kUnitCost>;
+  Work work;
+  constexpr int kShare = CS > 1 ? CS : 1;  // CTAs that share a unit's slices
+  const int c = blockIdx.x, rank = c % kShare;
+  if (c == 0 && tid == 0) p.status[1] = p.status[2] = 0;  // no wait of this kernel can give up
+  if constexpr (CS == 0) {
+    __shared__ int64_t s_carry[kWarps];
+    work.template build<kThreads>(a, smem + kWarps * kRing, s_carry);
+    if (tid == 0 && p.row_tiles == 0) p.records[c].b = -1;
   }
 
   uint8_t* ring = smem + warp * kRing;
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
   Segment seg;
-  int64_t at = work.begin;
-  while (work.next(a, at, seg)) {
+  int64_t at = 0;
+  if constexpr (CS == 0) {
+    at = work.begin;
+  } else {
+    if (!work.unit(a, c / kShare, seg)) return;  // the same for the whole cluster
+  }
+  while (CS > 0 || work.next(a, at, seg)) {
     const SeqShape& s = seg.s;
     const int b = seg.b, head = seg.head, rt = seg.rt, rows = seg.rows, ta = seg.ta, tb = seg.tb;
     const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
@@ -119,10 +154,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
     int64_t k_lo = static_cast<int64_t>(seg.tile0 + ta) * kTileTokens;
     const int64_t k_hi = min(static_cast<int64_t>(seg.tile0 + tb) * kTileTokens, static_cast<int64_t>(seg.keys.hi));
     k_lo = max(k_lo, static_cast<int64_t>(seg.keys.lo & ~(kSlice - 1)));
-    // this warp's slices: first + 8 i, from the slice of k_lo on
-    const int first = static_cast<int>(k_lo / kSlice) + warp;
+    // this warp's slices: first + kSpread i, from the slice of k_lo on
+    constexpr int kSpread = kWarps * kShare;
+    const int first = static_cast<int>(k_lo / kSlice) + rank * kWarps + warp;
     const int n = k_hi > static_cast<int64_t>(first) * kSlice
-                      ? static_cast<int>(((k_hi + kSlice - 1) / kSlice - first + kWarps - 1) / kWarps)
+                      ? static_cast<int>(((k_hi + kSlice - 1) / kSlice - first + kSpread - 1) / kSpread)
                       : 0;
 
     // keys [all_lo, all_hi) are seen by every row of the tile; n_all: slices of
@@ -137,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
       ks = vs = 0.0f;
       const int i = base + lane;
       if (i < n) {
-        const int64_t tok = static_cast<int64_t>(first + i * kWarps) * kSlice;
+        const int64_t tok = static_cast<int64_t>(first + i * kSpread) * kSlice;
         const int pg = a.page_table[b * a.table_stride + (tok >> p.page_shift)];
         if (pg >= 0 && pg < a.cache.num_pages) {
           page = pg;
@@ -160,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
     auto issue = [&](int i, int rel_i) {  // slice i of this warp, rel_i from the base of page0
       const int page = rel_i < 32 ? __shfl_sync(0xffffffffu, page0, rel_i & 31) : __shfl_sync(0xffffffffu, page1, rel_i & 31);
       if (i < n) {
-        const int64_t off = max(page, 0) * a.cache.page_stride + (((first + i * kWarps) * kSlice) & in_page) * D;
+        const int64_t off = max(page, 0) * a.cache.page_stride + (((first + i * kSpread) * kSlice) & in_page) * D;
         const int8_t *kp = k_head + off, *vp = v_head + off;
         const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
 #pragma unroll
@@ -243,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
       const int page = __shfl_sync(0xffffffffu, page0, ri);
       const float ks = __shfl_sync(0xffffffffu, ks0, ri);
       float vs = __shfl_sync(0xffffffffu, vs0, ri);
-      const int64_t tok0 = static_cast<int64_t>(first + i * kWarps) * kSlice;
+      const int64_t tok0 = static_cast<int64_t>(first + i * kSpread) * kSlice;
 
       // scores, transposed: 16 tokens x 8 NR rows, in two chains of products
       float sc[NR][4], s2[NR][4];
@@ -419,7 +455,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
 #pragma unroll
       for (int i = 0; i < kEach; ++i) acc[i] = __fmaf_rn(from[r * D + d0 + i], f, acc[i]);
     }
-    if (ta == 0 && tb == seg.tiles) {
+    if constexpr (CS > 1) {
+      // the CTA's part in place of its first warp's; each CTA joins R / CS rows
+      static_assert(R % CS == 0, "");
+      __syncthreads();
+      float* mine = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) mine[r * D + d0 + i] = acc[i];
+      if (tid % kPerRow == 0) mine[R * D + r] = top, mine[R * D + R + r] = sum;
+      cluster_sync();
+      const uint32_t part = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+      for (int i = tid; i < R / CS * (D / 2); i += kThreads) {  // two channels of a row
+        const int jr = rank * (R / CS) + i / (D / 2), ch = i % (D / 2) * 2;
+        if (jr >= rows) continue;
+        float m1[CS], l1[CS], x1[CS], y1[CS];
+#pragma unroll
+        for (int w = 0; w < CS; ++w) {
+          m1[w] = cluster_read(part + (R * D + jr) * 4, w);
+          l1[w] = cluster_read(part + (R * D + R + jr) * 4, w);
+          x1[w] = cluster_read(part + (jr * D + ch) * 4, w);
+          y1[w] = cluster_read(part + (jr * D + ch + 1) * 4, w);
+        }
+        float most = -INFINITY, total = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < CS; ++w) most = fmaxf(most, m1[w]);
+        const float from = most == -INFINITY ? 0.0f : most;
+#pragma unroll
+        for (int w = 0; w < CS; ++w) {
+          const float f = exp2_fast(__fsub_rn(m1[w], from));
+          total = __fmaf_rn(l1[w], f, total);
+          x = __fmaf_rn(x1[w], f, x);
+          y = __fmaf_rn(y1[w], f, y);
+        }
+        const int row = rt * R + jr, j = row / a.group_size, hq = row - j * a.group_size;
+        const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : (total == 0.0f ? 0.0f : total);
+        T* out = static_cast<T*>(a.out) +
+                 (static_cast<int64_t>(s.q0 + j) * a.cache.kv_heads * a.group_size + head * a.group_size + hq) * D + ch;
+        *reinterpret_cast<uint32_t*>(out) = pack2<T>(__fmul_rn(x, inv), __fmul_rn(y, inv));
+      }
+      cluster_sync();  // the parts are read before their CTA ends
+      return;
+    } else if (CS == 1 || (ta == 0 && tb == seg.tiles)) {
+      if (CS == 0 && tid == 0 && p.row_tiles > 0) p.records[(b * a.cache.kv_heads + head) * p.row_tiles + rt].b = -1;
       if (r < rows) {
         const int row = rt * R + r, j = row / a.group_size, hq = row - j * a.group_size;
         const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
@@ -429,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         for (int i = 0; i < kEach; i += 2)
           *reinterpret_cast<uint32_t*>(out + i) = pack2<T>(__fmul_rn(acc[i], inv), __fmul_rn(acc[i + 1], inv));
       }
+      if (CS == 1) return;
     } else {
       const int64_t slot = 2 * static_cast<int64_t>(c) + (ta > 0 ? 0 : 1);
       float* po = p.part_o + (slot * R + r) * D + d0;
@@ -439,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         p.part_ml[(slot * R + r) * 2 + 1] = sum;
       }
       if (tb == seg.tiles && tid == 0) {
-        p.records[c] = Record{b, head, rt, work.cta_of(seg.first_piece)};
+        const int at_record = p.row_tiles > 0 ? (b * a.cache.kv_heads + head) * p.row_tiles + rt : c;
+        p.records[at_record] = Record{b, head, rt, work.cta_of(seg.first_piece), c};
       }
     }
     __syncthreads();
@@ -450,26 +529,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
 
 namespace {
 
-// Joins the parts of a unit that several CTAs shared.  CTA (c, y) takes 16 /
-// JW rows of the unit that CTA c finished, JW warps a row: warp i sums every
-// JW-th part, a lane D / 32 channels, and the JW sums are added in a fixed
+// Joins the parts of a unit that several CTAs shared.  CTA (i, y) takes 16 /
+// JW rows of the unit of record i, JW warps a row: a warp sums every JW-th
+// part, a lane D / 32 channels, and the JW sums are added in a fixed
 // order.  The maxima are read first, so that the parts' loads depend on
-// nothing but their addresses.  Units of few rows have many parts (JW = 4),
-// units of 256 rows two or three (JW = 1).
+// nothing but their addresses.  Few units have many parts each (JW = 16,
+// records by unit: the CTAs of most records would have nothing to do), many
+// units few (JW = 4), units of 256 rows two or three (JW = 1).
 constexpr int kJoinThreads = 512;
-template <typename T, int D, int R, int TILE, int JW>
+template <typename T, int D, int R, int JW>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttnParams p) {
   constexpr int kEach = D / 32, kRowsHere = 16 / JW;
   __shared__ float s_acc[kRowsHere][JW][D];
   __shared__ float s_sum[kRowsHere][JW];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r4 = warp / JW, part = warp % JW, r = blockIdx.y * kRowsHere + r4;
-  const Record rec = p.records[c];
-  if (rec.b < 0) return;
+  const Record rec = p.records[blockIdx.x];
   const moe_layer_kv_attention_args_t& a = p.a;
-  const int np = c - rec.c0 + 1;
+  if (p.row_tiles > 0) {  // a sequence of fewer rows leaves no record
+    const int b = blockIdx.x / p.row_tiles / a.cache.kv_heads, rt = blockIdx.x % p.row_tiles;
+    if (rt * R >= seq_shape(a, b).qlen * a.group_size) return;
+  }
+  if (rec.b < 0) return;
+  const int np = rec.c1 - rec.c0 + 1;
   // the first CTA left its part in slot 1, the others in slot 0
   auto slot_row = [&](int i) { return (2 * static_cast<int64_t>(rec.c0 + i) + (i == 0 ? 1 : 0)) * R + r; };
   float top = -INFINITY;
@@ -515,26 +599,51 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const A
 
 int grid_max(int num_sms, int per_sm) { return num_sms * per_sm < kMaxSlots ? num_sms * per_sm : kMaxSlots; }
 
+template <typename T, int D, int NR, int CS>
+cudaError_t launch_whole(const AttnParams& p, int64_t units, size_t smem, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  const void* k = (const void*)kv_attention_kernel<T, D, NR, CS>;
+  if (const cudaError_t e = allow_smem(k, static_cast<int>(smem), allowed); e != cudaSuccess) return e;
+  AttnParams arg = p;
+  void* args[] = {&arg};
+  return launch_after(k, dim3(static_cast<unsigned>(units) * CS), dim3(kThreads), args, smem, s, CS);
+}
+
 template <typename T, int D, int NR>
 cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   const moe_layer_kv_attention_args_t& a = p.a;
   using Work = Schedule<8 * NR, kTileTokens, kUnitCost>;
-  const size_t smem = kWarps * kStagesOf<NR> * 2 * kSlice * D + Work::bytes(a.batch);
+  const size_t ring = kWarps * kStagesOf<NR> * 2 * kSlice * D;
+  const int64_t keys = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
+  const int64_t rows = static_cast<int64_t>(a.max_q) * a.group_size;
+  const int row_tiles = static_cast<int>((rows + 8 * NR - 1) / (8 * NR));
+  const int64_t units = static_cast<int64_t>(a.batch) * a.cache.kv_heads * row_tiles;
+  const int full = grid_max(num_sms, kCtasPerSm<NR>);
+  AttnParams arg = p;
+  // a cluster a unit: as many CTAs as let all units run at once
+  const int share = units * 8 <= full ? 8 : units * 4 <= full ? 4 : units * 2 <= full ? 2 : 1;
+  if (keys <= kWholeKeys * share && units <= kWholeUnits) {
+    if (share == 8) return launch_whole<T, D, NR, 8>(arg, units, ring, s);
+    if (share == 4) return launch_whole<T, D, NR, 4>(arg, units, ring, s);
+    if (share == 2) return launch_whole<T, D, NR, 2>(arg, units, ring, s);
+    return launch_whole<T, D, NR, 1>(arg, units, ring, s);
+  }
+  void* args[] = {&arg};
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem((const void*)kv_attention_kernel<T, D, NR>, kMaxSmem - 1024, allowed);
+  const void* k = (const void*)kv_attention_kernel<T, D, NR, 0>;
+  cudaError_t e = allow_smem(k, kMaxSmem - 1024, allowed);
   if (e != cudaSuccess) return e;
   // no more CTAs than pieces of work there can be
-  const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.cache.page_size + kTileTokens - 1) / kTileTokens;
-  const int64_t rows = static_cast<int64_t>(a.max_q) * a.group_size;
-  const double most = static_cast<double>(a.batch) * a.cache.kv_heads * ((rows + 8 * NR - 1) / (8 * NR)) *
-                      ((tiles > 0 ? tiles : 1) + kUnitCost);
-  const int full = grid_max(num_sms, kCtasPerSm<NR>);
+  const int64_t tiles = (keys + kTileTokens - 1) / kTileTokens;
+  const double most = static_cast<double>(units) * ((tiles > 0 ? tiles : 1) + kUnitCost);
   const int grid = most < full ? static_cast<int>(most) : full;
-  AttnParams arg = p;
-  void* args[] = {&arg};
-  e = launch_after((const void*)kv_attention_kernel<T, D, NR>, dim3(grid), dim3(kThreads), args, smem, s);
+  const bool few = share == 8;
+  if (few) arg.row_tiles = row_tiles;
+  e = launch_after(k, dim3(grid), dim3(kThreads), args, ring + Work::bytes(a.batch), s);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D, 8 * NR, kTileTokens>(p, grid, rows < 8 * NR ? static_cast<int>(rows) : 8 * NR, s);
+  const int most_rows = rows < 8 * NR ? static_cast<int>(rows) : 8 * NR;
+  return few ? launch_join<T, D, 8 * NR, 16>(arg, static_cast<int>(units), most_rows, s)
+             : launch_join<T, D, 8 * NR, 4>(arg, grid, most_rows, s);
 }
 
 template <typename T, int D>
@@ -547,18 +656,17 @@ cudaError_t launch_typed(const AttnParams& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-template <typename T, int D, int R, int TILE>
-cudaError_t launch_join(const AttnParams& p, int grid, int rows, cudaStream_t s) {
-  constexpr int JW = R > 16 ? 1 : 4;
+template <typename T, int D, int R, int JW>
+cudaError_t launch_join(const AttnParams& p, int records, int rows, cudaStream_t s) {
   AttnParams arg = p;
   void* args[] = {&arg};
-  return launch_after((const void*)kv_attention_join_kernel<T, D, R, TILE, JW>,
-                      dim3(grid, (rows + 16 / JW - 1) / (16 / JW)), dim3(kJoinThreads), args, 0, s);
+  return launch_after((const void*)kv_attention_join_kernel<T, D, R, JW>, dim3(records, (rows + 16 / JW - 1) / (16 / JW)),
+                      dim3(kJoinThreads), args, 0, s);
 }
-template cudaError_t launch_join<__nv_bfloat16, 64, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
-template cudaError_t launch_join<__nv_bfloat16, 128, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
-template cudaError_t launch_join<__half, 64, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
-template cudaError_t launch_join<__half, 128, kChunkRows, 128>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__nv_bfloat16, 64, kChunkRows, 1>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__nv_bfloat16, 128, kChunkRows, 1>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__half, 64, kChunkRows, 1>(const AttnParams&, int, int, cudaStream_t);
+template cudaError_t launch_join<__half, 128, kChunkRows, 1>(const AttnParams&, int, int, cudaStream_t);
 
 namespace {
 // rows of all parts: 4 CTAs an SM of 8 or 3 of 16, or one of kChunkRows
@@ -574,6 +682,7 @@ size_t attention_workspace(int head_dim, int num_sms) {
 cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s) {
   AttnParams p;
   p.a = a;
+  p.row_tiles = 0;
   p.status = static_cast<int32_t*>(ws);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   p.part_ml = p.part_o + part_rows(num_sms) * a.cache.head_dim;

@@ -7,14 +7,16 @@
 namespace moe_layer {
 
 struct Record {  // a unit that several CTAs share, left by the CTA that holds its last piece
-  int b, head, rt, c0;  // c0: its first CTA; b < 0: none
+  int b, head, rt;  // b < 0: none
+  int c0, c1;       // its CTAs
 };
 
 struct AttnParams {
   moe_layer_kv_attention_args_t a;
   float* part_o;      // [2 * grid][rows of a unit][D]
   float* part_ml;     // [2 * grid][rows of a unit][2]
-  Record* records;    // [grid]
+  Record* records;    // [grid]: of the unit that a CTA finished; or of each unit, where row_tiles > 0
+  int row_tiles;      // a unit's number is (b * kv_heads + head) * row_tiles + rt
   int32_t* status;    // [4] words of the workspace: a wait that gave up is noted here
   float scale_log2;   // sm_scale * log2(e)
   int page_shift;
@@ -159,6 +161,24 @@ struct Schedule {
     return false;
   }
 
+  // unit u of all that the shapes of the call allow, whole; false where this sequence has no such rows
+  static __device__ __forceinline__ bool unit(const moe_layer_kv_attention_args_t& a, int u, Segment& g) {
+    const int row_tiles = static_cast<int>((static_cast<int64_t>(a.max_q) * a.group_size + R - 1) / R);
+    g.rt = u % row_tiles;
+    g.head = u / row_tiles % a.cache.kv_heads;
+    g.b = u / row_tiles / a.cache.kv_heads;
+    g.s = seq_shape(a, g.b);
+    g.rows = min(R, g.s.qlen * a.group_size - g.rt * R);
+    if (g.rows <= 0) return false;
+    g.keys = keys_of<R>(a, g.s, g.rt);
+    g.tile0 = g.keys.lo / TILE;
+    g.tiles = pieces(g.keys);
+    g.ta = 0;
+    g.tb = g.tiles;
+    g.first_piece = 0;
+    return true;
+  }
+
   // the CTA that holds piece x: the last c with total c / G <= x
   __device__ __forceinline__ int cta_of(int64_t x) const {
     int64_t c = x * G / total;
@@ -179,9 +199,10 @@ __device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& h
   hi = *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Joins the parts of units that several CTAs shared (kv_attention.cu); rows: the most that a unit has.
-template <typename T, int D, int R, int TILE>
-cudaError_t launch_join(const AttnParams& p, int grid, int rows, cudaStream_t s);
+// Joins the parts of units that several CTAs shared (kv_attention.cu).  records: how many there are; rows: the
+// most that a unit has; JW: warps that share a row's parts.
+template <typename T, int D, int R, int JW>
+cudaError_t launch_join(const AttnParams& p, int records, int rows, cudaStream_t s);
 
 // kv_attention_chunk.cu: tensor-memory kernel for many query rows a kv head.
 constexpr int kChunkRows = 256;

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
         p.part_ml[slot_row * 2] = m;
         p.part_ml[slot_row * 2 + 1] = l;
         if (seg.tb == seg.tiles && row == 0)
-          p.records[blockIdx.x] = Record{seg.b, seg.head, seg.rt, work.cta_of(seg.first_piece)};
+          p.records[blockIdx.x] = Record{seg.b, seg.head, seg.rt, work.cta_of(seg.first_piece), static_cast<int>(blockIdx.x)};
       }
     }
   } else if (warp < kWarpMma) {
@@ -713,7 +713,7 @@ cudaError_t launch_chunk(const AttnParams& p, int num_sms, cudaStream_t s) {
   void* args[] = {&arg};
   e = launch_after(k, dim3(grid), dim3(kThreads), args, chunk_smem<T, D>(a.batch), s);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D, kChunkRows, kTile>(p, grid, rows < kChunkRows ? static_cast<int>(rows) : kChunkRows, s);
+  return launch_join<T, D, kChunkRows, 1>(p, grid, rows < kChunkRows ? static_cast<int>(rows) : kChunkRows, s);
 }
 template cudaError_t launch_chunk<__nv_bfloat16, 64>(const AttnParams&, int, cudaStream_t);
 template cudaError_t launch_chunk<__nv_bfloat16, 128>(const AttnParams&, int, cudaStream_t);

@@ -37,17 +37,21 @@ constexpr int kMaxSmem = 227 * 1024;  // dynamic shared memory that a block can 
 
 // Launch that may begin while the stream's previous kernel still runs: every
 // kernel here starts with grid_dependency_wait, before it touches memory.
-inline cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args, size_t smem, cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+inline cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args, size_t smem, cudaStream_t s,
+                                int cluster = 1) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
