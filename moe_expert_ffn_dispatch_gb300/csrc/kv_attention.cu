@@ -6,7 +6,7 @@
 // how many there can be and how many keys a page table has room for, not the
 // lengths, and by these takes one of two forms:
 //
-// Whole units, where a table is short: a cluster of 8, 4, 2 or 1 CTAs, as many
+// Whole units, where a table or the window is short: a cluster of 8, 4, 2 or 1 CTAs, as many
 // as let all units run at once, takes a unit, deals its slices out to the
 // warps and joins them over distributed shared memory.  One launch: 1 context
 // of 1009 tokens 5.4 us (the other form 9.3), 64 of 500 15 (23), 256 of 100 21
@@ -67,7 +67,7 @@ constexpr int kStagesOf = NR == 1 ? 3 : 4;
 constexpr int kMaxSlots = 4096;                  // CTAs of a launch (at most 4 an SM)
 // what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces
 constexpr int kUnitCost = 4;
-// A cluster of CTAs takes a whole unit where the table has no more keys than this for each of them
+// A cluster of CTAs takes a whole unit where the table (or the window) leaves no more keys than this for each of them
 constexpr int kWholeKeys = 768;
 constexpr int kWholeUnits = 1 << 20;  // a grid's size stays far below 2^31
 // query rows of a kv head (the longest sequence's) from which the tensor-memory kernel takes over
@@ -622,7 +622,8 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   AttnParams arg = p;
   // a cluster a unit: as many CTAs as let all units run at once
   const int share = units * 8 <= full ? 8 : units * 4 <= full ? 4 : units * 2 <= full ? 2 : 1;
-  if (keys <= kWholeKeys * share && units <= kWholeUnits) {
+  const int64_t seen = a.window > 0 && a.window + static_cast<int64_t>(8 * NR) < keys ? static_cast<int64_t>(a.window) + 8 * NR : keys;
+  if (seen <= kWholeKeys * share && units <= kWholeUnits) {
     if (share == 8) return launch_whole<T, D, NR, 8>(arg, units, ring, s);
     if (share == 4) return launch_whole<T, D, NR, 4>(arg, units, ring, s);
     if (share == 2) return launch_whole<T, D, NR, 2>(arg, units, ring, s);

@@ -410,6 +410,24 @@ def test_attention_window(window, qlen):
     run_attention([400, 16, 90, 1000, 333, 2], qlen, 2, 4, 128, 16, window=window, seed=window % 97)
 
 
+@pytest.mark.parametrize("G, D", [(4, 128), (6, 64)])
+@pytest.mark.parametrize("B", [9, 15, 30, 70, 160])
+def test_attention_any_number_of_short_sequences(B, G, D):
+    """Units from a few, which several CTAs share, to more than run at once; and one context far longer than the table's others."""
+    kv = [(37 * i) % 301 for i in range(B)]
+    run_attention(kv, [1] * B, 8, G, D, 16, seed=B)
+    qlen = [min(n, 1 + i % 3) for i, n in enumerate(kv)]
+    run_attention(kv, qlen, 4, G, D, 32, seed=B + 1, dtype=FP16)
+    run_attention([7001] + kv[1:], [1] * B, 2, G, D, 64, seed=B + 2)
+
+
+def test_attention_window_at_the_end_of_long_contexts():
+    run_attention([20000, 9000, 33], [1, 1, 1], 2, 4, 128, 64, window=500, seed=51)
+    run_attention([20000, 9000, 33], [3, 5, 2], 2, 4, 128, 64, window=700, seed=52)
+    run_attention([30000], [1], 1, 8, 64, 16, window=6130, seed=53)
+    run_attention([12000] * 30, [1] * 30, 8, 2, 128, 128, window=900, seed=54)
+
+
 @pytest.mark.parametrize("fused", [False, True])
 def test_attention_long_and_uneven(fused):
     """Many CTAs share a unit, beside units of a few keys; strided caches."""
