@@ -70,6 +70,7 @@ _lib = None
 # integers, without the objects of torch.cuda (which cost as much as a launch)
 _device_index = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_CONTIGUOUS = torch.contiguous_format
 
 
 def _entry(name: str):
@@ -170,20 +171,19 @@ def add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     a.weight = _dense(weight, "weight", wdtype, (hidden,), index)
     a.smooth = _dense(smooth, "smooth", torch.float32, (hidden,), index)
     a.rows, a.hidden, a.dtype, a.weight_dtype, a.eps = rows, hidden, code, DTYPE_CODES[wdtype], eps
-    device = x.device
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=device)
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=_CONTIGUOUS)
     if q_scale is None:
-        q_scale = torch.empty(rows, dtype=torch.float32, device=device)
+        q_scale = torch.empty(rows, dtype=torch.float32, device=x.device)
     if residual is not None:
         a.residual, a.residual_stride = _rows(residual, "residual", dtype, shape, index)
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dtype, device=device)
+            residual_out = torch.empty_like(x, memory_format=_CONTIGUOUS)
         a.residual_out, a.residual_out_stride = _rows(residual_out, "residual_out", dtype, shape, index)
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     if y is None and want_y:
-        y = torch.empty(shape, dtype=dtype, device=device)
+        y = torch.empty_like(x, memory_format=_CONTIGUOUS)
     a.y_out = _dense(y, "y", dtype, shape, index)
     a.q = _dense(q, "q", torch.int8, shape, index)
     a.q_scale = _dense(q_scale, "q_scale", torch.float32, (rows,), index)
@@ -395,7 +395,7 @@ class KvCache:
         a.sm_scale = dim ** -0.5 if scale is None else scale
         ws = workspace if workspace is not None else self._ws if self._ws is not None else self.workspace()
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=self.device)
+            out = torch.empty_like(q, memory_format=_CONTIGUOUS)
             a.out = out.data_ptr()
         else:
             a.out = _dense(out, "out", dtype, shape, index)
