@@ -24,7 +24,7 @@
 // Bound by a tile's chain (S, weights, O: about 5000 cycles a piece, of which the
 // products are 1100) at 42 % of the issue slots; two tiles overlap, a third has
 // no room in tensor memory.  8 chunks of 512 tokens over 8192 keys (32 heads on
-// 8, channels 128): 630 us, 845 TFLOP/s.
+// 8, channels 128): 622 us, 856 TFLOP/s.
 #include "kv_attention.cuh"
 
 #include "device_prims.cuh"
