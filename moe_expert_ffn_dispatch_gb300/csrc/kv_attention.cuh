@@ -188,17 +188,6 @@ struct Schedule {
   }
 };
 
-// four int8 codes -> two pairs of fp16: (0, 1) and (2, 3)
-__device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t off = 0x64806480u;  // 1152
-  const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&off));
-  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&off));
-  lo = *reinterpret_cast<const uint32_t*>(&a);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
-}
-
 // Joins the parts of units that several CTAs shared (kv_attention.cu).  records: how many there are; rows: the
 // most that a unit has; JW: warps that share a row's parts.
 template <typename T, int D, int R, int JW>

@@ -73,6 +73,12 @@ __device__ __forceinline__ float scale_value(uint32_t b, int dt) {
   return __uint_as_float(dt == MOE_LAYER_BF16 ? b << 16 : b);
 }
 
+// a pair of fp16 times a power of two
+__device__ __forceinline__ uint32_t half_mul(uint32_t v, float f) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
@@ -216,11 +222,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         const int k8 = first + u * 32 * parts + lane;
         if (k8 - lane >= n8) break;
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        float f[8];
+        // pairs (0,4) (1,5) (2,6) (3,7) x 2^(8 - e); the second and the last meet codes four bits higher
+        uint4 x;
+        float sum;
         int e = 7;  // codes of up to 127: [2^6, 2^7)
         if constexpr (kInt8) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int8_t>((w[j >> 2] >> ((j & 3) * 8)) & 0xFFu));
+          half_pairs(__byte_perm(w[0], w[1], 0x5140), x.x, x.y);
+          half_pairs(__byte_perm(w[0], w[1], 0x7362), x.z, x.w);
+          x.x = half_mul(x.x, 2.0f), x.y = half_mul(x.y, 0.125f);
+          x.z = half_mul(x.z, 2.0f), x.w = half_mul(x.w, 0.125f);
+          sum = static_cast<float>(__dp4a(static_cast<int>(w[0]), 0x01010101, __dp4a(static_cast<int>(w[1]), 0x01010101, 0)));
         } else {
           // magnitudes are ordered as 16-bit integers
           uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
@@ -231,21 +242,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
           const float2 big = unpack2<X>(top);
           // an infinity or a NaN stays one; elements of 2^-110 and less may vanish
           e = min(max(static_cast<int>(__float_as_uint(big.x) >> 23), 17), 254) - 127;
+          float f[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 h = unpack2<X>(w[j]);
             f[2 * j] = h.x, f[2 * j + 1] = h.y;
           }
+          sum = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                          __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
+          const float up = pow2(8 - e), up16 = pow2(4 - e);
+          x.x = pack2<__half>(__fmul_rn(f[0], up), __fmul_rn(f[4], up));
+          x.y = pack2<__half>(__fmul_rn(f[1], up16), __fmul_rn(f[5], up16));
+          x.z = pack2<__half>(__fmul_rn(f[2], up), __fmul_rn(f[6], up));
+          x.w = pack2<__half>(__fmul_rn(f[3], up16), __fmul_rn(f[7], up16));
         }
-        float sum = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
-                              __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
-        // pairs (0,4) (1,5) (2,6) (3,7) x 2^(8 - e); the second and the last meet codes four bits higher
-        const float up = pow2(8 - e), up16 = pow2(4 - e);
-        uint4 x;
-        x.x = pack2<__half>(__fmul_rn(f[0], up), __fmul_rn(f[4], up));
-        x.y = pack2<__half>(__fmul_rn(f[1], up16), __fmul_rn(f[5], up16));
-        x.z = pack2<__half>(__fmul_rn(f[2], up), __fmul_rn(f[6], up));
-        x.w = pack2<__half>(__fmul_rn(f[3], up16), __fmul_rn(f[7], up16));
 #pragma unroll
         for (int o = 1; o < 16 / GPS; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
         if (k8 < n8) {
