@@ -94,18 +94,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the float at shared address `at` of CTA `rank` of the cluster
-__device__ __forceinline__ float cluster_read(uint32_t at, uint32_t rank) {
-  uint32_t remote;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-  return v;
-}
-
 // CS 0: the CTAs divide the work of all units by the schedule.  Otherwise a
 // cluster of CS CTAs takes a unit, all of its pieces, and joins its parts itself.
 template <typename T, int D, int NR, int CS>

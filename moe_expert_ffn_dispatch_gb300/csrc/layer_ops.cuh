@@ -139,6 +139,19 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// every thread of a cluster: what was written before is seen after
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the float at shared address `at` of CTA `rank` of the cluster
+__device__ __forceinline__ float cluster_read(uint32_t at, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
 // shared-memory reads by address: plain loads, which the compiler may move between barriers
 __device__ __forceinline__ uint4 lds128(uint32_t a) { return *static_cast<const uint4*>(__cvta_shared_to_generic(a)); }
 __device__ __forceinline__ uint2 lds64(uint32_t a) { return *static_cast<const uint2*>(__cvta_shared_to_generic(a)); }

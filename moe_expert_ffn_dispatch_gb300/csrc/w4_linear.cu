@@ -27,7 +27,10 @@
 // warps in WR groups of rows x (16 / WR) parts of K; a warp streams its own
 // 16-row tiles through a ring of 128-k steps by asynchronous copies, which
 // needs no barrier.  One part of K is written straight from the accumulators;
-// several are summed in shared memory, in a fixed order.
+// several are summed in shared memory, in a fixed order.  Where a CTA's shared
+// memory does not hold x (8 rows beyond k 8192, 16 beyond 4096), a cluster of
+// up to 8 shares K and sums over distributed shared memory: 16 x 4096 x 14336 19
+// us, where CTAs that took x in pieces took 38; 64 x 8000 x 16384 114 (186).
 //
 // k order.  Both operands may take the k of a group in any common order.  A
 // lane takes neighbouring words of a weight row, as many as the group allows
@@ -47,6 +50,7 @@ constexpr int kStepK = 128;                    // k of one ring stage
 constexpr int kStageBytes = kRows * kStepK / 2;
 constexpr int kXSmall = 66 * 1024;             // bytes of x that leave room for 8 stages of a warp
 constexpr int kXMost = 130 * 1024;             // and for 4
+constexpr int kMostCtas = 8;                   // of a cluster
 
 // bytes of a warp's own: the scales and scale x zero of 8 groups, or its partial sums
 template <int NT>
@@ -58,6 +62,9 @@ struct W4Params {
   int pieces;     // pieces of kc that cover k
   int wr;         // row groups of a CTA: 1, 2, 4 or 8
   int tiles;      // tiles of kRows weight rows
+  int cs;         // CTAs of a cluster, which share K between them
+  int cta_steps;  // steps of one of them (all, where cs is 1)
+  int at_once;    // clusters that run at once
   int xpitch;     // bytes of a row of x in shared memory
   int ngroups;    // k / group
   int gsteps;     // steps of a group (1 for groups of 128 and less)
@@ -90,7 +97,8 @@ __device__ __forceinline__ uint32_t stage_at(int r, int c) {
 }
 
 // NT: tiles of 8 rows of x.  GPS: groups of a 128-k step (1, 2 or 4)
-template <int NT, int GPS, int kStages>
+// SPLIT: the CTAs of a cluster share K
+template <int NT, int GPS, int kStages, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int M = 8 * NT;                            // rows of x of a CTA
@@ -104,7 +112,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   const int row_group = warp / wk, kpart = warp - row_group * wk;
   const int m0 = blockIdx.y * M;
   const int mrows = min(a.m - m0, M);
-  const int steps = (a.k + kStepK - 1) / kStepK, steps_pp = p.kc / kStepK;
+  const int all_steps = (a.k + kStepK - 1) / kStepK, steps_pp = p.kc / kStepK;
+  const int rank = SPLIT ? blockIdx.x % p.cs : 0, cid = SPLIT ? blockIdx.x / p.cs : blockIdx.x;
+  const int ncl = SPLIT ? gridDim.x / p.cs : gridDim.x;
+  const int s_base = SPLIT ? rank * p.cta_steps : 0;  // this CTA's steps: [s_base, s_base + steps)
+  const int steps = SPLIT ? max(0, min(p.cta_steps, all_steps - s_base)) : all_steps;
   // x | of each group of a step and pair of rows, the sums and the powers of two [steps_pp * GPS][M / 2] | private | rings
   uint8_t* xs = smem;
   float4* xsum = reinterpret_cast<float4*>(smem + M * p.xpitch);
@@ -115,8 +127,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   const uint32_t xs_u = static_cast<uint32_t>(__cvta_generic_to_shared(xs));
   const uint32_t xsum_u = static_cast<uint32_t>(__cvta_generic_to_shared(xsum));
 
-  // row group r of CTA c takes tiles (r + wr i) grid + c: every SM gets as many, to one
-  const int first_tile = row_group * gridDim.x + blockIdx.x, next_tile = wr * gridDim.x;
+  // row group r of CTA (or cluster) c of C takes tiles (r + wr i) C + c: every SM gets as many, to one
+  const int first_tile = row_group * ncl + cid, next_tile = wr * ncl;
   const int rounds = (p.tiles + next_tile - 1) / next_tile;  // the same for every warp
   const int run = steps_pp / wk;                             // steps of a part of K in a piece
   const int row_bytes = a.k / 2;
@@ -131,10 +143,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   const uint8_t *c_row0 = a.w, *c_row1 = a.w;
   bool c_last = false;  // the run ends with K, whose last step this lane may be past
   auto copy_run = [&]() {  // the start of a run
-    const int step = c_piece * steps_pp + kpart * run, kb = step * (kStepK / 2) + cc * 16;
+    const int step = c_piece * steps_pp + kpart * run, kb = (s_base + step) * (kStepK / 2) + cc * 16;
     c_row0 = a.w + static_cast<int64_t>(min(c_tile * kRows + cr, a.n - 1)) * row_bytes + kb;
     c_row1 = a.w + static_cast<int64_t>(min(c_tile * kRows + cr + 8, a.n - 1)) * row_bytes + kb;
-    c_last = step + c_left == steps && cc * 16 >= tail;
+    c_last = s_base + step + c_left == all_steps && cc * 16 >= tail;
   };
   if (c_left <= 0) c_tile = p.tiles;  // no part of K for this warp
   if (c_tile < p.tiles) copy_run();
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   };
   if (kpart * run < steps) {
     scale_tile(min(first_tile, p.tiles - 1));
-    load_scales(kpart * run);
+    load_scales(s_base + kpart * run);
   }
   const uint32_t mine_u = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
 
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   auto load_x_as = [&](auto type, int piece) {
     using X = decltype(type);
     constexpr bool kInt8 = sizeof(X) == 1;
-    const int k0 = piece * p.kc, n8 = p.kc / 8;
+    const int k0 = s_base * kStepK + piece * p.kc, n8 = p.kc / 8;
     const int m = warp & ((1 << row_shift) - 1), part = warp >> row_shift, parts = kWarps >> row_shift;
     if (m >= mrows) return;
     const X* row = static_cast<const X*>(a.x) + static_cast<int64_t>(m0 + m) * a.x_stride + k0;
@@ -294,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         __syncthreads();
       }
       const int todo = tile < p.tiles ? run_of(piece) : 0;
-      const int s0 = piece * steps_pp + kpart * run;
+      const int s0 = s_base + piece * steps_pp + kpart * run;
       uint32_t xa = xs_u + g * p.xpitch + t * 16 + kpart * run * kStepK * 2;
       uint32_t xg = xsum_u + (kpart * run * GPS * (M / 2) + t) * 16;
       for (int base = 0; base < todo; base += kBlock) {
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
           load_scales(s0 + steps_pp);
         } else if (tile + next_tile < p.tiles) {
           scale_tile(tile + next_tile);
-          load_scales(kpart * run);
+          load_scales(s_base + kpart * run);
         }
         uint32_t sa = mine_u + g * 16;
         const int here = min(kBlock, todo - base);
@@ -388,7 +400,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
       else if (a.out_dtype == MOE_LAYER_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(y);
       else static_cast<__half*>(a.y)[at] = __float2half_rn(y);
     };
-    if (wk == 1) {
+    if (!SPLIT && wk == 1) {
       if (tile < p.tiles) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -406,39 +418,81 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) mine[(n * 8 + 2 * t + (e & 1)) * kRows + g + 8 * (e >> 1)] = acc[n][e];
-    __syncthreads();
+    if constexpr (SPLIT) cluster_sync();
+    else __syncthreads();
     const int cshift = wr_shift + 4;  // columns: 16 x wr
-    for (int i = tid; i < mrows << cshift; i += kWarps * 32) {
+    const int sharers = SPLIT ? p.cs : 1;
+    for (int i = rank * kWarps * 32 + tid; i < mrows << cshift; i += sharers * kWarps * 32) {
       const int m = i >> cshift, c = i & ((1 << cshift) - 1), rg = c >> 4;
-      const int n = (rg * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + it * next_tile) * kRows + (c & 15);
+      const int n = (rg * ncl + cid + it * next_tile) * kRows + (c & 15);
       const float* from = priv + rg * wk * (kPrivate / 4) + m * kRows + (c & 15);
       float y = 0.0f;
-      for (int q = 0; q < wk; ++q) y = __fadd_rn(y, from[q * (kPrivate / 4)]);
+      if constexpr (SPLIT) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(from));
+        for (int w = 0; w < sharers; ++w)
+#pragma unroll 4
+          for (int q = 0; q < wk; ++q) y = __fadd_rn(y, cluster_read(at + q * kPrivate, w));
+      } else {
+        for (int q = 0; q < wk; ++q) y = __fadd_rn(y, from[q * (kPrivate / 4)]);
+      }
       if (n < a.n) store(m, n, y);
     }
-    __syncthreads();  // the sums are read before the next block's scales take their place
+    if constexpr (SPLIT) cluster_sync();
+    else __syncthreads();  // the sums are read before the next block's scales take their place
   }
   cp_async_wait<0>();
 }
 
-template <int NT, int GPS, int kStages>
-cudaError_t launch_stages(const W4Params& p, int num_sms, cudaStream_t s) {
+// Clusters of `cs` CTAs, one CTA an SM, that the current device runs at once:
+// fewer than SMs / cs, as a cluster lies within a part of the GPU (one cluster too
+// many doubles the time: 16 x 16384 x 16384 92 us).  Asked once a device and size.
+cudaError_t clusters_at_once(int cs, int num_sms, int& n) {
+  static std::atomic<int> known[64][3];
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  const int slot = cs == 2 ? 0 : cs == 4 ? 1 : 2;
+  n = dev < 64 ? known[dev][slot].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return cudaSuccess;
   static std::atomic<uint64_t> allowed{0};
-  const void* k = (const void*)w4_linear_kernel<NT, GPS, kStages>;
+  const void* k = (const void*)w4_linear_kernel<1, 1, 4, true>;
+  if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms / cs * cs);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k, &cfg); e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  n = n < num_sms / cs ? n : num_sms / cs;
+  if (dev < 64) known[dev][slot].store(n, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+template <int NT, int GPS, int kStages, bool SPLIT>
+cudaError_t launch_stages(const W4Params& p, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  const void* k = (const void*)w4_linear_kernel<NT, GPS, kStages, SPLIT>;
   if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
   const int smem = 8 * NT * (p.xpitch + p.kc / kStepK * GPS * 8) + kWarps * kPrivateOf<NT> +
                    kWarps * kStages * kStageBytes;
   W4Params arg = p;
   void* args[] = {&arg};
   const int groups = (p.tiles + p.wr - 1) / p.wr;
-  return launch_after(k, dim3(groups < num_sms ? groups : num_sms, (p.a.m + 8 * NT - 1) / (8 * NT)), dim3(kWarps * 32),
-                      args, smem, s);
+  return launch_after(k, dim3((groups < p.at_once ? groups : p.at_once) * p.cs, (p.a.m + 8 * NT - 1) / (8 * NT)),
+                      dim3(kWarps * 32), args, smem, s, p.cs);
 }
 
 template <int NT, int GPS>
-cudaError_t launch_gps(const W4Params& p, int num_sms, cudaStream_t s) {
-  if (8 * NT * p.xpitch <= kXSmall) return launch_stages<NT, GPS, 8>(p, num_sms, s);
-  return launch_stages<NT, GPS, 4>(p, num_sms, s);
+cudaError_t launch_gps(const W4Params& p, cudaStream_t s) {
+  const bool small = 8 * NT * p.xpitch <= kXSmall;
+  if (p.cs > 1)
+    return small ? launch_stages<NT, GPS, 8, true>(p, s) : launch_stages<NT, GPS, 4, true>(p, s);
+  return small ? launch_stages<NT, GPS, 8, false>(p, s) : launch_stages<NT, GPS, 4, false>(p, s);
 }
 
 template <int NT>
@@ -448,8 +502,16 @@ cudaError_t launch_nt(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
   p.ngroups = a.k / a.group;
   p.gsteps = a.group > kStepK ? a.group / kStepK : 1;
   p.tiles = (a.n + kRows - 1) / kRows;
-  const int steps = (a.k + kStepK - 1) / kStepK;
+  const int all_steps = (a.k + kStepK - 1) / kStepK;
   const int fit = (kXMost / (8 * NT) - 64) / (2 * kStepK);  // steps of x that shared memory takes
+  // x that does not fit one CTA's shared memory is shared out over a cluster's
+  p.cs = 1;
+  while (p.cs < kMostCtas && (all_steps + p.cs - 1) / p.cs > fit) p.cs *= 2;
+  p.cta_steps = (all_steps + p.cs - 1) / p.cs;
+  const int steps = p.cta_steps;
+  p.at_once = num_sms;
+  if (p.cs > 1)
+    if (const cudaError_t e = clusters_at_once(p.cs, num_sms, p.at_once); e != cudaSuccess) return e;
   // Row groups: the split with the least work in the longest warp, in steps.
   // A tile costs about one step beside its own, about six where parts of K
   // are summed (measured: 130001 x 4096 took 58 us in one part, 83 us in eight).
@@ -458,8 +520,9 @@ cudaError_t launch_nt(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
   for (int wr = kWarps; wr >= 1; wr /= 2) {
     const int wk = kWarps / wr;
     if (wk > steps || wk > fit) break;
-    const int64_t rounds = (p.tiles + static_cast<int64_t>(wr) * num_sms - 1) / (static_cast<int64_t>(wr) * num_sms);
-    const int64_t cost = rounds * ((steps + wk - 1) / wk + (wk > 1 ? 6 : 1));
+    const int64_t tiles_at_once = static_cast<int64_t>(wr) * p.at_once;
+    const int64_t rounds = (p.tiles + tiles_at_once - 1) / tiles_at_once;
+    const int64_t cost = rounds * ((steps + wk - 1) / wk + (wk > 1 || p.cs > 1 ? 6 : 1));
     if (cost < best) best = cost, p.wr = wr;
   }
   const int wk = kWarps / p.wr;
@@ -473,9 +536,9 @@ cudaError_t launch_nt(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
   p.pieces = (steps + p.kc - 1) / p.kc;
   p.kc *= kStepK;
   p.xpitch = p.kc * 2 + 64;  // a multiple of 128 plus 64: rows 2i and 2i + 1 of a 16-byte read fall on other banks
-  if (a.group == 32) return launch_gps<NT, 4>(p, num_sms, s);
-  if (a.group == 64) return launch_gps<NT, 2>(p, num_sms, s);
-  return launch_gps<NT, 1>(p, num_sms, s);
+  if (a.group == 32) return launch_gps<NT, 4>(p, s);
+  if (a.group == 64) return launch_gps<NT, 2>(p, s);
+  return launch_gps<NT, 1>(p, s);
 }
 
 }  // namespace

@@ -183,6 +183,17 @@ def test_w4_sizes(M, N, K, group, dtype):
     assert torch.equal(out, got.to(dtype))  # one rounding of the same sums, and every element written
 
 
+@pytest.mark.parametrize("M, N, K, group", [
+    (16, 20000, 8352, 32), (8, 30001, 8224, 32), (16, 41, 65536, 64), (30, 9000, 12832, 32), (8, 700, 40960, 128)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_w4_rows_longer_than_shared_memory(M, N, K, group, x8):
+    """Clusters that share K, over several rounds of tiles and several pieces."""
+    code, w, ws, z, x, xs = w4_case(M, N, K, group, BF16, N + K, x8=x8, zero=True)
+    got = m.w4_linear(x, w, ws, zero=z, x_scale=xs, out_dtype=F32)
+    check_w4(code, ws, z, x, xs, got)
+    assert torch.equal(got, m.w4_linear(x, w, ws, zero=z, x_scale=xs, out_dtype=F32))
+
+
 @pytest.mark.parametrize("M, N, K, group", [(1, 40, 64, 32), (8, 200, 4096, 64), (13, 77, 1024, 128), (40, 30, 8320, 64)])
 @pytest.mark.parametrize("sdtype", [BF16, FP16, F32])
 def test_w4_int8_rows_and_scale_types(M, N, K, group, sdtype):
