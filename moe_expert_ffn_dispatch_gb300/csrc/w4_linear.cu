@@ -27,10 +27,11 @@
 // warps in WR groups of rows x (16 / WR) parts of K; a warp streams its own
 // 16-row tiles through a ring of 128-k steps by asynchronous copies, which
 // needs no barrier.  One part of K is written straight from the accumulators;
-// several are summed in shared memory, in a fixed order.  Where a CTA's shared
-// memory does not hold x (8 rows beyond k 8192, 16 beyond 4096), a cluster of
-// up to 8 shares K and sums over distributed shared memory: 16 x 4096 x 14336 19
-// us, where CTAs that took x in pieces took 38; 64 x 8000 x 16384 114 (186).
+// several are summed in shared memory, in a fixed order.  Where tiles are
+// few or a CTA's shared memory does not hold x (8 rows beyond k 8192, 16 beyond
+// 4096), a cluster of up to 8 CTAs shares K, so that each lays out its part of x
+// alone, and sums over distributed shared memory: 16 x 4096 x 14336 19 us, where
+// CTAs that took x in pieces took 38; 64 x 8000 x 16384 114 (186).
 //
 // k order.  Both operands may take the k of a group in any common order.  A
 // lane takes neighbouring words of a weight row, as many as the group allows
@@ -504,27 +505,41 @@ cudaError_t launch_nt(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
   p.tiles = (a.n + kRows - 1) / kRows;
   const int all_steps = (a.k + kStepK - 1) / kStepK;
   const int fit = (kXMost / (8 * NT) - 64) / (2 * kStepK);  // steps of x that shared memory takes
-  // x that does not fit one CTA's shared memory is shared out over a cluster's
-  p.cs = 1;
-  while (p.cs < kMostCtas && (all_steps + p.cs - 1) / p.cs > fit) p.cs *= 2;
-  p.cta_steps = (all_steps + p.cs - 1) / p.cs;
-  const int steps = p.cta_steps;
-  p.at_once = num_sms;
-  if (p.cs > 1)
-    if (const cudaError_t e = clusters_at_once(p.cs, num_sms, p.at_once); e != cudaSuccess) return e;
-  // Row groups: the split with the least work in the longest warp, in steps.
-  // A tile costs about one step beside its own, about six where parts of K
-  // are summed (measured: 130001 x 4096 took 58 us in one part, 83 us in eight).
+  // CTAs that share K, and row groups: the split with the least work in the
+  // longest warp, in steps of 128 k (cost: 64ths of one).  A tile costs about
+  // one step beside its own, about six where parts of K are summed (130001 x
+  // 4096 took 58 us in one part, 83 us in eight).  x costs a step for every 64
+  // of its rows x steps, once; every round, and six steps a piece, in pieces.  A
+  // cluster costs 1 + cs / 4 steps, and its sums twice as much from the
+  // second round on.  So few tiles are split (16 x 4096 x 4096: 11.6 us by one CTA
+  // each, 10.0 by two, 9.2 by four) and many are not (16 x 28672 x 4096: 27 us by
+  // one, 30 by two; 64 x 40000 x 4096 123 and 148).
+  const int rows = a.m < 8 * NT ? a.m : 8 * NT;
   int64_t best = INT64_MAX;
-  p.wr = 1;
-  for (int wr = kWarps; wr >= 1; wr /= 2) {
-    const int wk = kWarps / wr;
-    if (wk > steps || wk > fit) break;
-    const int64_t tiles_at_once = static_cast<int64_t>(wr) * p.at_once;
-    const int64_t rounds = (p.tiles + tiles_at_once - 1) / tiles_at_once;
-    const int64_t cost = rounds * ((steps + wk - 1) / wk + (wk > 1 || p.cs > 1 ? 6 : 1));
-    if (cost < best) best = cost, p.wr = wr;
+  p.wr = p.cs = 1;
+  p.cta_steps = all_steps;
+  p.at_once = num_sms;
+  for (int cs = 1; cs <= kMostCtas; cs *= 2) {
+    const int steps = (all_steps + cs - 1) / cs, pieces = (steps + fit - 1) / fit;
+    if (cs > 1 && (cs - 1) * steps >= all_steps) break;  // nothing for the last CTA
+    int at_once = num_sms;
+    if (cs > 1)
+      if (const cudaError_t e = clusters_at_once(cs, num_sms, at_once); e != cudaSuccess) return e;
+    for (int wr = kWarps; wr >= 1; wr /= 2) {
+      const int wk = kWarps / wr;
+      if (wk > steps || wk > fit) break;
+      const int64_t tiles_at_once = static_cast<int64_t>(wr) * at_once;
+      const int64_t rounds = (p.tiles + tiles_at_once - 1) / tiles_at_once;
+      int64_t cost = 64 * rounds * ((steps + wk - 1) / wk + (wk > 1 || cs > 1 ? 6 : 1));
+      cost += pieces > 1 ? rounds * (static_cast<int64_t>(rows) * steps + 64 * 6 * pieces) : rows * steps;
+      if (cs > 1) cost += 64 * 6 * (rounds - 1) + 32 * cs + 32;
+      if (cost < best) {
+        best = cost;
+        p.wr = wr, p.cs = cs, p.cta_steps = steps, p.at_once = at_once;
+      }
+    }
   }
+  const int steps = p.cta_steps;
   const int wk = kWarps / p.wr;
   // pieces of whole rounds of the parts of K
   p.kc = (steps + wk - 1) / wk * wk;
