@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           int c_lo = 0, c_hi = kTile - 1;
           if (mine) {
             c_hi = static_cast<int>(max(min(pos - key0, static_cast<int64_t>(kTile - 1)), static_cast<int64_t>(-1)));
-            if (a.window > 0) c_lo = static_cast<int>(max(min(pos - a.window + 1 - key0, static_cast<int64_t>(kTile)), static_cast<int64_t>(0)));
+            if (a.window > 0)
+              c_lo = static_cast<int>(max(min(pos - a.window + 1 - key0, static_cast<int64_t>(kTile)), static_cast<int64_t>(0)));
           }
           const uint32_t gone = __ballot_sync(0xffffffffu, page < 0);  // blocks on pages that do not exist
           const bool whole = gone == 0 && __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kTile - 1);
@@ -610,78 +611,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (warp == kWarpMma) {
-    // ------------------------------------------------ the products, by one lane
-    const uint32_t idesc_s = moe::umma_idesc_f16(kTile, kTile);
-    const uint32_t idesc_o = moe::umma_idesc_f16(kTile, D) | (1u << 16);  // V's contiguous dimension is N
-    const uint64_t q_desc = moe::umma_desc_sw128(moe::smem_u32(smem + L::kQ));
-    const uint64_t k_desc = moe::umma_desc_sw128(moe::smem_u32(smem + L::kK));
-    const uint64_t v_desc = desc_transposed(moe::smem_u32(smem + L::kV));
-    constexpr uint64_t kOp = L::kOperand >> 4, kHalf = (kTile * 128) >> 4;
-    uint32_t t = 0, u = 0, np[2] = {0, 0};  // pieces, units, and weights taken of each tile
-    bool ok = true;
-    // S of tile q: 16 channels a product, 64 to a half
-    auto product_s = [&](int q, int st) {
-      if (moe::elect_one()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          moe::umma_f16(s_at(q), q_desc + q * kOp + (k >> 2) * kHalf + (k & 3) * 2,
-                        k_desc + st * kOp + (k >> 2) * kHalf + (k & 3) * 2, idesc_s, k != 0);
-        moe::umma_commit(&bar.s_full[q]);
-      }
-      __syncwarp();
-    };
-    // O of tile q: 16 keys a product
-    auto product_o = [&](int q, uint32_t piece, bool first) {
-      const int st = piece & 1;
-      if (!wait(&bar.p_full[q], np[q] & 1, kSite + 5 + q)) return false;
-      ++np[q];
-      if (!wait(&bar.v_full[st], (piece >> 1) & 1, kSite + 7)) return false;
-      moe::tc_fence_after();
-      if (moe::elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          moe::umma_f16_ts(o_at(q), s_at(q) + k * 8, v_desc + st * kOp + k * (16 * 128 >> 4), idesc_o, !first || k != 0);
-      }
-      __syncwarp();
-      return true;
-    };
-    auto commit = [&](uint64_t* b) {
-      if (moe::elect_one()) moe::umma_commit(b);
-      __syncwarp();
-    };
-    while (ok && next_segment()) {
-      const Pieces pc = pieces_of(seg);
-      if (pc.n == 0) continue;
-      const bool two = seg.rows > 128;
-      ok = wait(&bar.q_full, u & 1, kSite + 8);
-      ++u;
-      for (int i = 0; ok && i < pc.n; ++i, ++t) {
-        ok = wait(&bar.k_full[t & 1], (t >> 1) & 1, kSite + 9);
-        if (!ok) break;
-        moe::tc_fence_after();
-        product_s(0, t & 1);
-        if (two) {
-          if (i > 0) {
-            ok = product_o(1, t - 1, i == 1);
-            if (!ok) break;
-            commit(&bar.v_empty[(t - 1) & 1]);
-          }
-          product_s(1, t & 1);
+      // ------------------------------------------------ the products, by one lane
+      const uint32_t idesc_s = moe::umma_idesc_f16(kTile, kTile);
+      const uint32_t idesc_o = moe::umma_idesc_f16(kTile, D) | (1u << 16);  // V's contiguous dimension is N
+      const uint64_t q_desc = moe::umma_desc_sw128(moe::smem_u32(smem + L::kQ));
+      const uint64_t k_desc = moe::umma_desc_sw128(moe::smem_u32(smem + L::kK));
+      const uint64_t v_desc = desc_transposed(moe::smem_u32(smem + L::kV));
+      constexpr uint64_t kOp = L::kOperand >> 4, kHalf = (kTile * 128) >> 4;
+      uint32_t t = 0, u = 0, np[2] = {0, 0};  // pieces, units, and weights taken of each tile
+      bool ok = true;
+      // S of tile q: 16 channels a product, 64 to a half
+      auto product_s = [&](int q, int st) {
+        if (moe::elect_one()) {
+  #pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            moe::umma_f16(s_at(q), q_desc + q * kOp + (k >> 2) * kHalf + (k & 3) * 2,
+                          k_desc + st * kOp + (k >> 2) * kHalf + (k & 3) * 2, idesc_s, k != 0);
+          moe::umma_commit(&bar.s_full[q]);
         }
-        commit(&bar.k_empty[t & 1]);
-        ok = product_o(0, t, i == 0);
-        if (ok && !two) commit(&bar.v_empty[t & 1]);
+        __syncwarp();
+      };
+      // O of tile q: 16 keys a product
+      auto product_o = [&](int q, uint32_t piece, bool first) {
+        const int st = piece & 1;
+        if (!wait(&bar.p_full[q], np[q] & 1, kSite + 5 + q)) return false;
+        ++np[q];
+        if (!wait(&bar.v_full[st], (piece >> 1) & 1, kSite + 7)) return false;
+        moe::tc_fence_after();
+        if (moe::elect_one()) {
+  #pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            moe::umma_f16_ts(o_at(q), s_at(q) + k * 8, v_desc + st * kOp + k * (16 * 128 >> 4), idesc_o, !first || k != 0);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto commit = [&](uint64_t* b) {
+        if (moe::elect_one()) moe::umma_commit(b);
+        __syncwarp();
+      };
+      while (ok && next_segment()) {
+        const Pieces pc = pieces_of(seg);
+        if (pc.n == 0) continue;
+        const bool two = seg.rows > 128;
+        ok = wait(&bar.q_full, u & 1, kSite + 8);
+        ++u;
+        for (int i = 0; ok && i < pc.n; ++i, ++t) {
+          ok = wait(&bar.k_full[t & 1], (t >> 1) & 1, kSite + 9);
+          if (!ok) break;
+          moe::tc_fence_after();
+          product_s(0, t & 1);
+          if (two) {
+            if (i > 0) {
+              ok = product_o(1, t - 1, i == 1);
+              if (!ok) break;
+              commit(&bar.v_empty[(t - 1) & 1]);
+            }
+            product_s(1, t & 1);
+          }
+          commit(&bar.k_empty[t & 1]);
+          ok = product_o(0, t, i == 0);
+          if (ok && !two) commit(&bar.v_empty[t & 1]);
+        }
+        if (ok && two) {
+          ok = product_o(1, t - 1, pc.n == 1);
+          if (ok) commit(&bar.v_empty[(t - 1) & 1]);
+        }
+        if (ok) commit(&bar.o_full);
       }
-      if (ok && two) {
-        ok = product_o(1, t - 1, pc.n == 1);
-        if (ok) commit(&bar.v_empty[(t - 1) & 1]);
-      }
-      if (ok) commit(&bar.o_full);
-    }
-    // nothing of this CTA is in flight when its tensor memory goes back
-    commit(&bar.drain);
-    moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 10);
-    __syncwarp();
+      // nothing of this CTA is in flight when its tensor memory goes back
+      commit(&bar.drain);
+      moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 10);
+      __syncwarp();
     }
   }
   moe::tc_fence_before();

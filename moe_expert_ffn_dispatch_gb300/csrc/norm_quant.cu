@@ -116,9 +116,9 @@ __device__ __forceinline__ void store_codes(int8_t* p, const uint4* buf, int tid
   }
 }
 
-// 8 elements of a vector that all rows share, from i on: 16-byte loads where it is aligned
+// 8 elements from i on, of an aligned row or of a vector that all rows share (16-byte loads where that is aligned)
 template <typename E, bool VEC>
-struct Shared8 {
+struct Chunk8 {
   uint32_t w[sizeof(E) * 2];
   __device__ __forceinline__ void load(const E* p, int i, int h) {
     const bool wide = VEC ? i < h : (i + 8 <= h && (reinterpret_cast<uintptr_t>(p) & 15u) == 0);
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
 
   // every load of the row before the first use or store
   RowIn<T, C> xs, rs;
-  Shared8<T, true> xr[C], rr[C];
-  Shared8<W, VEC> wr[C];
+  Chunk8<T, true> xr[C], rr[C];
+  Chunk8<W, VEC> wr[C];
   if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
       else if (i < h) *reinterpret_cast<uint4*>(y_out + i) = pack8<T>(v[c]);
     }
     if (a.smooth) {
-      Shared8<float, VEC> sr;
+      Chunk8<float, VEC> sr;
       sr.load(a.smooth, i, h);
       sr.take(f);
 #pragma unroll
