@@ -168,7 +168,7 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
 /* Attention over the cache.  Sequence b has the query tokens cu_q[b] ..
  * cu_q[b + 1] - 1 (token b alone when cu_q is NULL), qlen of them, and
  * seq_lens[b] keys, its query tokens' own (already appended) among them.
- * Query token j stands at position p = seq_lens[b] - qlen + j and sees the keys i with
+ * Query token j stands at position p = seq_lens[b] - qlen + j (for every qlen) and sees the keys i with
  * 0 <= i <= p, and i > p - window where window > 0.  Query head
  * n uses kv head n / group_size:
  *   out[t, n] = sum_i softmax_i(sm_scale * <q[t, n], key_i>) * value_i
@@ -179,7 +179,7 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
  * q_stride (a multiple of 8), heads dense, 16-byte aligned.  out: the same
  * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the largest
  * number of query tokens of a sequence (1 without cu_q); a larger one in cu_q
- * leaves the tokens past max_q unwritten.
+ * leaves that sequence's tokens past the first max_q unwritten and the others as they are.
  * Scores, softmax statistics and sums are fp32; the softmax weights are
  * rounded to fp16 (11 bits) for the product with the values.  Where max_q *
  * group_size is 64 or more the products run on the tensor memory units.

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
   while (CS > 0 || work.next(a, at, seg)) {
     const SeqShape& s = seg.s;
     const int b = seg.b, head = seg.head, rt = seg.rt, rows = seg.rows, ta = seg.ta, tb = seg.tb;
-    const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;  // position of query token 0
+    const int64_t pos0 = s.pos0;
     // keys that any row of the tile sees, cut to this CTA's pieces
     const int64_t last = pos0 + (rt * R + rows - 1) / a.group_size;
     int64_t k_lo = static_cast<int64_t>(seg.tile0 + ta) * kTileTokens;

@@ -24,21 +24,25 @@ struct AttnParams {
 
 // What a sequence contributes, from its lengths.
 struct SeqShape {
-  int q0, qlen;     // query tokens
+  int q0, qlen;     // query tokens that are computed
   int len;          // keys
+  int pos0;         // position of query token q0: negative where there are more query tokens than keys
 };
 
 __device__ __forceinline__ SeqShape seq_shape(const moe_layer_kv_attention_args_t& a, int b) {
   SeqShape s;
+  int end = b + 1;  // of the sequence's query tokens, those past max_q among them: the last stands at len - 1
   if (a.cu_q) {
+    end = max(a.cu_q[b + 1], 0);
     s.q0 = min(max(a.cu_q[b], 0), a.tokens);
-    s.qlen = min(max(min(a.cu_q[b + 1], a.tokens) - s.q0, 0), a.max_q);
+    s.qlen = min(max(min(end, a.tokens) - s.q0, 0), a.max_q);
   } else {
     s.q0 = b;
     s.qlen = 1;
   }
   const int64_t most = static_cast<int64_t>(a.max_pages) * a.cache.page_size;
   s.len = static_cast<int>(min(static_cast<int64_t>(max(a.seq_lens[b], 0)), most));
+  s.pos0 = s.len - max(end - s.q0, 0);
   return s;
 }
 
@@ -48,7 +52,7 @@ struct KeyRange {
 };
 template <int R>
 __device__ __forceinline__ KeyRange keys_of(const moe_layer_kv_attention_args_t& a, const SeqShape& s, int rt) {
-  const int64_t pos0 = static_cast<int64_t>(s.len) - s.qlen;
+  const int64_t pos0 = s.pos0;
   const int last_row = min((rt + 1) * R, s.qlen * a.group_size) - 1;
   KeyRange k;
   k.hi = static_cast<int>(max(static_cast<int64_t>(0), pos0 + last_row / a.group_size + 1));
@@ -75,7 +79,7 @@ struct Segment {
 template <int R, int TILE, int COST>
 struct Schedule {
   int64_t* prefix;  // shared memory: [batch + 1]
-  int4* shapes;     // shared memory: [batch], q0, qlen, len
+  int4* shapes;     // shared memory: [batch], q0, qlen, len, pos0
   int64_t total, begin, end;  // of all the work; this CTA's
   int G;
 
@@ -102,7 +106,7 @@ struct Schedule {
         int64_t one = 0;  // of one head
         for (int rt = 0; rt < row_tiles; ++rt) one += pieces(keys_of<R>(a, s, rt)) + COST;
         v = a.cache.kv_heads * one;
-        shapes[b] = make_int4(s.q0, s.qlen, s.len, 0);
+        shapes[b] = make_int4(s.q0, s.qlen, s.len, s.pos0);
       }
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -137,7 +141,7 @@ struct Schedule {
       }
       const int4 sh = shapes[lo];
       g.b = lo;
-      g.s.q0 = sh.x, g.s.qlen = sh.y, g.s.len = sh.z;
+      g.s.q0 = sh.x, g.s.qlen = sh.y, g.s.len = sh.z, g.s.pos0 = sh.w;
       const int64_t rel = at - prefix[lo], one = (prefix[lo + 1] - prefix[lo]) / a.cache.kv_heads;
       g.head = static_cast<int>(rel / one);
       int64_t rem = rel - g.head * one;

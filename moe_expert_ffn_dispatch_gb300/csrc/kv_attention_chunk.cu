@@ -69,11 +69,11 @@ static_assert(sizeof(Barriers) <= 2560, "");
 struct Pieces {
   int first, n;
   int lo, hi;       // keys that any row sees
-  int64_t pos0;     // position of query token 0
+  int64_t pos0;     // position of the first query token
 };
 __device__ __forceinline__ Pieces pieces_of(const Segment& g) {
   Pieces r;
-  r.pos0 = static_cast<int64_t>(g.s.len) - g.s.qlen;
+  r.pos0 = g.s.pos0;
   r.lo = g.keys.lo, r.hi = g.keys.hi;
   r.first = g.tile0 + g.ta;
   r.n = max(0, min(g.tile0 + g.tb, (r.hi + kTile - 1) / kTile) - r.first);

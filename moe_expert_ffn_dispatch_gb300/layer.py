@@ -362,15 +362,16 @@ class KvCache:
             _raise(rc, "moe_layer_kv_append")
 
     def attention(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
-                  cu_q: Optional[torch.Tensor] = None, max_q: int = 1, scale: Optional[float] = None, window: int = 0,
+                  cu_q: Optional[torch.Tensor] = None, max_q: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Attention of the query tokens over their sequences' keys
         (moe_layer_kv_attention).  q [tokens, heads, head_dim] bf16 or fp16
         (tokens may be strided), heads a multiple of kv_heads; seq_lens
         [batch] int32, the query tokens' own keys counted; cu_q [batch + 1]
-        int32 with max_q, the most query tokens of a sequence, where that is
-        not one each; scale: head_dim ** -0.5 without it; window: keys that a
+        int32 with max_q, the most query tokens of a sequence (tokens past
+        it stay unwritten, so it has to be given), where that is not one
+        each; scale: head_dim ** -0.5 without it; window: keys that a
         token sees at most, itself among them (0: no limit).  Returns out
         [tokens, heads, head_dim]."""
         code, index, shape, dtype = _act(q, "q"), self._index, q.shape, q.dtype
@@ -389,8 +390,12 @@ class KvCache:
         a.seq_lens = _dense(seq_lens, "seq_lens", torch.int32, (batch,), index)
         if cu_q is not None:
             a.cu_q = _dense(cu_q, "cu_q", torch.int32, (batch + 1,), index)
-        elif tokens != batch or max_q != 1:
-            raise ValueError("q: %d tokens (max_q %d) for %d sequences without cu_q" % (tokens, max_q, batch))
+            if max_q is None:
+                raise ValueError("max_q is required with cu_q")
+        else:
+            max_q = 1 if max_q is None else max_q
+            if tokens != batch or max_q != 1:
+                raise ValueError("q: %d tokens (max_q %d) for %d sequences without cu_q" % (tokens, max_q, batch))
         a.tokens, a.max_q, a.group_size, a.window, a.dtype = tokens, max_q, heads // self.kv_heads, window, code
         a.sm_scale = dim ** -0.5 if scale is None else scale
         ws = workspace if workspace is not None else self._ws if self._ws is not None else self.workspace()

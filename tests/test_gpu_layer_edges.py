@@ -1,0 +1,64 @@
+"""The decoder-layer operators where their definitions are easily missed: query
+tokens past what a call computes, page scales far apart or not finite, empty
+tables, workspaces of the caller's own.  References and tolerances are those of
+the operators' other tests unless a test derives its own."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import moe_expert_ffn_dispatch_gb300 as m  # noqa: E402
+from test_gpu_layer_ops import (BF16, DEV, FP16, TINY, U, attention_reference, close, gen, new_cache, page_table,  # noqa: E402
+                                randn)
+
+pytestmark = pytest.mark.gpu
+
+
+def cum(v):
+    return torch.tensor(np.cumsum([0] + list(v)), dtype=torch.int32, device=DEV)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------ query tokens past max_q or past the tensor
+@pytest.mark.parametrize("window", [0, 5])
+@pytest.mark.parametrize("kv, qlen, max_q, G", [
+    ([10], [8], 4, 2), ([10, 300, 7], [8, 2, 7], 4, 2), ([40, 500, 3], [30, 3, 9], 5, 3), ([70, 2000], [70, 1], 1, 4),
+    ([400, 900, 20], [300, 64, 20], 100, 4), ([1300], [700], 130, 2), ([5, 40], [20, 11], 6, 4)])
+def test_attention_leaves_tokens_past_max_q_and_keeps_the_others_where_they_stand(kv, qlen, max_q, G, window):
+    """The first max_q query tokens of a longer sequence stand where they would with all of them."""
+    H, D, page = 2, 128, 16
+    need = [-(-n // page) for n in kv]
+    cache, table = new_cache(sum(need) + 1, H, page, D, seed=kv[0]), page_table(need, sum(need) + 1, seed=kv[0])
+    q = randn(sum(qlen), G * H, D, g=gen(kv[0]), std=2.0).to(BF16)
+    out = torch.full(q.shape, 7.0, dtype=BF16, device=DEV)
+    cache.attention(q, table.to(DEV), i32(kv), cu_q=cum(qlen), max_q=max_q, window=window, out=out)
+    ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, kv, qlen, window, D ** -0.5)
+    done = torch.cat([torch.arange(n, device=DEV) < max_q for n in qlen])
+    close(out[done], ref[done], (tol + ref.abs() * U[BF16] + TINY[BF16])[done])
+    assert not done.all() and (out[~done] == 7).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 90])
+def test_attention_of_the_leading_query_tokens_of_a_call(tokens):
+    """cu_q goes past the rows of q: those that are there stay where they stand."""
+    H, G, D, page, kv, qlen = 2, 4, 64, 32, 200, 150
+    cache, table = new_cache(8, H, page, D, seed=5), page_table([7], 8, seed=5)
+    q = randn(qlen, G * H, D, g=gen(6), std=2.0).to(FP16)
+    ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, [kv], [qlen], 0, D ** -0.5)
+    got = cache.attention(q[:tokens], table.to(DEV), i32([kv]), cu_q=i32([0, qlen]), max_q=qlen)
+    close(got, ref[:tokens], (tol + ref.abs() * U[FP16] + TINY[FP16])[:tokens])
+
+
+def test_attention_wants_max_q_with_cu_q():
+    cache, table = new_cache(4, 1, 16, 64), i32([[0, 1]])
+    q = torch.zeros(3, 2, 64, dtype=BF16, device=DEV)
+    with pytest.raises(ValueError):
+        cache.attention(q, table, i32([20]), cu_q=i32([0, 3]))
+    cache.attention(q, table, i32([20]), cu_q=i32([0, 3]), max_q=3)
+    cache.attention(q[:1], table, i32([20]))
+    cache.attention(q[:1], table, i32([20]), max_q=1)
