@@ -328,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
             if ((gone >> (c >> 4)) & 2u) b &= 0x0000FFFFu;
             return b;
           };
-          auto scale_o = [&](float corr) {  // S(i) is there, so the products of earlier pieces are done
+          // S(i) is there, so the products of earlier pieces are done.  The stores have arrived when this
+          // returns: a piece can scale O more than once.
+          auto scale_o = [&](float corr) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float v[32];
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
               for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__fmul_rn(v[e], corr));
               moe::tmem_st32(o_at(q) + lanes + c, w);
             }
+            moe::tmem_st_wait();
           };
           if (vbig > 8.0f * vref) {  // the same for the whole warp
             const float vnew = fmaxf(vref, vbig);

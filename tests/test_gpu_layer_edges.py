@@ -62,3 +62,23 @@ def test_attention_wants_max_q_with_cu_q():
     cache.attention(q, table, i32([20]), cu_q=i32([0, 3]), max_q=3)
     cache.attention(q[:1], table, i32([20]))
     cache.attention(q[:1], table, i32([20]), max_q=1)
+
+
+# ------------------------------------------------------------ prompt chunks: one piece that scales the output twice
+@pytest.mark.parametrize("odd", [0.0, -0.02, 1e-9, -1e-30])
+@pytest.mark.parametrize("D, page", [(128, 16), (64, 16), (128, 32)])
+def test_attention_chunk_where_scale_and_row_reference_grow_in_one_piece(D, page, odd):
+    """In pieces past the first: a page whose scale of V is many times those before it, beside one with an odd
+    scale, and keys that score far above all earlier ones.  All rows see them."""
+    H, G, kv, qlen = 2, 4, 1100, 70
+    need = -(-kv // page)
+    cache, table = new_cache(need + 1, H, page, D, seed=71), page_table([need], need + 1, seed=71)
+    for at, v_times, k_times in ((256, 20, 1), (512, 300, 6), (768, 3000, 12)):
+        p = table[0, at // page:at // page + 4].long().to(DEV)
+        cache.v_scale[p[0]] *= v_times
+        cache.v_scale[p[1]] = odd
+        cache.k_scale[p[2:]] *= k_times
+    q = randn(qlen, G * H, D, g=gen(72), std=2.0).to(BF16)
+    got = cache.attention(q, table.to(DEV), i32([kv]), cu_q=i32([0, qlen]), max_q=qlen)
+    ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, [kv], [qlen], 0, D ** -0.5)
+    close(got, ref, tol + ref.abs() * U[BF16] + TINY[BF16])
