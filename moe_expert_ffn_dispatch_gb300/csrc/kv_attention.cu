@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
           page = pg;
           ks = a.cache.k_scale[pg * a.cache.scale_stride + head];
           vs = a.cache.v_scale[pg * a.cache.scale_stride + head];
+          if (!(fabsf(ks) < INFINITY)) ks = 0.0f, vs = NAN;  // a key's score of minus infinity would hide it
         }
       }
     };

@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
               n_page = pg;
               n_ks = a.cache.k_scale[pg * a.cache.scale_stride + seg.head];
               n_vs = a.cache.v_scale[pg * a.cache.scale_stride + seg.head];
+              if (!(fabsf(n_ks) < INFINITY)) n_ks = 0.0f, n_vs = NAN;  // as in the kernel for few rows
             }
           }
         };

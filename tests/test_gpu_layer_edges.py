@@ -82,3 +82,23 @@ def test_attention_chunk_where_scale_and_row_reference_grow_in_one_piece(D, page
     got = cache.attention(q, table.to(DEV), i32([kv]), cu_q=i32([0, qlen]), max_q=qlen)
     ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, [kv], [qlen], 0, D ** -0.5)
     close(got, ref, tol + ref.abs() * U[BF16] + TINY[BF16])
+
+
+# ------------------------------------------------------------ what is not finite
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("kv, qlen, G, page, bad, window", [
+    (52, 1, 4, 16, 2, 0), (52, 1, 16, 16, 2, 0), (3000, 1, 4, 64, 5, 0), (52, 8, 2, 16, 3, 0), (68, 8, 2, 16, 3, 3),
+    (100, 100, 2, 16, 3, 20), (700, 300, 2, 32, 15, 0), (700, 300, 2, 32, 15, 100), (300, 200, 4, 128, 1, 0)])
+def test_attention_is_not_finite_where_a_scale_of_k_is_not(kv, qlen, G, page, bad, window, value):
+    """Also where it would make scores of minus infinity; the tokens and heads that do not see the page stay."""
+    H, D, need = 2, 128, -(-kv // page)
+    cache, table = new_cache(need + 1, H, page, D, seed=kv), page_table([need], need + 1, seed=kv)
+    q = randn(qlen, G * H, D, g=gen(kv), std=2.0).to(BF16)
+    ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, [kv], [qlen], window, D ** -0.5)
+    cache.k_scale[table[0, bad], 1] = value
+    got = cache.attention(q, table.to(DEV), i32([kv]), cu_q=None if qlen == 1 else i32([0, qlen]), max_q=qlen, window=window)
+    p = torch.arange(kv - qlen, kv, device=DEV)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[(p >= bad * page) & ((p - (window or kv + 1)) < (bad + 1) * page - 1), G:] = True
+    assert hit.any() and not torch.isfinite(got[hit]).any()
+    close(got[~hit], ref[~hit], (tol + ref.abs() * U[BF16] + TINY[BF16])[~hit])
