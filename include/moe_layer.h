@@ -174,7 +174,8 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
  *   out[t, n] = sum_i softmax_i(sm_scale * <q[t, n], key_i>) * value_i
  * and zeros where no key is seen.  Keys on a page-table entry outside [0,
  * num_pages) are not seen; a scale that is not finite reaches only the query tokens
- * that see a key of its page, whose outputs are then not finite; lengths are held to [0, max_pages * page_size].
+ * that see a key of its page, whose outputs are then not finite, and so does an element of q its row;
+ * lengths are held to [0, max_pages * page_size].
  * q: [tokens, kv_heads * group_size, head_dim] of `dtype` (BF16 or FP16), token stride
  * q_stride (a multiple of 8), heads dense, 16-byte aligned.  out: the same
  * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the largest

@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
       // exponent of the largest element, inside what 2^-e can hold
       const int e = min(max(static_cast<int>(top >> 23), 1), 253);
       const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - e)
-      const float up = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
+      // a query that is not finite makes every score NaN: scores of minus infinity alone would hide it
+      const float up = top < 0x7F800000u ? __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2) : NAN;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const float2 f0 = unpack2<T>(w[2 * i]), f1 = unpack2<T>(w[2 * i + 1]);

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
               const int rr = (warp & 3) * 32 + r4 + x * kRowsAt + rl;
               *reinterpret_cast<uint4*>(smem + L::kQ + q * L::kOperand + operand_at(rr, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
               // to the thread that has the row
-              const float up1 = __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2);
+              const float up1 = top < 0x7F800000u ? __fmul_rn(__uint_as_float(static_cast<uint32_t>(e) << 23), p.scale_log2) : NAN;
               const float mine_up = __shfl_sync(0xffffffffu, up1, ((lane - r4 - x * kRowsAt) & (kRowsAt - 1)) * kLanes);
               if (lane >= r4 + x * kRowsAt && lane < r4 + (x + 1) * kRowsAt) up = mine_up;
             }

@@ -102,3 +102,22 @@ def test_attention_is_not_finite_where_a_scale_of_k_is_not(kv, qlen, G, page, ba
     hit[(p >= bad * page) & ((p - (window or kv + 1)) < (bad + 1) * page - 1), G:] = True
     assert hit.any() and not torch.isfinite(got[hit]).any()
     close(got[~hit], ref[~hit], (tol + ref.abs() * U[BF16] + TINY[BF16])[~hit])
+
+
+@pytest.mark.parametrize("kv, qlen, G, page", [(1, 1, 4, 16), (40, 1, 4, 16), (3000, 1, 12, 64), (50, 9, 4, 32), (300, 100, 4, 32),
+                                               (20, 40, 4, 16)])
+@pytest.mark.parametrize("value", [-math.inf, math.inf, math.nan])
+def test_attention_is_not_finite_where_a_query_is_not(kv, qlen, G, page, value):
+    """Also where all scores of the row are minus infinity; a row that sees no key stays 0."""
+    H, D, need = 2, 128, -(-kv // page)
+    cache, table = new_cache(need + 1, H, page, D, seed=kv), page_table([need], need + 1, seed=kv)
+    cache.k[..., 3] = 5
+    q = randn(qlen, G * H, D, g=gen(kv), std=2.0).to(BF16)
+    ref, tol = attention_reference(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, [kv], [qlen], 0, D ** -0.5)
+    q[::3, 1, 3] = value
+    got = cache.attention(q, table.to(DEV), i32([kv]), cu_q=None if qlen == 1 else i32([0, qlen]), max_q=qlen)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[::3, 1] = True
+    hit &= (torch.arange(kv - qlen, kv, device=DEV) >= 0)[:, None]
+    assert hit.any() and not torch.isfinite(got[hit]).any()
+    close(got[~hit], ref[~hit], (tol + ref.abs() * U[BF16] + TINY[BF16])[~hit])
