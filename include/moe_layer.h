@@ -181,8 +181,11 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
  * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the largest
  * number of query tokens of a sequence (1 without cu_q); a larger one in cu_q
  * leaves that sequence's tokens past the first max_q unwritten and the others as they are.
- * Scores, softmax statistics and sums are fp32; the softmax weights are
- * rounded to fp16 (11 bits) for the product with the values.  Where max_q *
+ * Scores, softmax statistics and sums are fp32.  For the product with the
+ * values a softmax weight times its page's scale of V is rounded to fp16: 11 bits
+ * down to 2^-21 of the row's largest such product, below that a step of 2^-31
+ * of it (for scales that lie within 2^64 of one another).  Query rows are fp16 too, after a power of two a row: elements below
+ * 2^-14 (fp16) or 2^-17 (bf16) of the row's largest keep a step of 2^-24 of it.  Where max_q *
  * group_size is 64 or more the products run on the tensor memory units.
  * workspace: moe_layer_kv_attention_workspace_size bytes, 256-byte aligned,
  * no initial content needed; calls that share one must be ordered. */

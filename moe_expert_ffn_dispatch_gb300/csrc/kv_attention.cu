@@ -39,10 +39,10 @@
 // of 1024, minus 1152).  A query row is scaled by a power of two to [1, 2) at
 // its largest element, so bf16 rows are exact in fp16 as far as an fp32 sum
 // can tell.  With x the scores times log2(e), the page scale of K and the
-// row's power of two enter x in fp32; the page scale of V enters the weight
-// exp2(x - reference) as its ratio to a reference page scale, and that product
-// is rounded to fp16: 11 bits, where the output has 8 or 11.  Sums of weights
-// are taken before that rounding, in fp32.
+// row's power of two enter x in fp32.  The page scale of V enters the weight of
+// the second product, which is rounded to fp16: 11 bits, where the output has 8
+// or 11 (kv_attention.cuh).  Sums of weights are taken before that rounding, in
+// fp32.
 // Both products let the k index run over channels (or tokens) in whatever
 // order makes shared-memory reads whole 16-byte chunks: a permuted sum is the
 // same sum.
@@ -50,6 +50,8 @@
 // Bound by the cache's bytes at 8 rows (two contexts of 200003 and 100000
 // tokens, 8 kv heads of 128, 4 rows each: 101 us, 6.1 TB/s of 6.8), by
 // instructions at 16 (64 contexts of 2000 tokens: 76 us, 3.5 TB/s).
+#include <climits>
+
 #include "kv_attention.cuh"
 
 namespace moe_layer {
@@ -167,21 +169,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
           page = pg;
           ks = a.cache.k_scale[pg * a.cache.scale_stride + head];
           vs = a.cache.v_scale[pg * a.cache.scale_stride + head];
-          if (!(fabsf(ks) < INFINITY)) ks = 0.0f, vs = NAN;  // a key's score of minus infinity would hide it
         }
       }
     };
+    // log2 of the scales of V of the slices that come next, in units of 2^unit; infinity stands for any
+    // that is not between kScaleLeast and kScaleMost, or beside a scale of K that is not finite
+    float unit = INFINITY;
+    auto log_scale = [&](int page, float ks, float vs) {
+      if (unit == INFINITY) unit = scale_base(vs, true);
+      const float lv = __fsub_rn(log2_fast(vs), unit);
+      return page < 0 ? 0.0f : lv >= kScaleLeast && lv <= kScaleMost && fabsf(ks) < INFINITY ? lv : INFINITY;
+    };
     int page0, page1;
-    float ks0, vs0, ks1, vs1;
+    float ks0, vs0, ks1, vs1, lv0;
     look_up(0, page0, ks0, vs0);
     look_up(32, page1, ks1, vs1);
     const int in_page = a.cache.page_size - 1;
-    // lane offsets of the copies of a slice
     const int8_t* k_head = a.cache.k + head * a.cache.head_stride + lane * 16;
     const int8_t* v_head = a.cache.v + head * a.cache.head_stride + lane * 16;
-    uint32_t to[kCopies];
-#pragma unroll
-    for (int x = 0; x < kCopies; ++x) to[x] = chunk_at<D>((x * 32 + lane) / (D / 16), (x * 32 + lane) % (D / 16));
+    // where this lane's copies of a slice go: the rows of copy x lie 512 bytes after those of copy x - 1, at the
+    // same place in the swizzle or (D = 128) at the place that differs by 4 chunks
+    const uint32_t to0 = chunk_at<D>(lane / (D / 16), lane % (D / 16));
+    auto to = [&](int x) { return D == 128 ? (x & 1 ? to0 ^ 64u : to0) + x * 512 : to0 + x * 512; };
     auto issue = [&](int i, int rel_i) {  // slice i of this warp, rel_i from the base of page0
       const int page = rel_i < 32 ? __shfl_sync(0xffffffffu, page0, rel_i & 31) : __shfl_sync(0xffffffffu, page1, rel_i & 31);
       if (i < n) {
@@ -190,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
 #pragma unroll
         for (int x = 0; x < kCopies; ++x) {
-          cp_async16(dst + to[x], kp + x * 512, page >= 0);
-          cp_async16(dst + kSliceBytes + to[x], vp + x * 512, page >= 0);
+          cp_async16(dst + to(x), kp + x * 512, page >= 0);
+          cp_async16(dst + kSliceBytes + to(x), vp + x * 512, page >= 0);
         }
       }
       cp_async_commit();
@@ -247,8 +256,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         row_pos[nr][e2] = __shfl_sync(0xffffffffu, pos, (2 * t + e2) * 4);
       }
     }
+    // whether a row sees this lane's key of a half slice: as many tokens back as the window has, or any (32 bits
+    // do, as a key in front of the row is a large number without its sign)
+    const uint32_t reach = a.window > 0 ? a.window : INT_MAX;
+    auto sees = [&](int pos, int half, int64_t tok0) {
+      return static_cast<uint32_t>(pos) - (static_cast<uint32_t>(tok0) + half * 8 + token_of<D>(g)) < reach;
+    };
     float o[NR][NT][4];  // transposed: channels g D / 8 + 2 i and + 1 of column tile i, rows 2t and 2t + 1
-    float m[NR][2], l[NR][2], vref = 0.0f, vinv = 1.0f;
+    float m[NR][2], l[NR][2];
+    bool far = false;  // a scale of V above kScaleMost has been met
+    lv0 = log_scale(page0, ks0, vs0);
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -260,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
     for (int i = 0; i < n; ++i) {
       const int ri = i & 31;
       if (ri == 0 && i > 0) {
-        page0 = page1, ks0 = ks1, vs0 = vs1;
+        page0 = page1, ks0 = ks1, lv0 = log_scale(page1, ks1, vs1);
         look_up(i + 32, page1, ks1, vs1);
       }
       cp_async_wait<kStages - 2>();
@@ -268,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
       const uint32_t kb = ring_u + (i % kStages) * kStageBytes, vb = kb + kSliceBytes;
       const int page = __shfl_sync(0xffffffffu, page0, ri);
       const float ks = __shfl_sync(0xffffffffu, ks0, ri);
-      float vs = __shfl_sync(0xffffffffu, vs0, ri);
+      float lv = __shfl_sync(0xffffffffu, lv0, ri);
       const int64_t tok0 = static_cast<int64_t>(first + i * kSpread) * kSlice;
 
       // scores, transposed: 16 tokens x 8 NR rows, in two chains of products
@@ -313,37 +330,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int64_t key = tok0 + (e >> 1) * 8 + token_of<D>(g), pos = row_pos[nr][e & 1];
-            if (page < 0 || key > pos || (a.window > 0 && key <= pos - a.window)) sc[nr][e] = -INFINITY;
+            if (page < 0 || !sees(row_pos[nr][e & 1], e >> 1, tok0)) sc[nr][e] = -INFINITY;
           }
       }
-      // A page scale of V that is not finite makes the rows that see the page
-      // NaN, through their sums, and stays out of what the rows share.
-      if (!(fabsf(vs) < INFINITY)) {
-        vs = 0.0f;
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (sc[nr][e] != -INFINITY) l[nr][e & 1] = NAN;
-      }
-      // The references of the weights move only when a weight would pass 2^8
-      // (a page scale of V 8 times its reference): weights of up to 2^11 are
-      // as exact in fp16 as weights up to 1, and most slices rescale nothing.
-      float top[NR][2];
-      bool move = fabsf(vs) > 8.0f * vref;
+      // The references move only when a product would pass what fp16 is to
+      // hold: most slices rescale nothing.
+      uint32_t sign = 0;
+      float top[NR][2], rv = exp2_fast(__fsub_rn(kSumShift, lv));
+      const bool odd = far || lv == INFINITY;
+      bool move = odd;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           top[nr][e] = fmaxf(sc[nr][e], sc[nr][2 + e]);
-          move |= top[nr][e] > m[nr][e] + 8.0f;
+          move |= top[nr][e] > m[nr][e] + (kWeightMost - lv);
         }
-      if (__any_sync(0xffffffffu, move)) {
-        const float vnew = fmaxf(vref, fabsf(vs));
-        const float vcorr = vnew > vref ? __fdiv_rn(vref, vnew) : 1.0f;
-        vref = vnew;
-        vinv = vnew > 0.0f ? __fdiv_rn(1.0f, vnew) : 1.0f;
+      if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
+        float lr = lv;
+        if (odd && page >= 0) {
+          const float k1 = a.cache.k_scale[page * a.cache.scale_stride + head], v1 = a.cache.v_scale[page * a.cache.scale_stride + head];
+          rv = 0.0f;
+          lv = __fsub_rn(log2_fast(fabsf(v1)), unit);
+          if (v1 < 0.0f) sign = 0x80008000u;
+          if (!(fabsf(k1) < INFINITY && fabsf(v1) < INFINITY)) {
+            // a scale that is not finite makes the rows that see the page NaN, through
+            // their sums, and stays out of what the rows share
+            lv = -INFINITY;
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (sees(row_pos[nr][e & 1], e >> 1, tok0)) l[nr][e & 1] = NAN;
+                sc[nr][e] = top[nr][e & 1] = -INFINITY;
+              }
+          }
+          lr = fmaxf(lv, kScaleLeast);
+          far = far || lv > kScaleMost;
+        }
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           float corr[2];
@@ -351,31 +375,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top[nr][e] = fmaxf(top[nr][e], __shfl_xor_sync(0xffffffffu, top[nr][e], x));
-            const float mn = fmaxf(m[nr][e], top[nr][e]);
+            const float mn = fmaxf(m[nr][e], __fadd_rn(top[nr][e], lr - kWeightLand));
             corr[e] = mn == m[nr][e] ? 1.0f : exp2_fast(__fsub_rn(m[nr][e], mn));
             m[nr][e] = mn;
             l[nr][e] = __fmul_rn(l[nr][e], corr[e]);
-            corr[e] = __fmul_rn(corr[e], vcorr);
           }
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nr][q][e] = __fmul_rn(o[nr][q][e], corr[e & 1]);
+          if (odd) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = __fsub_rn(sc[nr][e], m[nr][e & 1] == -INFINITY ? 0.0f : m[nr][e & 1]);
+              l[nr][e & 1] = __fadd_rn(l[nr][e & 1], exp2_fast(__fadd_rn(x, kSumShift)));
+            }
+          }
         }
       }
-      const float vw = __fmul_rn(vs, vinv);
       uint32_t pb[NR][2];  // weights: tokens 2t.. (and 2t + 8..) of row g
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nr][e & 1];
-          const float w = exp2_fast(__fsub_rn(sc[nr][e], ref == -INFINITY ? 0.0f : ref));
-          l[nr][e & 1] = __fadd_rn(l[nr][e & 1], w);
-          sc[nr][e] = __fmul_rn(w, vw);
+        for (int e = 0; e < 2; ++e) {
+          const float by = __fsub_rn(lv, m[nr][e] == -INFINITY ? 0.0f : m[nr][e]);
+          sc[nr][e] = exp2_fast(__fadd_rn(sc[nr][e], by));
+          sc[nr][2 + e] = exp2_fast(__fadd_rn(sc[nr][2 + e], by));
+          l[nr][e] = __fmaf_rn(__fadd_rn(sc[nr][e], sc[nr][2 + e]), rv, l[nr][e]);
         }
-        pb[nr][0] = transpose8x8(pack2<__half>(sc[nr][0], sc[nr][1]));
-        pb[nr][1] = transpose8x8(pack2<__half>(sc[nr][2], sc[nr][3]));
+        pb[nr][0] = transpose8x8(pack2<__half>(sc[nr][0], sc[nr][1]) ^ sign);
+        pb[nr][1] = transpose8x8(pack2<__half>(sc[nr][2], sc[nr][3]) ^ sign);
       }
       // values: lane row g holds channels [g D / 8, (g + 1) D / 8), two a channel tile
       uint32_t w[4][NT / 2];
@@ -424,10 +453,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NR>) kv_attention_kernel(
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = nr * 8 + 2 * t + e;
+        const float by = settle(m[nr][e], l[nr][e], unit == INFINITY ? 0.0f : unit);
 #pragma unroll
         for (int q = 0; q < NT; ++q)
           *reinterpret_cast<float2*>(wo + r * D + g * (D / 8) + 2 * q) =
-              make_float2(__fmul_rn(o[nr][q][e], vref), __fmul_rn(o[nr][q][2 + e], vref));
+              make_float2(__fmul_rn(o[nr][q][e], by), __fmul_rn(o[nr][q][2 + e], by));
         if (g == 0) wm[r] = m[nr][e], wm[R + r] = l[nr][e];
       }
     __syncthreads();

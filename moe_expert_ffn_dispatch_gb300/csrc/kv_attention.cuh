@@ -22,6 +22,42 @@ struct AttnParams {
   int page_shift;
 };
 
+// With x a score times log2(e) and v the page scale of V, a row's running sums
+// are
+//   O = sum v 2^(x - M) V  and  l = sum 2^(x - M + kSumShift)
+// with one reference M, that of the products v 2^x (taken of the weights 2^x
+// alone, a page with a large v would push all others out of fp16's range).  Each
+// v 2^(x - M) is rounded to fp16.  M moves so that none passes 2^kWeightMost and
+// the largest lands at 2^kWeightLand: what is 2^-21 of the largest still has 11
+// bits, and a step below that is 2^-31 of it.
+// A warp measures v in units of 2^base, the smallest of the first scales that it meets.  While
+// log2 v lies in [kScaleLeast, kScaleMost] of that, l is the sum of the products
+// divided by v; a weight too small for fp32 in that form is below 2^-46 of the
+// row's largest.  Other scales (0, negative ones, and all that come after one
+// above kScaleMost) take an exponential more.  One below kScaleLeast counts as
+// that in M, which holds l in range.
+constexpr float kWeightLand = 8.0f, kWeightMost = 15.0f;
+constexpr float kScaleLeast = -50.0f, kScaleMost = 40.0f, kSumShift = 31.0f;
+
+// log2 of the unit of V's scales, from the smallest that a lane has (where `counts`) and that is neither 0 nor
+// not finite; infinity where there is none
+__device__ __forceinline__ float scale_base(float v, bool counts) {
+  const uint32_t b = abs_bits(v), least = __reduce_min_sync(0xffffffffu, counts && b != 0 && b < 0x7F800000u ? b : 0x7F800000u);
+  return least < 0x7F800000u ? fmaxf(floorf(log2_fast(__uint_as_float(least))), -126.0f) : INFINITY;
+}
+
+// A row's sums at the end: l in [1, 2) (or 0, or not finite) relative to m, and what makes O relative to it
+__device__ __forceinline__ float settle(float& m, float& l, float base) {
+  if (!(l > 0.0f && l < INFINITY)) {
+    if (l == 0.0f) m = -INFINITY;
+    return 1.0f;
+  }
+  const int e = static_cast<int>(__float_as_uint(l) >> 23) - 127;
+  l = __uint_as_float((__float_as_uint(l) & 0x7FFFFFu) | 0x3F800000u);
+  m = __fadd_rn(m, static_cast<float>(e) - kSumShift);
+  return exp2_fast(__fadd_rn(base, kSumShift - static_cast<float>(e)));
+}
+
 // What a sequence contributes, from its lengths.
 struct SeqShape {
   int q0, qlen;     // query tokens that are computed

@@ -16,10 +16,10 @@
 // each.  Keys lie [key][channel] in both operands; V's is the transposed
 // (channel-contiguous) form.  The arithmetic of the weights is that of the
 // kernel for few rows: row scaled by a power of two, page scale of K in the
-// score, page scale of V in the weight as its ratio to a reference.  The rows'
+// score, page scale of V in the weight.  The rows'
 // references move by whole powers of two, and only when a weight would pass
-// 2^11, so that S is read once: weights of the same piece that are already
-// written move with the reference, exactly.
+// fp16's range, so that S is read once: weights of the same piece that are already
+// written move with the reference (exactly, but for those that become subnormal).
 //
 // Bound by a tile's chain (S, weights, O: about 5000 cycles a piece, of which the
 // products are 1100) at 42 % of the issue slots; two tiles overlap, a third has
@@ -147,11 +147,6 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float log2_fast(float v) {
-  float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const AttnParams p) {
@@ -222,7 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       const int row = q * 128 + r;
       const bool mine = row < seg.rows, active = q * 128 < seg.rows;  // active: uniform over the tile
       const int grow = seg.rt * kChunkRows + row, j = grow / a.group_size, hq = grow - j * a.group_size;
-      float m = -INFINITY, l = 0.0f, vref = 0.0f, vinv = 1.0f, up = 0.0f;
+      float m = -INFINITY, l = 0.0f, up = 0.0f;
+      // of the warp: the unit of V's scales, and whether one above kScaleMost has been met
+      float base = INFINITY;
+      bool far = false;
       if (pc.n > 0) {
         // The rows of Q, each scaled by a power of two to [1, 2) at its largest
         // element: D / 8 lanes a row, 16 bytes a lane, 4 loads in flight.
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
               n_page = pg;
               n_ks = a.cache.k_scale[pg * a.cache.scale_stride + seg.head];
               n_vs = a.cache.v_scale[pg * a.cache.scale_stride + seg.head];
-              if (!(fabsf(n_ks) < INFINITY)) n_ks = 0.0f, n_vs = NAN;  // as in the kernel for few rows
+              if (!(fabsf(n_ks) < INFINITY)) n_ks = 0.0f, n_vs = NAN;  // a score of minus infinity would hide it
             }
           }
         };
@@ -313,7 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           const bool hidden = page < 0 || 16 * lane > high || 16 * lane + 15 < low;
           // (nor does one that is not finite: the rows that see it take it in their weights)
           const bool counts = !hidden && lane < 8 && fabsf(vs) < INFINITY;
-          const float vbig = __uint_as_float(__reduce_max_sync(0xffffffffu, counts ? abs_bits(vs) : 0u));
+          if (base == INFINITY) base = scale_base(vs, counts);
+          const float lv = __fsub_rn(log2_fast(fabsf(vs)), base);
+          far = __any_sync(0xffffffffu, far || (counts && lv > kScaleMost));
           if (!wait(&bar.s_full[q], s_phase & 1, kSite + q)) {
             ok = false;
             break;
@@ -343,18 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
             }
             moe::tmem_st_wait();
           };
-          if (vbig > 8.0f * vref) {  // the same for the whole warp
-            const float vnew = fmaxf(vref, vbig);
-            if (i > 0) scale_o(__fdiv_rn(vref, vnew));
-            vref = vnew;
-            vinv = __fdiv_rn(1.0f, vnew);
-          }
-          // Where every scale of V is an ordinary positive number (or no row
-          // sees its keys), its ratio to the reference joins the exponent, and the
-          // sum of a block's weights is divided by it.
-          const float vw = __fmul_rn(vs, vinv);
-          if (__all_sync(0xffffffffu, lane >= 8 || hidden || (vw >= 0x1p-60f && vw <= 16.0f))) {
-            const float lv = hidden ? 0.0f : log2_fast(vw), rv = hidden ? 0.0f : __fdiv_rn(1.0f, vw);
+          // every scale of V an ordinary positive number (or no row sees its keys)
+          if (!far && __all_sync(0xffffffffu, lane >= 8 || hidden || (counts && vs > 0.0f && lv >= kScaleLeast))) {
+            const float lb = hidden ? 0.0f : lv, rv = hidden ? 0.0f : exp2_fast(__fsub_rn(kSumShift, lv));
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
               const uint32_t bits = whole ? 0xFFFFFFFFu : bits_of(c);
@@ -372,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-                const float b = __fsub_rn(__shfl_sync(0xffffffffu, lv, (c >> 4) + h), ref);
+                const float b = __fsub_rn(__shfl_sync(0xffffffffu, lb, (c >> 4) + h), ref);
                 const uint64_t ff = pair_of(f, f), bb = pair_of(b, b);
 #pragma unroll
                 for (int e = h * 16; e < h * 16 + 16; e += 2) {
@@ -387,11 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
 #pragma unroll
               for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
               // The reference moves, by whole powers of two, when a weight would
-              // pass 2^11 (or is a row's first): what the row has so far moves
-              // exactly with it, this piece's weights among it.
+              // pass what fp16 holds (or is a row's first): what the row has so
+              // far moves with it, this piece's weights among it.
               const bool fresh = m == -INFINITY && top > -INFINITY;
-              if (__any_sync(0xffffffffu, top > 11.0f || fresh)) {
-                const float d = top > 11.0f || fresh ? ceilf(top) : 0.0f;
+              if (__any_sync(0xffffffffu, top > kWeightMost || fresh)) {
+                const float d = top > kWeightLand || fresh ? __fsub_rn(ceilf(top), kWeightLand) : 0.0f;
                 const float corr = fresh ? 1.0f : exp2_fast(-d);  // a fresh row has nothing yet
                 m = __fadd_rn(ref, d) + (m == -INFINITY && !fresh ? -INFINITY : 0.0f);
                 l = __fmul_rn(l, corr);
@@ -433,6 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
             }
           } else {
             // any scales: the maximum first, then the weights
+            const float lr = fmaxf(lv, kScaleLeast), neg = vs < 0.0f ? -1.0f : 1.0f;
+            const float ref0 = m == -INFINITY ? 0.0f : m;
             float top = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
@@ -442,14 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
+                const float b = __fsub_rn(__shfl_sync(0xffffffffu, lr, (c >> 4) + h), ref0);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                  top = fmaxf(top, bits & (1u << (h * 16 + e)) ? __fmul_rn(v[h * 16 + e], f) : -INFINITY);
+                  top = fmaxf(top, bits & (1u << (h * 16 + e)) ? __fmaf_rn(v[h * 16 + e], f, b) : -INFINITY);
               }
             }
-            if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-              const float mn = fmaxf(m, top), corr = mn == m ? 1.0f : exp2_fast(__fsub_rn(m, mn));
-              m = mn;
+            const bool fresh = m == -INFINITY && top > -INFINITY;
+            if (__any_sync(0xffffffffu, top > kWeightMost || fresh)) {
+              const float d = top > kWeightLand || fresh ? __fsub_rn(ceilf(top), kWeightLand) : 0.0f;
+              const float corr = fresh ? 1.0f : exp2_fast(-d);
+              m = __fadd_rn(ref0, d) + (m == -INFINITY && !fresh ? -INFINITY : 0.0f);
               l = __fmul_rn(l, corr);
               if (i > 0) scale_o(corr);
             }
@@ -463,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float f = __fmul_rn(__shfl_sync(0xffffffffu, ks, (c >> 4) + h), up);
-                const float vb = __shfl_sync(0xffffffffu, vw, (c >> 4) + h);
+                const float vb = __shfl_sync(0xffffffffu, lv, (c >> 4) + h), sb = __shfl_sync(0xffffffffu, neg, (c >> 4) + h);
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                   float p2[2];
@@ -471,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
                   for (int z = 0; z < 2; ++z) {
                     // a scale that is not finite stays out of what is not seen
                     const bool on = bits & (1u << (h * 16 + e + z));
-                    const float w1 = on ? exp2_fast(__fmaf_rn(v[h * 16 + e + z], f, -ref)) : 0.0f;
-                    l = __fadd_rn(l, w1);
-                    p2[z] = on ? __fmul_rn(w1, vb) : 0.0f;
+                    const float x = __fmaf_rn(v[h * 16 + e + z], f, -ref);
+                    l = __fadd_rn(l, on ? exp2_fast(__fadd_rn(x, kSumShift)) : 0.0f);
+                    p2[z] = on ? __fmul_rn(exp2_fast(__fadd_rn(x, vb)), sb) : 0.0f;
                   }
                   w[h * 8 + e / 2] = pack2<__half>(p2[0], p2[1]);
                 }
@@ -492,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
       if (!active) continue;
       // ---- the rows' results
       const bool whole_unit = seg.ta == 0 && seg.tb == seg.tiles;
-      const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
+      float by = settle(m, l, base == INFINITY ? 0.0f : base);
+      if (whole_unit) by = l > 0.0f ? __fdiv_rn(by, l) : (l == 0.0f ? 0.0f : l);
       const int64_t slot_row = (2 * static_cast<int64_t>(blockIdx.x) + (seg.ta > 0 ? 0 : 1)) * kChunkRows + row;
       T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(seg.s.q0 + j) * a.cache.kv_heads * a.group_size +
                                          seg.head * a.group_size + hq) * D;
@@ -506,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
           for (int e = 0; e < 32; ++e) v[e] = 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(v[e], vref);
+        for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(v[e], by);
         if (whole_unit) {
           if (mine) {
 #pragma unroll
@@ -514,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
               uint32_t w[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                w[x] = pack2<T>(__fmul_rn(v[e + 2 * x], inv), __fmul_rn(v[e + 2 * x + 1], inv));
+                w[x] = pack2<T>(v[e + 2 * x], v[e + 2 * x + 1]);
               *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }

@@ -131,6 +131,12 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
+__device__ __forceinline__ float log2_fast(float v) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // asynchronous 16-byte copy global -> shared; `ok` false fills with zeros and reads nothing
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");

@@ -121,3 +121,102 @@ def test_attention_is_not_finite_where_a_query_is_not(kv, qlen, G, page, value):
     hit &= (torch.arange(kv - qlen, kv, device=DEV) >= 0)[:, None]
     assert hit.any() and not torch.isfinite(got[hit]).any()
     close(got[~hit], ref[~hit], (tol + ref.abs() * U[BF16] + TINY[BF16])[~hit])
+
+
+# ------------------------------------------------------------ weights and page scales far apart
+def far_reference(q, cache, table, kv, qlen, window, scale):
+    """(out, tolerance) in 64 bits.  Beside the terms of attention_reference a weight times its page's scale of V
+    may be off by half a step of 2^-31 of the row's largest such product.  The codes that these errors meet are
+    independent and of either sign (and at most 127), so their sum stays within 8 sqrt(keys) of one."""
+    P, H, D = cache.k.shape[2], cache.k.shape[1], cache.k.shape[3]
+    G = q.shape[1] // H
+    out, tol = torch.zeros(q.shape, dtype=torch.float64, device=DEV), torch.zeros(q.shape, dtype=torch.float64, device=DEV)
+    pages = table[0, :-(-kv // P)].long().to(DEV)
+    i, p = torch.arange(kv, device=DEV), torch.arange(kv - qlen, kv, device=DEV)[:, None]
+    seen = (i <= p) & (i > p - (window or kv + qlen + 1))
+    for h in range(H):
+        vs = cache.v_scale[pages, h].double().repeat_interleave(P)[:kv]
+        kd = (cache.k[pages, h].double() * cache.k_scale[pages, h].double()[:, None, None]).reshape(-1, D)[:kv]
+        vd = cache.v[pages, h].double().reshape(-1, D)[:kv] * vs[:, None]
+        heads = slice(h * G, (h + 1) * G)
+        qd = q[:, heads].double()
+        w = torch.softmax((torch.einsum("cgd,nd->cgn", qd, kd) * scale).masked_fill(~seen[:, None], -math.inf), -1).nan_to_num(0.0)
+        out[:, heads] = torch.einsum("cgn,nd->cgd", w, vd)
+        mag = (torch.einsum("cgd,nd->cgn", qd.abs(), kd.abs()) * abs(scale)).masked_fill(~seen[:, None], 0)
+        # rounding of the score, of the exponential and the logarithm (2^-21 together), and of what is added to it
+        rel = 2.0 ** -11 + 2 * ((D / 16 + 24) * 2.0 ** -23 * mag.amax(-1) + 2.0 ** -20) + kv * 2.0 ** -24 + 2.0 ** -16
+        step = 8 * kv ** 0.5 * 127 * 2.0 ** -32 * (w * vs.abs()).amax(-1)
+        tol[:, heads] = rel[..., None] * torch.einsum("cgn,nd->cgd", w, vd.abs()) + step[..., None]
+    return out, tol
+
+
+def check_far(kv, qlen, G, D, page, edit, window=0, dtype=FP16):
+    H, need = 2, -(-kv // page)
+    cache, table = new_cache(need + 1, H, page, D, seed=kv + G), page_table([need], need + 1, seed=kv + G)
+    q = randn(qlen, G * H, D, g=gen(kv + G), std=1.0).to(dtype)
+    edit(cache, table[0].long().to(DEV), q)
+    got = cache.attention(q, table.to(DEV), i32([kv]), cu_q=None if qlen == 1 else i32([0, qlen]), max_q=qlen, window=window)
+    ref, tol = far_reference(q, cache, table, kv, qlen, window, D ** -0.5)
+    close(got, ref, tol + ref.abs() * U[dtype] + TINY[dtype])
+
+
+FAR_SHAPES = [(8192, 1, 4, 128, 64, 0), (500, 1, 8, 64, 16, 0), (8192, 1, 16, 128, 64, 0), (3000, 4, 4, 128, 16, 0),
+              (3000, 40, 4, 128, 64, 0), (8192, 100, 4, 128, 64, 0), (900, 300, 2, 64, 128, 0), (2000, 8, 2, 128, 16, 300),
+              (2000, 200, 4, 128, 16, 300), (4000, 30, 8, 64, 32, 700)]
+
+
+@pytest.mark.parametrize("log2", [16, 20, 24, 45, 70])
+@pytest.mark.parametrize("kv, qlen, G, D, page, window", FAR_SHAPES)
+def test_attention_keeps_its_precision_beside_a_page_with_a_large_scale(kv, qlen, G, D, page, window, log2):
+    """One page has a scale of V 2^log2 times the others' and weights that leave it next to no share in any row."""
+    def edit(cache, pages, q):
+        q[..., 0] = 12.0 * 2.0 ** 6
+        cache.k[..., 0] = 0
+        at = pages[min(len(pages) - 1, (kv - qlen) // page - 1)]  # before the last query tokens; the window leaves it to some
+        cache.k[at, :, :, 0] = -100  # scores about 100 octaves below the others'
+        cache.k_scale[at] = 0.02
+        cache.v_scale[at] *= 2.0 ** log2
+        cache.v_scale /= 64
+    check_far(kv, qlen, G, D, page, edit, window=window)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.01, 1e-8])
+@pytest.mark.parametrize("log2", [16, 24, 70])
+@pytest.mark.parametrize("kv, qlen, G, D, page, window", FAR_SHAPES)
+def test_attention_keeps_its_precision_beside_large_zero_and_negative_scales(kv, qlen, G, D, page, window, log2, scale):
+    def edit(cache, pages, q):
+        q[..., 0] = 12.0 * 2.0 ** 6
+        cache.k[..., 0] = 0
+        cache.k[pages[1], :, :, 0] = -100
+        cache.k_scale[pages[1]] = 0.02
+        cache.v_scale[pages[1]] *= 2.0 ** log2
+        cache.v_scale[pages[2::5]] = scale
+        cache.v_scale /= 64
+    check_far(kv, qlen, G, D, page, edit, window=window)
+
+
+@pytest.mark.parametrize("nats", [16, 18, 22])
+@pytest.mark.parametrize("kv, qlen, G, D, page, window", FAR_SHAPES)
+def test_attention_keeps_its_precision_beside_a_dominant_key_of_zero_value(kv, qlen, G, D, page, window, nats):
+    """What remains of such a row comes from weights of 2^-23 to 2^-32 of the largest, where fp16 still has steps."""
+    def edit(cache, pages, q):
+        q[:] = q / 4
+        q[..., 0] = 2.0
+        cache.k[..., 0] = 0
+        cache.k_scale.fill_(0.01)
+        cache.k_scale[pages[0]] = nats * D ** 0.5 / 2.0 / 100
+        cache.k[pages[0], :, 3:] = 0
+        cache.k[pages[0], :, 3] = 0
+        cache.k[pages[0], :, 3, 0] = 100
+        cache.v[pages[0], :, 3] = 0
+    check_far(kv, qlen, G, D, page, edit, window=window)
+
+
+def test_attention_of_scales_at_the_ends_of_fp32():
+    """Large scales in some pages, small ones in others, for both kernels: outputs as in fp32."""
+    for kv, qlen, G in ((700, 1, 4), (700, 90, 4), (40000, 1, 4), (9000, 100, 2)):
+        for lo, hi in ((-70, 60), (-20, 100), (-100, -80)):
+            def edit(cache, pages, q):
+                r = torch.randint(lo, hi, cache.v_scale.shape, device=DEV, generator=gen(kv + hi)).float()
+                cache.v_scale *= torch.exp2(r)
+            check_far(kv, qlen, G, 128, 64, edit, dtype=BF16)
