@@ -1,0 +1,31 @@
+"""What of the decoder-layer operators' edges shows without a GPU."""
+import os
+import re
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "moe_expert_ffn_dispatch_gb300", "csrc")
+
+
+def test_bounded_waits_of_the_chunk_kernel_have_one_answer_for_a_warp():
+    """A wait that gives up ends its warp's role.  If lanes decided alone, one could pass the barrier in the poll in
+    which its neighbour gives up, go on, and stand at the next warp-wide operation for ever, the neighbour being at the
+    kernel's last barrier.  So every wait asks all lanes, at once or before any lane can leave or meet the others; the
+    one after the last role, whose answer nobody takes, is the exception."""
+    src = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "kv_attention_chunk.cu")).read())
+    calls = [m.start() for m in re.finditer(r"\bmbar_(wait_bounded|try_wait)\s*\(", src)]
+    assert calls
+    alone = []
+    for at in calls:
+        end = src.index(";", at)
+        statement = src[max(src.rfind(c, 0, at) for c in ";{}") + 1:end]
+        if "__all_sync(" in statement or re.search(r"&bar\.drain,[^;]*nullptr", statement):
+            continue
+        vote = src.find("if (!__all_sync(0xffffffffu, ok)) break;", end)
+        if not re.search(r"\bok = (moe::)?mbar_wait_bounded", statement) or vote < 0 or \
+                re.search(r"\b(break|return|continue|goto|wait|\w+_segment|pages_of_next|__\w+_sync|__sync\w+)\b", src[end:vote]):
+            alone.append(statement.strip())
+    assert alone == []
+    # and each answer is taken: no call of the voted wait stands by itself
+    assert not re.search(r"[;{}]\s*wait\(", src)
