@@ -67,9 +67,10 @@ def declare(L: ctypes.CDLL) -> None:
 
 _lib = None
 # the current device's index, and the raw handle of a device's current stream: plain
-# integers, without the objects of torch.cuda (which cost as much as a launch)
-_device_index = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# integers, without the objects of torch.cuda (which cost as much as a launch).
+# A torch without CUDA has neither, and imports this module all the same.
+_device_index = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _CONTIGUOUS = torch.contiguous_format
 
 

@@ -29,3 +29,25 @@ def test_bounded_waits_of_the_chunk_kernel_have_one_answer_for_a_warp():
     assert alone == []
     # and each answer is taken: no call of the voted wait stands by itself
     assert not re.search(r"[;{}]\s*wait\(", src)
+
+
+def test_the_package_imports_where_torch_has_no_cuda_build():
+    prog = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+import moe_expert_ffn_dispatch_gb300 as m
+x, w = torch.ones(2, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.bfloat16)
+code, scale = torch.zeros(16, 32, dtype=torch.uint8), torch.ones(16, 2, dtype=torch.bfloat16)
+for call in (lambda: m.add_rmsnorm_quant(x, w), lambda: m.w4_linear(x, code, scale),
+             lambda: m.KvCache.empty(2, 1, 16, 64, device="cpu")):
+    try:
+        call()
+    except ValueError as e:
+        assert "CUDA" in str(e), e
+    else:
+        raise AssertionError("ran without a GPU")
+print("imported")
+"""
+    out = subprocess.run([sys.executable, "-c", prog], cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0 and "imported" in out.stdout, out.stderr
