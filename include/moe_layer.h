@@ -213,7 +213,9 @@ int moe_layer_kv_attention(const moe_layer_kv_attention_args_t* args, void* work
                            void* stream);
 /* Synchronise `stream` and say whether a wait inside the last call that used
  * `workspace` gave up (MOE_ERR_DEVICE_TIMEOUT; its output is then not to be
- * used).  Every wait inside a kernel is bounded. */
+ * used).  Every wait inside a kernel is bounded.  A call without tokens or
+ * sequences does not use the workspace; one that no call has used, and whose
+ * first 256 bytes are not zero, has nothing to say. */
 int moe_layer_kv_attention_status(const void* workspace, void* stream);
 
 #ifdef __cplusplus

@@ -317,7 +317,16 @@ class KvCache:
                 raise MoeError(rc, "moe_layer_kv_attention_workspace_size")
             buf = torch.empty(nb.value + 256, dtype=torch.uint8, device=self.device)
             self._ws = buf[(-buf.data_ptr()) % 256:]
+            self._ws[:256].zero_()  # the status words: status() may come before the first attention
         return self._ws
+
+    def _workspace(self, ws: torch.Tensor) -> Tuple[int, int]:
+        """Pointer and bytes of a workspace of the caller's own."""
+        if ws.get_device() != self._index:
+            raise ValueError("workspace: on %s, expected %s" % (ws.device, self.device))
+        if not ws.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def _table(self, a, page_table: torch.Tensor) -> int:
         """Sets the page table's fields of `a`; returns the batch."""
@@ -399,20 +408,25 @@ class KvCache:
                 raise ValueError("q: %d tokens (max_q %d) for %d sequences without cu_q" % (tokens, max_q, batch))
         a.tokens, a.max_q, a.group_size, a.window, a.dtype = tokens, max_q, heads // self.kv_heads, window, code
         a.sm_scale = dim ** -0.5 if scale is None else scale
-        ws = workspace if workspace is not None else self._ws if self._ws is not None else self.workspace()
+        if workspace is not None:
+            ws_at, ws_bytes = self._workspace(workspace)
+        else:
+            ws = self._ws if self._ws is not None else self.workspace()
+            ws_at, ws_bytes = ws.data_ptr(), ws.numel()
         if out is None:
             out = torch.empty_like(q, memory_format=_CONTIGUOUS)
             a.out = out.data_ptr()
         else:
             a.out = _dense(out, "out", dtype, shape, index)
-        rc = _entry("moe_layer_kv_attention")(ctypes.byref(a), ws.data_ptr(), ws.numel(), _raw_stream(index))
+        rc = _entry("moe_layer_kv_attention")(ctypes.byref(a), ws_at, ws_bytes, _raw_stream(index))
         if rc:
             _raise(rc, "moe_layer_kv_attention")
         return out
 
     def status(self, workspace: Optional[torch.Tensor] = None) -> int:
         """Synchronises the current stream; the code of the last attention on
-        this workspace: 0, or MOE_ERR_DEVICE_TIMEOUT where a wait inside it
-        gave up."""
-        ws = self.workspace() if workspace is None else workspace
-        return _entry("moe_layer_kv_attention_status")(ws.data_ptr(), torch.cuda.current_stream(self.device).cuda_stream)
+        this workspace that had query tokens: 0, or MOE_ERR_DEVICE_TIMEOUT
+        where a wait inside it gave up.  A workspace of the caller's own has
+        to have been used by one."""
+        at = self.workspace().data_ptr() if workspace is None else self._workspace(workspace)[0]
+        return _entry("moe_layer_kv_attention_status")(at, torch.cuda.current_stream(self.device).cuda_stream)

@@ -220,3 +220,41 @@ def test_attention_of_scales_at_the_ends_of_fp32():
                 r = torch.randint(lo, hi, cache.v_scale.shape, device=DEV, generator=gen(kv + hi)).float()
                 cache.v_scale *= torch.exp2(r)
             check_far(kv, qlen, G, 128, 64, edit, dtype=BF16)
+
+
+# ------------------------------------------------------------ workspaces
+def small_attention(cache, **kw):
+    return cache.attention(torch.ones(1, 2, 64, dtype=BF16, device=DEV), i32([[0, 1]]), i32([20]), **kw)
+
+
+def test_status_of_a_handle_that_has_run_nothing():
+    full = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device=DEV)  # what the handle's memory held before
+    del full
+    cache = new_cache(4, 1, 16, 64)
+    assert cache.status() == m.MOE_OK
+    cache = new_cache(4, 1, 16, 64)
+    cache.attention(torch.ones(0, 2, 64, dtype=BF16, device=DEV), i32([[0, 1]])[:0], i32([]))
+    assert cache.status() == m.MOE_OK
+
+
+def test_status_says_that_a_wait_gave_up_until_the_next_attention():
+    """The words that a kernel leaves when a wait runs out, written by the host."""
+    for qlen, kw in ((1, {}), (40, {"cu_q": i32([0, 40]), "max_q": 40})):
+        cache = new_cache(4, 1, 16, 64)
+        ws = cache.workspace()
+        ws[:16].view(torch.int32)[1:3] = i32([1, 256])
+        assert cache.status() == m.MOE_ERR_DEVICE_TIMEOUT and cache.status(ws) == m.MOE_ERR_DEVICE_TIMEOUT
+        cache.attention(torch.ones(qlen, 2, 64, dtype=BF16, device=DEV), i32([[0, 1, 2]]), i32([45]), **kw)
+        assert cache.status() == m.MOE_OK
+
+
+def test_a_workspace_of_the_callers_own():
+    cache = new_cache(4, 1, 16, 64)
+    want, ws = small_attention(cache), torch.empty_like(cache.workspace())
+    assert torch.equal(small_attention(cache, workspace=ws), want) and cache.status(ws) == m.MOE_OK
+    assert torch.equal(small_attention(cache, workspace=ws[:ws.numel() // 4 * 4].view(torch.float32)), want)
+    for bad in (torch.empty(ws.numel(), dtype=torch.uint8), torch.empty(ws.numel(), 2, dtype=torch.uint8, device=DEV)[:, 0]):
+        with pytest.raises(ValueError):
+            small_attention(cache, workspace=bad)
+        with pytest.raises(ValueError):
+            cache.status(bad)
