@@ -298,6 +298,7 @@ class KvCache:
         self._args = c
         self._index = k.get_device()
         self._ws = None
+        self._ws_stream = 0
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
@@ -317,6 +318,7 @@ class KvCache:
                 raise MoeError(rc, "moe_layer_kv_attention_workspace_size")
             buf = torch.empty(nb.value + 256, dtype=torch.uint8, device=self.device)
             self._ws = buf[(-buf.data_ptr()) % 256:]
+            self._ws_stream = _raw_stream(self._index)
             self._ws[:256].zero_()  # the status words: status() may come before the first attention
         return self._ws
 
@@ -413,6 +415,8 @@ class KvCache:
         else:
             ws = self._ws if self._ws is not None else self.workspace()
             ws_at, ws_bytes = ws.data_ptr(), ws.numel()
+            if _raw_stream(index) != self._ws_stream:  # its memory stays until this stream is done, whatever becomes of the handle
+                ws.record_stream(torch.cuda.current_stream(index))
         if out is None:
             out = torch.empty_like(q, memory_format=_CONTIGUOUS)
             a.out = out.data_ptr()

@@ -258,3 +258,21 @@ def test_a_workspace_of_the_callers_own():
             small_attention(cache, workspace=bad)
         with pytest.raises(ValueError):
             cache.status(bad)
+
+
+def test_the_handles_workspace_outlives_it_on_a_stream_that_still_uses_it():
+    cache = new_cache(4, 1, 16, 64)
+    torch.cuda.empty_cache()  # nothing else of its size is free
+    args = torch.ones(1, 2, 64, dtype=BF16, device=DEV), i32([[0, 1]]), i32([20])
+    cache.attention(*args)  # allocates the workspace for the current stream
+    at, size, side = cache.workspace().data_ptr(), cache.workspace().numel(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)  # a few tenths of a second
+        out = cache.attention(*args)
+    assert not side.query()
+    del cache
+    taken = torch.empty(size, dtype=torch.uint8, device=DEV)
+    assert taken.data_ptr() + size <= at or taken.data_ptr() >= at + size
+    side.synchronize()
+    assert torch.isfinite(out).all()
