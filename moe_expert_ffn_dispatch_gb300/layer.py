@@ -82,6 +82,13 @@ def _entry(name: str):
     return getattr(_lib, name)
 
 
+_I32_MAX = 2 ** 31 - 1
+
+
+def _too_large(name: str, size: int):
+    raise ValueError("%s: %d does not fit 32 bits" % (name, size))
+
+
 def _raise(rc: int, name: str):
     from . import MoeError
     raise MoeError(rc, name)
@@ -164,6 +171,8 @@ def add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         with _On(x.device, stream):
             return add_rmsnorm_quant(x, weight, eps, residual, smooth, want_y, q, q_scale, residual_out, y)
     rows, hidden = shape
+    if rows > _I32_MAX or hidden > _I32_MAX:
+        _too_large("x", max(shape))
     dtype, wdtype = x.dtype, weight.dtype
     if wdtype is not dtype and wdtype is not torch.float32:
         raise TypeError("weight: dtype %s, expected %s or float32" % (wdtype, dtype))
@@ -214,6 +223,8 @@ def w4_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, zero: Opt
         raise ValueError("x and w_scale have 2 dimensions")
     m, k = shape
     n, groups = gshape
+    if m > _I32_MAX or k > _I32_MAX or n > _I32_MAX:
+        _too_large("x or w_scale", max(m, k, n))
     xcode = DTYPE_CODES.get(xdtype, 2)
     if xcode == 2:
         raise TypeError("x: dtype %s, expected bfloat16, float16 or int8" % xdtype)
@@ -267,6 +278,8 @@ class KvCache:
             raise ValueError("k and v: shapes %s and %s, expected one [num_pages, kv_heads, page_size, head_dim]" %
                              (tuple(k.shape), tuple(v.shape)))
         pages, heads, page_size, dim = k.shape
+        if max(k.shape) > _I32_MAX:
+            _too_large("k and v", max(k.shape))
         for t, name in ((k, "k"), (v, "v")):
             if t.dtype != torch.int8:
                 raise TypeError("%s: dtype %s, expected int8" % (name, t.dtype))
@@ -340,6 +353,8 @@ class KvCache:
         if page_table.get_device() != self._index:
             raise ValueError("page_table: on %s, expected %s" % (page_table.device, self.device))
         batch, pages = shape
+        if batch > _I32_MAX or pages > _I32_MAX:
+            _too_large("page_table", max(shape))
         if pages > 1 and strides[1] != 1:
             raise ValueError("page_table: the pages of a sequence must be dense")
         a.cache = self._args
@@ -359,6 +374,8 @@ class KvCache:
                 return self.append(k_new, v_new, page_table, start, cu_tokens)
         if len(shape) != 3 or shape[1] != self.kv_heads or shape[2] != self.head_dim:
             raise ValueError("k_new: shape %s, expected [tokens, %d, %d]" % (tuple(shape), self.kv_heads, self.head_dim))
+        if shape[0] > _I32_MAX:
+            _too_large("k_new", shape[0])
         a = KvAppendArgs()
         batch = self._table(a, page_table)
         a.k_new, a.k_stride = _rows(k_new, "k_new", dtype, shape, index)
@@ -396,6 +413,8 @@ class KvCache:
         if dim != self.head_dim or heads % self.kv_heads:
             raise ValueError("q: %d heads of %d do not fit %d kv heads of %d" %
                              (heads, dim, self.kv_heads, self.head_dim))
+        if tokens > _I32_MAX or heads > _I32_MAX:
+            _too_large("q", max(tokens, heads))
         a = KvAttentionArgs()
         batch = self._table(a, page_table)
         a.q, a.q_stride = _rows(q, "q", dtype, shape, index)
@@ -408,7 +427,11 @@ class KvCache:
             max_q = 1 if max_q is None else max_q
             if tokens != batch or max_q != 1:
                 raise ValueError("q: %d tokens (max_q %d) for %d sequences without cu_q" % (tokens, max_q, batch))
-        a.tokens, a.max_q, a.group_size, a.window, a.dtype = tokens, max_q, heads // self.kv_heads, window, code
+        if max_q > _I32_MAX:
+            _too_large("max_q", max_q)
+        # positions end below 2^31: a wider window sees what that sees
+        a.window = -1 if window < 0 else min(window, _I32_MAX)
+        a.tokens, a.max_q, a.group_size, a.dtype = tokens, max(max_q, 0), heads // self.kv_heads, code
         a.sm_scale = dim ** -0.5 if scale is None else scale
         if workspace is not None:
             ws_at, ws_bytes = self._workspace(workspace)

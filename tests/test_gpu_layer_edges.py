@@ -276,3 +276,26 @@ def test_the_handles_workspace_outlives_it_on_a_stream_that_still_uses_it():
     assert taken.data_ptr() + size <= at or taken.data_ptr() >= at + size
     side.synchronize()
     assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------ numbers that do not fit the C structures
+def test_numbers_past_32_bits_are_not_cut():
+    cache, table = new_cache(8, 1, 16, 64, seed=3), i32([[0, 1, 2, 3, 4, 5, 6]])
+    q = randn(30, 2, 64, g=gen(4)).to(BF16)
+    want = cache.attention(q, table, i32([100]), cu_q=i32([0, 30]), max_q=30)
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 40):
+        assert torch.equal(cache.attention(q, table, i32([100]), cu_q=i32([0, 30]), max_q=30, window=window), want)
+    for window in (-1, -2 ** 32, -2 ** 32 + 5):
+        with pytest.raises(m.MoeError):
+            cache.attention(q, table, i32([100]), cu_q=i32([0, 30]), max_q=30, window=window)
+    with pytest.raises(ValueError):
+        cache.attention(q, table, i32([100]), cu_q=i32([0, 30]), max_q=2 ** 32 + 1)
+    with pytest.raises(m.MoeError):
+        cache.attention(q, table, i32([100]), cu_q=i32([0, 30]), max_q=-2 ** 32 + 1)
+    one = torch.ones(1, 1, dtype=BF16, device=DEV)
+    with pytest.raises(ValueError):
+        m.add_rmsnorm_quant(one.expand(2 ** 32 + 5, 1), one[0])
+    with pytest.raises(ValueError):
+        m.w4_linear(one.expand(2 ** 32 + 5, 64), torch.zeros(16, 32, dtype=torch.uint8, device=DEV), one.expand(16, 1).contiguous())
+    with pytest.raises(ValueError):
+        cache.attention(q[:1], table[:, :1].expand(1, 2 ** 32 + 5), i32([16]))
