@@ -114,7 +114,8 @@ int moe_layer_w4_linear(const moe_layer_w4_args_t* args, void* stream);
  * aligned, page and head strides in elements (multiples of 16), and the scales
  * fp32 [num_pages, kv_heads] with a page stride (heads contiguous).
  * Row b of page_table ([batch, max_pages] int32, row stride table_stride)
- * lists the pages of sequence b in order; entries past its length are not read.
+ * lists the pages of sequence b in order; entries past its length are not read
+ * (without any, max_pages is 0 and page_table may be NULL: no keys).
  * page_size: 16, 32, 64 or 128; head_dim: 64 or 128; 1 <= kv_heads <= 1024;
  * 0 <= batch <= 4096. */
 typedef struct {

@@ -110,7 +110,7 @@ int moe_layer_kv_attention(const moe_layer_kv_attention_args_t* a, void* workspa
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (a->window < 0 || std::isnan(a->sm_scale)) return MOE_ERR_INVALID_ARG;
   if (a->tokens == 0 || a->batch == 0) return MOE_OK;
-  if (!a->q || !a->out || !a->page_table || !a->seq_lens || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!a->q || !a->out || (!a->page_table && a->max_pages > 0) || !a->seq_lens || !workspace) return MOE_ERR_INVALID_ARG;
   if (!a->cu_q && (a->tokens != a->batch || a->max_q != 1)) return MOE_ERR_INVALID_ARG;
   const int64_t row = static_cast<int64_t>(a->cache.kv_heads) * a->group_size * a->cache.head_dim;
   if (a->q_stride < row || a->table_stride < a->max_pages) return MOE_ERR_INVALID_ARG;

@@ -299,3 +299,17 @@ def test_numbers_past_32_bits_are_not_cut():
         m.w4_linear(one.expand(2 ** 32 + 5, 64), torch.zeros(16, 32, dtype=torch.uint8, device=DEV), one.expand(16, 1).contiguous())
     with pytest.raises(ValueError):
         cache.attention(q[:1], table[:, :1].expand(1, 2 ** 32 + 5), i32([16]))
+
+
+@pytest.mark.parametrize("qlen, G", [([1, 1, 1], 4), ([1, 1, 1], 16), ([3, 0, 40], 4), ([2, 1, 5], 1)])
+def test_a_page_table_without_pages(qlen, G):
+    """No sequence of the batch has a key yet: nothing is written, and attention gives zeros."""
+    cache, table = new_cache(4, 2, 16, 64, seed=8), torch.empty(3, 0, dtype=torch.int32, device=DEV)
+    before = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    q = randn(sum(qlen), 2 * G, 64, g=gen(9)).to(BF16)
+    cu = None if qlen == [1, 1, 1] else cum(qlen)
+    out = cache.attention(q, table, i32([0, 0, 7]), cu_q=cu, max_q=max(qlen), out=torch.full(q.shape, 7.0, dtype=BF16, device=DEV))
+    assert (out == 0).all()
+    cache.append(q[:, :2], q[:, :2], table, i32([0, 0, 0]), cu_tokens=cu)
+    for a, b in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+        assert torch.equal(a, b)
