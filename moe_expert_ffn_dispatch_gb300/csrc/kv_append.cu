@@ -135,6 +135,14 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const moe_layer_kv_a
         *reinterpret_cast<uint2*>(codes + (lo + i / kRowChunks) * D + (i % kRowChunks) * 8) = make_uint2(o[0], o[1]);
       }
     }
+    if (__builtin_expect(to < 0x1p-126f, 0)) {
+      // a held page's scale can be so small that its inverse is coarse or infinite: no code of -128 even so
+#pragma unroll 1
+      for (int i = tid; i < chunks; i += THREADS) {
+        uint2* at = reinterpret_cast<uint2*>(codes + (lo + i / kRowChunks) * D + (i % kRowChunks) * 8);  // this thread's own
+        *at = make_uint2(__vmaxs4(at->x, 0x81818181u), __vmaxs4(at->y, 0x81818181u));
+      }
+    }
     if (tid == 0) (kv ? a.cache.v_scale : a.cache.k_scale)[scale_at] = to;
   }
 }

@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 }
 
 // four fp32 -> int8 codes of one word, round half to even; NaN gives 0.  The
-// conversion saturates at -128 and 127; the callers' values are quotients by
-// amax / 127 and stay within 127.0001 of zero, so -128 does not occur.
+// conversion saturates at -128 and 127; quotients by amax / 127 stay within
+// 127.0001 of zero, so -128 does not occur where that quotient is a normal number.
 __device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d) {
   uint32_t hi, r;
   asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(__float2int_rn(d)), "r"(__float2int_rn(c)), "r"(0));

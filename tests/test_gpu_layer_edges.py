@@ -313,3 +313,17 @@ def test_a_page_table_without_pages(qlen, G):
     cache.append(q[:, :2], q[:, :2], table, i32([0, 0, 0]), cu_tokens=cu)
     for a, b in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ codes
+@pytest.mark.parametrize("size", [1e-36, 3e-37, 1e-38, 2e-40])
+def test_append_of_the_smallest_numbers_to_a_held_page_gives_codes_of_127_at_most(size):
+    """A page that holds tokens of zeros only has a scale of 0, and takes the new tokens' scale without a floor."""
+    cache = m.KvCache.empty(2, 1, 16, 64)
+    g = gen(10)
+    k, v = ((torch.rand(5, 1, 64, device=DEV, generator=g) - 0.5).sign() * size for _ in "kv")
+    k, v = k.to(BF16), v.to(BF16)
+    cache.append(k, v, i32([[1]]), i32([4]), cu_tokens=i32([0, 5]))
+    for code, x in ((cache.k, k), (cache.v, v)):
+        new = code[1, 0, 4:9].int()
+        assert int(code.min()) >= -127 and (new.sign() == x[:, 0].sign()).all() and (code[1, 0, :4] == 0).all()
