@@ -16,7 +16,8 @@
 // below the largest, which keep a step of 2^-28 of it: nothing that an fp32
 // sum over them can tell.  Products are exact, a group's sum is one fp32
 // accumulator chain and enters the row's sum through an fp32 fma with the
-// group's scale and the power of two.
+// group's scale and the power of two.  X and the row's sum are held times 2^-16,
+// so that neither passes fp32 where x and y do not.
 //
 // Bound by the weights' bytes, and close behind by instructions (about 140 a KB
 // of weights at one row, 180 at 16): 130001 x 4096 takes 54 us for one row (5.0
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
   for (int i = 0; i < kStages - 1; ++i) issue();
 
   // Scales and zeros come 8 groups at a time: lane t of a quad loads groups 2t
-  // and 2t + 1 of rows g and g + 8, one block ahead, and lays scale x 2^16 and
+  // and 2t + 1 of rows g and g + 8, one block ahead, and lays scale and
   // -scale x zero out as [group][g][row] for one 16-byte read a group.
   uint32_t sraw[2][2], zraw[2][2] = {{8u, 8u}, {8u, 8u}};
   int64_t s_row0 = 0, s_row1 = 0;
@@ -261,8 +262,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
             const float2 h = unpack2<X>(w[j]);
             f[2 * j] = h.x, f[2 * j + 1] = h.y;
           }
-          sum = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
-                          __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
+          // times 2^-16, as all sums are: no x that fp32 holds makes one pass it on the way
+          sum = __fadd_rn(__fadd_rn(__fmaf_rn(f[0], 0x1p-16f, __fmul_rn(f[1], 0x1p-16f)), __fmaf_rn(f[2], 0x1p-16f, __fmul_rn(f[3], 0x1p-16f))),
+                          __fadd_rn(__fmaf_rn(f[4], 0x1p-16f, __fmul_rn(f[5], 0x1p-16f)), __fmaf_rn(f[6], 0x1p-16f, __fmul_rn(f[7], 0x1p-16f))));
           const float up = pow2(8 - e), up16 = pow2(4 - e);
           x.x = pack2<__half>(__fmul_rn(f[0], up), __fmul_rn(f[4], up));
           x.y = pack2<__half>(__fmul_rn(f[1], up16), __fmul_rn(f[5], up16));
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         if (k8 < n8) {
           if (lane % (16 / GPS) == 0) {
             float* at = sums + (k8 / (16 / GPS)) * (M * 2);
-            at[0] = sum;
+            at[0] = kInt8 ? __fmul_rn(sum, 0x1p-16f) : sum;
             at[2] = pow2(e);
           }
           // block k8 of a step belongs to lane xt, word xj: it is read as block 4 xj + xt
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
         for (int i = 0; i < 2; ++i) {
           const float v0 = scale_value(sraw[0][i], a.scale_dtype), v1 = scale_value(sraw[1][i], a.scale_dtype);
           *reinterpret_cast<float4*>(mine + ((2 * t + i) * 8 + g) * 4) =
-              make_float4(v0 * 0x1p16f, v1 * 0x1p16f, -__fmul_rn(v0, static_cast<float>(zraw[0][i])),
+              make_float4(v0, v1, -__fmul_rn(v0, static_cast<float>(zraw[0][i])),
                           -__fmul_rn(v1, static_cast<float>(zraw[1][i])));
         }
         // the next block: of this run, of the next piece, or of the next tile
@@ -395,6 +397,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) w4_linear_kernel(const W4Param
       }
     }
     auto store = [&](int m, int n, float y) {
+      y = __fmul_rn(y, 0x1p16f);
       if (a.x_scale) y = __fmul_rn(y, __ldg(a.x_scale + m0 + m));
       const int64_t at = static_cast<int64_t>(m0 + m) * a.n + n;
       if (a.out_dtype == MOE_LAYER_FP32) static_cast<float*>(a.y)[at] = y;

@@ -10,8 +10,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import moe_expert_ffn_dispatch_gb300 as m  # noqa: E402
-from test_gpu_layer_ops import (BF16, DEV, FP16, TINY, U, attention_reference, close, gen, new_cache, page_table,  # noqa: E402
-                                randn)
+from test_gpu_layer_ops import (BF16, DEV, F32, FP16, TINY, U, attention_reference, check_w4, close, gen,  # noqa: E402
+                                new_cache, page_table, randn, w4_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -327,3 +327,28 @@ def test_append_of_the_smallest_numbers_to_a_held_page_gives_codes_of_127_at_mos
     for code, x in ((cache.k, k), (cache.v, v)):
         new = code[1, 0, 4:9].int()
         assert int(code.min()) >= -127 and (new.sign() == x[:, 0].sign()).all() and (code[1, 0, :4] == 0).all()
+
+
+# ------------------------------------------------------------ 4-bit products of large and small rows
+@pytest.mark.parametrize("size", [1e30, 1e36, 3e37, 1e-25])
+@pytest.mark.parametrize("M, N, K, group, zero", [(1, 40, 128, 32, True), (8, 200, 1024, 64, False), (16, 64, 4096, 128, True),
+                                                  (20, 33, 16384, 128, False)])
+def test_w4_rows_of_any_size_that_fp32_holds(M, N, K, group, zero, size):
+    """Sums of x times scale that fp32 holds are found, though x alone, or x times its power of two, passes it."""
+    code, w, ws, z, x, _ = w4_case(M, N, K, group, BF16, M + K, zero=zero)
+    x = (x.float() * size).to(BF16)
+    x[0, ::7] *= 2.0 ** -6
+    ws = (ws.float() * 2.0 ** -14).to(BF16)
+    check_w4(code, ws, z, x, None, m.w4_linear(x, w, ws, zero=z, out_dtype=F32))
+    check_w4(code, ws, z, x, None, m.w4_linear(x, w, ws, zero=z))
+
+
+@pytest.mark.parametrize("sdtype", [BF16, FP16, F32])
+@pytest.mark.parametrize("M, N, K, group", [(1, 40, 64, 32), (8, 200, 4096, 64), (13, 77, 1024, 128), (40, 30, 8320, 64)])
+def test_w4_int8_rows_in_every_output_type(M, N, K, group, sdtype):
+    code, w, ws, z, x, xs = w4_case(M, N, K, group, BF16, 7 * M + N, x8=True, zero=True, sdtype=sdtype)
+    xs = xs * 2.0 ** -10  # outputs of a few hundred, which fp16 holds
+    for out in (BF16, FP16, F32):
+        got = m.w4_linear(x, w, ws, zero=z, x_scale=xs, out_dtype=out)
+        assert got.dtype == out
+        check_w4(code, ws, z, x, xs, got)
