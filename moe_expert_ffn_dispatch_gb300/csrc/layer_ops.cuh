@@ -62,18 +62,6 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 
 constexpr float kAmaxFloor = 1e-4f;  // floor of an amax before 127 / amax, as in the block's quant
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-
 // two 16-bit elements of one 32-bit word, widened
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w);
