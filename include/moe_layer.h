@@ -169,25 +169,28 @@ int moe_layer_kv_append(const moe_layer_kv_append_args_t* args, void* stream);
 /* Attention over the cache.  Sequence b has the query tokens cu_q[b] ..
  * cu_q[b + 1] - 1 (token b alone when cu_q is NULL), qlen of them, and
  * seq_lens[b] keys, its query tokens' own (already appended) among them.
- * Query token j stands at position p = seq_lens[b] - qlen + j (for every qlen) and sees the keys i with
- * 0 <= i <= p, and i > p - window where window > 0.  Query head
- * n uses kv head n / group_size:
+ * Query token j stands at position p = seq_lens[b] - qlen + j (whatever max_q
+ * is) and sees the keys i with 0 <= i <= p, and i > p - window where window > 0.
+ * Query head n uses kv head n / group_size:
  *   out[t, n] = sum_i softmax_i(sm_scale * <q[t, n], key_i>) * value_i
  * and zeros where no key is seen.  Keys on a page-table entry outside [0,
- * num_pages) are not seen; a scale that is not finite reaches only the query tokens
- * that see a key of its page, whose outputs are then not finite, and so does an element of q its row;
- * lengths are held to [0, max_pages * page_size].
+ * num_pages) are not seen.  A scale that is not finite reaches only the query
+ * tokens that see a key of its page, whose outputs are then not finite; an element
+ * of q that is not, its row.  Lengths are held to [0, max_pages * page_size].
  * q: [tokens, kv_heads * group_size, head_dim] of `dtype` (BF16 or FP16), token stride
  * q_stride (a multiple of 8), heads dense, 16-byte aligned.  out: the same
- * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the largest
- * number of query tokens of a sequence (1 without cu_q); a larger one in cu_q
- * leaves that sequence's tokens past the first max_q unwritten and the others as they are.
- * Scores, softmax statistics and sums are fp32.  For the product with the
- * values a softmax weight times its page's scale of V is rounded to fp16: 11 bits
- * down to 2^-21 of the row's largest such product, below that a step of 2^-31
- * of it (for scales that lie within 2^64 of one another).  Query rows are fp16 too, after a power of two a row: elements below
- * 2^-14 (fp16) or 2^-17 (bf16) of the row's largest keep a step of 2^-24 of it.  Where max_q *
- * group_size is 64 or more the products run on the tensor memory units.
+ * shape and type, dense, 16-byte aligned.  1 <= group_size <= 128.  max_q: the
+ * largest number of query tokens of a sequence (1 without cu_q); a larger one in
+ * cu_q leaves that sequence's tokens past the first max_q unwritten and the others
+ * as they are.
+ * Scores, softmax statistics and sums are fp32, exponentials and logarithms
+ * (base 2) good to about 2^-22.  For the product with the values a softmax weight
+ * times its page's scale of V is rounded to fp16: 11 bits down to 2^-21 of the
+ * row's largest such product, below that a step of 2^-31 of it (for scales that lie
+ * within 2^64 of one another).  Query rows are fp16 too, after a power of two a
+ * row: elements below 2^-14 (fp16) or 2^-17 (bf16) of the row's largest keep a
+ * step of 2^-24 of it.  Where max_q * group_size is 64 or more the products run on
+ * the tensor memory units.
  * workspace: moe_layer_kv_attention_workspace_size bytes, 256-byte aligned,
  * no initial content needed; calls that share one must be ordered. */
 typedef struct {

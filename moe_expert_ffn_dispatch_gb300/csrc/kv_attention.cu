@@ -9,7 +9,7 @@
 // Whole units, where a table or the window is short: a cluster of 8, 4, 2 or 1 CTAs, as many
 // as let all units run at once, takes a unit, deals its slices out to the
 // warps and joins them over distributed shared memory.  One launch: 1 context
-// of 1009 tokens 5.4 us (the other form 9.3), 64 of 500 15 (23), 256 of 100 21
+// of 1009 tokens 5.2 us (the other form 9.3), 64 of 500 14.3 (23), 256 of 100 20
 // (32).
 //
 // A schedule, where tables are long, for then one context may be far longer
@@ -19,8 +19,8 @@
 // last unit that it meets can be shared with other CTAs.  Those leave (row
 // reference, row sum, unnormalised output) in the workspace, and a second
 // kernel joins them in CTA order.  64 contexts, one of 2000 tokens and the others
-// of 50: 13 us (whole units 28); from 768 keys a CTA on the whole form loses on
-// such lengths and wins on even ones (64 of 2000: 46 us for 53).
+// of 50: 12.6 us (whole units 28); from 768 keys a CTA on the whole form loses on
+// such lengths and wins on even ones (64 of 2000: 46 us for 52).
 //
 // Within a CTA each of 4 warps streams its own 16-token slices of keys and
 // values through a ring of asynchronous copies and keeps a running softmax of
@@ -32,8 +32,9 @@
 // m16n8k16, fp32 accumulators): tokens and channels are the 16-wide M side, 8
 // query rows the N side, so 8 rows fill what they occupy (with rows on the M
 // side the same kernel took 84 us where this one takes 68).  The weights turn
-// from one layout into the other by movmatrix.  The tensor-memory product would
-// pad 8 rows to 128 and stage every operand through shared memory as fp16.
+// from one layout into the other by movmatrix.  (The same shape on the
+// tensor-memory product, keys as its 128-wide side and 8 rows as N, has not been
+// built: each code would still be converted here, and written to tensor memory.)
 //
 // Arithmetic: the int8 codes become exact fp16 (a byte set into the mantissa
 // of 1024, minus 1152).  A query row is scaled by a power of two to [1, 2) at
@@ -48,8 +49,11 @@
 // same sum.
 //
 // Bound by the cache's bytes at 8 rows (two contexts of 200003 and 100000
-// tokens, 8 kv heads of 128, 4 rows each: 101 us, 6.1 TB/s of 6.8), by
-// instructions at 16 (64 contexts of 2000 tokens: 76 us, 3.5 TB/s).
+// tokens, 8 kv heads of 128, 4 rows each: 100 us, 6.1 TB/s of 6.8; heads of 64:
+// 59 us, 5.2 TB/s), by instructions at 16 (64 contexts of 2000 tokens: 77 us, 3.4
+// TB/s).  More rows than 16 take more units, which convert every key again: 16
+// contexts of 4000 tokens with 2 query tokens of 4 rows 32 us, with 4 46, with 8
+// 70.
 #include <climits>
 
 #include "kv_attention.cuh"
@@ -67,12 +71,16 @@ constexpr int kCtasPerSm = NR == 1 ? 4 : 3;
 template <int NR>
 constexpr int kStagesOf = NR == 1 ? 3 : 4;
 constexpr int kMaxSlots = 4096;                  // CTAs of a launch (at most 4 an SM)
-// what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces
+// what a unit costs beside its pieces (its queries, a cold ring, the join of the warps), in pieces.  64 ragged
+// contexts with 0, 2, 4 or 8: 69, 36.9, 33.8 and 36.8 us; 64 even ones of 2000 tokens 53.0, 52.4, 52.1 and 51.6.
 constexpr int kUnitCost = 4;
 // A cluster of CTAs takes a whole unit where the table (or the window) leaves no more keys than this for each of them
 constexpr int kWholeKeys = 768;
 constexpr int kWholeUnits = 1 << 20;  // a grid's size stays far below 2^31
-// query rows of a kv head (the longest sequence's) from which the tensor-memory kernel takes over
+// Query rows of a kv head (the longest sequence's) from which the tensor-memory kernel takes over.  Its time
+// hardly depends on them up to 128, this kernel's grows with every 16.  us here / there at 32, 48, 64, 96 and 128
+// rows: 16 contexts of 4000 tokens 70/91, 95/92, 118/93, 166/95, 212/97; 64 of 500 39/73, 57/74, 72/76, 105/78,
+// 135/83; 4 of 2000 19/28, 19/29, 32/29, 39/30, 46/30; 1 of 4000 15/24, 15/24, 19/25, 19/26, 30/27.
 constexpr int kChunkFrom = 64;
 
 // position of channel chunk `c` (16 bytes) of token row `r` in a slice of [16][D] bytes

@@ -16,15 +16,17 @@
 // each.  Keys lie [key][channel] in both operands; V's is the transposed
 // (channel-contiguous) form.  The arithmetic of the weights is that of the
 // kernel for few rows: row scaled by a power of two, page scale of K in the
-// score, page scale of V in the weight.  The rows'
-// references move by whole powers of two, and only when a weight would pass
-// fp16's range, so that S is read once: weights of the same piece that are already
-// written move with the reference (exactly, but for those that become subnormal).
+// score, page scale of V in the weight.  The rows' references move by whole
+// powers of two, and only when a weight would pass what fp16 is to hold, so that S
+// is read once: weights of the same piece that are already written move with the
+// reference (exactly, but for those that become subnormal).
 //
 // Bound by a tile's chain (S, weights, O: about 5000 cycles a piece, of which the
 // products are 1100) at 42 % of the issue slots; two tiles overlap, a third has
 // no room in tensor memory.  8 chunks of 512 tokens over 8192 keys (32 heads on
-// 8, channels 128): 622 us, 856 TFLOP/s.
+// 8, channels 128): 632 us, 843 TFLOP/s; channels 64: 534 us, 499 TFLOP/s.  A unit
+// of fewer than 256 rows pays for 128 or 256: 16 contexts of 4000 keys and 64 rows
+// take 94 us, with 256 rows 119.
 #include "kv_attention.cuh"
 
 #include "device_prims.cuh"
@@ -33,13 +35,13 @@ namespace moe_layer {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 4;  // in pieces; with 0, 2, 4 or 8 chunks of 512 tokens over 5011 take 163, 102, 95 and 105 us
 constexpr int kSoftWarps = 8, kConvWarps = 8, kWarpMma = kSoftWarps + kConvWarps;
 constexpr int kThreads = (kSoftWarps + kConvWarps + 4) * 32;  // warps in fours, which share a register limit
 // Registers a thread: 96 at launch (640 x 96 = 61440 of the SM's 65536); the
 // weights' warps take 120 once the others have gone down to 80 (256 x 120 + 256
-// x 80 + 128 x 80 = 61440).  With 96 for all the weights' warps spill: 864 us in
-// place of 633 (8 chunks of 512 tokens at 8192 keys, 32 heads on 8).
+// x 80 + 128 x 80 = 61440).  With 96 for all the weights' warps spill: 835 us in
+// place of 632 (8 chunks of 512 tokens at 8192 keys, 32 heads on 8).
 constexpr int kSoftRegs = 120, kConvRegs = 80, kMmaRegs = 80;
 static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "the split fits what the launch has");
 constexpr int kConvThreads = kConvWarps * 32;

@@ -20,19 +20,21 @@
 // so that neither passes fp32 where x and y do not.
 //
 // Bound by the weights' bytes, and close behind by instructions (about 140 a KB
-// of weights at one row, 180 at 16): 130001 x 4096 takes 54 us for one row (5.0
-// TB/s of 6.8), 57 for 8, 74 for 16; 4096 x 4096 for one row 6 us, of which a
-// launch and the first trip to memory are 3.6.  On the tensor-memory product
-// every weight would go through shared memory as fp16, four times the bytes
-// that registers take here.  A CTA has 16
+// of weights at one row, 180 at 16): 130001 x 4096 takes 55 us for one row (4.9
+// TB/s of 6.8), 57 for 8, 74 for 16; groups of 32, with four times the scales and
+// fp32 steps, 97 for 8 rows.  4096 x 4096 for one row 6 us, of which a
+// launch and the first trip to memory are 3.6.  Every 16 rows of x read the
+// weights again: 6144 x 4096 takes 12 us for 16 rows, 34 for 64, 244 for 512 and
+// 1920 for 4096.  The tensor-memory product, with weights converted into tensor
+// memory as its M side, has not been built here; it is what many rows would need.  A CTA has 16
 // warps in WR groups of rows x (16 / WR) parts of K; a warp streams its own
 // 16-row tiles through a ring of 128-k steps by asynchronous copies, which
 // needs no barrier.  One part of K is written straight from the accumulators;
 // several are summed in shared memory, in a fixed order.  Where tiles are
 // few or a CTA's shared memory does not hold x (8 rows beyond k 8192, 16 beyond
 // 4096), a cluster of up to 8 CTAs shares K, so that each lays out its part of x
-// alone, and sums over distributed shared memory: 16 x 4096 x 14336 19 us, where
-// CTAs that took x in pieces took 38; 64 x 8000 x 16384 114 (186).
+// alone, and sums over distributed shared memory: 16 x 4096 x 14336 18 us, where
+// CTAs that took x in pieces took 38; 64 x 8000 x 16384 113 (186).
 //
 // k order.  Both operands may take the k of a group in any common order.  A
 // lane takes neighbouring words of a weight row, as many as the group allows
