@@ -310,8 +310,7 @@ class KvCache:
         c.num_pages, c.kv_heads, c.page_size, c.head_dim = pages, heads, page_size, dim
         self._args = c
         self._index = k.get_device()
-        self._ws = None
-        self._ws_stream = 0
+        self._ws, self._ws_at, self._ws_stream = None, (0, 0), 0
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
@@ -331,7 +330,7 @@ class KvCache:
                 raise MoeError(rc, "moe_layer_kv_attention_workspace_size")
             buf = torch.empty(nb.value + 256, dtype=torch.uint8, device=self.device)
             self._ws = buf[(-buf.data_ptr()) % 256:]
-            self._ws_stream = _raw_stream(self._index)
+            self._ws_at, self._ws_stream = (self._ws.data_ptr(), self._ws.numel()), _raw_stream(self._index)
             self._ws[:256].zero_()  # the status words: status() may come before the first attention
         return self._ws
 
@@ -430,22 +429,24 @@ class KvCache:
         if max_q > _I32_MAX:
             _too_large("max_q", max_q)
         # positions end below 2^31: a wider window sees what that sees
-        a.window = -1 if window < 0 else min(window, _I32_MAX)
-        a.tokens, a.max_q, a.group_size, a.dtype = tokens, max(max_q, 0), heads // self.kv_heads, code
+        a.window = -1 if window < 0 else window if window <= _I32_MAX else _I32_MAX
+        a.tokens, a.max_q, a.group_size, a.dtype = tokens, max_q if max_q > 0 else 0, heads // self.kv_heads, code
         a.sm_scale = dim ** -0.5 if scale is None else scale
+        s = _raw_stream(index)
         if workspace is not None:
             ws_at, ws_bytes = self._workspace(workspace)
         else:
-            ws = self._ws if self._ws is not None else self.workspace()
-            ws_at, ws_bytes = ws.data_ptr(), ws.numel()
-            if _raw_stream(index) != self._ws_stream:  # its memory stays until this stream is done, whatever becomes of the handle
-                ws.record_stream(torch.cuda.current_stream(index))
+            if self._ws is None:
+                self.workspace()
+            ws_at, ws_bytes = self._ws_at
+            if s != self._ws_stream:  # its memory stays until this stream is done, whatever becomes of the handle
+                self._ws.record_stream(torch.cuda.current_stream(index))
         if out is None:
             out = torch.empty_like(q, memory_format=_CONTIGUOUS)
             a.out = out.data_ptr()
         else:
             a.out = _dense(out, "out", dtype, shape, index)
-        rc = _entry("moe_layer_kv_attention")(ctypes.byref(a), ws_at, ws_bytes, _raw_stream(index))
+        rc = _entry("moe_layer_kv_attention")(ctypes.byref(a), ws_at, ws_bytes, s)
         if rc:
             _raise(rc, "moe_layer_kv_attention")
         return out
