@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
                 l = __fmul_rn(l, corr);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = __fsub_rn(v[e], d);
-                const __half2 ch = __float2half2_rn(corr);
                 moe::tmem_st_wait();
 #pragma unroll 1
                 for (int x = 0; x < c; x += 32) {
@@ -398,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_chunk_kernel(const A
                   tmem_ld16(s_col + x / 2, pv);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) {
-                    const uint32_t u = __float_as_uint(pv[e]);
-                    const __half2 s = __hmul2(*reinterpret_cast<const __half2*>(&u), ch);
-                    w[e] = *reinterpret_cast<const uint32_t*>(&s);
+                    // (in fp32, as fp16 has no 2^-25: a weight of 2^15 outlives a step of 39)
+                    const float2 f = unpack2<__half>(__float_as_uint(pv[e]));
+                    w[e] = pack2<__half>(__fmul_rn(f.x, corr), __fmul_rn(f.y, corr));
                   }
                   tmem_st16(s_col + x / 2, w);
                   moe::tmem_st_wait();

@@ -352,3 +352,21 @@ def test_w4_int8_rows_in_every_output_type(M, N, K, group, sdtype):
         got = m.w4_linear(x, w, ws, zero=z, x_scale=xs, out_dtype=out)
         assert got.dtype == out
         check_w4(code, ws, z, x, xs, got)
+
+
+@pytest.mark.parametrize("nats", [10, 17, 18, 20])
+@pytest.mark.parametrize("kv, qlen, G, D, page, window", FAR_SHAPES)
+def test_attention_keeps_the_weights_of_keys_before_a_dominant_one(kv, qlen, G, D, page, window, nats):
+    """The dominant key, of no value, comes late in its 128 keys: what lies before it moves with the reference."""
+    def edit(cache, pages, q):
+        at = (kv - qlen) // 128 * 128 - 28
+        page_at, slot = pages[at // page], at % page
+        q[:] = q / 4
+        q[..., 0] = 2.0
+        cache.k[..., 0] = 0
+        cache.k_scale.fill_(0.01)
+        cache.k_scale[page_at] = nats * D ** 0.5 / 2.0 / 100
+        cache.k[page_at, :, :, 1:] = 0
+        cache.k[page_at, :, slot, 0] = 100
+        cache.v[page_at, :, slot] = 0
+    check_far(kv, qlen, G, D, page, edit, window=window)
