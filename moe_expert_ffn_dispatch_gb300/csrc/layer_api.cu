@@ -9,6 +9,8 @@ namespace {
 bool at(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool act(int32_t dt) { return dt == MOE_LAYER_BF16 || dt == MOE_LAYER_FP16; }
 
+constexpr int32_t kMostRows = 2147483647 - (1 << 20);
+
 int done(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // SM count of the current device, asked once a device; 0 if it cannot be asked
@@ -60,7 +62,8 @@ int moe_layer_w4_linear(const moe_layer_w4_args_t* a, void* stream) {
   if (!a || (!act(a->x_dtype) && a->x_dtype != MOE_LAYER_INT8) || (!act(a->out_dtype) && a->out_dtype != MOE_LAYER_FP32) ||
       (!act(a->scale_dtype) && a->scale_dtype != MOE_LAYER_FP32))
     return MOE_ERR_INVALID_ARG;
-  if (a->m < 0 || a->m > 1000000 || a->n < 1 || a->k < 32 || a->k > 65536 || a->group < 32 ||
+  // (the last round of tiles can go 16 x 16 x SMs rows past n, and row numbers are 32 bits)
+  if (a->m < 0 || a->m > 1000000 || a->n < 1 || a->n > kMostRows || a->k < 32 || a->k > 65536 || a->group < 32 ||
       (a->group != 32 && a->group != 64 && a->group % 128) || a->k % a->group)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (a->m == 0) return MOE_OK;

@@ -51,3 +51,21 @@ print("imported")
 """
     out = subprocess.run([sys.executable, "-c", prog], cwd=ROOT, capture_output=True, text=True)
     assert out.returncode == 0 and "imported" in out.stdout, out.stderr
+
+
+def test_w4_refuses_row_numbers_that_could_pass_32_bits():
+    """The tiles of a launch go past n by up to 16 rows for each of 16 warps of every SM; a row number that wrapped
+    would pass for one below n."""
+    import ctypes
+    import moe_expert_ffn_dispatch_gb300 as m
+    from moe_expert_ffn_dispatch_gb300 import _build, layer
+    _build.build()
+    at = 1 << 20  # an aligned address that nothing reads
+    for n, code in ((2 ** 31 - 1, m.MOE_ERR_UNSUPPORTED_SHAPE), (2 ** 31 - 2 ** 20, m.MOE_ERR_UNSUPPORTED_SHAPE),
+                    (2 ** 31 - 2 ** 20 - 1, m.MOE_OK)):
+        a = layer.W4Args(x=at, w=at, w_scale=at, y=at, x_stride=256, m=0, n=n, k=256, group=128, x_dtype=0, scale_dtype=0,
+                         out_dtype=0)
+        assert m.lib().moe_layer_w4_linear(ctypes.byref(a), 0) == code
+    most = 2 ** 31 - 2 ** 20 - 1
+    past = 16 * 16 * 1024  # a thousand SMs
+    assert -(-most // 16) * 16 + past < 2 ** 31
