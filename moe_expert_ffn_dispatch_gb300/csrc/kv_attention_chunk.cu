@@ -24,9 +24,9 @@
 // Bound by a tile's chain (S, weights, O: about 5000 cycles a piece, of which the
 // products are 1100) at 42 % of the issue slots; two tiles overlap, a third has
 // no room in tensor memory.  8 chunks of 512 tokens over 8192 keys (32 heads on
-// 8, channels 128): 632 us, 843 TFLOP/s; channels 64: 534 us, 499 TFLOP/s.  A unit
+// 8, channels 128): 635 us, 839 TFLOP/s; channels 64: 539 us, 494 TFLOP/s.  A unit
 // of fewer than 256 rows pays for 128 or 256: 16 contexts of 4000 keys and 64 rows
-// take 94 us, with 256 rows 119.
+// take 94 us, with 256 rows 120.
 #include "kv_attention.cuh"
 
 #include "device_prims.cuh"
