@@ -310,7 +310,7 @@ class KvCache:
         c.num_pages, c.kv_heads, c.page_size, c.head_dim = pages, heads, page_size, dim
         self._args = c
         self._index = k.get_device()
-        self._ws, self._ws_at, self._ws_stream = None, (0, 0), 0
+        self._ws, self._ws_at, self._ws_streams = None, (0, 0), set()
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
@@ -330,7 +330,7 @@ class KvCache:
                 raise MoeError(rc, "moe_layer_kv_attention_workspace_size")
             buf = torch.empty(nb.value + 256, dtype=torch.uint8, device=self.device)
             self._ws = buf[(-buf.data_ptr()) % 256:]
-            self._ws_at, self._ws_stream = (self._ws.data_ptr(), self._ws.numel()), _raw_stream(self._index)
+            self._ws_at, self._ws_streams = (self._ws.data_ptr(), self._ws.numel()), {_raw_stream(self._index)}
             self._ws[:256].zero_()  # the status words: status() may come before the first attention
         return self._ws
 
@@ -439,8 +439,9 @@ class KvCache:
             if self._ws is None:
                 self.workspace()
             ws_at, ws_bytes = self._ws_at
-            if s != self._ws_stream:  # its memory stays until this stream is done, whatever becomes of the handle
+            if s not in self._ws_streams:  # its memory stays until this stream is done, whatever becomes of the handle
                 self._ws.record_stream(torch.cuda.current_stream(index))
+                self._ws_streams.add(s)
         if out is None:
             out = torch.empty_like(q, memory_format=_CONTIGUOUS)
             a.out = out.data_ptr()
