@@ -86,9 +86,10 @@ int moe_layer_add_rmsnorm_quant(const moe_layer_norm_args_t* args, void* stream)
  * 65536; 1 <= n < 2^31 - 2^20; 0 <= m <= 1000000.  x is held in fp16 with a
  * power of two for every 128 k of a row: exact but for elements 2^18 below the
  * largest of them, which keep a step of 2^-28 of it.  Products are exact, sums are
- * fp32, y is rounded once; elements of x and y below 2^-110 may lose bits or vanish.  A row of x that holds a NaN or an infinity gives no finite
- * value in its own row of y and touches no other.  The call is made for few
- * rows (the weights are read once for every 16 rows of x); it is right for any m. */
+ * fp32, y is rounded once; elements of x and y below 2^-110 may lose bits or
+ * vanish.  A row of x that holds a NaN or an infinity gives no finite value in its
+ * own row of y and touches no other.  The call is made for few rows (the weights
+ * are read once for every 16 rows of x); it is right for any m. */
 typedef struct {
   const void* x;
   const float* x_scale;
