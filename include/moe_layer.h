@@ -8,6 +8,14 @@
  *   moe_layer_kv_append          quantised write of new keys and values into a
  *                                paged INT8 cache, one scale a page and head
  *   moe_layer_kv_attention       attention of new tokens over that cache
+ *   moe_layer_norm_add_rmsnorm_quant  RMS norm of a block's output, gate and
+ *                                scale, residual addition, RMS norm, INT8 quant
+ *   moe_layer_w8_linear          products of INT8 codes with a scale a token and a
+ *                                scale a channel, any number of tokens
+ *   moe_layer_page_plan          a step's page table, prefix sums and slots from
+ *                                the lengths of its requests
+ *   moe_layer_token_logprobs     log probabilities of given tokens, entropy and
+ *                                the top alternatives of rows of logits
  *
  * Conventions are those of moe_fused.h: device pointers owned by the caller,
  * no device memory allocated here, work enqueued asynchronously on `stream`
@@ -222,6 +230,161 @@ int moe_layer_kv_attention(const moe_layer_kv_attention_args_t* args, void* work
  * sequences does not use the workspace; one that no call has used, and whose
  * first 256 bytes are not zero, has nothing to say. */
 int moe_layer_kv_attention_status(const void* workspace, void* stream);
+
+/* RMS norm of a block's output, its gate and scale, the residual addition, and
+ * RMS norm with INT8 quant for the next block, row t of `rows`, in fp32:
+ *   p = x[t] * (1 / sqrt(mean(x[t]^2) + eps)) * post_weight
+ *   p = p * gate[t]                     (as it is without gate)
+ *   s = residual[t] + branch_scale * p
+ *   residual_out[t] = T(s)              T: rounding to `dtype`, to nearest even
+ *   y = s * (1 / sqrt(mean(s^2) + eps)) * weight
+ * and y_out, q and q_scale of y as in moe_layer_add_rmsnorm_quant.  The second
+ * norm takes the unrounded s.  A row that holds a NaN or an infinity
+ * (in x, the residual or the gate) gets a NaN scale, so that q * q_scale is NaN,
+ * and a y by the formula (a root of infinity makes the finite ones zeros).
+ * x, residual, residual_out: [rows, hidden] of `dtype` (BF16 or FP16) with their
+ * own row strides (>= hidden); residual_out may be residual or x itself (same
+ * stride).  post_weight, weight: [hidden] of `weight_dtype` (`dtype` or FP32).
+ * gate: of `dtype`, row stride gate_stride (>= hidden), or gate_stride 0 for one
+ * [hidden] that all rows share; NULL for none.  smooth: [hidden] fp32 or NULL.
+ * y_out: [rows, hidden] of `dtype` or NULL.  q: [rows, hidden], q_scale: [rows],
+ * both given or both NULL.  y_out or q is given.  1 <= hidden <= 16384 (any
+ * number), rows >= 0.  Every pointer aligned to its element. */
+typedef struct {
+  const void* x;
+  const void* residual;
+  const void* post_weight;
+  const void* gate;
+  const void* weight;
+  const float* smooth;
+  void* residual_out;
+  void* y_out;
+  int8_t* q;
+  float* q_scale;
+  int64_t x_stride;
+  int64_t residual_stride;
+  int64_t gate_stride;
+  int64_t residual_out_stride;
+  int32_t rows;
+  int32_t hidden;
+  int32_t dtype;
+  int32_t weight_dtype;
+  float eps;
+  float branch_scale;
+} moe_layer_norm_pair_args_t;
+int moe_layer_norm_add_rmsnorm_quant(const moe_layer_norm_pair_args_t* args, void* stream);
+
+/* Products of INT8 codes, as add_rmsnorm_quant leaves them, with INT8 weights:
+ *   y[m, n] = T((float(sum over k of x[m, k] * w[n, k]) * w_scale[n]) * x_scale[m])
+ * The sum is an exact 32-bit integer whatever the sizes, so that a row of y does
+ * not depend on the rows beside it; the conversion and the two products are fp32,
+ * each rounded once, and T rounds to `out_dtype`.  A scale that is not finite
+ * gives no finite value in its own row or column (but zeros of the sum with an
+ * infinite scale are NaN) and touches no other.
+ * x: [m, k] with row stride x_stride (a multiple of 16), w: [n, k] dense, both
+ * 16-byte aligned.  x_scale: [m] fp32.  w_scale: [n] of `scale_dtype` (BF16,
+ * FP16 or FP32).  y: [m, n] of `out_dtype` (BF16, FP16 or FP32), dense.
+ * k: a multiple of 16, 16 <= k <= 65536; 1 <= n < 2^31 - 2^20; 0 <= m <= 1000000.
+ * workspace: moe_layer_w8_linear_workspace_size bytes, 256-byte aligned, no
+ * initial content needed (NULL where that is 0); calls that share one must be
+ * ordered. */
+typedef struct {
+  const int8_t* x;
+  const float* x_scale;
+  const int8_t* w;
+  const void* w_scale;
+  void* y;
+  int64_t x_stride;
+  int32_t m;
+  int32_t n;
+  int32_t k;
+  int32_t scale_dtype;
+  int32_t out_dtype;
+} moe_layer_w8_args_t;
+/* Bytes for a call of these sizes on the current device. */
+int moe_layer_w8_linear_workspace_size(int32_t m, int32_t n, int32_t k, size_t* workspace_bytes);
+int moe_layer_w8_linear(const moe_layer_w8_args_t* args, void* workspace, size_t workspace_bytes, void* stream);
+/* Synchronise `stream` and say whether a wait inside the last call that used
+ * `workspace` gave up (MOE_ERR_DEVICE_TIMEOUT; its output is then not to be
+ * used).  Only for a workspace that such a call has used. */
+int moe_layer_w8_linear_status(const void* workspace, void* stream);
+
+/* The plan of a step over a paged cache: sequence b holds held[b] tokens and
+ * gets new_tokens[b] more (negative numbers count as 0), in order behind one
+ * another in the step's buffers.
+ *   cu_tokens[b]: tokens of the sequences before b (batch + 1 of them)
+ *   seq_lens[b] = held[b] + new_tokens[b]
+ * Pages ceil(held / page_size) .. ceil(seq_len / page_size) - 1 of a sequence,
+ * up to max_pages, are new: in the order of the sequences they take the entries
+ * taken, taken + 1, ... of free_pages ([num_free], a list of unused pages; taken
+ * is read from the device, 0 where it is NULL) and are written into page_table,
+ * -1 where the list has run out.  No other entry of page_table is written.
+ *   taken_out = min(taken + new pages, num_free)
+ * Token t < min(cu_tokens[batch], tokens) belongs to sequence[t], stands at
+ * position[t] there and in slot[t] = page * page_size + position % page_size of
+ * the cache, -1 where its page is outside [0, num_pages) or its position is not
+ * inside [0, max_pages * page_size).  For t up to `tokens` all three are -1.
+ *   unplaced: how many of the first `tokens` tokens have no slot
+ * cu_tokens and seq_lens are held to 2^31 - 1.  taken_out may be taken itself.
+ * sequence, position and slot are [tokens], each NULL where it is not wanted.
+ * page_table: [batch, max_pages] with row stride table_stride.  page_size: 16,
+ * 32, 64 or 128; 0 <= batch <= 4096; batch * max_pages < 2^31; num_free >= 0;
+ * tokens >= 0.  A call without sequences still writes cu_tokens[0], taken_out
+ * and unplaced. */
+typedef struct {
+  int32_t* page_table;
+  const int32_t* held;
+  const int32_t* new_tokens;
+  const int32_t* free_pages;
+  const int32_t* taken;
+  int32_t* taken_out;
+  int32_t* unplaced;
+  int32_t* cu_tokens;
+  int32_t* seq_lens;
+  int32_t* sequence;
+  int32_t* position;
+  int64_t* slot;
+  int64_t table_stride;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t num_free;
+  int32_t tokens;
+} moe_layer_page_plan_args_t;
+int moe_layer_page_plan(const moe_layer_page_plan_args_t* args, void* stream);
+
+/* Log probabilities, row t of `rows`, l = logits[t] in fp32, M its largest:
+ *   S = sum_i exp(l_i - M)
+ *   logprob[t, j] = (l_c - M) - log S, c = tokens[t, j]
+ *   entropy[t] = log S - sum_i exp(l_i - M) (l_i - M) / S
+ *   top_id[t, r], top_logprob[t, r]: the r-th largest logit's index (the lower
+ *     index first among equals) and its log probability
+ * -inf is a logit without probability.  A token outside [0, vocab) has the log
+ * probability -inf.  A row of -inf only gives NaN values; so does one that holds
+ * a NaN or +inf, whose top_id are -1.
+ * logits: [rows, vocab] of `dtype` (BF16, FP16 or FP32), row stride >= vocab,
+ * aligned to its element.  tokens: [rows, num_tokens] int32, or int64 where
+ * tokens_64 is 1; NULL with num_tokens 0.  logprob: [rows, num_tokens] fp32.
+ * entropy: [rows] fp32 or NULL.  top_logprob fp32, top_id int32: [rows, top], NULL
+ * with top 0.  1 <= vocab < 2^31, 0 <= top <= min(32, vocab), rows >= 0.
+ * Sums are fp32, exponentials good to about 2^-22. */
+typedef struct {
+  const void* logits;
+  const void* tokens;
+  float* logprob;
+  float* entropy;
+  float* top_logprob;
+  int32_t* top_id;
+  int64_t logits_stride;
+  int32_t rows;
+  int32_t vocab;
+  int32_t num_tokens;
+  int32_t top;
+  int32_t dtype;
+  int32_t tokens_64;
+} moe_layer_logprobs_args_t;
+int moe_layer_token_logprobs(const moe_layer_logprobs_args_t* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,9 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from .layer import LAYER_EXPORTS, KvCache, add_rmsnorm_quant, declare as declare_layer, w4_linear  # noqa: F401
+from .layer import (LAYER_EXPORTS, KvCache, PagePlan, add_rmsnorm_quant, declare as declare_layer,  # noqa: F401
+                    norm_add_rmsnorm_quant, page_plan, token_logprobs, w4_linear, w8_linear, w8_linear_status,
+                    w8_linear_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_moe_fused.so")

@@ -24,6 +24,10 @@ int sm_count() {
   return n;
 }
 
+bool w8_sizes(int32_t m, int32_t n, int32_t k) {
+  return m >= 0 && m <= 1000000 && n >= 1 && n <= kMostRows && k >= 16 && k <= 65536 && k % 16 == 0;
+}
+
 int check_cache(const moe_layer_kv_cache_t& c) {
   if (!c.k || !c.v || !c.k_scale || !c.v_scale) return MOE_ERR_INVALID_ARG;
   if (c.num_pages < 1 || c.kv_heads < 1 || c.kv_heads > 1024) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -135,6 +139,96 @@ int moe_layer_kv_attention_status(const void* workspace, void* stream) {
       cudaStreamSynchronize(s) != cudaSuccess)
     return MOE_ERR_CUDA;
   return words[1] ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+}
+
+int moe_layer_norm_add_rmsnorm_quant(const moe_layer_norm_pair_args_t* a, void* stream) {
+  if (!a || !act(a->dtype) || (a->weight_dtype != a->dtype && a->weight_dtype != MOE_LAYER_FP32))
+    return MOE_ERR_INVALID_ARG;
+  if (a->rows < 0 || a->hidden < 1 || a->hidden > 16384) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!(a->eps >= 0.0f) || !std::isfinite(a->eps) || !std::isfinite(a->branch_scale)) return MOE_ERR_INVALID_ARG;
+  if (a->rows == 0) return MOE_OK;
+  if (!a->x || !a->residual || !a->post_weight || !a->weight || !a->residual_out ||
+      (a->q == nullptr) != (a->q_scale == nullptr) || (!a->q && !a->y_out))
+    return MOE_ERR_INVALID_ARG;
+  if (a->x_stride < a->hidden || a->residual_stride < a->hidden || a->residual_out_stride < a->hidden ||
+      (a->gate && a->gate_stride != 0 && a->gate_stride < a->hidden))
+    return MOE_ERR_INVALID_ARG;
+  const size_t wsize = a->weight_dtype == MOE_LAYER_FP32 ? 4 : 2;
+  if (!at(a->x, 2) || !at(a->residual, 2) || !at(a->gate, 2) || !at(a->residual_out, 2) || !at(a->y_out, 2) ||
+      !at(a->post_weight, wsize) || !at(a->weight, wsize) || !at(a->smooth, 4) || !at(a->q_scale, 4))
+    return MOE_ERR_ALIGNMENT;
+  return done(moe_layer::launch_norm_pair(*a, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_layer_w8_linear_workspace_size(int32_t m, int32_t n, int32_t k, size_t* workspace_bytes) {
+  if (!workspace_bytes) return MOE_ERR_INVALID_ARG;
+  if (!w8_sizes(m, n, k)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int sms = sm_count();
+  if (!sms) return MOE_ERR_CUDA;
+  *workspace_bytes = m ? moe_layer::w8_workspace(m, n, k, sms) : 0;
+  return MOE_OK;
+}
+
+int moe_layer_w8_linear(const moe_layer_w8_args_t* a, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!a || (!act(a->out_dtype) && a->out_dtype != MOE_LAYER_FP32) ||
+      (!act(a->scale_dtype) && a->scale_dtype != MOE_LAYER_FP32))
+    return MOE_ERR_INVALID_ARG;
+  if (!w8_sizes(a->m, a->n, a->k)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a->m == 0) return MOE_OK;
+  if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->y || a->x_stride < a->k) return MOE_ERR_INVALID_ARG;
+  if (!at(a->x, 16) || a->x_stride % 16 || !at(a->w, 16) || !at(a->x_scale, 4) ||
+      !at(a->w_scale, a->scale_dtype == MOE_LAYER_FP32 ? 4 : 2) || !at(a->y, a->out_dtype == MOE_LAYER_FP32 ? 4 : 2) ||
+      !at(workspace, 256))
+    return MOE_ERR_ALIGNMENT;
+  const int sms = sm_count();
+  if (!sms) return MOE_ERR_CUDA;
+  const size_t need = moe_layer::w8_workspace(a->m, a->n, a->k, sms);
+  if (need && !workspace) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return done(moe_layer::launch_w8(*a, workspace, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_layer_w8_linear_status(const void* workspace, void* stream) {
+  return moe_layer_kv_attention_status(workspace, stream);  // the same words
+}
+
+int moe_layer_page_plan(const moe_layer_page_plan_args_t* a, void* stream) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->batch > 4096 || a->max_pages < 0 || a->num_pages < 0 || a->num_free < 0 || a->tokens < 0 ||
+      static_cast<int64_t>(a->batch) * a->max_pages > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a->page_size != 16 && a->page_size != 32 && a->page_size != 64 && a->page_size != 128)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!a->taken_out || !a->unplaced || !a->cu_tokens ||
+      (a->batch > 0 && (!a->held || !a->new_tokens || !a->seq_lens || (a->max_pages > 0 && !a->page_table))) ||
+      (a->num_free > 0 && !a->free_pages) || (a->batch > 0 && a->table_stride < a->max_pages))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(a->page_table), static_cast<const void*>(a->held),
+                        static_cast<const void*>(a->new_tokens), static_cast<const void*>(a->free_pages),
+                        static_cast<const void*>(a->taken), static_cast<const void*>(a->taken_out),
+                        static_cast<const void*>(a->unplaced), static_cast<const void*>(a->cu_tokens),
+                        static_cast<const void*>(a->seq_lens), static_cast<const void*>(a->sequence),
+                        static_cast<const void*>(a->position)})
+    if (!at(p, 4)) return MOE_ERR_ALIGNMENT;
+  if (!at(a->slot, 8)) return MOE_ERR_ALIGNMENT;
+  return done(moe_layer::launch_page_plan(*a, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_layer_token_logprobs(const moe_layer_logprobs_args_t* a, void* stream) {
+  if (!a || (!act(a->dtype) && a->dtype != MOE_LAYER_FP32) || (a->tokens_64 != 0 && a->tokens_64 != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (a->rows < 0 || a->vocab < 1 || a->num_tokens < 0 || a->top < 0 || a->top > 32 || a->top > a->vocab)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a->rows == 0) return MOE_OK;
+  if (!a->logits || a->logits_stride < a->vocab || (a->num_tokens > 0 && (!a->tokens || !a->logprob)) ||
+      (a->top > 0 && (!a->top_logprob || !a->top_id)))
+    return MOE_ERR_INVALID_ARG;
+  if (!at(a->logits, a->dtype == MOE_LAYER_FP32 ? 4 : 2) || !at(a->tokens, a->tokens_64 ? 8 : 4) || !at(a->logprob, 4) ||
+      !at(a->entropy, 4) || !at(a->top_logprob, 4) || !at(a->top_id, 4))
+    return MOE_ERR_ALIGNMENT;
+  const int sms = sm_count();
+  if (!sms) return MOE_ERR_CUDA;
+  return done(moe_layer::launch_logprobs(*a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // Declarations and device helpers shared by the decoder-layer operators
-// (layer_api.cu checks arguments and launches; norm_quant.cu, w4_linear.cu,
-// kv_append.cu and kv_attention.cu hold the kernels).
+// (layer_api.cu checks arguments and launches; norm_quant.cu, norm_pair.cu,
+// w4_linear.cu, w8_linear.cu, kv_append.cu, kv_attention.cu, page_plan.cu and
+// token_logprobs.cu hold the kernels).
 #pragma once
 
 #include <atomic>
@@ -20,6 +21,11 @@ cudaError_t launch_w4(const moe_layer_w4_args_t& a, int num_sms, cudaStream_t s)
 cudaError_t launch_append(const moe_layer_kv_append_args_t& a, cudaStream_t s);
 size_t attention_workspace(int head_dim, int num_sms);
 cudaError_t launch_attention(const moe_layer_kv_attention_args_t& a, void* ws, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_pair(const moe_layer_norm_pair_args_t& a, cudaStream_t s);
+size_t w8_workspace(int m, int n, int k, int num_sms);
+cudaError_t launch_w8(const moe_layer_w8_args_t& a, void* ws, int num_sms, cudaStream_t s);
+cudaError_t launch_page_plan(const moe_layer_page_plan_args_t& a, cudaStream_t s);
+cudaError_t launch_logprobs(const moe_layer_logprobs_args_t& a, int num_sms, cudaStream_t s);
 
 // Lets `kernel` have `most` bytes of dynamic shared memory on the current
 // device, asking the runtime once a device and kernel (`done`: one bit a device).

@@ -1,0 +1,244 @@
+// RMS norm of a block's output, gate and scale, residual addition, RMS norm and
+// INT8 quant of the next block's input.
+//
+// Three reductions over the row (sum of squares of the block's output, of the new
+// residual, then the maximum of |z|) and one pass over memory, as norm_quant.cu
+// has it: the row stays in registers as fp32 between them, a CTA a row (a warp up
+// to 1024 wide), every load of a row's own data issued before the first use.  The
+// vectors that all rows share come from the cache when they are needed.
+// Bound by memory: 4 bytes read (6 with a gate a token) and 2 to 5 written an
+// element.
+#include "norm_rows.cuh"
+
+namespace moe_layer {
+namespace {
+
+constexpr int kMaxWarps = 16;
+constexpr int kRowWarps = 4;
+
+template <bool ROW_WARP>
+__device__ __forceinline__ float row_sum(float v, float* s_part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (!ROW_WARP) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    if (lane == 0) s_part[warp] = v;
+    __syncthreads();
+    v = lane < nw ? s_part[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  } else {
+    __syncwarp();
+  }
+  return v;
+}
+
+// ROW_WARP: a warp takes a row by itself, kRowWarps rows a CTA
+template <typename T, typename W, int C, bool VEC, bool ROW_WARP>
+__global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP ? 5 : 6 / C)
+    norm_pair_kernel(const moe_layer_norm_pair_args_t a) {
+  __shared__ float s_sum[kMaxWarps], s_sum2[kMaxWarps];
+  __shared__ uint32_t s_max[kMaxWarps];
+  extern __shared__ __align__(16) uint4 s_rows[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int nt = ROW_WARP ? 32 : blockDim.x, tid = ROW_WARP ? lane : threadIdx.x;
+  const int h = a.hidden;
+  const int64_t row = ROW_WARP ? static_cast<int64_t>(blockIdx.x) * kRowWarps + warp : blockIdx.x;
+  if (ROW_WARP && row >= a.rows) return;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const T* res = static_cast<const T*>(a.residual) + row * a.residual_stride;
+  const T* gate = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_stride : nullptr;
+  const bool own_gate = a.gate && a.gate_stride != 0;  // a row's own, rather than one that all rows share
+  T* res_out = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
+  T* y_out = a.y_out ? static_cast<T*>(a.y_out) + row * h : nullptr;
+  const W *post = static_cast<const W*>(a.post_weight), *w = static_cast<const W*>(a.weight);
+  uint4 *buf_x = s_rows + (ROW_WARP ? warp * 3 * row_slots(C, 32) : 0), *buf_r = buf_x + row_slots(C, nt),
+        *buf_g = buf_r + row_slots(C, nt);
+  auto sync_row = [] {
+    if constexpr (ROW_WARP) __syncwarp();
+    else __syncthreads();
+  };
+
+  RowIn<T, C> xs, rs, gs;
+  Chunk8<T, true> xr[C], rr[C], gr[C];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = (c * nt + tid) * 8;
+      xr[c].load(x, i, h);
+      rr[c].load(res, i, h);
+      if (gate) gr[c].load(gate, i, h);
+    }
+  } else {
+    xs.load(x, row, a.rows - 1 - row, a.x_stride, tid, nt, h);
+    rs.load(res, row, a.rows - 1 - row, a.residual_stride, tid, nt, h);
+    if (own_gate) gs.load(gate, row, a.rows - 1 - row, a.gate_stride, tid, nt, h);
+    xs.stage(buf_x, tid, nt);
+    rs.stage(buf_r, tid, nt);
+    if (own_gate) gs.stage(buf_g, tid, nt);
+    sync_row();
+  }
+
+  float v[C][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if constexpr (VEC) xr[c].take(v[c]);
+    else take_row<T>(buf_x, c * nt + tid, xs.off, h, v[c]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = __fmaf_rn(v[c][j], v[c][j], sum);
+  }
+  sum = row_sum<ROW_WARP>(sum, s_sum);
+  const float r1 = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps));
+
+  // the new residual, and its sum of squares
+  sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int n = c * nt + tid, i = n * 8;
+    float f[8];
+    Chunk8<W, VEC> pr;
+    pr.load(post, i, h);
+    pr.take(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(__fmul_rn(v[c][j], r1), f[j]);
+    if (gate) {
+      if constexpr (VEC) {
+        gr[c].take(f);
+      } else if (own_gate) {
+        take_row<T>(buf_g, n, gs.off, h, f);
+      } else {
+        Chunk8<T, false> shared;
+        shared.load(gate, i, h);
+        shared.take(f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(v[c][j], f[j]);
+    }
+    if constexpr (VEC) rr[c].take(f);
+    else take_row<T>(buf_r, n, rs.off, h, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[c][j] = i + j < h ? __fmaf_rn(a.branch_scale, v[c][j], f[j]) : 0.0f;
+      sum = __fmaf_rn(v[c][j], v[c][j], sum);
+    }
+    if constexpr (VEC) {
+      if (i < h) *reinterpret_cast<uint4*>(res_out + i) = pack8<T>(v[c]);
+    } else {
+      buf_x[n] = pack8<T>(v[c]);  // every thread has taken x, at the sum's barrier
+    }
+  }
+  sum = row_sum<ROW_WARP>(sum, s_sum2);
+  if constexpr (!VEC) store_row(res_out, buf_x, tid, nt, h);
+  const float r2 = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps));
+
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int n = c * nt + tid, i = n * 8;
+    float f[8];
+    Chunk8<W, VEC> wr;
+    wr.load(w, i, h);
+    wr.take(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(__fmul_rn(v[c][j], r2), f[j]) : 0.0f;
+    if (y_out) {
+      if constexpr (!VEC) buf_r[n] = pack8<T>(v[c]);  // the residual has left it
+      else if (i < h) *reinterpret_cast<uint4*>(y_out + i) = pack8<T>(v[c]);
+    }
+    if (a.q) {
+      if (a.smooth) {
+        Chunk8<float, VEC> sr;
+        sr.load(a.smooth, i, h);
+        sr.take(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(v[c][j], f[j]) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[c][j]));
+    }
+  }
+  if (a.q) {  // the maximum of the row
+    top = __reduce_max_sync(0xffffffffu, top);
+    if constexpr (!ROW_WARP) {
+      if (lane == 0) s_max[warp] = top;
+      __syncthreads();
+      top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+    } else if constexpr (!VEC) {
+      __syncwarp();
+    }
+  } else if constexpr (!VEC) {
+    sync_row();
+  }
+  if constexpr (!VEC) {
+    if (y_out) store_row(y_out, buf_r, tid, nt, h);
+  }
+  if (!a.q) return;
+  // a NaN or an infinity in the row is a NaN here (infinity times r = 0), and so in the scale
+  float amax = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : top);
+  if (amax < kAmaxFloor) amax = kAmaxFloor;
+  const float m = __fdiv_rn(127.0f, amax);
+  int8_t* q = a.q + row * h;
+  uint2* codes = reinterpret_cast<uint2*>(buf_g);  // the gate has left it
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int n = c * nt + tid;
+    uint32_t o[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      o[j] = codes_of(__fmul_rn(v[c][4 * j], m), __fmul_rn(v[c][4 * j + 1], m), __fmul_rn(v[c][4 * j + 2], m),
+                      __fmul_rn(v[c][4 * j + 3], m));
+    if constexpr (!VEC) codes[n] = make_uint2(o[0], o[1]);
+    else if (n * 8 < h) *reinterpret_cast<uint2*>(q + n * 8) = make_uint2(o[0], o[1]);
+  }
+  if constexpr (!VEC) {
+    sync_row();
+    store_codes(q, buf_g, tid, nt, h);
+  }
+  if (tid == 0) a.q_scale[row] = __fdiv_rn(1.0f, m);
+}
+
+template <typename T, typename W, int C, bool ROW_WARP>
+cudaError_t launch_shape(const moe_layer_norm_pair_args_t& a, bool vec, cudaStream_t s) {
+  const int chunks = (a.hidden + 7) / 8;
+  const int nt = ROW_WARP ? kRowWarps * 32 : ((chunks + C - 1) / C + 31) / 32 * 32;
+  const void* k = vec ? (const void*)norm_pair_kernel<T, W, C, true, ROW_WARP>
+                      : (const void*)norm_pair_kernel<T, W, C, false, ROW_WARP>;
+  moe_layer_norm_pair_args_t arg = a;
+  void* args[] = {&arg};
+  size_t smem = 0;
+  if (!vec) {
+    smem = (ROW_WARP ? kRowWarps * row_slots(C, 32) : row_slots(C, nt)) * 3 * sizeof(uint4);
+    static std::atomic<uint64_t> allowed{0};
+    if (const cudaError_t e = allow_smem(k, kMaxSmem / 2, allowed); e != cudaSuccess) return e;
+  }
+  return launch_after(k, dim3(ROW_WARP ? (a.rows + kRowWarps - 1) / kRowWarps : a.rows), dim3(nt), args, smem, s);
+}
+
+template <typename T, typename W>
+cudaError_t launch_typed(const moe_layer_norm_pair_args_t& a, cudaStream_t s) {
+  auto at = [](const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+  const bool vec = a.hidden % 8 == 0 && at(a.x, 16) && a.x_stride % 8 == 0 && at(a.residual, 16) &&
+                   a.residual_stride % 8 == 0 && at(a.residual_out, 16) && a.residual_out_stride % 8 == 0 &&
+                   at(a.gate, 16) && a.gate_stride % 8 == 0 && at(a.post_weight, 16) && at(a.weight, 16) && at(a.q, 8) &&
+                   at(a.y_out, 16) && at(a.smooth, 16);
+  // The form goes by hidden alone, so that a row's results do not depend on
+  // the rows beside it.
+  if (a.hidden <= 512) return launch_shape<T, W, 2, true>(a, vec, s);
+  if (a.hidden <= 1024) return launch_shape<T, W, 4, true>(a, vec, s);
+  if (a.hidden <= 4096) return launch_shape<T, W, 2, false>(a, vec, s);
+  return launch_shape<T, W, 4, false>(a, vec, s);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_pair(const moe_layer_norm_pair_args_t& a, cudaStream_t s) {
+  if (a.dtype == MOE_LAYER_BF16)
+    return a.weight_dtype == MOE_LAYER_FP32 ? launch_typed<__nv_bfloat16, float>(a, s)
+                                            : launch_typed<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return a.weight_dtype == MOE_LAYER_FP32 ? launch_typed<__half, float>(a, s) : launch_typed<__half, __half>(a, s);
+}
+
+}  // namespace moe_layer

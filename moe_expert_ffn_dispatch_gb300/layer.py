@@ -1,6 +1,8 @@
 """Torch binding of the decoder-layer operators in include/moe_layer.h: the
-residual addition with RMS norm and int8 quant, products with 4-bit weights,
-and the paged int8 key / value cache with its attention.
+residual addition with RMS norm and int8 quant, the same behind the norm and
+gate of the block before, products with 4-bit and 8-bit weights, the paged int8
+key / value cache with its attention and the plan of its pages, and log
+probabilities of tokens.
 
 Like the block's binding it only marshals arguments: dtypes, shapes, strides
 and devices are checked here, sizes and alignment by the C entry points, and
@@ -11,7 +13,8 @@ does not pass are allocated for that stream.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+import functools
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -20,7 +23,9 @@ I32 = ctypes.c_int32
 I64 = ctypes.c_int64
 
 LAYER_EXPORTS = ["moe_layer_add_rmsnorm_quant", "moe_layer_w4_linear", "moe_layer_kv_append",
-                 "moe_layer_kv_attention_workspace_size", "moe_layer_kv_attention", "moe_layer_kv_attention_status"]
+                 "moe_layer_kv_attention_workspace_size", "moe_layer_kv_attention", "moe_layer_kv_attention_status",
+                 "moe_layer_norm_add_rmsnorm_quant", "moe_layer_w8_linear_workspace_size", "moe_layer_w8_linear",
+                 "moe_layer_w8_linear_status", "moe_layer_page_plan", "moe_layer_token_logprobs"]
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3}
 
 
@@ -53,13 +58,42 @@ class KvAttentionArgs(ctypes.Structure):
                 ("max_q", I32), ("group_size", I32), ("window", I32), ("dtype", I32), ("sm_scale", ctypes.c_float)]
 
 
+class NormPairArgs(ctypes.Structure):
+    _fields_ = [("x", P), ("residual", P), ("post_weight", P), ("gate", P), ("weight", P), ("smooth", P),
+                ("residual_out", P), ("y_out", P), ("q", P), ("q_scale", P), ("x_stride", I64), ("residual_stride", I64),
+                ("gate_stride", I64), ("residual_out_stride", I64), ("rows", I32), ("hidden", I32), ("dtype", I32),
+                ("weight_dtype", I32), ("eps", ctypes.c_float), ("branch_scale", ctypes.c_float)]
+
+
+class W8Args(ctypes.Structure):
+    _fields_ = [("x", P), ("x_scale", P), ("w", P), ("w_scale", P), ("y", P), ("x_stride", I64), ("m", I32), ("n", I32),
+                ("k", I32), ("scale_dtype", I32), ("out_dtype", I32)]
+
+
+class PagePlanArgs(ctypes.Structure):
+    _fields_ = [("page_table", P), ("held", P), ("new_tokens", P), ("free_pages", P), ("taken", P), ("taken_out", P),
+                ("unplaced", P), ("cu_tokens", P), ("seq_lens", P), ("sequence", P), ("position", P), ("slot", P),
+                ("table_stride", I64), ("batch", I32), ("max_pages", I32), ("page_size", I32), ("num_pages", I32),
+                ("num_free", I32), ("tokens", I32)]
+
+
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [("logits", P), ("tokens", P), ("logprob", P), ("entropy", P), ("top_logprob", P), ("top_id", P),
+                ("logits_stride", I64), ("rows", I32), ("vocab", I32), ("num_tokens", I32), ("top", I32), ("dtype", I32),
+                ("tokens_64", I32)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of the entry points of a loaded library."""
     for name, args in (("moe_layer_add_rmsnorm_quant", NormArgs), ("moe_layer_w4_linear", W4Args),
-                       ("moe_layer_kv_append", KvAppendArgs)):
+                       ("moe_layer_kv_append", KvAppendArgs), ("moe_layer_norm_add_rmsnorm_quant", NormPairArgs),
+                       ("moe_layer_page_plan", PagePlanArgs), ("moe_layer_token_logprobs", LogprobsArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), P]
     L.moe_layer_kv_attention.argtypes = [ctypes.POINTER(KvAttentionArgs), P, ctypes.c_size_t, P]
     L.moe_layer_kv_attention_status.argtypes = [P, P]
+    L.moe_layer_w8_linear.argtypes = [ctypes.POINTER(W8Args), P, ctypes.c_size_t, P]
+    L.moe_layer_w8_linear_status.argtypes = [P, P]
+    L.moe_layer_w8_linear_workspace_size.argtypes = [I32, I32, I32, ctypes.POINTER(ctypes.c_size_t)]
     L.moe_layer_kv_attention_workspace_size.argtypes = [I32, ctypes.POINTER(ctypes.c_size_t)]
     for name in LAYER_EXPORTS:
         getattr(L, name).restype = ctypes.c_int
@@ -133,6 +167,15 @@ def _dense(t: Optional[torch.Tensor], name: str, dtype, shape, index: int) -> in
     return t.data_ptr()
 
 
+def _workspace(ws: torch.Tensor, index: int) -> Tuple[int, int]:
+    """Pointer and bytes of a workspace of the caller's own."""
+    if ws.get_device() != index:
+        raise ValueError("workspace: on %s, expected cuda:%d" % (ws.device, index))
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _rows(t: torch.Tensor, name: str, dtype, shape, index: int) -> Tuple[int, int]:
     """Pointer and row stride of a tensor whose inner dimensions are dense."""
     if t.dtype is not dtype:
@@ -201,6 +244,288 @@ def add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if rc:
         _raise(rc, "moe_layer_add_rmsnorm_quant")
     return q, q_scale, residual_out, y
+
+
+def norm_add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tensor, weight: torch.Tensor,
+                           eps: float = 1e-6, gate: Optional[torch.Tensor] = None, branch_scale: float = 1.0,
+                           smooth: Optional[torch.Tensor] = None, want_q: bool = True, want_y: bool = False,
+                           q: Optional[torch.Tensor] = None, q_scale: Optional[torch.Tensor] = None,
+                           residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None):
+    """(q, q_scale, residual_out, y) of moe_layer_norm_add_rmsnorm_quant: the
+    norm of a block's output x, its gate and scale, the residual addition, and
+    the norm before the next block.
+
+    x, residual [rows, hidden] bf16 or fp16, their rows may be strided;
+    post_weight and weight [hidden], both of x's dtype or both fp32; gate
+    [hidden], or [rows, hidden] (rows may be strided), of x's dtype;
+    smooth [hidden] fp32.  residual_out is residual + branch_scale * gate *
+    norm(x) in x's dtype (pass residual itself to add in place); q int8 and
+    q_scale fp32 [rows] are the quantised norm of that (None where `want_q` is
+    false and no tensors are given), y the norm in x's dtype (None unless
+    `want_y` or a tensor for it is given)."""
+    code, shape, index = _act(x, "x"), x.shape, x.get_device()
+    if len(shape) != 2:
+        raise ValueError("x: %d dimensions, expected 2" % len(shape))
+    if stream is not None or index < 0 or index != _device_index():
+        with _On(x.device, stream):
+            return norm_add_rmsnorm_quant(x, residual, post_weight, weight, eps, gate, branch_scale, smooth, want_q,
+                                          want_y, q, q_scale, residual_out, y)
+    rows, hidden = shape
+    if rows > _I32_MAX or hidden > _I32_MAX:
+        _too_large("x", max(shape))
+    dtype, wdtype = x.dtype, weight.dtype
+    if wdtype is not dtype and wdtype is not torch.float32:
+        raise TypeError("weight: dtype %s, expected %s or float32" % (wdtype, dtype))
+    a = NormPairArgs()
+    a.x, a.x_stride = _rows(x, "x", dtype, shape, index)
+    a.residual, a.residual_stride = _rows(residual, "residual", dtype, shape, index)
+    a.post_weight = _dense(post_weight, "post_weight", wdtype, (hidden,), index)
+    a.weight = _dense(weight, "weight", wdtype, (hidden,), index)
+    if gate is not None:
+        if gate.dim() == 1:
+            a.gate = _dense(gate, "gate", dtype, (hidden,), index)
+        else:
+            a.gate, a.gate_stride = _rows(gate, "gate", dtype, shape, index)
+    a.smooth = _dense(smooth, "smooth", torch.float32, (hidden,), index)
+    a.rows, a.hidden, a.dtype, a.weight_dtype = rows, hidden, code, DTYPE_CODES[wdtype]
+    a.eps, a.branch_scale = eps, branch_scale
+    if residual_out is None:
+        residual_out = torch.empty_like(x, memory_format=_CONTIGUOUS)
+    a.residual_out, a.residual_out_stride = _rows(residual_out, "residual_out", dtype, shape, index)
+    if want_q or q is not None or q_scale is not None:
+        if q is None:
+            q = torch.empty_like(x, dtype=torch.int8, memory_format=_CONTIGUOUS)
+        if q_scale is None:
+            q_scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        a.q = _dense(q, "q", torch.int8, shape, index)
+        a.q_scale = _dense(q_scale, "q_scale", torch.float32, (rows,), index)
+    if y is None and want_y:
+        y = torch.empty_like(x, memory_format=_CONTIGUOUS)
+    a.y_out = _dense(y, "y", dtype, shape, index)
+    rc = _entry("moe_layer_norm_add_rmsnorm_quant")(ctypes.byref(a), _raw_stream(index))
+    if rc:
+        _raise(rc, "moe_layer_norm_add_rmsnorm_quant")
+    return q, q_scale, residual_out, y
+
+
+def w8_linear_workspace(m: int, n: int, k: int, device="cuda") -> Optional[torch.Tensor]:
+    """A workspace for w8_linear of these sizes; None where it needs none."""
+    device = torch.device(device)
+    with _On(device, None):
+        nb = _w8_workspace_bytes(m, n, k, torch.cuda.current_device())
+        if not nb:
+            return None
+        buf = torch.empty(nb + 256, dtype=torch.uint8, device="cuda")
+        return buf[(-buf.data_ptr()) % 256:][:nb]
+
+
+@functools.lru_cache(maxsize=1024)
+def _w8_workspace_bytes(m: int, n: int, k: int, index: int) -> int:
+    nb = ctypes.c_size_t(0)
+    rc = _entry("moe_layer_w8_linear_workspace_size")(m, n, k, ctypes.byref(nb))
+    if rc:
+        _raise(rc, "moe_layer_w8_linear_workspace_size")
+    return nb.value
+
+
+def w8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor,
+              out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """y [m, n] of moe_layer_w8_linear: int8 codes times the transposed int8
+    weights, exact in int32, times both scales.
+
+    x [m, k] int8 with x_scale [m] fp32, as add_rmsnorm_quant leaves them; its
+    rows may be strided.  w [n, k] int8, w_scale [n] bf16, fp16 or fp32.
+    out_dtype: bf16 (without it), fp16 or fp32.  workspace: one of
+    w8_linear_workspace; without it memory of torch's allocator is used for
+    the call."""
+    index, shape = x.get_device(), x.shape
+    if stream is not None or index < 0 or index != _device_index():
+        with _On(x.device, stream):
+            return w8_linear(x, w, w_scale, x_scale, out_dtype, out, workspace)
+    wshape = w.shape
+    if len(shape) != 2 or len(wshape) != 2:
+        raise ValueError("x and w have 2 dimensions")
+    m, k = shape
+    n = wshape[0]
+    if m > _I32_MAX or k > _I32_MAX or n > _I32_MAX:
+        _too_large("x or w", max(m, k, n))
+    sdtype = w_scale.dtype
+    scode = DTYPE_CODES.get(sdtype, 3)
+    if scode == 3:
+        raise TypeError("w_scale: dtype %s, expected bfloat16, float16 or float32" % sdtype)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    ocode = DTYPE_CODES.get(out_dtype, 3)
+    if ocode == 3:
+        raise TypeError("out_dtype: %s, expected bfloat16, float16 or float32" % out_dtype)
+    a = W8Args()
+    a.x, a.x_stride = _rows(x, "x", torch.int8, shape, index)
+    a.x_scale = _dense(x_scale, "x_scale", torch.float32, (m,), index)
+    a.w = _dense(w, "w", torch.int8, (n, k), index)
+    a.w_scale = _dense(w_scale, "w_scale", sdtype, (n,), index)
+    a.m, a.n, a.k, a.scale_dtype, a.out_dtype = m, n, k, scode, ocode
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        a.y = out.data_ptr()
+    else:
+        a.y = _dense(out, "out", out_dtype, (m, n), index)
+    ws_at = ws_bytes = 0
+    if workspace is not None:
+        ws_at, ws_bytes = _workspace(workspace, index)
+    elif m:
+        need = _w8_workspace_bytes(m, n, k, index)
+        if need:
+            workspace = torch.empty(need + 256, dtype=torch.uint8, device=x.device)
+            ws_at, ws_bytes = -(-workspace.data_ptr() // 256) * 256, need
+    rc = _entry("moe_layer_w8_linear")(ctypes.byref(a), ws_at, ws_bytes, _raw_stream(index))
+    if rc:
+        _raise(rc, "moe_layer_w8_linear")
+    return out
+
+
+def w8_linear_status(workspace: torch.Tensor) -> int:
+    """Synchronises the current stream; the code of the last w8_linear that
+    used this workspace (there has to have been one): 0, or
+    MOE_ERR_DEVICE_TIMEOUT where a wait inside it gave up."""
+    with _On(workspace.device, None):
+        index = workspace.get_device()
+        return _entry("moe_layer_w8_linear_status")(_workspace(workspace, index)[0], _raw_stream(index))
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """(logprob, entropy, top_logprob, top_id) of moe_layer_token_logprobs.
+
+    logits [rows, vocab] bf16, fp16 or fp32, its rows may be strided; tokens
+    [rows] or [rows, n] int32 or int64.  logprob fp32 has the shape of tokens
+    (None without tokens), entropy fp32 [rows]; top_logprob fp32 and top_id
+    int32 [rows, top] are the `top` (at most 32) likeliest tokens, the lower
+    id first among equals (None with top 0)."""
+    index, shape, code = logits.get_device(), logits.shape, DTYPE_CODES.get(logits.dtype, 3)
+    if code == 3:
+        raise TypeError("logits: dtype %s, expected bfloat16, float16 or float32" % logits.dtype)
+    if stream is not None or index < 0 or index != _device_index():
+        with _On(logits.device, stream):
+            return token_logprobs(logits, tokens, top)
+    if len(shape) != 2:
+        raise ValueError("logits: %d dimensions, expected 2" % len(shape))
+    rows, vocab = shape
+    if rows > _I32_MAX or vocab > _I32_MAX:
+        _too_large("logits", max(shape))
+    if not 0 <= top <= min(32, vocab):
+        raise ValueError("top: %d, expected 0 to %d" % (top, min(32, vocab)))
+    a = LogprobsArgs()
+    a.logits, a.logits_stride = _rows(logits, "logits", logits.dtype, shape, index)
+    if rows == 1:
+        a.logits_stride = vocab
+    device = logits.device
+    logprob = top_logprob = top_id = None
+    if tokens is not None:
+        tdtype, tshape = tokens.dtype, tokens.shape
+        if tdtype is not torch.int32 and tdtype is not torch.int64:
+            raise TypeError("tokens: dtype %s, expected int32 or int64" % tdtype)
+        if not 1 <= len(tshape) <= 2 or tshape[0] != rows:
+            raise ValueError("tokens: shape %s, expected [%d] or [%d, n]" % (tuple(tshape), rows, rows))
+        a.num_tokens = tshape[1] if len(tshape) == 2 else 1
+        if a.num_tokens:
+            a.tokens = _dense(tokens, "tokens", tdtype, tshape, index)
+        a.tokens_64 = tdtype is torch.int64
+        logprob = torch.empty(tshape, dtype=torch.float32, device=device)
+        a.logprob = logprob.data_ptr()
+    entropy = torch.empty(rows, dtype=torch.float32, device=device)
+    a.entropy = entropy.data_ptr()
+    if top:
+        top_logprob = torch.empty((rows, top), dtype=torch.float32, device=device)
+        top_id = torch.empty((rows, top), dtype=torch.int32, device=device)
+        a.top_logprob, a.top_id = top_logprob.data_ptr(), top_id.data_ptr()
+    a.rows, a.vocab, a.top, a.dtype = rows, vocab, top, code
+    rc = _entry("moe_layer_token_logprobs")(ctypes.byref(a), _raw_stream(index))
+    if rc:
+        _raise(rc, "moe_layer_token_logprobs")
+    return logprob, entropy, top_logprob, top_id
+
+
+class PagePlan(NamedTuple):
+    """What a step over a paged cache needs (moe_layer_page_plan): cu_tokens
+    [batch + 1] and seq_lens [batch] as KvCache's append and attention take
+    them; sequence, position (int32) and slot (int64) [tokens] of every token of
+    the step, -1 past the last; taken [1], the entries of the list of free pages
+    that are in use now; unplaced [1], how many tokens have no slot."""
+    cu_tokens: torch.Tensor
+    seq_lens: torch.Tensor
+    sequence: torch.Tensor
+    position: torch.Tensor
+    slot: torch.Tensor
+    taken: torch.Tensor
+    unplaced: torch.Tensor
+
+
+def page_plan(page_table: torch.Tensor, held: torch.Tensor, new_tokens: torch.Tensor, free_pages: torch.Tensor,
+              page_size: int, num_pages: int, tokens: int, taken: Optional[torch.Tensor] = None,
+              taken_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> PagePlan:
+    """Plan a step whose sequences hold `held` [batch] tokens and get
+    `new_tokens` [batch] more (int32): writes the new pages, taken from
+    free_pages (int32, from entry `taken` [1] on, 0 without it), into page_table
+    [batch, max_pages] int32 and returns a PagePlan.
+
+    num_pages: pages of the cache; tokens: rows of the step's buffers, at least
+    as many as there are new tokens (those past it are left out).  taken_out:
+    where to write the plan's `taken` (pass `taken` itself to move it on in
+    place, as a captured step does)."""
+    index = page_table.get_device()
+    if stream is not None or index < 0 or index != _device_index():
+        with _On(page_table.device, stream):
+            return page_plan(page_table, held, new_tokens, free_pages, page_size, num_pages, tokens, taken, taken_out)
+    a = PagePlanArgs()
+    a.page_table, batch, a.max_pages, a.table_stride = _page_table(page_table, index)
+    if max(page_size, num_pages, tokens, free_pages.numel()) > _I32_MAX:
+        _too_large("page_plan", max(page_size, num_pages, tokens, free_pages.numel()))
+    i32 = torch.int32
+    a.held = _dense(held, "held", i32, (batch,), index)
+    a.new_tokens = _dense(new_tokens, "new_tokens", i32, (batch,), index)
+    a.free_pages = _dense(free_pages, "free_pages", i32, (free_pages.numel(),), index)
+    if taken is not None:
+        a.taken = _dense(taken, "taken", i32, (1,), index)
+    if tokens < 0:
+        raise ValueError("tokens: %d" % tokens)
+    # one allocation for the numbers of 32 bits, each part on a 16-byte boundary
+    up = (tokens + 3) // 4 * 4
+    lens_at, cu_at = 2 * up, 2 * up + (batch + 3) // 4 * 4
+    buf = torch.empty(cu_at + batch + 3, dtype=i32, device=page_table.device)
+    slot = torch.empty(tokens, dtype=torch.int64, device=page_table.device)
+    at = buf.data_ptr()
+    a.sequence, a.position, a.slot = at, at + 4 * up, slot.data_ptr()
+    a.seq_lens, a.cu_tokens, a.unplaced = at + 4 * lens_at, at + 4 * cu_at, at + 4 * (cu_at + batch + 1)
+    if taken_out is None:
+        taken_out = buf[cu_at + batch + 2:]
+        a.taken_out = at + 4 * (cu_at + batch + 2)
+    else:
+        a.taken_out = _dense(taken_out, "taken_out", i32, (1,), index)
+    a.batch, a.page_size, a.num_pages, a.num_free, a.tokens = batch, page_size, num_pages, free_pages.numel(), tokens
+    rc = _entry("moe_layer_page_plan")(ctypes.byref(a), _raw_stream(index))
+    if rc:
+        _raise(rc, "moe_layer_page_plan")
+    return PagePlan(buf[cu_at:cu_at + batch + 1], buf[lens_at:lens_at + batch], buf[:tokens], buf[up:up + tokens], slot,
+                    taken_out, buf[cu_at + batch + 1:cu_at + batch + 2])
+
+
+def _page_table(page_table: torch.Tensor, index: int) -> Tuple[int, int, int, int]:
+    """Pointer, batch, pages and row stride of a page table."""
+    if page_table.dtype is not torch.int32:
+        raise TypeError("page_table: dtype %s, expected int32" % page_table.dtype)
+    shape, strides = page_table.shape, page_table.stride()
+    if len(shape) != 2:
+        raise ValueError("page_table: %d dimensions, expected 2" % len(shape))
+    if page_table.get_device() != index:
+        raise ValueError("page_table: on %s, expected cuda:%d" % (page_table.device, index))
+    batch, pages = shape
+    if batch > _I32_MAX or pages > _I32_MAX:
+        _too_large("page_table", max(shape))
+    if pages > 1 and strides[1] != 1:
+        raise ValueError("page_table: the pages of a sequence must be dense")
+    return page_table.data_ptr(), batch, pages, strides[0] if batch > 1 else pages
 
 
 def w4_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
@@ -334,32 +659,21 @@ class KvCache:
             self._ws[:256].zero_()  # the status words: status() may come before the first attention
         return self._ws
 
-    def _workspace(self, ws: torch.Tensor) -> Tuple[int, int]:
-        """Pointer and bytes of a workspace of the caller's own."""
-        if ws.get_device() != self._index:
-            raise ValueError("workspace: on %s, expected %s" % (ws.device, self.device))
-        if not ws.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        return ws.data_ptr(), ws.numel() * ws.element_size()
-
     def _table(self, a, page_table: torch.Tensor) -> int:
         """Sets the page table's fields of `a`; returns the batch."""
-        if page_table.dtype is not torch.int32:
-            raise TypeError("page_table: dtype %s, expected int32" % page_table.dtype)
-        shape, strides = page_table.shape, page_table.stride()
-        if len(shape) != 2:
-            raise ValueError("page_table: %d dimensions, expected 2" % len(shape))
+        a.cache = self._args
+        a.page_table, a.batch, a.max_pages, a.table_stride = _page_table(page_table, self._index)
+        return a.batch
+
+    def plan(self, page_table: torch.Tensor, held: torch.Tensor, new_tokens: torch.Tensor, free_pages: torch.Tensor,
+             tokens: int, taken: Optional[torch.Tensor] = None, taken_out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> PagePlan:
+        """page_plan for this cache's pages: held is then `start` of append,
+        the plan's cu_tokens and seq_lens go to append and attention."""
         if page_table.get_device() != self._index:
             raise ValueError("page_table: on %s, expected %s" % (page_table.device, self.device))
-        batch, pages = shape
-        if batch > _I32_MAX or pages > _I32_MAX:
-            _too_large("page_table", max(shape))
-        if pages > 1 and strides[1] != 1:
-            raise ValueError("page_table: the pages of a sequence must be dense")
-        a.cache = self._args
-        a.page_table, a.batch, a.max_pages = page_table.data_ptr(), batch, pages
-        a.table_stride = strides[0] if batch > 1 else pages
-        return batch
+        return page_plan(page_table, held, new_tokens, free_pages, self.page_size, self._args.num_pages, tokens, taken,
+                         taken_out, stream)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
                cu_tokens: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -434,7 +748,7 @@ class KvCache:
         a.sm_scale = dim ** -0.5 if scale is None else scale
         s = _raw_stream(index)
         if workspace is not None:
-            ws_at, ws_bytes = self._workspace(workspace)
+            ws_at, ws_bytes = _workspace(workspace, self._index)
         else:
             if self._ws is None:
                 self.workspace()
@@ -457,5 +771,5 @@ class KvCache:
         this workspace that had query tokens: 0, or MOE_ERR_DEVICE_TIMEOUT
         where a wait inside it gave up.  A workspace of the caller's own has
         to have been used by one."""
-        at = self.workspace().data_ptr() if workspace is None else self._workspace(workspace)[0]
+        at = self.workspace().data_ptr() if workspace is None else _workspace(workspace, self._index)[0]
         return _entry("moe_layer_kv_attention_status")(at, torch.cuda.current_stream(self.device).cuda_stream)
