@@ -17,9 +17,9 @@ BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(HERE, "_moe_fused.so")
 SOURCES = ["api.cu", "dispatch_quant.cu", "moe_gemm.cu", "tc_gemm.cu",
            "layer_api.cu", "norm_quant.cu", "w4_linear.cu", "kv_append.cu", "kv_attention.cu",
-           "kv_attention_chunk.cu", "norm_pair.cu", "w8_linear.cu", "page_plan.cu", "token_logprobs.cu"]
+           "kv_attention_chunk.cu", "norm_pair.cu", "w8_linear.cu", "w8_linear_tc.cu", "page_plan.cu", "token_logprobs.cu"]
 HEADERS = ["device_prims.cuh", "epilogue_ops.cuh", "moe_internal.h", "quant_ops.cuh", "layer_ops.cuh", "kv_attention.cuh",
-           "norm_rows.cuh"]
+           "norm_rows.cuh", "w8_linear.cuh", "tensor_map.cuh"]
 PUBLIC_HEADERS = ["moe_fused.h", "moe_layer.h"]
 
 NVCC_FLAGS = [

@@ -24,6 +24,7 @@
 #include "device_prims.cuh"
 #include "moe_fused.h"
 #include "moe_internal.h"
+#include "tensor_map.cuh"
 
 struct TimingRecord {
   int kernel;
@@ -232,37 +233,7 @@ cudaError_t timed(moe_fused_handle* hd, int kernel, cudaStream_t s, F fn) {
 }
 
 // ---- TMA descriptors for the tensor-core path -----------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  }
-  return fn;
-}
-
-// 2-D row-major [rows][cols] tensor, box {box_cols, box_rows}
-bool encode_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, size_t elem, uint64_t rows, uint64_t cols,
-               uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * elem};
-  const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+using moe::encode_2d;
 
 // Build (or reuse) the tensor maps of this forward's operands.
 int prepare_maps(moe_fused_handle* hd, const moe::FwdParams& p) {

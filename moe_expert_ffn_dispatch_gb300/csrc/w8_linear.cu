@@ -7,7 +7,7 @@
 // of a token) at a time, 64 apart: the four words of a load are k-words of four
 // products, in the same order for weights and tokens, which is all that the sum
 // asks for.
-#include "layer_ops.cuh"
+#include "w8_linear.cuh"
 
 namespace moe_layer {
 namespace {
@@ -24,17 +24,6 @@ __device__ __forceinline__ void mma_s8(int32_t (&d)[4], uint32_t a0, uint32_t a1
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float scale_at(const void* s, int64_t i, int dtype) {
-  if (dtype == MOE_LAYER_FP32) return static_cast<const float*>(s)[i];
-  const uint32_t w = static_cast<const uint16_t*>(s)[i];
-  return dtype == MOE_LAYER_BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
-}
-__device__ __forceinline__ void store_y(void* y, int64_t i, float v, int dtype) {
-  if (dtype == MOE_LAYER_FP32) static_cast<float*>(y)[i] = v;
-  else if (dtype == MOE_LAYER_BF16) static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(y)[i] = __float2half_rn(v);
 }
 
 template <int NT>
@@ -93,37 +82,26 @@ __global__ void __launch_bounds__(kFewThreads, 2) w8_few_kernel(const moe_layer_
     int32_t sum = 0;
 #pragma unroll
     for (int q = 0; q < kFewWarps; ++q) sum += s_part[q][tok][r];
-    const float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), scale_at(a.w_scale, n0 + r, a.scale_dtype)), a.x_scale[m0 + tok]);
-    store_y(a.y, static_cast<int64_t>(m0 + tok) * a.n + n0 + r, v, a.out_dtype);
+    store_y(a.y, static_cast<int64_t>(m0 + tok) * a.n + n0 + r,
+            scaled(sum, scale_at(a.w_scale, n0 + r, a.scale_dtype), a.x_scale[m0 + tok]), a.out_dtype);
   }
 }
 
 template <int NT>
 cudaError_t launch_few(const moe_layer_w8_args_t& a, cudaStream_t s) {
   moe_layer_w8_args_t arg = a;
-  // the grid's second dimension ends at 65535: more tokens go in several launches
-  for (int m0 = 0; m0 < a.m; m0 += 65535 * 8 * NT) {
-    arg.m = a.m - m0 < 65535 * 8 * NT ? a.m - m0 : 65535 * 8 * NT;
-    arg.x = a.x + m0 * a.x_stride;
-    arg.x_scale = a.x_scale + m0;
-    arg.y = static_cast<char*>(a.y) + static_cast<int64_t>(m0) * a.n * (a.out_dtype == MOE_LAYER_FP32 ? 4 : 2);
-    void* args[] = {&arg};
-    const dim3 grid((a.n + kFewRows - 1) / kFewRows, (arg.m + 8 * NT - 1) / (8 * NT));
-    if (const cudaError_t e = launch_after((const void*)w8_few_kernel<NT>, grid, dim3(kFewThreads), args, 0, s);
-        e != cudaSuccess)
-      return e;
-  }
-  return cudaSuccess;
+  void* args[] = {&arg};
+  const dim3 grid((a.n + kFewRows - 1) / kFewRows, (a.m + 8 * NT - 1) / (8 * NT));
+  return launch_after((const void*)w8_few_kernel<NT>, grid, dim3(kFewThreads), args, 0, s);
 }
 
 }  // namespace
 
-size_t w8_workspace(int, int, int, int) { return 0; }
+size_t w8_workspace(int m, int n, int k, int num_sms) { return m <= 8 ? 0 : w8_tc_workspace(m, n, k, num_sms); }
 
-cudaError_t launch_w8(const moe_layer_w8_args_t& a, void*, int, cudaStream_t s) {
+cudaError_t launch_w8(const moe_layer_w8_args_t& a, void* ws, int num_sms, cudaStream_t s) {
   if (a.m <= 8) return launch_few<1>(a, s);
-  if (a.m <= 16) return launch_few<2>(a, s);
-  return launch_few<4>(a, s);
+  return launch_w8_tc(a, ws, num_sms, s);
 }
 
 }  // namespace moe_layer
