@@ -11,9 +11,13 @@
 // converted in the CTA into tensor memory, the products' A operand, so that they
 // cross memory and L2 as bytes.  Tokens are converted once by a kernel before this
 // one, into the workspace, and arrive as f16 in shared memory.
-// The two halves of a wide tile have an accumulator each, and each step of 128 k
-// issues the first half's products before the second's: one is drained while the
-// other's products run.  A tile of one half alternates between two accumulators.
+// The two halves of a wide tile have an accumulator each, side by side: most steps of
+// 128 k multiply both at once, the first and the last of a 1024 k the first half
+// before the second, so that one is drained while the other's products run.  A tile
+// of one half alternates between two accumulators.
+// What bounds a step is how fast one warp can wait, issue and commit (about 100 cycles
+// a wait, 40 a product): weights and tokens of a step complete one barrier, and its
+// products one other.
 // Roles: warp 0 copies weights, warp 2 copies tokens, warp 1 issues products, warps
 // 4..7 convert weights (a row a thread), warps 8..15 drain and write.
 // Where there are fewer tiles than SMs a cluster shares k out, and adds its int32
@@ -29,13 +33,11 @@ namespace {
 constexpr int kRows = 128;          // weight rows of a tile
 constexpr int kHalf = 128;          // tokens of a half at most
 constexpr int kStage = 128;         // k of a weight stage
-constexpr int kAtom = 64;           // k of a token slot: one 128-byte row of f16
+constexpr int kAtom = 64;           // k of one 128-byte row of f16
 constexpr int kChunk = 1024 / kStage;  // stages that a sum stays exact for
-constexpr int kA16 = 4;             // converted weight stages in tensor memory
-constexpr int kA16Cols = kStage / 2;
+constexpr int kA16Cols = kStage / 2;  // of a converted weight stage in tensor memory
 constexpr int kAccCols = 2 * kHalf;
 constexpr int kTmemCols = 512;
-static_assert(kAccCols + kA16 * kA16Cols <= kTmemCols, "tensor memory");
 constexpr int kThreads = 512;
 constexpr int kConvWarps = 4, kDrainWarps = 8;
 // Registers a thread where a tile has two halves: 128 at launch, and what the drain warps have more the others give.
@@ -45,31 +47,29 @@ static_assert(128 * kRoleRegs + 128 * kConvRegs + 256 * kDrainRegs <= kThreads *
 constexpr int kA8Bytes = kRows * kStage;
 constexpr int kSite = 2 << 8;       // of the waits, in the status
 
-// HALVES: of a tile's tokens.  Shared memory: token slots, weight stages, barriers
+// HALVES: of a tile's tokens.  Shared memory: tokens of each step, weight stages, barriers
 template <int HALVES>
 struct Layout {
-  static constexpr int kSlotBytes = HALVES * kHalf * kAtom * 2;
-  static constexpr int kSlots = HALVES == 2 ? 5 : 6;
-  static constexpr int kA8 = HALVES == 2 ? 4 : 7;
-  static constexpr int kOffA8 = kSlots * kSlotBytes, kOffBar = kOffA8 + kA8 * kA8Bytes;
+  static constexpr int kAtomBytes = HALVES * kHalf * kAtom * 2;
+  static constexpr int kSteps = HALVES == 2 ? 3 : 4;  // tokens in shared memory, converted weights in tensor memory
+  static constexpr int kA8 = HALVES == 2 ? 2 : 6;     // weights as they arrive
+  static constexpr int kOffA8 = kSteps * 2 * kAtomBytes, kOffBar = kOffA8 + kA8 * kA8Bytes;
   static constexpr int kBytes = kOffBar + 512;
+  static_assert(kBytes + 1024 <= kMaxSmem, "shared memory");
+  static_assert(kAccCols + kSteps * kA16Cols <= kTmemCols, "tensor memory");
 };
-static_assert(Layout<2>::kBytes + 1024 <= kMaxSmem && Layout<1>::kBytes + 1024 <= kMaxSmem, "shared memory");
 static_assert(Layout<1>::kOffBar >= kHalf * kRows * 4, "the sums of a tile of one half fit the rings");
 
-template <int HALVES>
 struct Barriers {
-  using L = Layout<HALVES>;
-  uint64_t a8_full[L::kA8], a8_empty[L::kA8], a16_full[kA16], a16_empty[kA16], b_full[L::kSlots], b_empty[L::kSlots],
-      acc_full[2], acc_empty[2], drain;
+  uint64_t a8_full[8], a8_empty[8], full[4], empty[4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Barriers<1>) <= 512 && sizeof(Barriers<2>) <= 512, "");
+static_assert(sizeof(Barriers) <= 512, "");
 
 struct alignas(64) Maps {
   CUtensorMap w;  // int8 [n, k], box {128, 128}, 128-byte swizzle
-  CUtensorMap x;  // f16 [m, k], box {64, tokens of a half}, 128-byte swizzle
+  CUtensorMap x;  // f16 [m, k], box {64, tokens of a tile}, 128-byte swizzle
 };
 
 struct Params {
@@ -115,12 +115,40 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int n, int s, uint32_
   }
 }
 
+__device__ __forceinline__ void put(float* y, float v) { *y = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* y, float v) { *y = __float2half_rn(v); }
+
+// `most` (at most 64) tokens of one weight row a lane, `stride` apart; every lane of the warp
+template <typename T>
+__device__ __forceinline__ void write_tokens(T* y, int64_t stride, const int32_t (&acc)[64], float ws, float xs0, float xs1,
+                                             int most, bool mine) {
+#pragma unroll
+  for (int j = 0; j < 64; ++j) {
+    const float xs = __shfl_sync(0xffffffffu, j < 32 ? xs0 : xs1, j & 31);
+    if (j < most && mine) put(y, scaled(acc[j], ws, xs));
+    y += stride;
+  }
+}
+
+// The same for the steps, whose barriers the converters complete too: where they have given up, a phase never completes
+// and the copies get a while to land.
+__device__ __forceinline__ void drain_steps(uint64_t* full, int n, int s, uint32_t ph, bool wrapped, volatile int* abort,
+                                            int32_t* status, int site) {
+  for (int i = 0; i < n; ++i) {
+    const uint32_t parity = i < s ? ph : ph ^ 1u;
+    if (i < s || wrapped) moe::mbar_wait_bounded(&full[i], parity, abort, status, site);
+  }
+  if (*abort)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
 template <int HALVES>
 __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
   using L = Layout<HALVES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (moe::smem_u32(smem_raw) & 1023u)) & 1023u);
-  Barriers<HALVES>& bar = *reinterpret_cast<Barriers<HALVES>*>(smem + L::kOffBar);
+  Barriers& bar = *reinterpret_cast<Barriers*>(smem + L::kOffBar);
   const moe_layer_w8_args_t& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t rank, parts;  // of the cluster that shares k out
@@ -136,13 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       moe::mbar_init(&bar.a8_full[i], 1);
       moe::mbar_init(&bar.a8_empty[i], kConvWarps);
     }
-    for (int i = 0; i < kA16; ++i) {
-      moe::mbar_init(&bar.a16_full[i], kConvWarps);
-      moe::mbar_init(&bar.a16_empty[i], 1);
-    }
-    for (int i = 0; i < L::kSlots; ++i) {
-      moe::mbar_init(&bar.b_full[i], 1);
-      moe::mbar_init(&bar.b_empty[i], 1);
+    for (int i = 0; i < L::kSteps; ++i) {
+      moe::mbar_init(&bar.full[i], kConvWarps + 1);
+      moe::mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       moe::mbar_init(&bar.acc_full[i], 1);
@@ -193,73 +217,77 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       int s = 0;
       uint32_t ph = 0;
       bool wrapped = false, ok = true;
-      const uint32_t half_bytes = p.half * kAtom * 2;
+      const int tokens = p.half * HALVES;
       for (int64_t it = first; ok && it < p.tiles; it += step) {
-        const int m0 = static_cast<int>(it % p.blocks) * p.half * HALVES;
-        for (int ka = 2 * kb0; ka < 2 * kb1; ++ka) {
-          if (wrapped && !wait(&bar.b_empty[s], ph ^ 1u, 3)) {
+        const int m0 = static_cast<int>(it % p.blocks) * tokens;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (wrapped && !wait(&bar.empty[s], ph ^ 1u, 3)) {
             ok = false;
             break;
           }
           if (moe::elect_one()) {
-            moe::mbar_arrive_expect_tx(&bar.b_full[s], HALVES * half_bytes);
+            moe::mbar_arrive_expect_tx(&bar.full[s], 2 * tokens * kAtom * 2);
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-              moe::tma_load_2d(smem + s * L::kSlotBytes + h * kHalf * kAtom * 2, &maps.x, ka * kAtom, m0 + h * p.half,
-                               &bar.b_full[s]);
+            for (int h = 0; h < 2; ++h)
+              moe::tma_load_2d(smem + (2 * s + h) * L::kAtomBytes, &maps.x, kb * kStage + h * kAtom, m0, &bar.full[s]);
           }
           __syncwarp();
-          if (++s == L::kSlots) s = 0, ph ^= 1u, wrapped = true;
+          if (++s == L::kSteps) s = 0, ph ^= 1u, wrapped = true;
         }
       }
-      drain_ring(bar.b_full, L::kSlots, s, ph, wrapped, p.status, kSite + 4);
+      // what it armed has landed, or (the converters having given up) is past where a barrier could tell
+      drain_steps(bar.full, L::kSteps, s, ph, wrapped, abort, p.status, kSite + 4);
     } else if (warp == 1) {
       // ---------------------------------------------------- products
-      const uint32_t idesc = moe::umma_idesc_f16(kRows, p.half);
+      const uint32_t idesc = moe::umma_idesc_f16(kRows, p.half), idesc_both = moe::umma_idesc_f16(kRows, HALVES * p.half);
       const uint64_t b0 = moe::umma_desc_sw128(moe::smem_u32(smem));
-      constexpr uint64_t kSlot = L::kSlotBytes >> 4, kHalfAt = (kHalf * kAtom * 2) >> 4;
-      int sa = 0, sb = 0;
-      uint32_t pa = 0, pb = 0;
+      constexpr uint64_t kAtomAt = L::kAtomBytes >> 4;
+      const uint64_t half_at = (p.half * kAtom * 2) >> 4;
+      // eight products of 16 k
+      auto products = [&](uint32_t d, uint32_t at, uint64_t bd, uint32_t form, bool fresh) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          moe::umma_f16_ts(d, at + 8 * k, bd + (k >> 2) * kAtomAt + 2 * (k & 3), form, !fresh || k != 0);
+      };
+      int s = 0;
+      uint32_t ph = 0;
       int64_t chunk = 0;
       bool ok = true;
       for (int64_t it = first; ok && it < p.tiles; it += step) {
-        int kc = 0;  // stage of the chunk
-        for (int kb = kb0; ok && kb < kb1; ++kb) {
+        int kc = 0;  // step of the chunk
+        for (int kb = kb0; kb < kb1; ++kb) {
           const bool last = kc + 1 == kChunk || kb + 1 == kb1;
-          const int sb1 = sb + 1 == L::kSlots ? 0 : sb + 1;
-          ok = wait(&bar.a16_full[sa], pa, 5) && wait(&bar.b_full[sb], pb, 6) &&
-               wait(&bar.b_full[sb1], sb1 ? pb : pb ^ 1u, 6);
-          if (!ok) break;
-          const uint32_t at = tmem + kAccCols + sa * kA16Cols;
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h) {
-            // the accumulator's uses so far: a half's own one a chunk, or two in turn
-            const int buf = HALVES == 2 ? h : static_cast<int>(chunk & 1);
-            const int64_t used = HALVES == 2 ? chunk : chunk >> 1;
-            if (kc == 0 && used > 0 && !wait(&bar.acc_empty[buf], (used - 1) & 1, 7)) {
-              ok = false;
-              break;
-            }
+          const uint32_t at = tmem + kAccCols + s * kA16Cols;
+          const uint64_t bd = b0 + 2 * s * kAtomAt;
+          if (HALVES == 2 && kc != 0 && !last) {
+            ok = wait(&bar.full[s], ph, 5);
+            if (!ok) break;
             moe::tc_fence_after();
             if (moe::elect_one()) {
-              const uint32_t d = tmem + buf * kHalf;
-              const uint64_t bd = b0 + sb * kSlot + h * kHalfAt, bd1 = b0 + sb1 * kSlot + h * kHalfAt;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) moe::umma_f16_ts(d, at + 8 * k, bd + 2 * k, idesc, kc != 0 || k != 0);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) moe::umma_f16_ts(d, at + 32 + 8 * k, bd1 + 2 * k, idesc, 1u);
-              if (h == HALVES - 1) {
-                moe::umma_commit(&bar.a16_empty[sa]);
-                moe::umma_commit(&bar.b_empty[sb]);
-                moe::umma_commit(&bar.b_empty[sb1]);
-              }
-              if (last) moe::umma_commit(&bar.acc_full[buf]);
+              products(tmem, at, bd, idesc_both, false);
+              moe::umma_commit(&bar.empty[s]);
             }
-            __syncwarp();
+          } else {
+            ok = wait(&bar.full[s], ph, 6);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+              // the accumulator's uses so far: a half's own one a chunk, or two in turn
+              const int buf = HALVES == 2 ? h : static_cast<int>(chunk & 1);
+              const int64_t used = HALVES == 2 ? chunk : chunk >> 1;
+              if (kc == 0 && used > 0) ok = ok && wait(&bar.acc_empty[buf], (used - 1) & 1, 7);
+              if (!ok) break;
+              moe::tc_fence_after();
+              if (moe::elect_one()) {
+                products(tmem + buf * p.half, at, bd + h * half_at, idesc, kc == 0);
+                if (h == HALVES - 1) moe::umma_commit(&bar.empty[s]);
+                if (last) moe::umma_commit(&bar.acc_full[buf]);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
           }
-          if (++sa == kA16) sa = 0, pa ^= 1u;
-          sb += 2;
-          if (sb >= L::kSlots) sb -= L::kSlots, pb ^= 1u;
+          __syncwarp();
+          if (++s == L::kSteps) s = 0, ph ^= 1u;
           if (last) ++chunk, kc = 0;
           else ++kc;
         }
@@ -277,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     const int row = (warp - 4) * 32 + lane;
     const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kAccCols;
     const int64_t mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0, n_stages = mine * (kb1 - kb0);
-    int s8 = 0, sa = 0;
-    uint32_t p8 = 0, pa = 0;
+    int s8 = 0, s = 0;
+    uint32_t p8 = 0, ph = 0;
     uint4 c[8];
     auto load = [&]() {
       if (!wait(&bar.a8_full[s8], p8, 9)) return false;
@@ -292,21 +320,21 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     };
     bool ok = n_stages > 0 && load();
     for (int64_t k = 0; ok && k < n_stages; ++k) {
-      if (k >= kA16 && !wait(&bar.a16_empty[sa], pa ^ 1u, 10)) break;
+      if (k >= L::kSteps && !wait(&bar.empty[s], ph ^ 1u, 10)) break;
       moe::tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t v[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) widen16(c[4 * h + j], v + 8 * j);
-        moe::tmem_st32(to + sa * kA16Cols + 32 * h, v);
+        moe::tmem_st32(to + s * kA16Cols + 32 * h, v);
       }
       if (k + 1 < n_stages) ok = load();
       moe::tmem_st_wait();  // also on the way out after a wait that gave up: no store left in flight
       moe::tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) moe::mbar_arrive(&bar.a16_full[sa]);
-      if (++sa == kA16) sa = 0, pa ^= 1u;
+      if (ok && lane == 0) moe::mbar_arrive(&bar.full[s]);
+      if (++s == L::kSteps) s = 0, ph ^= 1u;
     }
   } else {
     if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
@@ -333,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
           for (int j = 0; j < 4; ++j) {
             if (64 * side + 16 * j < p.half) {
               uint32_t v[16];
-              moe::tmem_ld16(from + buf * kHalf + 16 * j, v);
+              moe::tmem_ld16(from + buf * p.half + 16 * j, v);
 #pragma unroll
               for (int e = 0; e < 16; ++e) acc[h][16 * j + e] += __float2int_rn(__uint_as_float(v[e]));
             }
@@ -357,12 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       const float ws = n < a.n ? scale_at(a.w_scale, n, a.scale_dtype) : 0.0f;
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
-        const int most = min(min(64, p.half - 64 * side), a.m - m0 - h * p.half);  // tokens of mine that there are
-        const int64_t row = m0 + h * p.half;
-#pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (j < most && n < a.n)
-            store_y(a.y, (row + j) * a.n + n, scaled(acc[h][j], ws, __ldg(a.x_scale + row + j)), a.out_dtype);
+        const int row = m0 + h * p.half;
+        const int most = min(min(64, p.half - 64 * side), a.m - row);  // tokens of mine that there are
+        // their scales: a lane holds two, and hands them round
+        const float xs0 = lane < most ? __ldg(a.x_scale + row + lane) : 0.0f;
+        const float xs1 = lane + 32 < most ? __ldg(a.x_scale + row + lane + 32) : 0.0f;
+        const int64_t at = static_cast<int64_t>(row) * a.n + n;
+        if (a.out_dtype == MOE_LAYER_FP32) write_tokens(static_cast<float*>(a.y) + at, a.n, acc[h], ws, xs0, xs1, most, n < a.n);
+        else if (a.out_dtype == MOE_LAYER_BF16)
+          write_tokens(static_cast<__nv_bfloat16*>(a.y) + at, a.n, acc[h], ws, xs0, xs1, most, n < a.n);
+        else write_tokens(static_cast<__half*>(a.y) + at, a.n, acc[h], ws, xs0, xs1, most, n < a.n);
       }
     }
   }
@@ -441,7 +473,7 @@ cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cu
   Params p{a, static_cast<int32_t*>(ws), shape.half, shape.blocks, shape.tiles};
   Maps maps;
   if (!moe::encode_2d(&maps.w, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.n, a.k, kStage, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !moe::encode_2d(&maps.x, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.m, a.k, kAtom, shape.half,
+      !moe::encode_2d(&maps.x, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.m, a.k, kAtom, shape.halves * shape.half,
                       CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   void* args[] = {&arg, &x16, &p.status};
