@@ -26,13 +26,13 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D row-major [rows][cols] tensor, box {box_cols, box_rows}
+// 2-D row-major [rows][cols] tensor, rows `stride` elements apart (dense without it), box {box_cols, box_rows}
 inline bool encode_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, size_t elem, uint64_t rows, uint64_t cols,
-                      uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw) {
+                      uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw, uint64_t stride = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * elem};
+  const cuuint64_t strides[1] = {(stride ? stride : cols) * elem};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,

@@ -9,8 +9,9 @@
 // A tile is 128 weight rows (M, the tensor memory's lanes) by up to 256 tokens (N, in
 // one or two halves of at most 128 columns).  Weights arrive as int8 by TMA and are
 // converted in the CTA into tensor memory, the products' A operand, so that they
-// cross memory and L2 as bytes.  Tokens are converted once by a kernel before this
-// one, into the workspace, and arrive as f16 in shared memory.
+// cross memory and L2 as bytes.  Tokens are the B operand, f16 in shared memory: up to
+// 64 of them arrive as int8 too and are converted by every CTA; more are converted
+// once, by a kernel before this one into the workspace, and arrive as f16.
 // The two halves of a wide tile have an accumulator each, side by side: most steps of
 // 128 k multiply both at once, the first and the last of a 1024 k the first half
 // before the second, so that one is drained while the other's products run.  A tile
@@ -19,7 +20,9 @@
 // a wait, 40 a product): weights and tokens of a step complete one barrier, and its
 // products one other.
 // Roles: warp 0 copies weights, warp 2 copies tokens, warp 1 issues products, warps
-// 4..7 convert weights (a row a thread), warps 8..15 drain and write.
+// 4..7 convert weights (a row a thread), warps 8..15 drain and write.  Up to 64 tokens
+// warps 4..7 and 8..11 convert weights and tokens of every other step, and warps
+// 12..15 drain: one group's chain of waits, loads and stores is 850 cycles a step.
 // Where there are fewer tiles than SMs a cluster shares k out, and adds its int32
 // sums up over distributed shared memory, a share of the tile's columns each.
 #include "w8_linear.cuh"
@@ -31,45 +34,53 @@ namespace moe_layer {
 namespace {
 
 constexpr int kRows = 128;          // weight rows of a tile
-constexpr int kHalf = 128;          // tokens of a half at most
 constexpr int kStage = 128;         // k of a weight stage
 constexpr int kAtom = 64;           // k of one 128-byte row of f16
 constexpr int kChunk = 1024 / kStage;  // stages that a sum stays exact for
 constexpr int kA16Cols = kStage / 2;  // of a converted weight stage in tensor memory
-constexpr int kAccCols = 2 * kHalf;
 constexpr int kTmemCols = 512;
 constexpr int kThreads = 512;
-constexpr int kConvWarps = 4, kDrainWarps = 8;
 // Registers a thread where a tile has two halves: 128 at launch, and what the drain warps have more the others give.
 // (With one half nobody needs more, and the sums over a cluster are every warp's.)
-constexpr int kRoleRegs = 72, kConvRegs = 104, kDrainRegs = 168;
+constexpr int kRoleRegs = 64, kConvRegs = 96, kDrainRegs = 176;
 static_assert(128 * kRoleRegs + 128 * kConvRegs + 256 * kDrainRegs <= kThreads * 128, "the split fits what the launch has");
 constexpr int kA8Bytes = kRows * kStage;
 constexpr int kSite = 2 << 8;       // of the waits, in the status
+constexpr float kNan = NAN;
+constexpr uint32_t kMostParts = 8;  // CTAs that share k out
 
-// HALVES: of a tile's tokens.  Shared memory: tokens of each step, weight stages, barriers
-template <int HALVES>
+// How a tile's tokens lie: up to 64, up to 128, or two halves
+enum Form { kFew = 0, kOne = 1, kTwo = 2 };
+
+// Shared memory: tokens of each step, weight stages, barriers
+template <int FORM>
 struct Layout {
-  static constexpr int kAtomBytes = HALVES * kHalf * kAtom * 2;
-  static constexpr int kSteps = HALVES == 2 ? 3 : 4;  // tokens in shared memory, converted weights in tensor memory
-  static constexpr int kA8 = HALVES == 2 ? 2 : 6;     // weights as they arrive
-  static constexpr int kOffA8 = kSteps * 2 * kAtomBytes, kOffBar = kOffA8 + kA8 * kA8Bytes;
+  static constexpr int kHalves = FORM == kTwo ? 2 : 1;
+  static constexpr int kHalf = FORM == kFew ? 64 : 128;  // tokens of a half at most
+  static constexpr int kAtomBytes = kHalves * kHalf * kAtom * 2;
+  static constexpr int kSteps = FORM == kTwo ? 3 : 4;  // of tokens, and of converted weights
+  static constexpr int kA8 = FORM == kTwo ? 2 : 6;     // weights (up to 64 tokens: and tokens) as they arrive
+  static constexpr int kStageBytes = kA8Bytes + (FORM == kFew ? kHalf * kStage : 0);
+  static constexpr int kOffA8 = kSteps * 2 * kAtomBytes, kOffBar = kOffA8 + kA8 * kStageBytes;
   static constexpr int kBytes = kOffBar + 512;
+  static constexpr int kAccCols = 2 * kHalf;
+  static constexpr int kDrainWarp0 = FORM == kFew ? 12 : 8, kDrainWarps = 16 - kDrainWarp0, kConvGroups = kDrainWarp0 / 4 - 1;
+  static_assert(kSteps % kConvGroups == 0 && kA8 % kConvGroups == 0, "a group's slots");
   static_assert(kBytes + 1024 <= kMaxSmem, "shared memory");
   static_assert(kAccCols + kSteps * kA16Cols <= kTmemCols, "tensor memory");
+  static_assert(kOffBar >= kHalf * kRows * 4, "the sums of a tile of one half fit the rings");
 };
-static_assert(Layout<1>::kOffBar >= kHalf * kRows * 4, "the sums of a tile of one half fit the rings");
 
 struct Barriers {
-  uint64_t a8_full[8], a8_empty[8], full[4], empty[4], acc_full[2], acc_empty[2], drain;
+  uint64_t a8_full[6], a8_empty[6], full[4], empty[4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
-  int abort;
+  int abort, broken;
 };
 static_assert(sizeof(Barriers) <= 512, "");
 
 struct alignas(64) Maps {
   CUtensorMap w;  // int8 [n, k], box {128, 128}, 128-byte swizzle
-  CUtensorMap x;  // f16 [m, k], box {64, tokens of a tile}, 128-byte swizzle
+  CUtensorMap x;  // f16 [m, k], box {64, tokens of a tile}, or int8, box {128, tokens of a tile}; 128-byte swizzle
 };
 
 struct Params {
@@ -131,6 +142,36 @@ __device__ __forceinline__ void write_tokens(T* y, int64_t stride, const int32_t
   }
 }
 
+// 32 columns of this warp's 32 lanes, and the wait for them
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// the two halves of a cluster barrier
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// 16 bytes at shared address `at` of CTA `rank` of the cluster
+__device__ __forceinline__ int4 cluster_read4(uint32_t at, uint32_t rank) {
+  uint32_t remote;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(remote)
+               : "memory");
+  return v;
+}
+
 // The same for the steps, whose barriers the converters complete too: where they have given up, a phase never completes
 // and the copies get a while to land.
 __device__ __forceinline__ void drain_steps(uint64_t* full, int n, int s, uint32_t ph, bool wrapped, volatile int* abort,
@@ -143,9 +184,10 @@ __device__ __forceinline__ void drain_steps(uint64_t* full, int n, int s, uint32
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-template <int HALVES>
+template <int FORM>
 __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
-  using L = Layout<HALVES>;
+  using L = Layout<FORM>;
+  constexpr int HALVES = L::kHalves, kAccCols = L::kAccCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (moe::smem_u32(smem_raw) & 1023u)) & 1023u);
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + L::kOffBar);
@@ -159,21 +201,23 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   const int kb0 = static_cast<int>(static_cast<int64_t>(stages) * rank / parts),
             kb1 = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / parts);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kA8; ++i) {
-      moe::mbar_init(&bar.a8_full[i], 1);
-      moe::mbar_init(&bar.a8_empty[i], kConvWarps);
+  if (warp == 0) {
+    if (lane < L::kA8) {
+      moe::mbar_init(&bar.a8_full[lane], 1);
+      moe::mbar_init(&bar.a8_empty[lane], 4);
     }
-    for (int i = 0; i < L::kSteps; ++i) {
-      moe::mbar_init(&bar.full[i], kConvWarps + 1);
-      moe::mbar_init(&bar.empty[i], 1);
+    if (lane < L::kSteps) {
+      moe::mbar_init(&bar.full[lane], FORM == kFew ? 4 : 5);  // the converting warps, and the tokens' copy
+      moe::mbar_init(&bar.empty[lane], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      moe::mbar_init(&bar.acc_full[i], 1);
-      moe::mbar_init(&bar.acc_empty[i], kDrainWarps);
+    if (lane < 2) {
+      moe::mbar_init(&bar.acc_full[lane], 1);
+      moe::mbar_init(&bar.acc_empty[lane], L::kDrainWarps);
     }
-    moe::mbar_init(&bar.drain, 1);
-    bar.abort = 0;
+    if (lane == 0) {
+      moe::mbar_init(&bar.drain, 1);
+      bar.abort = bar.broken = 0;
+    }
     moe::fence_barrier_init();
   }
   if (warp == 1) moe::tmem_alloc(&bar.tmem, kTmemCols);
@@ -182,11 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   const uint32_t tmem = bar.tmem;
   volatile int* abort = &bar.abort;
   // A bounded wait of a whole warp, with one answer for all of its lanes.  The status words are the widening kernel's
-  // to clear: what is reported before it is done would be lost, but nothing waits that long before it.
+  // to clear: what is reported before it is done would be lost, but nothing waits that long before it.  (Without one
+  // there are no status words.)  A tile whose wait gave up is written as NaN.
   auto wait = [&](uint64_t* b, uint32_t parity, int site) {
     return __all_sync(0xffffffffu, moe::mbar_wait_bounded(b, parity, abort, p.status, kSite + site)) != 0;
   };
 
+  if constexpr (FORM == kFew) grid_dependency_wait();  // no kernel of this call's own has done so
   if (warp < 4) {
     if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
     if (warp == 0) {
@@ -203,15 +249,17 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
             break;
           }
           if (moe::elect_one()) {
-            moe::mbar_arrive_expect_tx(&bar.a8_full[s], kA8Bytes);
-            moe::tma_load_2d(smem + L::kOffA8 + s * kA8Bytes, &maps.w, kb * kStage, n0, &bar.a8_full[s]);
+            uint8_t* to = smem + L::kOffA8 + s * L::kStageBytes;
+            moe::mbar_arrive_expect_tx(&bar.a8_full[s], kA8Bytes + (FORM == kFew ? p.half * kStage : 0));
+            moe::tma_load_2d(to, &maps.w, kb * kStage, n0, &bar.a8_full[s]);
+            if (FORM == kFew) moe::tma_load_2d(to + kA8Bytes, &maps.x, kb * kStage, 0, &bar.a8_full[s]);
           }
           __syncwarp();
           if (++s == L::kA8) s = 0, ph ^= 1u, wrapped = true;
         }
       }
       drain_ring(bar.a8_full, L::kA8, s, ph, wrapped, p.status, kSite + 2);
-    } else if (warp == 2) {
+    } else if (FORM != kFew && warp == 2) {
       // ---------------------------------------------------- tokens
       grid_dependency_wait();
       int s = 0;
@@ -297,29 +345,42 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       __syncwarp();
       moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 8);
     }
-  } else if (warp < 8) {
+  } else if (warp < L::kDrainWarp0) {
     if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-    // ------------------------------------------------------ weights to f16, a row a thread, into tensor memory
-    // (16-byte chunk j of row r lies at chunk j ^ (r % 8) of its 128 bytes).  The next stage's codes are loaded while
-    // this one's stores are on their way.
-    const int row = (warp - 4) * 32 + lane;
+    // ------------------------------------------------------ weights to f16, a row a thread, into tensor memory;
+    // 16-byte chunk j of row r lies at chunk j ^ (r % 8) of its 128 bytes.  The next codes are loaded while these ones'
+    // stores are on their way.  Two groups take steps in turn.
+    constexpr int kGroups = L::kConvGroups;
+    const int row = (warp & 3) * 32 + lane, group = (warp >> 2) - 1;
     const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kAccCols;
     const int64_t mine = first < p.tiles ? (p.tiles - first + step - 1) / step : 0, n_stages = mine * (kb1 - kb0);
-    int s8 = 0, s = 0;
+    int s8 = group, s = group;
     uint32_t p8 = 0, ph = 0;
     uint4 c[8];
+    // Tokens (up to 64): 16 codes of a token are two chunks of its f16 row; a thread has one of each 16 tokens.
+    const int tch = threadIdx.x & 7, tok0 = (threadIdx.x & 127) >> 3;  // (tok0 + 16 i) % 8 = tok0 % 8
+    const int tok_from = kA8Bytes + tok0 * kStage + ((tch ^ (tok0 & 7)) << 4);
+    const int tok_to = (tch >> 2) * L::kAtomBytes + tok0 * 128;
+    const int j0 = (((tch & 3) * 2) ^ (tok0 & 7)) << 4, j1 = (((tch & 3) * 2 + 1) ^ (tok0 & 7)) << 4;
+    uint4 x[4];
     auto load = [&]() {
       if (!wait(&bar.a8_full[s8], p8, 9)) return false;
-      const uint8_t* from = smem + L::kOffA8 + s8 * kA8Bytes + row * kStage;
+      const uint8_t* stage = smem + L::kOffA8 + s8 * L::kStageBytes;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(from + ((j ^ (row & 7)) << 4));
+      for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(stage + row * kStage + ((j ^ (row & 7)) << 4));
+      if constexpr (FORM == kFew) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok0 + 16 * i < p.half) x[i] = *reinterpret_cast<const uint4*>(stage + tok_from + i * 16 * kStage);
+      }
       __syncwarp();
       if (lane == 0) moe::mbar_arrive(&bar.a8_empty[s8]);
-      if (++s8 == L::kA8) s8 = 0, p8 ^= 1u;
+      s8 += kGroups;
+      if (s8 >= L::kA8) s8 -= L::kA8, p8 ^= 1u;
       return true;
     };
-    bool ok = n_stages > 0 && load();
-    for (int64_t k = 0; ok && k < n_stages; ++k) {
+    bool ok = group < n_stages && load();
+    for (int64_t k = group; ok && k < n_stages; k += kGroups) {
       if (k >= L::kSteps && !wait(&bar.empty[s], ph ^ 1u, 10)) break;
       moe::tc_fence_after();
 #pragma unroll
@@ -329,21 +390,40 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         for (int j = 0; j < 4; ++j) widen16(c[4 * h + j], v + 8 * j);
         moe::tmem_st32(to + s * kA16Cols + 32 * h, v);
       }
-      if (k + 1 < n_stages) ok = load();
+      if constexpr (FORM == kFew) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (tok0 + 16 * i < p.half) {
+            uint32_t o[8];
+            widen16(x[i], o);
+            uint8_t* at = smem + 2 * s * L::kAtomBytes + tok_to + i * 16 * 128;
+            *reinterpret_cast<uint4*>(at + j0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(at + j1) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        moe::fence_proxy_async_smem();
+      }
+      if (k + kGroups < n_stages) ok = load();
       moe::tmem_st_wait();  // also on the way out after a wait that gave up: no store left in flight
       moe::tc_fence_before();
       __syncwarp();
       if (ok && lane == 0) moe::mbar_arrive(&bar.full[s]);
-      if (++s == L::kSteps) s = 0, ph ^= 1u;
+      s += kGroups;
+      if (s >= L::kSteps) s -= L::kSteps, ph ^= 1u;
     }
   } else {
     if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
     // ------------------------------------------------------ sums, and what they are written as
-    const int q = warp & 3, side = (warp - 8) >> 2;  // lanes 32 q .., columns 64 side .. of each half
+    const int q = warp & 3, side = (warp - L::kDrainWarp0) >> 2;  // lanes 32 q .., columns 64 side .. of each half
     const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64 * side;
+    auto release = [&](int buf) {
+      moe::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) moe::mbar_arrive(&bar.acc_empty[buf]);
+    };
     int64_t chunk = 0;
     bool ok = true;
-    for (int64_t it = first; ok && it < p.tiles; it += step) {
+    for (int64_t it = first; it < p.tiles; it += step) {
       int32_t acc[HALVES][64];  // 64 tokens of each half, of one weight row
 #pragma unroll
       for (int h = 0; h < HALVES; ++h)
@@ -358,17 +438,17 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
           if (!ok) break;
           moe::tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (64 * side + 16 * j < p.half) {
-              uint32_t v[16];
-              moe::tmem_ld16(from + buf * p.half + 16 * j, v);
+          for (int j = 0; j < 2; ++j) {
+            // columns past the half's last are read along with it, and not looked at
+            if (64 * side + 32 * j < p.half) {
+              uint32_t v[32];
+              tmem_ld32(from + buf * p.half + 32 * j, v);
+              if (j == 1 || 64 * side + 32 >= p.half) release(buf);  // what is still to come is in registers
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[h][16 * j + e] += __float2int_rn(__uint_as_float(v[e]));
+              for (int e = 0; e < 32; ++e) acc[h][32 * j + e] += __float2int_rn(__uint_as_float(v[e]));
             }
           }
-          moe::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) moe::mbar_arrive(&bar.acc_empty[buf]);
+          if (64 * side >= p.half) release(buf);
         }
       }
       if (parts > 1) {
@@ -377,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 64; ++j)
           if (64 * side + j < p.half) sums[(64 * side + j) * kRows + 32 * q + lane] = acc[0][j];
+        if (!ok && lane == 0) bar.broken = 1;
         break;
       }
-      if (!ok) break;
       const int n = static_cast<int>(it / p.blocks) * kRows + 32 * q + lane;
       const int m0 = static_cast<int>(it % p.blocks) * p.half * HALVES + 64 * side;
-      const float ws = n < a.n ? scale_at(a.w_scale, n, a.scale_dtype) : 0.0f;
+      const float ws = !ok ? kNan : n < a.n ? scale_at(a.w_scale, n, a.scale_dtype) : 0.0f;
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
         const int row = m0 + h * p.half;
@@ -405,84 +485,144 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   }
   if constexpr (HALVES == 1) {
     if (parts > 1) {
-      // each CTA adds up its share of the tokens
-      const int32_t* sums = reinterpret_cast<const int32_t*>(smem);
-      cluster_sync();
-      const int m0 = static_cast<int>(first % p.blocks) * p.half, row = threadIdx.x & (kRows - 1);
+      // each CTA adds up its share of the tokens, a thread four weight rows of one
+      const int m0 = static_cast<int>(first % p.blocks) * p.half, row = (threadIdx.x & 31) * 4;
       const int n = static_cast<int>(first / p.blocks) * kRows + row;
-      const int c0 = static_cast<int>(p.half * rank / parts), c1 = static_cast<int>(p.half * (rank + 1) / parts);
-      const float ws = n < a.n ? scale_at(a.w_scale, n, a.scale_dtype) : 0.0f;
-      for (int c = c0 + static_cast<int>(threadIdx.x / kRows); c < c1; c += kThreads / kRows) {
-        int32_t sum = 0;
-        for (uint32_t r = 0; r < parts; ++r)
-          sum += __float_as_int(cluster_read(moe::smem_u32(sums + c * kRows + row), r));
-        if (n < a.n && m0 + c < a.m)
-          store_y(a.y, static_cast<int64_t>(m0 + c) * a.n + n, scaled(sum, ws, __ldg(a.x_scale + m0 + c)), a.out_dtype);
+      const int c0 = static_cast<int>(p.half * rank / parts), c1 = min(static_cast<int>(p.half * (rank + 1) / parts), a.m - m0);
+      static_assert(L::kHalf <= 8 * (kThreads / 32), "tokens of a warp");
+      float ws[4], xs[4];  // (two CTAs at least: four tokens a warp at most)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + warp + j * (kThreads / 32);
+        ws[j] = n + j < a.n ? scale_at(a.w_scale, n + j, a.scale_dtype) : 0.0f;
+        xs[j] = c < c1 ? __ldg(a.x_scale + m0 + c) : 0.0f;
       }
-      cluster_sync();  // no CTA ends while its sums are read
+      cluster_sync();
+      int broken = 0;
+      int4 sum[4];
+#pragma unroll
+      for (uint32_t r = 0; r < kMostParts; ++r)
+        if (r < parts) broken |= __float_as_int(cluster_read(moe::smem_u32(&bar.broken), r));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + warp + j * (kThreads / 32);
+        int4 part[kMostParts];
+        sum[j] = make_int4(0, 0, 0, 0);
+        if (c >= c1) continue;
+#pragma unroll
+        for (uint32_t r = 0; r < kMostParts; ++r)
+          if (r < parts) part[r] = cluster_read4(moe::smem_u32(smem) + (c * kRows + row) * 4, r);
+#pragma unroll
+        for (uint32_t r = 0; r < kMostParts; ++r)
+          if (r < parts) sum[j].x += part[r].x, sum[j].y += part[r].y, sum[j].z += part[r].z, sum[j].w += part[r].w;
+      }
+      cluster_arrive();  // what this CTA reads of the others has been read
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + warp + j * (kThreads / 32);
+        const int32_t v[4] = {sum[j].x, sum[j].y, sum[j].z, sum[j].w};
+        if (c >= c1) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.n)
+            store_y(a.y, static_cast<int64_t>(m0 + c) * a.n + n + e, scaled(v[e], broken ? kNan : ws[e], xs[j]), a.out_dtype);
+      }
+      cluster_wait();  // no CTA ends while its sums are read
     }
   }
   grid_dependency_wait();  // the next launch takes this grid's end for the widening kernel's too
 }
 
 struct Shape {
-  int halves, half, blocks, parts;
+  int form, half, blocks;
   int64_t tiles;
 };
-Shape shape_of(int m, int n, int k, int num_sms) {
+Shape shape_of(int m, int n, int num_sms) {
   const int64_t rows = (static_cast<int64_t>(n) + kRows - 1) / kRows;
+  if (m <= 128) return Shape{m <= 64 ? kFew : kOne, (m + 15) / 16 * 16, 1, rows};
+  // tiles as wide as they go, narrower ones where that fills the last round of SMs better
   Shape s{};
-  if (m <= kHalf) {
-    s = Shape{1, (m + 15) / 16 * 16, 1, 1, rows};
-  } else {
-    // tiles as wide as they go, narrower ones where that fills the last round of SMs better
-    double best = 0;
-    for (int blocks = (m + 255) / 256; blocks <= (m + 255) / 256 * 2; ++blocks) {
-      const int half = ((m + blocks - 1) / blocks + 31) / 32 * 16;
-      const int64_t tiles = rows * ((m + 2 * half - 1) / (2 * half));
-      const double cost = static_cast<double>((tiles + num_sms - 1) / num_sms) * (2 * half + 16);
-      if (best == 0 || cost < best) best = cost, s = Shape{2, half, (m + 2 * half - 1) / (2 * half), 1, tiles};
-    }
+  double best = 0;
+  for (int blocks = (m + 255) / 256; blocks <= (m + 255) / 256 * 2; ++blocks) {
+    const int half = ((m + blocks - 1) / blocks + 31) / 32 * 16, real = (m + 2 * half - 1) / (2 * half);
+    const double cost = static_cast<double>((rows * real + num_sms - 1) / num_sms) * (2 * half + 16);
+    if (best == 0 || cost < best) best = cost, s = Shape{kTwo, half, real, rows * real};
   }
-  const int stages = (k + kStage - 1) / kStage;
-  if (s.halves == 1)
-    while (s.parts < 8 && s.tiles * s.parts * 2 <= num_sms && stages >= s.parts * 4) s.parts *= 2;
   return s;
 }
 
-template <int HALVES>
-cudaError_t launch_tiles(const Maps& maps, const Params& p, int parts, int num_sms, cudaStream_t s) {
+// How many clusters of `parts` CTAs the current device runs at once; asked once a device and size.
+template <int FORM>
+int clusters_at_once(int parts) {
+  static std::atomic<int> known[64][9];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev][parts].load(std::memory_order_relaxed)) > 0) return n - 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<FORM>::kBytes + 1024;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, w8_tc_kernel<FORM>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (dev < 64) known[dev][parts].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int FORM>
+cudaError_t launch_tiles(const Maps& maps, const Params& p, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  const void* k = (const void*)w8_tc_kernel<HALVES>;
+  const void* k = (const void*)w8_tc_kernel<FORM>;
   if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
+  int parts = 1;
+  if constexpr (FORM != kTwo) {
+    // clusters that share k out, as large as all of them run at once and have two steps a CTA
+    const int steps = (p.a.k + kStage - 1) / kStage;
+    for (int c = kMostParts; c > 1 && parts == 1; --c)
+      if (p.tiles * c <= num_sms && steps >= 2 * c && clusters_at_once<FORM>(c) >= p.tiles) parts = c;
+  }
   Maps m = maps;
   Params arg = p;
   void* args[] = {&m, &arg};
   const int64_t grid = parts > 1 ? p.tiles * parts : p.tiles < num_sms ? p.tiles : num_sms;
-  return launch_after(k, dim3(static_cast<unsigned>(grid)), dim3(kThreads), args, Layout<HALVES>::kBytes + 1024, s, parts);
+  return launch_after(k, dim3(static_cast<unsigned>(grid)), dim3(kThreads), args, Layout<FORM>::kBytes + 1024, s, parts);
 }
 
 }  // namespace
 
-size_t w8_tc_workspace(int m, int, int k, int) { return 256 + static_cast<size_t>(m) * k * 2; }
+size_t w8_tc_workspace(int m, int, int k, int) { return m <= 64 ? 0 : 256 + static_cast<size_t>(m) * k * 2; }
 
 cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cudaStream_t s) {
-  const Shape shape = shape_of(a.m, a.n, a.k, num_sms);
-  moe_layer_w8_args_t arg = a;
-  __half* x16 = reinterpret_cast<__half*>(static_cast<char*>(ws) + 256);
-  Params p{a, static_cast<int32_t*>(ws), shape.half, shape.blocks, shape.tiles};
-  Maps maps;
-  if (!moe::encode_2d(&maps.w, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.n, a.k, kStage, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !moe::encode_2d(&maps.x, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.m, a.k, kAtom, shape.halves * shape.half,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+  const Shape shape = shape_of(a.m, a.n, num_sms);
+  Maps maps{};
+  if (!moe::encode_2d(&maps.w, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.n, a.k, kStage, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  Params p{a, nullptr, shape.half, shape.blocks, shape.tiles};
+  if (shape.form == kFew) {
+    if (!moe::encode_2d(&maps.x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.m, a.k, kStage, shape.half,
+                        CU_TENSOR_MAP_SWIZZLE_128B, a.x_stride))
+      return cudaErrorInvalidValue;
+    return launch_tiles<kFew>(maps, p, num_sms, s);
+  }
+  p.status = static_cast<int32_t*>(ws);
+  __half* x16 = reinterpret_cast<__half*>(static_cast<char*>(ws) + 256);
+  if (!moe::encode_2d(&maps.x, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.m, a.k, kAtom,
+                      shape.half * (shape.form == kTwo ? 2 : 1), CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  moe_layer_w8_args_t arg = a;
   void* args[] = {&arg, &x16, &p.status};
   const int64_t chunks = static_cast<int64_t>(a.m) * (a.k / 16);
   const cudaError_t e = launch_after((const void*)w8_widen_kernel, dim3(static_cast<unsigned>((chunks + 255) / 256)), dim3(256),
                                      args, 0, s);
   if (e != cudaSuccess) return e;
-  return shape.halves == 2 ? launch_tiles<2>(maps, p, shape.parts, num_sms, s)
-                           : launch_tiles<1>(maps, p, shape.parts, num_sms, s);
+  return shape.form == kTwo ? launch_tiles<kTwo>(maps, p, num_sms, s) : launch_tiles<kOne>(maps, p, num_sms, s);
 }
 
 }  // namespace moe_layer
