@@ -1,16 +1,19 @@
 // Log probabilities of given tokens, entropy, and the top alternatives of rows
 // of logits, in one pass over them.
 //
-// Every thread keeps a running maximum M of what it has seen and the sums
-//   S = sum exp(l - M),  U = sum exp(l - M) (l - M)
-// (in powers of two), moved to a new M as often as one turns up; sums of threads,
-// warps and CTAs join the same way.  logprob(c) = (l_c - M) - log S, and the
-// entropy is log S - U / S.
+// Every thread keeps the largest logit M that it has seen and the sums
+//   S = sum 2^d,  U = sum 2^d d,   d = (l - M) log2(e),
+// moved to a new M as often as a larger logit turns up; sums of threads, warps and
+// CTAs join the same way.  log p(c) = (l_c - M) - log S and the entropy is log S - (U /
+// S) ln 2.  -inf is raised to a number that gives 2^d = 0 and keeps 2^d d from being
+// NaN, except where M itself is so far out (kHuge, kFarDown) that this would change it.
 // The top logits are kept by warps: lane r holds the r-th best of what the warp
 // has seen, as one number that orders by value and then by the lower index.  A
 // thread's maximum of its 64 bytes, which the sums need anyway, says whether any
-// of them can enter; the worst entry of any warp's full list bounds all of them.
-// A row is one CTA's, or a cluster's where there are few rows.
+// of them can enter; only the elements of lanes that say so are looked at.
+// A row is a CTA's, or a cluster's where there are few rows, or a warp's where it is short.
+#include <type_traits>
+
 #include "layer_ops.cuh"
 
 namespace moe_layer {
@@ -18,9 +21,11 @@ namespace {
 
 constexpr int kMaxWarps = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kBlocks = 4;  // 16-byte blocks that a thread has in flight
+constexpr int kRowWarps = 4;  // rows of a CTA whose warps have one each
+constexpr int kBlocks = 4;    // 16-byte blocks that a thread has in flight
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -INFINITY;
+constexpr float kHuge = 1e30f;
 
 // Larger for larger values (-0 as 0); NaN does not get here.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -34,14 +39,104 @@ __device__ __forceinline__ uint64_t key_of(float v, uint32_t index) {
   return static_cast<uint64_t>(order_of(v)) << 32 | static_cast<uint32_t>(~index);
 }
 
-struct Sums {
-  float m, s, u;  // u in powers of two
+template <typename T>
+struct Type;
+// kDown: what -inf is raised to, so that d stays finite; kFarDown: nothing is lost by that where M is above it
+template <>
+struct Type<__nv_bfloat16> {
+  static constexpr float kFarDown = -1e30f;
+  static constexpr uint32_t kDown = 0xFE96FE96u;  // -1e38
+  static __device__ __forceinline__ uint32_t raise(uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(kDown));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
+template <>
+struct Type<__half> {
+  static constexpr float kFarDown = -60000.0f;
+  static constexpr uint32_t kDown = 0xFBFFFBFFu;  // -65504
+  static __device__ __forceinline__ uint32_t raise(uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(kDown));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+};
+template <>
+struct Type<float> {
+  static constexpr float kFarDown = -1e30f;
+  static __device__ __forceinline__ uint32_t raise(uint32_t w) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(w)), "f"(-1e38f));
+    return __float_as_uint(r);
+  }
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float widen(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return static_cast<float>(v);
+}
+// two elements from word w on: both of it, or (fp32) it and the next
+template <typename T>
+__device__ __forceinline__ float2 pair_at(const uint32_t* w) {
+  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+  else return unpack2<T>(w[0]);
+}
+
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+struct Sums {
+  float m, s, u;  // m: the largest logit
+};
+template <typename T>
+__device__ __forceinline__ bool far_out(float m) { return !(m > Type<T>::kFarDown && m < kHuge); }
+// d of a logit against the largest, m, or what sums with the reference l are to be multiplied by for m, as a power of two
+__device__ __forceinline__ float exponent(float l, float m) { return __fmul_rn(__fsub_rn(l, m), kLog2e); }
 // the sums of a and b with one reference; a side without elements (m = -inf) adds nothing
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   const float m = fmaxf(a.m, b.m);
   if (m == kNone) return Sums{m, __fadd_rn(a.s, b.s), 0.0f};  // a NaN stays one
-  const float da = fmaxf(__fmul_rn(a.m - m, kLog2e), -200.0f), db = fmaxf(__fmul_rn(b.m - m, kLog2e), -200.0f);
+  const float da = a.m == m ? 0.0f : fmaxf(exponent(a.m, m), -200.0f), db = b.m == m ? 0.0f : fmaxf(exponent(b.m, m), -200.0f);
   const float ea = exp2_fast(da), eb = exp2_fast(db);
   Sums r;
   r.m = m;
@@ -83,42 +178,25 @@ __device__ __forceinline__ uint32_t sort_lanes(uint32_t v) {
   return v;
 }
 
-template <typename T>
-struct Block {  // 16 bytes of a row
-  static constexpr int kN = 16 / sizeof(T);
-  __device__ static __forceinline__ void take(const uint4& b, float (&v)[kN]) {
-    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 2) {
-        const float2 f = unpack2<T>(w[j]);
-        v[2 * j] = f.x, v[2 * j + 1] = f.y;
-      } else {
-        v[j] = __uint_as_float(w[j]);
-      }
-    }
-  }
-};
-template <typename T>
-__device__ __forceinline__ float widen(T v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else return static_cast<float>(v);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(const moe_layer_logprobs_args_t a) {
-  constexpr int N = Block<T>::kN, E = N * kBlocks;
-  __shared__ Part s_part;
-  __shared__ Sums s_sums[kMaxWarps];
-  __shared__ uint64_t s_keys[kMaxWarps][32];
+// WARP_ROW: a warp takes a row by itself, kRowWarps rows a CTA
+template <typename T, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WARP_ROW ? 8 : 4)
+    logprobs_kernel(const moe_layer_logprobs_args_t a) {
+  constexpr int N = 16 / sizeof(T), E = N * kBlocks;  // elements of a block, and of a thread's step
+  __shared__ Part s_part[kMaxWarps];  // of warps, then (in the first CTA) of the cluster's CTAs
+  __shared__ uint4 s_raw[WARP_ROW ? kRowWarps : kMaxWarps][32 * kBlocks];
   __shared__ uint32_t s_bound;  // order of a value that `top` logits of the row reach
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  uint32_t rank, ctas;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-  const int64_t row = blockIdx.x / ctas;
+  const int lane = threadIdx.x & 31, own_warp = threadIdx.x >> 5;
+  const int warp = WARP_ROW ? 0 : own_warp, nw = WARP_ROW ? 1 : blockDim.x >> 5;
+  uint32_t rank = 0, ctas = 1;
+  if constexpr (!WARP_ROW) {
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  }
+  const int64_t row = WARP_ROW ? static_cast<int64_t>(blockIdx.x) * kRowWarps + own_warp : blockIdx.x / ctas;
+  if (WARP_ROW && row >= a.rows) return;
   const int top = a.top;
   const T* p = static_cast<const T*>(a.logits) + row * a.logits_stride;
   // The row lies in 16-byte blocks of memory, `off` elements past the start of the first.  The first and the last may
@@ -126,8 +204,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(const moe_l
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
   const int64_t blocks = (off + static_cast<int64_t>(a.vocab) + N - 1) / N;
   const uint4* base = reinterpret_cast<const uint4*>(p - off);
-  if (threadIdx.x == 0) s_bound = 0;
-  __syncthreads();
+  if constexpr (!WARP_ROW) {
+    if (threadIdx.x == 0) s_bound = 0;
+    __syncthreads();
+  }
 
   Sums sum{kNone, 0.0f, 0.0f};
   uint64_t list = 0;              // below every key
@@ -135,71 +215,128 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(const moe_l
   float bound = kNone;            // its value, or a larger one that `top` logits reach: smaller ones need not be looked at
   const int64_t tile = static_cast<int64_t>(nw) * 32 * kBlocks * ctas;
   for (int64_t t0 = (static_cast<int64_t>(rank) * nw + warp) * 32 * kBlocks; t0 < blocks; t0 += tile) {
-    uint4 raw[kBlocks];
+    uint32_t raw[4 * kBlocks];
+    if (t0 > 0 && t0 + 32 * kBlocks < blocks) {
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const int64_t n = t0 + b * 32 + lane, e = n * N - off;
-      if (e >= 0 && e + N <= a.vocab) raw[b] = __ldcs(base + n);
-    }
-    float v[E];
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const int64_t n = t0 + b * 32 + lane, e = n * N - off;
-      float f[N];
-      if (e >= 0 && e + N <= a.vocab) {
-        Block<T>::take(raw[b], f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) f[j] = e + j >= 0 && e + j < a.vocab ? widen<T>(p[e + j]) : kNone;
+      for (int b = 0; b < kBlocks; ++b) {
+        const uint4 u = __ldcs(base + t0 + b * 32 + lane);
+        raw[4 * b] = u.x, raw[4 * b + 1] = u.y, raw[4 * b + 2] = u.z, raw[4 * b + 3] = u.w;
       }
+    } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[b * N + j] = f[j];
+      for (int b = 0; b < kBlocks; ++b) {
+        const int64_t n = t0 + b * 32 + lane, e = n * N - off;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (e >= 0 && e + N <= a.vocab) {
+          u = __ldcs(base + n);
+          raw[4 * b] = u.x, raw[4 * b + 1] = u.y, raw[4 * b + 2] = u.z, raw[4 * b + 3] = u.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 4) {
+              raw[4 * b + j] = e + j >= 0 && e + j < a.vocab ? __float_as_uint(p[e + j]) : 0xFF800000u;
+            } else {
+              const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+              const uint32_t none = std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;
+              const int64_t i = e + 2 * j;
+              raw[4 * b + j] = (i >= 0 && i < a.vocab ? h[i] : none) |
+                               (i + 1 >= 0 && i + 1 < a.vocab ? h[i + 1] : none) << 16;
+            }
+          }
+        }
+      }
     }
-    float most = v[0];
+    // the largest of these: of the words as they are, then of a word's elements
+    uint32_t top_word = raw[0];
 #pragma unroll
-    for (int j = 1; j < E; ++j) most = fmaxf(most, v[j]);
+    for (int j = 1; j < 4 * kBlocks; ++j) top_word = Type<T>::most(top_word, raw[j]);
+    float most;
+    if constexpr (sizeof(T) == 4) {
+      most = __uint_as_float(top_word);
+    } else {
+      const float2 f = unpack2<T>(top_word);
+      most = fmaxf(f.x, f.y);
+    }
     if (most > sum.m) {
-      const float d = fmaxf(__fmul_rn(sum.m - most, kLog2e), -200.0f), e = exp2_fast(d);
+      const float d = fmaxf(exponent(sum.m, most), -200.0f), e = exp2_fast(d);
       sum.u = __fmul_rn(e, __fmaf_rn(sum.s, d, sum.u));
       sum.s = __fmul_rn(sum.s, e);
       sum.m = most;
     }
-    const float ref = sum.m == kNone ? 0.0f : sum.m;
+    if (!far_out<T>(sum.m)) {
+      const uint64_t scale = pack(kLog2e, kLog2e), less = pack(-sum.m, -sum.m);
+      uint64_t s2 = pack(0.0f, 0.0f), u2 = s2;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float d = __fmul_rn(__fsub_rn(v[j], ref), kLog2e), e = exp2_fast(d);
-      sum.s = __fadd_rn(sum.s, e);
-      sum.u = __fmaf_rn(e, fmaxf(d, -200.0f), sum.u);  // (-inf has e = 0)
+      for (int j = 0; j < E / 2; ++j) {
+        uint32_t w[2];
+        if constexpr (sizeof(T) == 4) w[0] = Type<T>::raise(raw[2 * j]), w[1] = Type<T>::raise(raw[2 * j + 1]);
+        else w[0] = Type<T>::raise(raw[j]);
+        const float2 l = pair_at<T>(w);
+        const uint64_t d2 = mul2(add2(pack(l.x, l.y), less), scale);
+        const float2 d = unpack(d2);
+        const uint64_t e2 = pack(exp2_fast(d.x), exp2_fast(d.y));
+        s2 = add2(s2, e2);
+        u2 = fma2(e2, d2, u2);
+      }
+      const float2 s = unpack(s2), u = unpack(u2);
+      sum.s = __fadd_rn(sum.s, __fadd_rn(s.x, s.y));
+      sum.u = __fadd_rn(sum.u, __fadd_rn(u.x, u.y));
+    } else {
+      const float m = sum.m == kNone ? 0.0f : sum.m;
+#pragma unroll 1
+      for (int j = 0; j < E; ++j) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * kBlocks; ++i)
+          if (i == (sizeof(T) == 4 ? j : j >> 1)) w = raw[i];
+        const uint32_t two[2] = {w, w};
+        const float2 f = pair_at<T>(two);
+        const float d = exponent(j & 1 ? f.y : f.x, m), e = exp2_fast(d);
+        sum.s = __fadd_rn(sum.s, e);
+        sum.u = __fmaf_rn(e, fmaxf(d, -200.0f), sum.u);  // (-inf has e = 0)
+      }
     }
     if (top == 0) continue;
-    bound = fmaxf(bound, value_of(max(*static_cast<volatile uint32_t*>(&s_bound), order_of(kNone))));
+    if constexpr (!WARP_ROW) bound = fmaxf(bound, value_of(max(*static_cast<volatile uint32_t*>(&s_bound), order_of(kNone))));
     uint32_t hit = __ballot_sync(0xffffffffu, most >= bound);
     if (!hit) continue;
     if (__popc(hit) >= top) {  // `top` lanes hold a logit of at least their own maximum
       const uint32_t sorted = sort_lanes(order_of(most));
       bound = fmaxf(bound, value_of(__shfl_sync(0xffffffffu, sorted, top - 1)));
+      hit = __ballot_sync(0xffffffffu, most >= bound);
     }
+    // what these lanes hold goes through shared memory, an element a lane
+    uint4* mine = s_raw[own_warp];
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int64_t e = (t0 + (j / N) * 32 + lane) * N - off + j % N;
-      const bool in = e >= 0 && e < a.vocab && v[j] >= bound;
-      const uint64_t key = in ? key_of(v[j], static_cast<uint32_t>(e)) : 0;
+    for (int b = 0; b < kBlocks; ++b)
+      if (most >= bound) mine[b * 32 + lane] = make_uint4(raw[4 * b], raw[4 * b + 1], raw[4 * b + 2], raw[4 * b + 3]);
+    __syncwarp();
+    while (hit) {
+      const int from = __ffs(hit) - 1;
+      hit &= hit - 1;
+      const int b = lane / N, j = lane % N;  // (a lane past the thread's E elements has none)
+      const int64_t e = (t0 + b * 32 + from) * N - off + j;
+      float v = kNone;
+      if (lane < E) v = widen<T>(reinterpret_cast<const T*>(mine + (b * 32 + from))[j]);
+      const bool in = lane < E && e >= 0 && e < a.vocab && v >= bound;
+      const uint64_t key = in ? key_of(v, static_cast<uint32_t>(e)) : 0;
       uint32_t todo = __ballot_sync(0xffffffffu, key > least);
       while (todo) {
-        const int from = __ffs(todo) - 1;
+        const int at = __ffs(todo) - 1;
         todo &= todo - 1;
-        const uint64_t k = __shfl_sync(0xffffffffu, key, from);
+        const uint64_t k = __shfl_sync(0xffffffffu, key, at);
         if (k <= least) continue;
-        const int at = __popc(__ballot_sync(0xffffffffu, list > k));
+        const int place = __popc(__ballot_sync(0xffffffffu, list > k));
         const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-        list = lane < at ? list : lane == at ? k : up;
+        list = lane < place ? list : lane == place ? k : up;
         least = __shfl_sync(0xffffffffu, list, top - 1);
       }
     }
+    __syncwarp();  // the elements have been read
     if (least) {
       const uint32_t o = static_cast<uint32_t>(least >> 32);
       bound = fmaxf(bound, value_of(o));
-      if (lane == 0) atomicMax(&s_bound, o);
+      if (!WARP_ROW && lane == 0) atomicMax(&s_bound, o);
     }
   }
 
@@ -210,36 +347,42 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(const moe_l
                  __shfl_xor_sync(0xffffffffu, sum.u, o)};
     sum = join(sum, b);
   }
-  if (lane == 0) s_sums[warp] = sum;
-  if (top) s_keys[warp][lane] = list;
-  __syncthreads();
-  if (warp == 0) {
-    sum = s_sums[0];
-    for (int w = 1; w < nw; ++w) {
-      sum = join(sum, s_sums[w]);
-      if (top) list = merge_lists(list, s_keys[w][lane]);
-    }
-    if (lane == 0) s_part.sums = sum;
-    s_part.keys[lane] = list;
-  }
-  if (ctas > 1) {
-    cluster_sync();
-    if (warp == 0 && rank == 0) {
-      const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_part));
-      for (uint32_t r = 1; r < ctas; ++r) {
-        const Sums b{cluster_read(at, r), cluster_read(at + 4, r), cluster_read(at + 8, r)};
-        sum = join(sum, b);
-        if (top) {
-          const uint32_t k = at + offsetof(Part, keys) + lane * 8;
-          const uint64_t lo = __float_as_uint(cluster_read(k, r)), hi = __float_as_uint(cluster_read(k + 4, r));
-          list = merge_lists(list, hi << 32 | lo);
+  if constexpr (!WARP_ROW) {
+    // n parts in shared memory, the first of them each warp's own, joined two by two
+    auto join_parts = [&](int n) {
+      for (int half = n >> 1; half > 0; half >>= 1) {
+        if (warp < 2 * half) {
+          if (lane == 0) s_part[warp].sums = sum;
+          s_part[warp].keys[lane] = list;
         }
+        __syncthreads();
+        if (warp < half) {
+          sum = join(sum, s_part[warp + half].sums);
+          if (top) list = merge_lists(list, s_part[warp + half].keys[lane]);
+        }
+        __syncthreads();
       }
+    };
+    join_parts(nw);
+    if (ctas > 1) {
+      if (warp == 0) {
+        if (lane == 0) s_part[0].sums = sum;
+        s_part[0].keys[lane] = list;
+      }
+      cluster_sync();
+      if (rank == 0 && warp < static_cast<int>(ctas)) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_part[0]));
+        const uint32_t k = at + offsetof(Part, keys) + lane * 8;
+        sum = Sums{cluster_read(at, warp), cluster_read(at + 4, warp), cluster_read(at + 8, warp)};
+        const uint64_t lo = __float_as_uint(cluster_read(k, warp)), hi = __float_as_uint(cluster_read(k + 4, warp));
+        list = hi << 32 | lo;
+      }
+      cluster_sync();  // no CTA ends, and nothing is overwritten, while the parts are read
+      if (rank != 0) return;
+      join_parts(static_cast<int>(ctas));
     }
-    cluster_sync();  // no CTA ends while its part is read
-    if (rank != 0) return;
+    if (warp != 0) return;
   }
-  if (warp != 0) return;
   // a NaN anywhere is one in s; so is +inf (less itself)
   const bool broken = !(sum.s == sum.s), none = broken || sum.m == kNone;
   const float nan = __uint_as_float(0x7FC00000u);
@@ -263,13 +406,16 @@ template <typename T>
 cudaError_t launch_typed(const moe_layer_logprobs_args_t& a, int num_sms, cudaStream_t s) {
   constexpr int64_t kTile = 32 * kBlocks * (16 / sizeof(T));  // elements of a warp's step
   const int64_t steps = (a.vocab + kTile - 1) / kTile;
+  moe_layer_logprobs_args_t arg = a;
+  void* args[] = {&arg};
+  if (steps <= 2)
+    return launch_after((const void*)logprobs_kernel<T, true>, dim3((static_cast<unsigned>(a.rows) + kRowWarps - 1) / kRowWarps),
+                        dim3(kRowWarps * 32), args, 0, s);
   int warps = 1, ctas = 1;
   while (warps < kMaxWarps && warps < steps) warps *= 2;
   while (ctas < kMaxCluster && ctas * warps < steps && static_cast<int64_t>(a.rows) * ctas < 2 * num_sms) ctas *= 2;
-  moe_layer_logprobs_args_t arg = a;
-  void* args[] = {&arg};
-  return launch_after((const void*)logprobs_kernel<T>, dim3(static_cast<unsigned>(a.rows) * ctas), dim3(warps * 32), args, 0,
-                      s, ctas);
+  return launch_after((const void*)logprobs_kernel<T, false>, dim3(static_cast<unsigned>(a.rows) * ctas), dim3(warps * 32), args,
+                      0, s, ctas);
 }
 
 }  // namespace
