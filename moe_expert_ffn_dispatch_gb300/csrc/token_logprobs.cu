@@ -10,7 +10,9 @@
 // The top logits are kept by warps: lane r holds the r-th best of what the warp
 // has seen, as one number that orders by value and then by the lower index.  A
 // thread's maximum of its 64 bytes, which the sums need anyway, says whether any
-// of them can enter; only the elements of lanes that say so are looked at.
+// of them can enter; only the elements of lanes that say so are looked at.  The bound
+// that they have to reach is the k-th largest of the threads' M, which k logits reach
+// and few others: taken over the CTA in its first step and its fourth.
 // A row is a CTA's, or a cluster's where there are few rows, or a warp's where it is short.
 #include <type_traits>
 
@@ -178,6 +180,18 @@ __device__ __forceinline__ uint32_t sort_lanes(uint32_t v) {
   return v;
 }
 
+// the best 32 of two sorted lists of 32-bit numbers, sorted
+__device__ __forceinline__ uint32_t merge_orders(uint32_t a, uint32_t b) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v = max(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint32_t w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = (lane & o) == 0 ? max(v, w) : min(v, w);
+  }
+  return v;
+}
+
 // WARP_ROW: a warp takes a row by itself, kRowWarps rows a CTA
 template <typename T, bool WARP_ROW>
 __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WARP_ROW ? 8 : 4)
@@ -185,6 +199,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
   constexpr int N = 16 / sizeof(T), E = N * kBlocks;  // elements of a block, and of a thread's step
   __shared__ Part s_part[kMaxWarps];  // of warps, then (in the first CTA) of the cluster's CTAs
   __shared__ uint4 s_raw[WARP_ROW ? kRowWarps : kMaxWarps][32 * kBlocks];
+  __shared__ uint32_t s_order[kMaxWarps][32];
   __shared__ uint32_t s_bound;  // order of a value that `top` logits of the row reach
   grid_dependency_wait();
   grid_launch_dependents();
@@ -214,7 +229,10 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
   uint64_t least = 0;             // the list's entry number `top`
   float bound = kNone;            // its value, or a larger one that `top` logits reach: smaller ones need not be looked at
   const int64_t tile = static_cast<int64_t>(nw) * 32 * kBlocks * ctas;
-  for (int64_t t0 = (static_cast<int64_t>(rank) * nw + warp) * 32 * kBlocks; t0 < blocks; t0 += tile) {
+  int64_t t0 = (static_cast<int64_t>(rank) * nw + warp) * 32 * kBlocks;
+  // as many steps for every warp of the CTA: some have nothing left to read in the last
+  const int64_t steps = (blocks - static_cast<int64_t>(rank) * nw * 32 * kBlocks + tile - 1) / tile;
+  for (int64_t step = 0; step < steps; ++step, t0 += tile) {
     uint32_t raw[4 * kBlocks];
     if (t0 > 0 && t0 + 32 * kBlocks < blocks) {
 #pragma unroll
@@ -297,10 +315,23 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
       }
     }
     if (top == 0) continue;
+    if constexpr (!WARP_ROW) {
+      if ((step == 0 && steps > 1) || (step == 3 && steps > 7 && top > 8)) {
+        // the `top` largest of the threads' maxima
+        uint32_t best = sort_lanes(order_of(sum.m));
+        for (int half = nw >> 1; half > 0; half >>= 1) {
+          if (warp >= half && warp < 2 * half) s_order[warp][lane] = best;
+          __syncthreads();
+          if (warp < half) best = merge_orders(best, s_order[warp + half][lane]);
+        }
+        if (warp == 0 && lane == top - 1) atomicMax(&s_bound, best);
+        __syncthreads();
+      }
+    }
     if constexpr (!WARP_ROW) bound = fmaxf(bound, value_of(max(*static_cast<volatile uint32_t*>(&s_bound), order_of(kNone))));
     uint32_t hit = __ballot_sync(0xffffffffu, most >= bound);
     if (!hit) continue;
-    if (__popc(hit) >= top) {  // `top` lanes hold a logit of at least their own maximum
+    if (__popc(hit) >= top && __popc(hit) > 2) {  // `top` lanes hold a logit of at least their own maximum
       const uint32_t sorted = sort_lanes(order_of(most));
       bound = fmaxf(bound, value_of(__shfl_sync(0xffffffffu, sorted, top - 1)));
       hit = __ballot_sync(0xffffffffu, most >= bound);
@@ -408,11 +439,14 @@ cudaError_t launch_typed(const moe_layer_logprobs_args_t& a, int num_sms, cudaSt
   const int64_t steps = (a.vocab + kTile - 1) / kTile;
   moe_layer_logprobs_args_t arg = a;
   void* args[] = {&arg};
-  if (steps <= 2)
+  // A row's end (joins, lists) costs a warp about as much as four steps.  Where there are rows for every SM its warps are
+  // as few as leave each eight steps; elsewhere a row is spread over up to 64 warps.
+  const bool many = a.rows >= 8 * num_sms;
+  if (steps <= (many ? 8 : 2))
     return launch_after((const void*)logprobs_kernel<T, true>, dim3((static_cast<unsigned>(a.rows) + kRowWarps - 1) / kRowWarps),
                         dim3(kRowWarps * 32), args, 0, s);
   int warps = 1, ctas = 1;
-  while (warps < kMaxWarps && warps < steps) warps *= 2;
+  while (warps < kMaxWarps && warps * (many ? 8 : 1) < steps) warps *= 2;
   while (ctas < kMaxCluster && ctas * warps < steps && static_cast<int64_t>(a.rows) * ctas < 2 * num_sms) ctas *= 2;
   return launch_after((const void*)logprobs_kernel<T, false>, dim3(static_cast<unsigned>(a.rows) * ctas), dim3(warps * 32), args,
                       0, s, ctas);
