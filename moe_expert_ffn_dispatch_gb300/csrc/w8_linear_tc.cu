@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   uint8_t* smem = smem_raw + ((1024u - (moe::smem_u32(smem_raw) & 1023u)) & 1023u);
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + L::kOffBar);
   const moe_layer_w8_args_t& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (handed round, so that the compiler knows it to be one number a warp and keeps what follows from it in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t rank, parts;  // of the cluster that shares k out
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));

@@ -478,37 +478,44 @@ def page_plan(page_table: torch.Tensor, held: torch.Tensor, new_tokens: torch.Te
     if stream is not None or index < 0 or index != _device_index():
         with _On(page_table.device, stream):
             return page_plan(page_table, held, new_tokens, free_pages, page_size, num_pages, tokens, taken, taken_out)
-    a = PagePlanArgs()
-    a.page_table, batch, a.max_pages, a.table_stride = _page_table(page_table, index)
-    if max(page_size, num_pages, tokens, free_pages.numel()) > _I32_MAX:
-        _too_large("page_plan", max(page_size, num_pages, tokens, free_pages.numel()))
-    i32 = torch.int32
-    a.held = _dense(held, "held", i32, (batch,), index)
-    a.new_tokens = _dense(new_tokens, "new_tokens", i32, (batch,), index)
-    a.free_pages = _dense(free_pages, "free_pages", i32, (free_pages.numel(),), index)
-    if taken is not None:
-        a.taken = _dense(taken, "taken", i32, (1,), index)
+    table_at, batch, pages, stride = _page_table(page_table, index)
+    num_free = free_pages.numel()
+    if page_size > _I32_MAX or num_pages > _I32_MAX or tokens > _I32_MAX or num_free > _I32_MAX:
+        _too_large("page_plan", max(page_size, num_pages, tokens, num_free))
     if tokens < 0:
         raise ValueError("tokens: %d" % tokens)
-    # one allocation for the numbers of 32 bits, each part on a 16-byte boundary
-    up = (tokens + 3) // 4 * 4
-    lens_at, cu_at = 2 * up, 2 * up + (batch + 3) // 4 * 4
-    buf = torch.empty(cu_at + batch + 3, dtype=i32, device=page_table.device)
-    slot = torch.empty(tokens, dtype=torch.int64, device=page_table.device)
+    i32 = torch.int32
+    # one allocation, its parts on 16-byte boundaries: slot (as int64), sequence, position, seq_lens, cu_tokens, the counts
+    rows, lens, cus = (tokens + 3) & -4, (batch + 3) & -4, (batch + 4) & -4
+    buf = torch.empty(4 * rows + lens + cus + 4, dtype=i32, device=page_table.device)
+    slot, sequence, position, seq_lens, cu_tokens, unplaced, own_taken, _ = buf.split_with_sizes(
+        [2 * rows, rows, rows, lens, cus, 1, 1, 2])
+    slot = slot.view(torch.int64)
+    if rows != tokens:
+        slot, sequence, position = slot[:tokens], sequence[:tokens], position[:tokens]
+    if lens != batch:
+        seq_lens = seq_lens[:batch]
+    if cus != batch + 1:
+        cu_tokens = cu_tokens[:batch + 1]
     at = buf.data_ptr()
-    a.sequence, a.position, a.slot = at, at + 4 * up, slot.data_ptr()
-    a.seq_lens, a.cu_tokens, a.unplaced = at + 4 * lens_at, at + 4 * cu_at, at + 4 * (cu_at + batch + 1)
+    sequence_at = at + 8 * rows
+    position_at = sequence_at + 4 * rows
+    lens_at = position_at + 4 * rows
+    cu_at = lens_at + 4 * lens
+    counts_at = cu_at + 4 * cus
     if taken_out is None:
-        taken_out = buf[cu_at + batch + 2:]
-        a.taken_out = at + 4 * (cu_at + batch + 2)
+        taken_out, taken_out_at = own_taken, counts_at + 4
     else:
-        a.taken_out = _dense(taken_out, "taken_out", i32, (1,), index)
-    a.batch, a.page_size, a.num_pages, a.num_free, a.tokens = batch, page_size, num_pages, free_pages.numel(), tokens
+        taken_out_at = _dense(taken_out, "taken_out", i32, (1,), index)
+    a = PagePlanArgs(table_at, _dense(held, "held", i32, (batch,), index),
+                     _dense(new_tokens, "new_tokens", i32, (batch,), index),
+                     _dense(free_pages, "free_pages", i32, (num_free,), index),
+                     0 if taken is None else _dense(taken, "taken", i32, (1,), index), taken_out_at, counts_at, cu_at,
+                     lens_at, sequence_at, position_at, at, stride, batch, pages, page_size, num_pages, num_free, tokens)
     rc = _entry("moe_layer_page_plan")(ctypes.byref(a), _raw_stream(index))
     if rc:
         _raise(rc, "moe_layer_page_plan")
-    return PagePlan(buf[cu_at:cu_at + batch + 1], buf[lens_at:lens_at + batch], buf[:tokens], buf[up:up + tokens], slot,
-                    taken_out, buf[cu_at + batch + 1:cu_at + batch + 2])
+    return PagePlan(cu_tokens, seq_lens, sequence, position, slot, taken_out, unplaced)
 
 
 def _page_table(page_table: torch.Tensor, index: int) -> Tuple[int, int, int, int]:
