@@ -20,9 +20,12 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v, int dtype) 
   else static_cast<__half*>(y)[i] = __float2half_rn(v);
 }
 
-// y of an exact sum
+// y of an exact sum, as fp32 has it
+__device__ __forceinline__ float scaled(float sum, float w_scale, float x_scale) {
+  return __fmul_rn(__fmul_rn(sum, w_scale), x_scale);
+}
 __device__ __forceinline__ float scaled(int32_t sum, float w_scale, float x_scale) {
-  return __fmul_rn(__fmul_rn(__int2float_rn(sum), w_scale), x_scale);
+  return scaled(__int2float_rn(sum), w_scale, x_scale);
 }
 
 }  // namespace moe_layer

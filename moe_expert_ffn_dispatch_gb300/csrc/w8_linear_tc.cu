@@ -4,7 +4,9 @@
 // The tensor cores of this chip have no integer kind: codes run as f16 (every
 // integer in [-128, 127] is exact), sums as fp32 in tensor memory.  A product of two
 // codes is at most 2^14, so 1024 consecutive k sum to at most 2^24, exactly; each
-// accumulator covers 1024 k at most and is then drained into int32 registers.
+// accumulator covers 1024 k at most and is then drained into registers.  There sums
+// stay fp32 as long as the largest that could have come together is below 2^24, which
+// is exact too, and are int32 from then on: the conversion is the drain's slowest part.
 //
 // A tile is 128 weight rows (M, the tensor memory's lanes) by up to 256 tokens (N, in
 // one or two halves of at most 128 columns).  Weights arrive as int8 by TMA and are
@@ -132,12 +134,12 @@ __device__ __forceinline__ void put(__half* y, float v) { *y = __float2half_rn(v
 
 // `most` (at most 64) tokens of one weight row a lane, `stride` apart; every lane of the warp
 template <typename T>
-__device__ __forceinline__ void write_tokens(T* y, int64_t stride, const int32_t (&acc)[64], float ws, float xs0, float xs1,
+__device__ __forceinline__ void write_tokens(T* y, int64_t stride, const uint32_t (&acc)[64], float ws, float xs0, float xs1,
                                              int most, bool mine) {
 #pragma unroll
   for (int j = 0; j < 64; ++j) {
     const float xs = __shfl_sync(0xffffffffu, j < 32 ? xs0 : xs1, j & 31);
-    if (j < most && mine) put(y, scaled(acc[j], ws, xs));
+    if (j < most && mine) put(y, scaled(__uint_as_float(acc[j]), ws, xs));
     y += stride;
   }
 }
@@ -425,11 +427,17 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     int64_t chunk = 0;
     bool ok = true;
     for (int64_t it = first; it < p.tiles; it += step) {
-      int32_t acc[HALVES][64];  // 64 tokens of each half, of one weight row
+      // 64 tokens of each half, of one weight row: fp32, or int32 for those 32 whose bit of `whole` is set (one answer for
+      // the warp's lanes); `reach`: what the sums of 32 are below in magnitude, while they are fp32
+      uint32_t acc[HALVES][64];
+      float reach[HALVES][2];
+      uint32_t whole = 0;
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h)
+      for (int h = 0; h < HALVES; ++h) {
+        reach[h][0] = reach[h][1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 64; ++j) acc[h][j] = 0;
+      }
       for (int kb = kb0; ok && kb < kb1; kb += kChunk, ++chunk) {
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
@@ -445,8 +453,30 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
               uint32_t v[32];
               tmem_ld32(from + buf * p.half + 32 * j, v);
               if (j == 1 || 64 * side + 32 >= p.half) release(buf);  // what is still to come is in registers
+              const uint32_t bit = 1u << (2 * h + j);
+              if (!(whole & bit)) {
+                float most = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) acc[h][32 * j + e] += __float2int_rn(__uint_as_float(v[e]));
+                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
+                if (64 * side + 32 * j + 16 < p.half) {
+#pragma unroll
+                  for (int e = 16; e < 32; ++e) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
+                }
+                reach[h][j] = __fadd_ru(reach[h][j], most);
+                if (__any_sync(0xffffffffu, reach[h][j] > 16777216.0f)) {
+                  whole |= bit;
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) acc[h][32 * j + e] = __float2int_rn(__uint_as_float(acc[h][32 * j + e]));
+                }
+              }
+              if (!(whole & bit)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  acc[h][32 * j + e] = __float_as_uint(__fadd_rn(__uint_as_float(acc[h][32 * j + e]), __uint_as_float(v[e])));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) acc[h][32 * j + e] += __float2int_rn(__uint_as_float(v[e]));
+              }
             }
           }
           if (64 * side >= p.half) release(buf);
@@ -457,12 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         int32_t* sums = reinterpret_cast<int32_t*>(smem);
 #pragma unroll
         for (int j = 0; j < 64; ++j)
-          if (64 * side + j < p.half) sums[(64 * side + j) * kRows + 32 * q + lane] = acc[0][j];
+          if (64 * side + j < p.half)
+            sums[(64 * side + j) * kRows + 32 * q + lane] =
+                whole >> (j >> 5) & 1 ? acc[0][j] : __float2int_rn(__uint_as_float(acc[0][j]));
         if (!ok && lane == 0) bar.broken = 1;
         break;
       }
       const int n = static_cast<int>(it / p.blocks) * kRows + 32 * q + lane;
       const int m0 = static_cast<int>(it % p.blocks) * p.half * HALVES + 64 * side;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (whole >> (2 * h + (j >> 5)) & 1) acc[h][j] = __float_as_uint(__int2float_rn(acc[h][j]));
       const float ws = !ok ? kNan : n < a.n ? scale_at(a.w_scale, n, a.scale_dtype) : 0.0f;
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
