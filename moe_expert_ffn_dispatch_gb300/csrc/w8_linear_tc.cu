@@ -575,16 +575,30 @@ struct Shape {
   int form, half, blocks;
   int64_t tiles;
 };
-Shape shape_of(int m, int n, int num_sms) {
+
+// The tiles that take the least time by a count of cycles: a step costs about 500 + 2.5 h with one half of h tokens
+// and 700 + 5.2 h with two (4096 k, 1 round of SMs: 128 tokens 18.6 us, 2 x 64 22.4, 2 x 128 28.0), a tile some more, and
+// SMs work in rounds.  Two halves read the weights half as often, and win from about 900 tokens x 4096 rows on; below,
+// tiles of one half are more, and fill the SMs: 512 x 4096 18.6 us for 28.0, 1024 x 4096 31.1 for 29.7.
+Shape shape_of(int m, int n, int k, int num_sms) {
   const int64_t rows = (static_cast<int64_t>(n) + kRows - 1) / kRows;
-  if (m <= 128) return Shape{m <= 64 ? kFew : kOne, (m + 15) / 16 * 16, 1, rows};
-  // tiles as wide as they go, narrower ones where that fills the last round of SMs better
+  if (m <= 64) return Shape{kFew, (m + 15) / 16 * 16, 1, rows};
+  const int steps = (k + kStage - 1) / kStage;
   Shape s{};
   double best = 0;
-  for (int blocks = (m + 255) / 256; blocks <= (m + 255) / 256 * 2; ++blocks) {
-    const int half = ((m + blocks - 1) / blocks + 31) / 32 * 16, real = (m + 2 * half - 1) / (2 * half);
-    const double cost = static_cast<double>((rows * real + num_sms - 1) / num_sms) * (2 * half + 16);
-    if (best == 0 || cost < best) best = cost, s = Shape{kTwo, half, real, rows * real};
+  for (int form = kOne; form <= kTwo; ++form) {
+    const int halves = form == kTwo ? 2 : 1, least = (m + 128 * halves - 1) / (128 * halves);
+    if (form == kTwo && m <= 128) break;
+    for (int b = least; b <= 2 * least; ++b) {
+      const int half = ((m + b - 1) / b + 16 * halves - 1) / (16 * halves) * 16, blocks = (m + halves * half - 1) / (halves * half);
+      const int64_t tiles = rows * blocks, rounds = (tiles + num_sms - 1) / num_sms;
+      int parts = 1;  // of k, in a cluster
+      if (form == kOne)
+        while (parts < static_cast<int>(kMostParts) && tiles * (parts + 1) <= num_sms && steps >= 2 * (parts + 1)) ++parts;
+      const double cost = rounds * (static_cast<double>(steps) / parts * (form == kTwo ? 700 + 5.2 * half : 500 + 2.5 * half) +
+                                    (form == kTwo ? 4000 : 2500) + (parts > 1 ? 2500 : 0));
+      if (best == 0 || cost < best) best = cost, s = Shape{form, half, blocks, tiles};
+    }
   }
   return s;
 }
@@ -638,7 +652,7 @@ cudaError_t launch_tiles(const Maps& maps, const Params& p, int num_sms, cudaStr
 size_t w8_tc_workspace(int m, int, int k, int) { return m <= 64 ? 0 : 256 + static_cast<size_t>(m) * k * 2; }
 
 cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cudaStream_t s) {
-  const Shape shape = shape_of(a.m, a.n, num_sms);
+  const Shape shape = shape_of(a.m, a.n, a.k, num_sms);
   Maps maps{};
   if (!moe::encode_2d(&maps.w, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.n, a.k, kStage, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
