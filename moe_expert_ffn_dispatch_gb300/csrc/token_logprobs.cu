@@ -281,8 +281,9 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
       sum.s = __fmul_rn(sum.s, e);
       sum.m = most;
     }
-    if (!far_out<T>(sum.m)) {
-      const uint64_t scale = pack(kLog2e, kLog2e), less = pack(-sum.m, -sum.m);
+    const float m = sum.m == kNone ? 0.0f : sum.m;  // (nothing but -inf yet, which adds nothing, or NaN)
+    if (!far_out<T>(m)) {
+      const uint64_t scale = pack(kLog2e, kLog2e), less = pack(-m, -m);
       uint64_t s2 = pack(0.0f, 0.0f), u2 = s2;
 #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
@@ -300,18 +301,12 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
       sum.s = __fadd_rn(sum.s, __fadd_rn(s.x, s.y));
       sum.u = __fadd_rn(sum.u, __fadd_rn(u.x, u.y));
     } else {
-      const float m = sum.m == kNone ? 0.0f : sum.m;
-#pragma unroll 1
-      for (int j = 0; j < E; ++j) {
-        uint32_t w = 0;
 #pragma unroll
-        for (int i = 0; i < 4 * kBlocks; ++i)
-          if (i == (sizeof(T) == 4 ? j : j >> 1)) w = raw[i];
-        const uint32_t two[2] = {w, w};
-        const float2 f = pair_at<T>(two);
-        const float d = exponent(j & 1 ? f.y : f.x, m), e = exp2_fast(d);
-        sum.s = __fadd_rn(sum.s, e);
-        sum.u = __fmaf_rn(e, fmaxf(d, -200.0f), sum.u);  // (-inf has e = 0)
+      for (int j = 0; j < E / 2; ++j) {
+        const float2 l = pair_at<T>(raw + (sizeof(T) == 4 ? 2 * j : j));
+        const float d0 = exponent(l.x, m), d1 = exponent(l.y, m), e0 = exp2_fast(d0), e1 = exp2_fast(d1);
+        sum.s = __fadd_rn(sum.s, __fadd_rn(e0, e1));
+        sum.u = __fmaf_rn(e0, fmaxf(d0, -200.0f), __fmaf_rn(e1, fmaxf(d1, -200.0f), sum.u));  // (-inf has 2^d = 0)
       }
     }
     if (top == 0) continue;

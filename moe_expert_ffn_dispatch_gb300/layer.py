@@ -485,24 +485,18 @@ def page_plan(page_table: torch.Tensor, held: torch.Tensor, new_tokens: torch.Te
     if tokens < 0:
         raise ValueError("tokens: %d" % tokens)
     i32 = torch.int32
-    # one allocation, its parts on 16-byte boundaries: slot (as int64), sequence, position, seq_lens, cu_tokens, the counts
-    rows, lens, cus = (tokens + 3) & -4, (batch + 3) & -4, (batch + 4) & -4
-    buf = torch.empty(4 * rows + lens + cus + 4, dtype=i32, device=page_table.device)
-    slot, sequence, position, seq_lens, cu_tokens, unplaced, own_taken, _ = buf.split_with_sizes(
-        [2 * rows, rows, rows, lens, cus, 1, 1, 2])
-    slot = slot.view(torch.int64)
-    if rows != tokens:
-        slot, sequence, position = slot[:tokens], sequence[:tokens], position[:tokens]
-    if lens != batch:
-        seq_lens = seq_lens[:batch]
-    if cus != batch + 1:
-        cu_tokens = cu_tokens[:batch + 1]
-    at = buf.data_ptr()
-    sequence_at = at + 8 * rows
-    position_at = sequence_at + 4 * rows
-    lens_at = position_at + 4 * rows
-    cu_at = lens_at + 4 * lens
-    counts_at = cu_at + 4 * cus
+    # one allocation for the numbers of 32 bits (whole numbers: nothing differentiates through parts that torch does not
+    # keep as views, which cost half as much)
+    device = page_table.device
+    buf = torch.empty(2 * tokens + 2 * batch + 3, dtype=i32, device=device)
+    sequence, position, seq_lens, cu_tokens, unplaced, own_taken = torch.unsafe_split_with_sizes(
+        buf, [tokens, tokens, batch, batch + 1, 1, 1])
+    slot = torch.empty(tokens, dtype=torch.int64, device=device)
+    sequence_at = buf.data_ptr()
+    position_at = sequence_at + 4 * tokens
+    lens_at = position_at + 4 * tokens
+    cu_at = lens_at + 4 * batch
+    counts_at = cu_at + 4 * batch + 4
     if taken_out is None:
         taken_out, taken_out_at = own_taken, counts_at + 4
     else:
@@ -511,7 +505,7 @@ def page_plan(page_table: torch.Tensor, held: torch.Tensor, new_tokens: torch.Te
                      _dense(new_tokens, "new_tokens", i32, (batch,), index),
                      _dense(free_pages, "free_pages", i32, (num_free,), index),
                      0 if taken is None else _dense(taken, "taken", i32, (1,), index), taken_out_at, counts_at, cu_at,
-                     lens_at, sequence_at, position_at, at, stride, batch, pages, page_size, num_pages, num_free, tokens)
+                     lens_at, sequence_at, position_at, slot.data_ptr(), stride, batch, pages, page_size, num_pages, num_free, tokens)
     rc = _entry("moe_layer_page_plan")(ctypes.byref(a), _raw_stream(index))
     if rc:
         _raise(rc, "moe_layer_page_plan")
