@@ -4,8 +4,8 @@
 // Three reductions over the row (sum of squares of the block's output, of the new
 // residual, then the maximum of |z|) and one pass over memory, as norm_quant.cu
 // has it: the row stays in registers as fp32 between them, a CTA a row (a warp up
-// to 1024 wide), every load of a row's own data issued before the first use.  The
-// vectors that all rows share come from the cache when they are needed.
+// to 1024 wide), every load of a row's own data issued before the first use, and the
+// weights' a barrier ahead of theirs.
 // Bound by memory: 4 bytes read (6 with a gate a token) and 2 to 5 written an
 // element.
 #include "norm_rows.cuh"
@@ -24,9 +24,11 @@ __device__ __forceinline__ float row_sum(float v, float* s_part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     if (lane == 0) s_part[warp] = v;
     __syncthreads();
-    v = lane < nw ? s_part[lane] : 0.0f;
+    // every thread adds up the warps' sums, in one order
+    v = s_part[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int w = 1; w < kMaxWarps; ++w)
+      if (w < nw) v = __fadd_rn(v, s_part[w]);
   } else {
     __syncwarp();
   }
@@ -35,7 +37,7 @@ __device__ __forceinline__ float row_sum(float v, float* s_part) {
 
 // ROW_WARP: a warp takes a row by itself, kRowWarps rows a CTA
 template <typename T, typename W, int C, bool VEC, bool ROW_WARP>
-__global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP ? 5 : 6 / C)
+__global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP ? 5 : VEC ? 10 / C : 8 / C)
     norm_pair_kernel(const moe_layer_norm_pair_args_t a) {
   __shared__ float s_sum[kMaxWarps], s_sum2[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
@@ -63,6 +65,9 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
 
   RowIn<T, C> xs, rs, gs;
   Chunk8<T, true> xr[C], rr[C], gr[C];
+  // weights are loaded ahead of the barrier before their use where there are registers for it
+  constexpr bool kAhead = ROW_WARP || (VEC && C == 2);
+  Chunk8<W, VEC> wr[C];
   if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -81,6 +86,10 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
     sync_row();
   }
 
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) wr[c].load(post, (c * nt + tid) * 8, h);
+  }
   float v[C][8];
   float sum = 0.0f;
 #pragma unroll
@@ -99,9 +108,8 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
   for (int c = 0; c < C; ++c) {
     const int n = c * nt + tid, i = n * 8;
     float f[8];
-    Chunk8<W, VEC> pr;
-    pr.load(post, i, h);
-    pr.take(f);
+    if constexpr (!kAhead) wr[c].load(post, i, h);
+    wr[c].take(f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(__fmul_rn(v[c][j], r1), f[j]);
     if (gate) {
@@ -130,6 +138,10 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
       buf_x[n] = pack8<T>(v[c]);  // every thread has taken x, at the sum's barrier
     }
   }
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) wr[c].load(w, (c * nt + tid) * 8, h);
+  }
   sum = row_sum<ROW_WARP>(sum, s_sum2);
   if constexpr (!VEC) store_row(res_out, buf_x, tid, nt, h);
   const float r2 = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps));
@@ -139,9 +151,8 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
   for (int c = 0; c < C; ++c) {
     const int n = c * nt + tid, i = n * 8;
     float f[8];
-    Chunk8<W, VEC> wr;
-    wr.load(w, i, h);
-    wr.take(f);
+    if constexpr (!kAhead) wr[c].load(w, i, h);
+    wr[c].take(f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(__fmul_rn(v[c][j], r2), f[j]) : 0.0f;
     if (y_out) {
@@ -165,7 +176,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
     if constexpr (!ROW_WARP) {
       if (lane == 0) s_max[warp] = top;
       __syncthreads();
-      top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+      for (int w = 0; w < nw; ++w) top = max(top, s_max[w]);
     } else if constexpr (!VEC) {
       __syncwarp();
     }
