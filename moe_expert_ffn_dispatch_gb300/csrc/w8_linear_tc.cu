@@ -158,6 +158,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 // the two halves of a cluster barrier
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
@@ -224,6 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     moe::fence_barrier_init();
   }
   if (warp == 1) moe::tmem_alloc(&bar.tmem, kTmemCols);
+  if (warp == 2 && lane == 0) {
+    prefetch_map(&maps.w);
+    prefetch_map(&maps.x);
+  }
   __syncthreads();
   moe::tc_fence_after();
   const uint32_t tmem = bar.tmem;
@@ -236,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   };
 
   if constexpr (FORM == kFew) grid_dependency_wait();  // no kernel of this call's own has done so
+  grid_launch_dependents();
   if (warp < 4) {
     if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
     if (warp == 0) {
