@@ -385,6 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i)
           if (tok0 + 16 * i < p.half) x[i] = *reinterpret_cast<const uint4*>(stage + tok_from + i * 16 * kStage);
       }
+      // The copy that refills the slot is of the async proxy: without this fence it can overtake loads that are still on
+      // their way to registers (seen as rows whose last chunks were those of two steps on).
+      moe::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) moe::mbar_arrive(&bar.a8_empty[s8]);
       s8 += kGroups;

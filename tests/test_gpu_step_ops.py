@@ -214,6 +214,17 @@ def test_w8_large(M, N, K):
     assert torch.equal(m.w8_linear(x, w, ws, xs), w8_reference(x, w, ws, xs, BF16))
 
 
+@pytest.mark.parametrize("M, N, K", [(4093, 6144, 4096), (2048, 6144, 4096), (1024, 6144, 4096), (300, 20000, 1024), (64, 60001, 2048),
+                                     (33, 60001, 2048), (128, 40000, 2048), (8, 60001, 2048), (16, 3000, 4096), (32, 2000, 2048)])
+def test_w8_many_tiles_a_cta_run_after_run(M, N, K):
+    """Rings that go round many times, at full speed: every run has every bit."""
+    g = gen(M + N)
+    x, w, ws, xs = w8_inputs(M, N, K, g)
+    want = w8_reference(x, w, ws, xs, F32)
+    for _ in range(10):
+        assert torch.equal(m.w8_linear(x, w, ws, xs, out_dtype=F32), want)
+
+
 @pytest.mark.parametrize("M", [3, 20, 150, 600])
 @pytest.mark.parametrize("K", [1024, 1040, 8192, 65536])
 def test_w8_sums_are_exact_at_the_limits(M, K):
