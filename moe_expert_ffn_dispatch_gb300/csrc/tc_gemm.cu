@@ -476,7 +476,9 @@ __global__ void __launch_bounds__(kBigThreads, 1)
       int s8 = 0, sa = 0;
       uint32_t p8 = 0, pa = 0;
       uint4 c[8];
-      // codes of the next stage into c, then its staging slot goes back to the weight TMA
+      int c_slot = 0;
+      // codes of the next stage into c; its staging slot goes back to the weight TMA once they have been converted (a
+      // refill that follows the loads themselves could overtake them)
       auto load_codes = [&]() -> bool {
         const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(&a8_full[s8], p8, abort_flag, status, site + 3));
         if (got) {
@@ -484,8 +486,7 @@ __global__ void __launch_bounds__(kBigThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
         }
-        __syncwarp();
-        if (got && lane == 0) mbar_arrive(&a8_empty[s8]);
+        c_slot = s8;
         if (++s8 == S8) { s8 = 0; p8 ^= 1u; }
         return got;
       };
@@ -507,6 +508,8 @@ __global__ void __launch_bounds__(kBigThreads, 1)
           }
           tmem_st32(lane_base + sa * kAStageCols + 32 * h2, v);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a8_empty[c_slot]);
         if (k + 1 < n_stages) ok = load_codes();
         tmem_st_wait();  // also on the way out after a failed wait: no store left in flight
         tc_fence_before();
