@@ -232,38 +232,45 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
   int64_t t0 = (static_cast<int64_t>(rank) * nw + warp) * 32 * kBlocks;
   // as many steps for every warp of the CTA: some have nothing left to read in the last
   const int64_t steps = (blocks - static_cast<int64_t>(rank) * nw * 32 * kBlocks + tile - 1) / tile;
-  for (int64_t step = 0; step < steps; ++step, t0 += tile) {
-    uint32_t raw[4 * kBlocks];
-    if (t0 > 0 && t0 + 32 * kBlocks < blocks) {
+  auto load = [&](int64_t at, uint32_t (&into)[4 * kBlocks]) {
+    if (at > 0 && at + 32 * kBlocks < blocks) {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        const uint4 u = __ldcs(base + t0 + b * 32 + lane);
-        raw[4 * b] = u.x, raw[4 * b + 1] = u.y, raw[4 * b + 2] = u.z, raw[4 * b + 3] = u.w;
+        const uint4 u = __ldcs(base + at + b * 32 + lane);
+        into[4 * b] = u.x, into[4 * b + 1] = u.y, into[4 * b + 2] = u.z, into[4 * b + 3] = u.w;
       }
     } else {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        const int64_t n = t0 + b * 32 + lane, e = n * N - off;
+        const int64_t n = at + b * 32 + lane, e = n * N - off;
         uint4 u = make_uint4(0, 0, 0, 0);
         if (e >= 0 && e + N <= a.vocab) {
           u = __ldcs(base + n);
-          raw[4 * b] = u.x, raw[4 * b + 1] = u.y, raw[4 * b + 2] = u.z, raw[4 * b + 3] = u.w;
+          into[4 * b] = u.x, into[4 * b + 1] = u.y, into[4 * b + 2] = u.z, into[4 * b + 3] = u.w;
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if constexpr (sizeof(T) == 4) {
-              raw[4 * b + j] = e + j >= 0 && e + j < a.vocab ? __float_as_uint(p[e + j]) : 0xFF800000u;
+              into[4 * b + j] = e + j >= 0 && e + j < a.vocab ? __float_as_uint(p[e + j]) : 0xFF800000u;
             } else {
               const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
               const uint32_t none = std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;
               const int64_t i = e + 2 * j;
-              raw[4 * b + j] = (i >= 0 && i < a.vocab ? h[i] : none) |
+              into[4 * b + j] = (i >= 0 && i < a.vocab ? h[i] : none) |
                                (i + 1 >= 0 && i + 1 < a.vocab ? h[i + 1] : none) << 16;
             }
           }
         }
       }
     }
+  };
+  uint32_t next[4 * kBlocks];  // the step after this one, on its way
+  if (steps > 0) load(t0, next);
+  for (int64_t step = 0; step < steps; ++step, t0 += tile) {
+    uint32_t raw[4 * kBlocks];
+#pragma unroll
+    for (int j = 0; j < 4 * kBlocks; ++j) raw[j] = next[j];
+    if (step + 1 < steps) load(t0 + tile, next);
     // the largest of these: of the words as they are, then of a word's elements
     uint32_t top_word = raw[0];
 #pragma unroll
