@@ -35,6 +35,16 @@ __device__ __forceinline__ float row_sum(float v, float* s_part) {
   return v;
 }
 
+__device__ __forceinline__ float sum_of(uint64_t pair) {
+  const float2 f = of_pair(pair);
+  return __fadd_rn(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&v)[4]) {
+  const float2 a = of_pair(v[0]), b = of_pair(v[1]), c = of_pair(v[2]), d = of_pair(v[3]);
+  return make_uint4(pack2<T>(a.x, a.y), pack2<T>(b.x, b.y), pack2<T>(c.x, c.y), pack2<T>(d.x, d.y));
+}
+
 // ROW_WARP: a warp takes a row by itself, kRowWarps rows a CTA
 template <typename T, typename W, int C, bool VEC, bool ROW_WARP>
 __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP ? 5 : VEC ? 10 / C : 8 / C)
@@ -58,6 +68,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
   const W *post = static_cast<const W*>(a.post_weight), *w = static_cast<const W*>(a.weight);
   uint4 *buf_x = s_rows + (ROW_WARP ? warp * 3 * row_slots(C, 32) : 0), *buf_r = buf_x + row_slots(C, nt),
         *buf_g = buf_r + row_slots(C, nt);
+  auto root = [&](float sum) { return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps)); };
   auto sync_row = [] {
     if constexpr (ROW_WARP) __syncwarp();
     else __syncthreads();
@@ -90,20 +101,24 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
 #pragma unroll
     for (int c = 0; c < C; ++c) wr[c].load(post, (c * nt + tid) * 8, h);
   }
-  float v[C][8];
-  float sum = 0.0f;
+  uint64_t v[C][4];  // pairs of neighbours; zeros past the row's end stay zeros, as weights and residual are zeros there
+  uint64_t sums = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if constexpr (VEC) xr[c].take(v[c]);
-    else take_row<T>(buf_x, c * nt + tid, xs.off, h, v[c]);
+    float f[8];
+    if constexpr (VEC) xr[c].take(f);
+    else take_row<T>(buf_x, c * nt + tid, xs.off, h, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = __fmaf_rn(v[c][j], v[c][j], sum);
+    for (int j = 0; j < 4; ++j) {
+      v[c][j] = pair_of(f[2 * j], f[2 * j + 1]);
+      sums = fma_pair(v[c][j], v[c][j], sums);
+    }
   }
-  sum = row_sum<ROW_WARP>(sum, s_sum);
-  const float r1 = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps));
+  const float r1 = root(row_sum<ROW_WARP>(sum_of(sums), s_sum));
 
   // the new residual, and its sum of squares
-  sum = 0.0f;
+  const uint64_t r1s = pair_of(r1, r1), scales = pair_of(a.branch_scale, a.branch_scale);
+  sums = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int n = c * nt + tid, i = n * 8;
@@ -111,7 +126,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
     if constexpr (!kAhead) wr[c].load(post, i, h);
     wr[c].take(f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(__fmul_rn(v[c][j], r1), f[j]);
+    for (int j = 0; j < 4; ++j) v[c][j] = mul_pair(mul_pair(v[c][j], r1s), pair_of(f[2 * j], f[2 * j + 1]));
     if (gate) {
       if constexpr (VEC) {
         gr[c].take(f);
@@ -123,30 +138,31 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
         shared.take(f);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = __fmul_rn(v[c][j], f[j]);
+      for (int j = 0; j < 4; ++j) v[c][j] = mul_pair(v[c][j], pair_of(f[2 * j], f[2 * j + 1]));
     }
     if constexpr (VEC) rr[c].take(f);
     else take_row<T>(buf_r, n, rs.off, h, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[c][j] = i + j < h ? __fmaf_rn(a.branch_scale, v[c][j], f[j]) : 0.0f;
-      sum = __fmaf_rn(v[c][j], v[c][j], sum);
+    for (int j = 0; j < 4; ++j) {
+      v[c][j] = fma_pair(scales, v[c][j], pair_of(f[2 * j], f[2 * j + 1]));
+      sums = fma_pair(v[c][j], v[c][j], sums);
     }
     if constexpr (VEC) {
-      if (i < h) *reinterpret_cast<uint4*>(res_out + i) = pack8<T>(v[c]);
+      if (i < h) *reinterpret_cast<uint4*>(res_out + i) = pack_pairs<T>(v[c]);
     } else {
-      buf_x[n] = pack8<T>(v[c]);  // every thread has taken x, at the sum's barrier
+      buf_x[n] = pack_pairs<T>(v[c]);  // every thread has taken x, at the sum's barrier
     }
   }
   if constexpr (kAhead) {
 #pragma unroll
     for (int c = 0; c < C; ++c) wr[c].load(w, (c * nt + tid) * 8, h);
   }
-  sum = row_sum<ROW_WARP>(sum, s_sum2);
+  const float sum = row_sum<ROW_WARP>(sum_of(sums), s_sum2);
   if constexpr (!VEC) store_row(res_out, buf_x, tid, nt, h);
-  const float r2 = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps));
+  const float r2 = root(sum);
 
   uint32_t top = 0;
+  const uint64_t r2s = pair_of(r2, r2);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int n = c * nt + tid, i = n * 8;
@@ -154,10 +170,10 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
     if constexpr (!kAhead) wr[c].load(w, i, h);
     wr[c].take(f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(__fmul_rn(v[c][j], r2), f[j]) : 0.0f;
+    for (int j = 0; j < 4; ++j) v[c][j] = mul_pair(mul_pair(v[c][j], r2s), pair_of(f[2 * j], f[2 * j + 1]));
     if (y_out) {
-      if constexpr (!VEC) buf_r[n] = pack8<T>(v[c]);  // the residual has left it
-      else if (i < h) *reinterpret_cast<uint4*>(y_out + i) = pack8<T>(v[c]);
+      if constexpr (!VEC) buf_r[n] = pack_pairs<T>(v[c]);  // the residual has left it
+      else if (i < h) *reinterpret_cast<uint4*>(y_out + i) = pack_pairs<T>(v[c]);
     }
     if (a.q) {
       if (a.smooth) {
@@ -165,10 +181,13 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
         sr.load(a.smooth, i, h);
         sr.take(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = i + j < h ? __fmul_rn(v[c][j], f[j]) : 0.0f;
+        for (int j = 0; j < 4; ++j) v[c][j] = mul_pair(v[c][j], pair_of(f[2 * j], f[2 * j + 1]));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[c][j]));
+      for (int j = 0; j < 4; ++j) {
+        const float2 z = of_pair(v[c][j]);
+        top = max(top, max(abs_bits(z.x), abs_bits(z.y)));
+      }
     }
   }
   if (a.q) {  // the maximum of the row
@@ -191,6 +210,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
   float amax = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : top);
   if (amax < kAmaxFloor) amax = kAmaxFloor;
   const float m = __fdiv_rn(127.0f, amax);
+  const uint64_t ms = pair_of(m, m);
   int8_t* q = a.q + row * h;
   uint2* codes = reinterpret_cast<uint2*>(buf_g);  // the gate has left it
 #pragma unroll
@@ -198,9 +218,10 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
     const int n = c * nt + tid;
     uint32_t o[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      o[j] = codes_of(__fmul_rn(v[c][4 * j], m), __fmul_rn(v[c][4 * j + 1], m), __fmul_rn(v[c][4 * j + 2], m),
-                      __fmul_rn(v[c][4 * j + 3], m));
+    for (int j = 0; j < 2; ++j) {
+      const float2 lo = of_pair(mul_pair(v[c][2 * j], ms)), hi = of_pair(mul_pair(v[c][2 * j + 1], ms));
+      o[j] = codes_of(lo.x, lo.y, hi.x, hi.y);
+    }
     if constexpr (!VEC) codes[n] = make_uint2(o[0], o[1]);
     else if (n * 8 < h) *reinterpret_cast<uint2*>(q + n * 8) = make_uint2(o[0], o[1]);
   }

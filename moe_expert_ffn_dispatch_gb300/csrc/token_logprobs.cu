@@ -99,34 +99,6 @@ __device__ __forceinline__ float2 pair_at(const uint32_t* w) {
   else return unpack2<T>(w[0]);
 }
 
-// two fp32 operations at once
-__device__ __forceinline__ uint64_t pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 struct Sums {
   float m, s, u;  // m: the largest logit
 };
@@ -290,21 +262,21 @@ __global__ void __launch_bounds__(WARP_ROW ? kRowWarps * 32 : kMaxWarps * 32, WA
     }
     const float m = sum.m == kNone ? 0.0f : sum.m;  // (nothing but -inf yet, which adds nothing, or NaN)
     if (!far_out<T>(m)) {
-      const uint64_t scale = pack(kLog2e, kLog2e), less = pack(-m, -m);
-      uint64_t s2 = pack(0.0f, 0.0f), u2 = s2;
+      const uint64_t scale = pair_of(kLog2e, kLog2e), less = pair_of(-m, -m);
+      uint64_t s2 = pair_of(0.0f, 0.0f), u2 = s2;
 #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
         uint32_t w[2];
         if constexpr (sizeof(T) == 4) w[0] = Type<T>::raise(raw[2 * j]), w[1] = Type<T>::raise(raw[2 * j + 1]);
         else w[0] = Type<T>::raise(raw[j]);
         const float2 l = pair_at<T>(w);
-        const uint64_t d2 = mul2(add2(pack(l.x, l.y), less), scale);
-        const float2 d = unpack(d2);
-        const uint64_t e2 = pack(exp2_fast(d.x), exp2_fast(d.y));
-        s2 = add2(s2, e2);
-        u2 = fma2(e2, d2, u2);
+        const uint64_t d2 = mul_pair(add_pair(pair_of(l.x, l.y), less), scale);
+        const float2 d = of_pair(d2);
+        const uint64_t e2 = pair_of(exp2_fast(d.x), exp2_fast(d.y));
+        s2 = add_pair(s2, e2);
+        u2 = fma_pair(e2, d2, u2);
       }
-      const float2 s = unpack(s2), u = unpack(u2);
+      const float2 s = of_pair(s2), u = of_pair(u2);
       sum.s = __fadd_rn(sum.s, __fadd_rn(s.x, s.y));
       sum.u = __fadd_rn(sum.u, __fadd_rn(u.x, u.y));
     } else {
