@@ -286,8 +286,9 @@ int moe_layer_norm_add_rmsnorm_quant(const moe_layer_norm_pair_args_t* args, voi
  * FP16 or FP32).  y: [m, n] of `out_dtype` (BF16, FP16 or FP32), dense.
  * k: a multiple of 16, 16 <= k <= 65536; 1 <= n < 2^31 - 2^20; 0 <= m <= 1000000.
  * workspace: moe_layer_w8_linear_workspace_size bytes, 256-byte aligned, no
- * initial content needed (NULL where that is 0); calls that share one must be
- * ordered. */
+ * initial content needed (NULL where that is 0, as it is up to 64 tokens); calls
+ * that share one must be ordered.  Every wait inside is bounded; what one that gave
+ * up would have led to is NaN in y. */
 typedef struct {
   const int8_t* x;
   const float* x_scale;

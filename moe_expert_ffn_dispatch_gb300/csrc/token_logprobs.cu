@@ -14,6 +14,10 @@
 // that they have to reach is the k-th largest of the threads' M, which k logits reach
 // and few others: taken over the CTA in its first step and its fourth.
 // A row is a CTA's, or a cluster's where there are few rows, or a warp's where it is short.
+// Bound by memory and instructions: 2039 x 130001 bf16 88 us without alternatives, 6.0
+// TB/s of 6.8; 108 with five of them (issue 75 %), 132 with twenty: the search of lanes that
+// can enter.  64 rows 8.5 / 14.5 us (twenty), one row of fp32 with five 9.3: latency of a few
+// steps and of the joins.
 #include <type_traits>
 
 #include "layer_ops.cuh"
@@ -414,7 +418,9 @@ cudaError_t launch_typed(const moe_layer_logprobs_args_t& a, int num_sms, cudaSt
   moe_layer_logprobs_args_t arg = a;
   void* args[] = {&arg};
   // A row's end (joins, lists) costs a warp about as much as four steps.  Where there are rows for every SM its warps are
-  // as few as leave each eight steps; elsewhere a row is spread over up to 64 warps.
+  // as few as leave each eight steps (us with 1 warp a row / 4 / 8 warps, five alternatives: 2039 x 8000 17 / 19 / 27, x
+  // 32000 39 / 39 / 44, x 130001 117 / 105 / 109); elsewhere a row is spread over up to 64 warps (8 / 16 / 32 / 64: 64 x
+  // 130001 21 / 15 / 12 / 13, 8 x 130001 20 / 14 / 11 / 9, 256 x 130001 24 / 24 / 29 / 40).
   const bool many = a.rows >= 8 * num_sms;
   if (steps <= (many ? 8 : 2))
     return launch_after((const void*)logprobs_kernel<T, true>, dim3((static_cast<unsigned>(a.rows) + kRowWarps - 1) / kRowWarps),

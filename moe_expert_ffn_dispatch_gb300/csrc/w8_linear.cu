@@ -8,7 +8,7 @@
 // and tokens, which is all that the sum asks for.
 // Bound by memory: the weights once.  Each warp has the loads of its next steps in
 // flight, those of the next 16 rows among them while it adds up these: 8 x 130001 x
-// 4096 84 us, 6.4 TB/s; 8 x 6144 x 4096 7.3 us, of which launch and first load are 3.
+// 4096 84 us, 6.4 TB/s; 8 x 6144 x 4096 7.3 to 8 us, of which launch and first load are 3.
 #include "w8_linear.cuh"
 
 namespace moe_layer {

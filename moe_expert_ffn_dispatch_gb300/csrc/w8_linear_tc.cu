@@ -27,6 +27,12 @@
 // 12..15 drain: one group's chain of waits, loads and stores is 850 cycles a step.
 // Where there are fewer tiles than SMs a cluster shares k out, and adds its int32
 // sums up over distributed shared memory, a share of the tile's columns each.
+//
+// Bound by: many tokens, the products (4093 x 6144 x 4096 132 us, 1.56 PFLOP/s, the
+// tensor pipe 72 % busy; 10 us of it is the tokens' conversion before, the rest the
+// ends of 1024 k and of tiles); 16 tokens x 130001 x 4096, memory (90 us, 5.9 TB/s); up
+// to 128 tokens on ordinary sizes, latency (64 x 4096 x 4096 10.6 us: 3 until the first
+// weights, 3 for the steps, 2 for the sums over the cluster, launch).
 #include "w8_linear.cuh"
 
 #include "device_prims.cuh"
@@ -589,9 +595,9 @@ struct Shape {
 };
 
 // The tiles that take the least time by a count of cycles: a step costs about 500 + 2.5 h with one half of h tokens
-// and 700 + 5.2 h with two (4096 k, 1 round of SMs: 128 tokens 18.6 us, 2 x 64 22.4, 2 x 128 28.0), a tile some more, and
-// SMs work in rounds.  Two halves read the weights half as often, and win from about 900 tokens x 4096 rows on; below,
-// tiles of one half are more, and fill the SMs: 512 x 4096 18.6 us for 28.0, 1024 x 4096 31.1 for 29.7.
+// and 700 + 5.2 h with two (512 x 4096 x 4096: tiles of 128 tokens 18.6 us, of 2 x 64 22.4, of 2 x 128 28.0), a tile some
+// more, and SMs work in rounds.  Two halves read the weights half as often, and win from about 900 tokens x 4096 rows on
+// (1024 x 4096 x 4096 29.7 us for 31.1); below, tiles of one half are more of them, and fill the SMs.
 Shape shape_of(int m, int n, int k, int num_sms) {
   const int64_t rows = (static_cast<int64_t>(n) + kRows - 1) / kRows;
   if (m <= 64) return Shape{kFew, (m + 15) / 16 * 16, 1, rows};

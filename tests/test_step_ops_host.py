@@ -147,3 +147,18 @@ def test_binding_has_no_cpu_path_and_checks_types():
         m.norm_add_rmsnorm_quant(x8, x, w, w)
     with pytest.raises(TypeError):
         m.token_logprobs(x8)
+
+
+def test_waits_of_the_w8_kernel_have_one_answer_for_a_warp():
+    """As in the attention's tensor-memory kernel: lanes that decided alone could part for ever.  Every wait goes through
+    the voted one, but for those after the roles, whose answers nobody takes."""
+    import re
+    src = open(os.path.join(ROOT, "moe_expert_ffn_dispatch_gb300", "csrc", "w8_linear_tc.cu")).read()
+    src = re.sub(r"//[^\n]*", "", src)
+    calls = [src[src.rfind("\n", 0, c.start()):src.index(";", c.start())].strip()
+             for c in re.finditer(r"\bmbar_(wait_bounded|try_wait|test_wait)\s*\(", src)]
+    voted = [c for c in calls if "__all_sync(0xffffffffu," in c]
+    after = [c for c in calls if re.search(r"&full\[i\]|&bar\.drain", c)]
+    assert len(voted) == 1 and len(voted) + len(after) == len(calls), calls
+    # and each answer is taken: no call of the voted wait stands by itself
+    assert not re.search(r"[;{}]\s*wait\(", src)
