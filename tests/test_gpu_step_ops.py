@@ -589,3 +589,43 @@ def test_results_do_not_change_from_call_to_call():
     for call in every_call(4):
         want = call()
         assert all(same(want, call()) for _ in range(5))
+
+
+# ------------------------------------------------------------ offsets past 32 bits
+def test_w8_outputs_and_weights_past_32_bits():
+    g = gen(11)
+    M, N, K = 17000, 130001, 64
+    x, w, ws, xs = w8_inputs(M, N, K, g)
+    y = m.w8_linear(x, w, ws, xs)
+    assert y.numel() > 2 ** 31
+    for rows in (slice(0, 5), slice(16500, 16530), slice(M - 7, M)):
+        assert torch.equal(y[rows], w8_reference(x[rows], w, ws, xs[rows], BF16))
+    del y
+    N, K = 600001, 4096
+    w = torch.randint(-128, 128, (N, K), device=DEV, generator=g, dtype=torch.int8)
+    assert w.numel() > 2 ** 31
+    ws = rand(N, g=g)
+    for M in (3, 20, 70, 200):
+        x, xs = codes(M, K, g=g), rand(M, g=g)
+        y = m.w8_linear(x, w, ws, xs)
+        for cols in (slice(0, 300), slice(524200, 524400), slice(N - 200, N)):
+            assert torch.equal(y[:, cols], w8_reference(x, w[cols], ws[cols], xs, BF16))
+
+
+def test_pair_and_logprobs_past_32_bits():
+    g = gen(12)
+    rows, h = 140000, 16384
+    x = torch.empty(rows, h, dtype=BF16, device=DEV).normal_(generator=g)
+    r = torch.empty(rows, h, dtype=BF16, device=DEV).normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    pw, w = (rand(h, g=g, lo=0.5, hi=1.5).to(BF16) for _ in "pw")
+    whole = m.norm_add_rmsnorm_quant(x, r, pw, w, gate=r, want_y=True)
+    for part in (slice(0, 3), slice(131071, 131074), slice(rows - 3, rows)):
+        for a, b in zip(whole, m.norm_add_rmsnorm_quant(x[part], r[part], pw, w, gate=r[part], want_y=True)):
+            assert torch.equal(a[part], b)
+    del whole, r
+    logits = x.view(-1)[:17000 * 130001].view(17000, 130001)
+    whole = m.token_logprobs(logits, torch.zeros(17000, dtype=torch.int32, device=DEV), 3)
+    for part in (slice(0, 2), slice(16515, 16520), slice(16998, 17000)):
+        check_logprobs(logits[part], torch.zeros(logits[part].shape[0], dtype=torch.int32, device=DEV), 3,
+                       tuple(t[part] for t in whole))
