@@ -8,32 +8,41 @@
 // stay fp32 as long as the largest that could have come together is below 2^24, which
 // is exact too, and are int32 from then on: the conversion is the drain's slowest part.
 //
-// A tile is 128 weight rows (M, the tensor memory's lanes) by up to 256 tokens (N, in
-// one or two halves of at most 128 columns).  Weights arrive as int8 by TMA and are
-// converted in the CTA into tensor memory, the products' A operand, so that they
-// cross memory and L2 as bytes.  Tokens are the B operand, f16 in shared memory: up to
-// 64 of them arrive as int8 too and are converted by every CTA; more are converted
-// once, by a kernel before this one into the workspace, and arrive as f16.
-// The two halves of a wide tile have an accumulator each, side by side: most steps of
-// 128 k multiply both at once, the first and the last of a 1024 k the first half
-// before the second, so that one is drained while the other's products run.  A tile
-// of one half alternates between two accumulators.
+// A tile is 128 weight rows (M, the tensor memory's lanes) by up to 128 tokens (N), or,
+// for many tokens, 256 rows by up to 256 tokens of a pair of CTAs: each has 128 of the
+// rows and half of the tokens, and the first issues products of both.  Weights arrive
+// as int8 by TMA and are converted in the CTA into tensor memory, the products' A
+// operand, so that they cross memory and L2 as bytes.  Tokens are the B operand, f16 in
+// shared memory: up to 64 of them arrive as int8 too and are converted by every CTA;
+// more are converted once, by a kernel before this one into the workspace, and arrive
+// as f16.  One CTA with 256 tokens of its own moves 146 KB a step of 128 k through
+// shared memory, all that it can in the step's time (4093 x 6144 x 4096 131 us); of a
+// pair each moves 98.
+// A pair's tile has an accumulator for each half of the tokens, side by side, and takes
+// two steps of one half, then of the other: at the end of 1024 k one accumulator is
+// drained while two steps' products run into the other (a step of each in turn 137 us
+// for 131).  Its halves need not be alike, so that tiles come in 32s of tokens: 19 x 24
+// tiles of 224 fill 76 pairs six times, 16 x 24 of 256 five times and a bit (121 us for
+// 128).  A tile of one half alternates between two accumulators.
 // What bounds a step is how fast one warp can wait, issue and commit (about 100 cycles
-// a wait, 40 a product): weights and tokens of a step complete one barrier, and its
-// products one other.
-// Roles: warp 0 copies weights, warp 2 copies tokens, warp 1 issues products, warps
-// 4..7 convert weights (a row a thread), warps 8..15 drain and write.  Up to 64 tokens
-// warps 4..7 and 8..11 convert weights and tokens of every other step, and warps
-// 12..15 drain: one group's chain of waits, loads and stores is 850 cycles a step.
+// a wait, 40 a product) and the conversion's chain of waits, loads and stores (830
+// cycles): weights and tokens of a step complete one barrier, and its products one other.
+// Roles: warp 0 copies weights, warp 2 copies tokens, warp 1 issues products (of a
+// pair's second CTA: tells the first that its tokens have landed), warps 4..7 convert
+// weights (a row a thread), warps 8..15 drain and write.  Up to 64 tokens warps 4..7 and
+// 8..11 convert weights and tokens of every other step, and warps 12..15 drain.
 // Where there are fewer tiles than SMs a cluster shares k out, and adds its int32
 // sums up over distributed shared memory, a share of the tile's columns each.
 //
-// Bound by: many tokens, the products (4093 x 6144 x 4096 132 us, 1.56 PFLOP/s, the
-// tensor pipe 72 % busy; 10 us of it is the tokens' conversion before, the rest the
-// ends of 1024 k and of tiles); 16 tokens x 130001 x 4096, memory (90 us, 5.9 TB/s); up
-// to 128 tokens on ordinary sizes, latency (64 x 4096 x 4096 10.6 us: 3 until the first
-// weights, 3 for the steps, 2 for the sums over the cluster, launch).
+// Bound by: many tokens, the products (4093 x 6144 x 4096 121 us, 1.70 PFLOP/s; 11 us of
+// it is the tokens' conversion before, the tensor pipe is busy for 172 of the 205
+// thousand cycles after, the rest is the ends of 1024 k and of tiles); 16 tokens x 130001
+// x 4096, memory (91 us, 5.9 TB/s); up to 128 tokens on ordinary sizes, latency (64 x 4096
+// x 4096 10.3 us: 3 until the first weights, 3 for the steps, 2 for the sums over the
+// cluster, launch).
 #include "w8_linear.cuh"
+
+#include <algorithm>
 
 #include "device_prims.cuh"
 #include "tensor_map.cuh"
@@ -57,7 +66,8 @@ constexpr int kSite = 2 << 8;       // of the waits, in the status
 constexpr float kNan = NAN;
 constexpr uint32_t kMostParts = 8;  // CTAs that share k out
 
-// How a tile's tokens lie: up to 64, up to 128, or two halves
+// A tile: 128 weight rows by up to 64 or up to 128 tokens, or 256 weight rows by up to 256 tokens in two halves, for a
+// pair of CTAs
 enum Form { kFew = 0, kOne = 1, kTwo = 2 };
 
 // Shared memory: tokens of each step, weight stages, barriers
@@ -65,9 +75,9 @@ template <int FORM>
 struct Layout {
   static constexpr int kHalves = FORM == kTwo ? 2 : 1;
   static constexpr int kHalf = FORM == kFew ? 64 : 128;  // tokens of a half at most
-  static constexpr int kAtomBytes = kHalves * kHalf * kAtom * 2;
-  static constexpr int kSteps = FORM == kTwo ? 3 : 4;  // of tokens, and of converted weights
-  static constexpr int kA8 = FORM == kTwo ? 2 : 6;     // weights (up to 64 tokens: and tokens) as they arrive
+  static constexpr int kAtomBytes = kHalf * kAtom * 2;  // (of a pair's tokens each CTA has one half)
+  static constexpr int kSteps = 4;  // of tokens, and of converted weights
+  static constexpr int kA8 = 6;     // weights (up to 64 tokens: and tokens) as they arrive
   static constexpr int kStageBytes = kA8Bytes + (FORM == kFew ? kHalf * kStage : 0);
   static constexpr int kOffA8 = kSteps * 2 * kAtomBytes, kOffBar = kOffA8 + kA8 * kStageBytes;
   static constexpr int kBytes = kOffBar + 512;
@@ -77,10 +87,13 @@ struct Layout {
   static_assert(kBytes + 1024 <= kMaxSmem, "shared memory");
   static_assert(kAccCols + kSteps * kA16Cols <= kTmemCols, "tensor memory");
   static_assert(kOffBar >= kHalf * kRows * 4, "the sums of a tile of one half fit the rings");
+  // arrivals of a step: the converting warps, the tokens' copy, and in a pair the other CTA's of both
+  static constexpr int kFull = FORM == kFew ? 4 : FORM == kOne ? 5 : 10;
+  static constexpr int kDrained = kDrainWarps * kHalves;
 };
 
 struct Barriers {
-  uint64_t a8_full[6], a8_empty[6], full[4], empty[4], acc_full[2], acc_empty[2], drain;
+  uint64_t a8_full[6], a8_empty[6], full[4], empty[4], tokens[4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort, broken;
 };
@@ -88,13 +101,15 @@ static_assert(sizeof(Barriers) <= 512, "");
 
 struct alignas(64) Maps {
   CUtensorMap w;  // int8 [n, k], box {128, 128}, 128-byte swizzle
-  CUtensorMap x;  // f16 [m, k], box {64, tokens of a tile}, or int8, box {128, tokens of a tile}; 128-byte swizzle
+  CUtensorMap x;  // f16 [m, k], box {64, tokens of a half}, or int8, box {128, tokens}; 128-byte swizzle
+  CUtensorMap y;  // of a pair: x is half of the first half's tokens, this half of the second's
 };
 
 struct Params {
   moe_layer_w8_args_t a;
   int32_t* status;
-  int half;     // tokens of a half, a multiple of 16
+  int half;     // tokens of a tile of one half, a multiple of 16, or of the first of two, of 32
+  int half1;    // of the second
   int blocks;   // tiles along m
   int64_t tiles;
 };
@@ -164,6 +179,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "memory");
 }
 
+// the largest of |a|, |b| and |c|
+__device__ __forceinline__ float most_of(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
@@ -182,6 +204,41 @@ __device__ __forceinline__ int4 cluster_read4(uint32_t at, uint32_t rank) {
                : "r"(remote)
                : "memory");
   return v;
+}
+
+// ---- a pair of CTAs: what one thread of the first issues works on the tensor memory of both
+__device__ __forceinline__ void pair_alloc(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(moe::smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (256 rows, 128 in each CTA) (+)= A (tensor memory, likewise) * B^T, whose N rows are half each CTA's
+__device__ __forceinline__ void pair_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on `bar` of both CTAs once every product issued so far by this thread is done
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          moe::smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// Arrive on `bar` of CTA `rank` of the cluster.  What the arrival tells of is tensor memory whose stores (or loads) have
+// been waited for and copies that a barrier of their own has completed, nothing that this thread wrote to memory: a
+// release over the cluster, which waits for all that it did, took 1200 cycles a step more.
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(moe::smem_u32(bar)), "r"(rank));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
 // The same for the steps, whose barriers the converters complete too: where they have given up, a phase never completes
@@ -206,10 +263,15 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   const moe_layer_w8_args_t& a = p.a;
   // (handed round, so that the compiler knows it to be one number a warp and keeps what follows from it in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  uint32_t rank, parts;  // of the cluster that shares k out
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
-  const int64_t first = blockIdx.x / parts, step = gridDim.x / parts;
+  uint32_t in_cluster, ctas;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(in_cluster));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int64_t first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  // a cluster shares k out, or is a pair that shares a tile
+  const uint32_t rank = FORM == kTwo ? 0 : in_cluster, parts = FORM == kTwo ? 1 : ctas;
+  const uint32_t side_of_pair = FORM == kTwo ? in_cluster : 0;
+  constexpr int kTileRows = kRows * HALVES;
+  const int tokens = HALVES == 2 ? p.half + p.half1 : p.half;
   const int stages = (a.k + kStage - 1) / kStage;
   const int kb0 = static_cast<int>(static_cast<int64_t>(stages) * rank / parts),
             kb1 = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / parts);
@@ -220,12 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       moe::mbar_init(&bar.a8_empty[lane], 4);
     }
     if (lane < L::kSteps) {
-      moe::mbar_init(&bar.full[lane], FORM == kFew ? 4 : 5);  // the converting warps, and the tokens' copy
+      moe::mbar_init(&bar.full[lane], L::kFull);
+      moe::mbar_init(&bar.tokens[lane], 1);
       moe::mbar_init(&bar.empty[lane], 1);
     }
     if (lane < 2) {
       moe::mbar_init(&bar.acc_full[lane], 1);
-      moe::mbar_init(&bar.acc_empty[lane], L::kDrainWarps);
+      moe::mbar_init(&bar.acc_empty[lane], L::kDrained);
     }
     if (lane == 0) {
       moe::mbar_init(&bar.drain, 1);
@@ -233,12 +296,16 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     }
     moe::fence_barrier_init();
   }
-  if (warp == 1) moe::tmem_alloc(&bar.tmem, kTmemCols);
+  if (warp == 1) {
+    if constexpr (FORM == kTwo) pair_alloc(&bar.tmem, kTmemCols);
+    else moe::tmem_alloc(&bar.tmem, kTmemCols);
+  }
   if (warp == 2 && lane == 0) {
     prefetch_map(&maps.w);
     prefetch_map(&maps.x);
   }
-  __syncthreads();
+  if constexpr (FORM == kTwo) cluster_sync();  // the other CTA's barriers are there
+  else __syncthreads();
   moe::tc_fence_after();
   const uint32_t tmem = bar.tmem;
   volatile int* abort = &bar.abort;
@@ -247,6 +314,15 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   // there are no status words.)  A tile whose wait gave up is written as NaN.
   auto wait = [&](uint64_t* b, uint32_t parity, int site) {
     return __all_sync(0xffffffffu, moe::mbar_wait_bounded(b, parity, abort, p.status, kSite + site)) != 0;
+  };
+  // the same, where the other CTA of a pair arrives
+  auto wait_both = [&](uint64_t* b, uint32_t parity, int site) {
+    return __all_sync(0xffffffffu, moe::mbar_wait_bounded<FORM == kTwo>(b, parity, abort, p.status, kSite + site)) != 0;
+  };
+  // what completes a step, or empties an accumulator, does so at the CTA that issues the products
+  auto arrive = [&](uint64_t* b) {
+    if (side_of_pair) arrive_at(b, 0);
+    else moe::mbar_arrive(b);
   };
 
   if constexpr (FORM == kFew) grid_dependency_wait();  // no kernel of this call's own has done so
@@ -260,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       uint32_t ph = 0;
       bool wrapped = false, ok = true;
       for (int64_t it = first; ok && it < p.tiles; it += step) {
-        const int n0 = static_cast<int>(it / p.blocks) * kRows;
+        const int n0 = static_cast<int>(it / p.blocks) * kTileRows + static_cast<int>(side_of_pair) * kRows;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (wrapped && !wait(&bar.a8_empty[s], ph ^ 1u, 1)) {
             ok = false;
@@ -283,7 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       int s = 0;
       uint32_t ph = 0;
       bool wrapped = false, ok = true;
-      const int tokens = p.half * HALVES;
+      // One half's tokens; or, of a pair, half of each half's, so that the columns of a product (the first CTA's tokens,
+      // then the second's) are neighbours.  The second CTA's copies complete a barrier of its own, which warp 1 hands on.
+      uint64_t* landed = side_of_pair ? bar.tokens : bar.full;
+      const int box = p.half / HALVES, box1 = p.half1 / 2;
       for (int64_t it = first; ok && it < p.tiles; it += step) {
         const int m0 = static_cast<int>(it % p.blocks) * tokens;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -292,28 +371,56 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
             break;
           }
           if (moe::elect_one()) {
-            moe::mbar_arrive_expect_tx(&bar.full[s], 2 * tokens * kAtom * 2);
+            moe::mbar_arrive_expect_tx(&landed[s], 2 * tokens / HALVES * kAtom * 2);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              moe::tma_load_2d(smem + (2 * s + h) * L::kAtomBytes, &maps.x, kb * kStage + h * kAtom, m0, &bar.full[s]);
+            for (int a = 0; a < 2; ++a) {
+              uint8_t* to = smem + (2 * s + a) * L::kAtomBytes;
+              const int k = kb * kStage + a * kAtom;
+              moe::tma_load_2d(to, &maps.x, k, m0 + side_of_pair * box, &landed[s]);
+              if (HALVES == 2)
+                moe::tma_load_2d(to + box * kAtom * 2, &maps.y, k, m0 + p.half + side_of_pair * box1, &landed[s]);
+            }
           }
           __syncwarp();
           if (++s == L::kSteps) s = 0, ph ^= 1u, wrapped = true;
         }
       }
       // what it armed has landed, or (the converters having given up) is past where a barrier could tell
-      drain_steps(bar.full, L::kSteps, s, ph, wrapped, abort, p.status, kSite + 4);
+      drain_steps(landed, L::kSteps, s, ph, wrapped, abort, p.status, kSite + 4);
+    } else if (warp == 1 && side_of_pair) {
+      // ---------------------------------------------------- the second CTA's tokens have landed
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t it = first; ok && it < p.tiles; it += step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = wait(&bar.tokens[s], ph, 13);
+          if (!ok) break;
+          if (lane == 0) arrive(&bar.full[s]);
+          __syncwarp();
+          if (++s == L::kSteps) s = 0, ph ^= 1u;
+        }
+      }
+      // the first CTA's products, which are of this one's memory too, are done
+      moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 8);
     } else if (warp == 1) {
       // ---------------------------------------------------- products
-      const uint32_t idesc = moe::umma_idesc_f16(kRows, p.half), idesc_both = moe::umma_idesc_f16(kRows, HALVES * p.half);
+      const uint32_t idescs[2] = {moe::umma_idesc_f16(kTileRows, p.half), moe::umma_idesc_f16(kTileRows, p.half1)};
       const uint64_t b0 = moe::umma_desc_sw128(moe::smem_u32(smem));
       constexpr uint64_t kAtomAt = L::kAtomBytes >> 4;
-      const uint64_t half_at = (p.half * kAtom * 2) >> 4;
+      const uint64_t half_at = (p.half / HALVES * kAtom * 2) >> 4;
       // eight products of 16 k
-      auto products = [&](uint32_t d, uint32_t at, uint64_t bd, uint32_t form, bool fresh) {
+      auto products = [&](uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, bool fresh) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          moe::umma_f16_ts(d, at + 8 * k, bd + (k >> 2) * kAtomAt + 2 * (k & 3), form, !fresh || k != 0);
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t bk = bd + (k >> 2) * kAtomAt + 2 * (k & 3);
+          if constexpr (FORM == kTwo) pair_mma_ts(d, at + 8 * k, bk, idesc, !fresh || k != 0);
+          else moe::umma_f16_ts(d, at + 8 * k, bk, idesc, !fresh || k != 0);
+        }
+      };
+      auto commit = [&](uint64_t* b) {
+        if constexpr (FORM == kTwo) pair_commit(b);
+        else moe::umma_commit(b);
       };
       int s = 0;
       uint32_t ph = 0;
@@ -321,45 +428,40 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       bool ok = true;
       for (int64_t it = first; ok && it < p.tiles; it += step) {
         int kc = 0;  // step of the chunk
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const bool last = kc + 1 == kChunk || kb + 1 == kb1;
-          const uint32_t at = tmem + kAccCols + s * kA16Cols;
-          const uint64_t bd = b0 + 2 * s * kAtomAt;
-          if (HALVES == 2 && kc != 0 && !last) {
-            ok = wait(&bar.full[s], ph, 5);
-            if (!ok) break;
-            moe::tc_fence_after();
-            if (moe::elect_one()) {
-              products(tmem, at, bd, idesc_both, false);
-              moe::umma_commit(&bar.empty[s]);
-            }
-          } else {
-            ok = wait(&bar.full[s], ph, 6);
+        for (int kb = kb0; ok && kb < kb1;) {
+          const int steps = HALVES == 2 && kc + 1 < kChunk && kb + 1 < kb1 ? 2 : 1;
+          const bool last = kc + steps == kChunk || kb + steps == kb1;
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-              // the accumulator's uses so far: a half's own one a chunk, or two in turn
-              const int buf = HALVES == 2 ? h : static_cast<int>(chunk & 1);
-              const int64_t used = HALVES == 2 ? chunk : chunk >> 1;
-              if (kc == 0 && used > 0) ok = ok && wait(&bar.acc_empty[buf], (used - 1) & 1, 7);
+          for (int h = 0; h < HALVES; ++h) {
+            // the accumulator's uses so far: a half's own one a chunk, or two in turn
+            const int buf = HALVES == 2 ? h : static_cast<int>(chunk & 1);
+            const int64_t used = HALVES == 2 ? chunk : chunk >> 1;
+            if (kc == 0 && used > 0) ok = ok && wait_both(&bar.acc_empty[buf], (used - 1) & 1, 7);
+#pragma unroll
+            for (int i = 0; i < HALVES; ++i) {
+              if (i == steps) break;
+              const int at = s + i < L::kSteps ? s + i : 0;
+              if (h == 0) ok = ok && wait_both(&bar.full[at], s + i < L::kSteps ? ph : ph ^ 1u, 6);
               if (!ok) break;
               moe::tc_fence_after();
               if (moe::elect_one()) {
-                products(tmem + buf * p.half, at, bd + h * half_at, idesc, kc == 0);
-                if (h == HALVES - 1) moe::umma_commit(&bar.empty[s]);
-                if (last) moe::umma_commit(&bar.acc_full[buf]);
+                products(tmem + buf * p.half, tmem + kAccCols + at * kA16Cols, b0 + 2 * at * kAtomAt + h * half_at,
+                         idescs[h], kc + i == 0);
+                if (h == HALVES - 1) commit(&bar.empty[at]);
+                if (last && i + 1 == steps) commit(&bar.acc_full[buf]);
               }
               __syncwarp();
             }
-            if (!ok) break;
           }
-          __syncwarp();
-          if (++s == L::kSteps) s = 0, ph ^= 1u;
+          s += steps;
+          if (s >= L::kSteps) s -= L::kSteps, ph ^= 1u;
+          kb += steps;
           if (last) ++chunk, kc = 0;
-          else ++kc;
+          else kc += steps;
         }
       }
       // nothing of this CTA is in flight when its tensor memory goes back
-      if (moe::elect_one()) moe::umma_commit(&bar.drain);
+      if (moe::elect_one()) commit(&bar.drain);
       __syncwarp();
       moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 8);
     }
@@ -381,8 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     const int tok_to = (tch >> 2) * L::kAtomBytes + tok0 * 128;
     const int j0 = (((tch & 3) * 2) ^ (tok0 & 7)) << 4, j1 = (((tch & 3) * 2 + 1) ^ (tok0 & 7)) << 4;
     uint4 x[4];
-    auto load = [&]() {
-      if (!wait(&bar.a8_full[s8], p8, 9)) return false;
+    bool free = true;  // the slot of the next step is known to be
+    auto load = [&](int64_t k) {
+      // two looks whose latencies overlap
+      const bool here = moe::mbar_test_wait(&bar.a8_full[s8], p8);
+      const int sn = s + kGroups < L::kSteps ? s + kGroups : s + kGroups - L::kSteps;
+      const uint32_t pn = s + kGroups < L::kSteps ? ph : ph ^ 1u;
+      free = k < L::kSteps || __all_sync(0xffffffffu, moe::mbar_test_wait(&bar.empty[sn], pn ^ 1u));
+      if (!__all_sync(0xffffffffu, here) && !wait(&bar.a8_full[s8], p8, 9)) return false;
       const uint8_t* stage = smem + L::kOffA8 + s8 * L::kStageBytes;
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(stage + row * kStage + ((j ^ (row & 7)) << 4));
@@ -391,18 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i)
           if (tok0 + 16 * i < p.half) x[i] = *reinterpret_cast<const uint4*>(stage + tok_from + i * 16 * kStage);
       }
-      // The copy that refills the slot is of the async proxy: without this fence it can overtake loads that are still on
-      // their way to registers (seen as rows whose last chunks were those of two steps on).
-      moe::fence_proxy_async_smem();
+      return true;
+    };
+    // The copy that refills the slot is of the async proxy and can overtake loads that are still on their way to
+    // registers (seen as rows whose last chunks were those of two steps on): the slot goes back once the codes have been
+    // converted, so that they have arrived.  (A proxy fence right after the loads costs 200 cycles a step.)
+    auto hand_back = [&]() {
       __syncwarp();
       if (lane == 0) moe::mbar_arrive(&bar.a8_empty[s8]);
       s8 += kGroups;
       if (s8 >= L::kA8) s8 -= L::kA8, p8 ^= 1u;
-      return true;
     };
-    bool ok = group < n_stages && load();
+    bool ok = group < n_stages && load(0);
     for (int64_t k = group; ok && k < n_stages; k += kGroups) {
-      if (k >= L::kSteps && !wait(&bar.empty[s], ph ^ 1u, 10)) break;
+      if (!free && !wait(&bar.empty[s], ph ^ 1u, 10)) break;
       moe::tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -424,11 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         }
         moe::fence_proxy_async_smem();
       }
-      if (k + kGroups < n_stages) ok = load();
+      hand_back();
+      if (k + kGroups < n_stages) ok = load(k + kGroups);
       moe::tmem_st_wait();  // also on the way out after a wait that gave up: no store left in flight
       moe::tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) moe::mbar_arrive(&bar.full[s]);
+      if (ok && lane == 0) arrive(&bar.full[s]);
       s += kGroups;
       if (s >= L::kSteps) s -= L::kSteps, ph ^= 1u;
     }
@@ -440,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     auto release = [&](int buf) {
       moe::tc_fence_before();
       __syncwarp();
-      if (lane == 0) moe::mbar_arrive(&bar.acc_empty[buf]);
+      if (lane == 0) arrive(&bar.acc_empty[buf]);
     };
     int64_t chunk = 0;
     bool ok = true;
@@ -461,24 +572,25 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         for (int h = 0; h < HALVES; ++h) {
           const int buf = HALVES == 2 ? h : static_cast<int>(chunk & 1);
           const int64_t used = HALVES == 2 ? chunk : chunk >> 1;
+          const int half = h == 0 ? p.half : p.half1;
           ok = ok && wait(&bar.acc_full[buf], used & 1, 11);
           if (!ok) break;
           moe::tc_fence_after();
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // columns past the half's last are read along with it, and not looked at
-            if (64 * side + 32 * j < p.half) {
+            if (64 * side + 32 * j < half) {
               uint32_t v[32];
               tmem_ld32(from + buf * p.half + 32 * j, v);
-              if (j == 1 || 64 * side + 32 >= p.half) release(buf);  // what is still to come is in registers
+              if (j == 1 || 64 * side + 32 >= half) release(buf);  // what is still to come is in registers
               const uint32_t bit = 1u << (2 * h + j);
               if (!(whole & bit)) {
                 float most = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
-                if (64 * side + 32 * j + 16 < p.half) {
+                for (int e = 0; e < 16; e += 2) most = most_of(most, v[e], v[e + 1]);
+                if (64 * side + 32 * j + 16 < half) {
 #pragma unroll
-                  for (int e = 16; e < 32; ++e) most = fmaxf(most, fabsf(__uint_as_float(v[e])));
+                  for (int e = 16; e < 32; e += 2) most = most_of(most, v[e], v[e + 1]);
                 }
                 reach[h][j] = __fadd_ru(reach[h][j], most);
                 if (__any_sync(0xffffffffu, reach[h][j] > 16777216.0f)) {
@@ -489,15 +601,19 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
               }
               if (!(whole & bit)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  acc[h][32 * j + e] = __float_as_uint(__fadd_rn(__uint_as_float(acc[h][32 * j + e]), __uint_as_float(v[e])));
+                for (int e = 0; e < 32; e += 2) {
+                  uint32_t* to = &acc[h][32 * j + e];
+                  const float2 sum = of_pair(add_pair(pair_of(__uint_as_float(to[0]), __uint_as_float(to[1])),
+                                                      pair_of(__uint_as_float(v[e]), __uint_as_float(v[e + 1]))));
+                  to[0] = __float_as_uint(sum.x), to[1] = __float_as_uint(sum.y);
+                }
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) acc[h][32 * j + e] += __float2int_rn(__uint_as_float(v[e]));
               }
             }
           }
-          if (64 * side >= p.half) release(buf);
+          if (64 * side >= half) release(buf);
         }
       }
       if (parts > 1) {
@@ -511,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         if (!ok && lane == 0) bar.broken = 1;
         break;
       }
-      const int n = static_cast<int>(it / p.blocks) * kRows + 32 * q + lane;
-      const int m0 = static_cast<int>(it % p.blocks) * p.half * HALVES + 64 * side;
+      const int n = static_cast<int>(it / p.blocks) * kTileRows + static_cast<int>(side_of_pair) * kRows + 32 * q + lane;
+      const int m0 = static_cast<int>(it % p.blocks) * tokens + 64 * side;
 #pragma unroll
       for (int h = 0; h < HALVES; ++h)
 #pragma unroll
@@ -522,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
         const int row = m0 + h * p.half;
-        const int most = min(min(64, p.half - 64 * side), a.m - row);  // tokens of mine that there are
+        const int most = min(min(64, (h == 0 ? p.half : p.half1) - 64 * side), a.m - row);  // tokens of mine that there are
         // their scales: a lane holds two, and hands them round
         const float xs0 = lane < most ? __ldg(a.x_scale + row + lane) : 0.0f;
         const float xs1 = lane + 32 < most ? __ldg(a.x_scale + row + lane + 32) : 0.0f;
@@ -534,10 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       }
     }
   }
-  __syncthreads();
+  // (of a pair: no CTA ends, or gives its tensor memory back, while the other's products or arrivals may be under way)
+  if constexpr (FORM == kTwo) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
     moe::tc_fence_after();
-    moe::tmem_dealloc(tmem, kTmemCols);
+    if constexpr (FORM == kTwo) pair_dealloc(tmem, kTmemCols);
+    else moe::tmem_dealloc(tmem, kTmemCols);
   }
   if constexpr (HALVES == 1) {
     if (parts > 1) {
@@ -590,17 +709,18 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
 }
 
 struct Shape {
-  int form, half, blocks;
+  int form, half, half1, blocks;
   int64_t tiles;
 };
 
-// The tiles that take the least time by a count of cycles: a step costs about 500 + 2.5 h with one half of h tokens
-// and 700 + 5.2 h with two (512 x 4096 x 4096: tiles of 128 tokens 18.6 us, of 2 x 64 22.4, of 2 x 128 28.0), a tile some
-// more, and SMs work in rounds.  Two halves read the weights half as often, and win from about 900 tokens x 4096 rows on
-// (1024 x 4096 x 4096 29.7 us for 31.1); below, tiles of one half are more of them, and fill the SMs.
+// The tiles that take the least time by a count of cycles, fitted to 33 sizes of 160..4093 tokens with every tile of
+// them (of 500 times within 4 %, the tile chosen on average 1 % off the best): with one half of t tokens a step costs 525 +
+// 1.4 t, a pair's 270 + 3.2 t and no less than the conversion of the weights, 830; a tile some more, and SMs work in rounds.
+// A pair reads weights and tokens half as often and wins once there are tiles for all SMs (1024 x 4096 x 4096 28.7 us for
+// 31.8; 512 x 4096 x 4096, where one half fills the SMs and a pair does not, 19.3 for 23.1).
 Shape shape_of(int m, int n, int k, int num_sms) {
   const int64_t rows = (static_cast<int64_t>(n) + kRows - 1) / kRows;
-  if (m <= 64) return Shape{kFew, (m + 15) / 16 * 16, 1, rows};
+  if (m <= 64) return Shape{kFew, (m + 15) / 16 * 16, 0, 1, rows};
   const int steps = (k + kStage - 1) / kStage;
   Shape s{};
   double best = 0;
@@ -608,14 +728,17 @@ Shape shape_of(int m, int n, int k, int num_sms) {
     const int halves = form == kTwo ? 2 : 1, least = (m + 128 * halves - 1) / (128 * halves);
     if (form == kTwo && m <= 128) break;
     for (int b = least; b <= 2 * least; ++b) {
-      const int half = ((m + b - 1) / b + 16 * halves - 1) / (16 * halves) * 16, blocks = (m + halves * half - 1) / (halves * half);
-      const int64_t tiles = rows * blocks, rounds = (tiles + num_sms - 1) / num_sms;
+      // (a pair's product is of a multiple of 32 tokens)
+      const int unit = form == kTwo ? 32 : 16, tokens = ((m + b - 1) / b + unit - 1) / unit * unit;
+      const int half1 = form == kTwo ? tokens / 64 * 32 : 0, half = tokens - half1, blocks = (m + tokens - 1) / tokens;
+      const int64_t tiles = (form == kTwo ? (rows + 1) / 2 : rows) * blocks, at_once = form == kTwo ? num_sms / 2 : num_sms;
+      const int64_t rounds = (tiles + at_once - 1) / at_once;
       int parts = 1;  // of k, in a cluster
       if (form == kOne)
         while (parts < static_cast<int>(kMostParts) && tiles * (parts + 1) <= num_sms && steps >= 2 * (parts + 1)) ++parts;
-      const double cost = rounds * (static_cast<double>(steps) / parts * (form == kTwo ? 700 + 5.2 * half : 500 + 2.5 * half) +
-                                    (form == kTwo ? 4000 : 2500) + (parts > 1 ? 2500 : 0));
-      if (best == 0 || cost < best) best = cost, s = Shape{form, half, blocks, tiles};
+      const double a_step = form == kTwo ? std::max(830.0, 270 + 3.2 * tokens) : (525 + 1.4 * tokens) / parts;
+      const double cost = rounds * (steps * a_step + (form == kTwo ? 2800 : 900) + (parts > 1 ? 4600 : 0));
+      if (best == 0 || cost < best) best = cost, s = Shape{form, half, half1, blocks, tiles};
     }
   }
   return s;
@@ -661,6 +784,12 @@ cudaError_t launch_tiles(const Maps& maps, const Params& p, int num_sms, cudaStr
   Maps m = maps;
   Params arg = p;
   void* args[] = {&m, &arg};
+  if constexpr (FORM == kTwo) {
+    int64_t pairs = clusters_at_once<FORM>(2);
+    if (pairs < 1) pairs = num_sms / 2;
+    if (p.tiles < pairs) pairs = p.tiles;
+    return launch_after(k, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), args, Layout<FORM>::kBytes + 1024, s, 2);
+  }
   const int64_t grid = parts > 1 ? p.tiles * parts : p.tiles < num_sms ? p.tiles : num_sms;
   return launch_after(k, dim3(static_cast<unsigned>(grid)), dim3(kThreads), args, Layout<FORM>::kBytes + 1024, s, parts);
 }
@@ -674,7 +803,7 @@ cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cu
   Maps maps{};
   if (!moe::encode_2d(&maps.w, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.n, a.k, kStage, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  Params p{a, nullptr, shape.half, shape.blocks, shape.tiles};
+  Params p{a, nullptr, shape.half, shape.half1, shape.blocks, shape.tiles};
   if (shape.form == kFew) {
     if (!moe::encode_2d(&maps.x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.m, a.k, kStage, shape.half,
                         CU_TENSOR_MAP_SWIZZLE_128B, a.x_stride))
@@ -684,7 +813,10 @@ cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cu
   p.status = static_cast<int32_t*>(ws);
   __half* x16 = reinterpret_cast<__half*>(static_cast<char*>(ws) + 256);
   if (!moe::encode_2d(&maps.x, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.m, a.k, kAtom,
-                      shape.half * (shape.form == kTwo ? 2 : 1), CU_TENSOR_MAP_SWIZZLE_128B))
+                      shape.half / (shape.form == kTwo ? 2 : 1), CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (shape.form == kTwo && !moe::encode_2d(&maps.y, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.m, a.k, kAtom, shape.half1 / 2,
+                                            CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   moe_layer_w8_args_t arg = a;
   void* args[] = {&arg, &x16, &p.status};

@@ -238,6 +238,47 @@ def test_w8_sums_are_exact_at_the_limits(M, K):
     assert torch.equal(m.w8_linear(x, w, *one, out_dtype=F32), w8_reference(x, w, *one, F32))
 
 
+PAIRS = [(1000, 5003, 4992), (700, 5100, 1040), (1500, 2000, 2192), (4093, 700, 1136), (2500, 2177, 1040), (1500, 5000, 1040),
+         (1300, 3500, 4000), (300, 9000, 4096), (129, 20000, 2048)]
+
+
+@pytest.mark.parametrize("M, N, K", PAIRS)
+def test_w8_two_ctas_a_tile(M, N, K):
+    """Sizes whose tiles are pairs of CTAs': tokens and weights that end in either half of a tile, or before its second
+    half; steps of k that are odd in number, or end in zeros."""
+    g = gen(M + N + K)
+    x, w, ws, xs = w8_inputs(M, N, K, g)
+    want = w8_reference(x, w, ws, xs, F32)
+    for _ in range(3):
+        y = torch.full((M + 1, N), 7.0, device=DEV)
+        m.w8_linear(x, w, ws, xs, out=y[:M])
+        assert torch.equal(y[:M], want) and bool((y[M] == 7).all())
+    assert torch.equal(m.w8_linear(x, w, ws, xs), want.to(BF16))
+
+
+@pytest.mark.parametrize("M, N, K", [(2500, 2177, 8192), (2000, 2100, 16384), (1500, 2177, 1040)])
+def test_w8_two_ctas_a_tile_at_the_limits(M, N, K):
+    x, w = (torch.full(s, -128, dtype=torch.int8, device=DEV) for s in ((M, K), (N, K)))
+    x[M // 2] = 127
+    x[::3, : K // 2] = 127  # sums that cross 2^24 and come back
+    w[1, ::2], w[1, 1::2] = 127, -128
+    x[0, 0], w[2, K - 1], w[N - 1, K - 3] = 5, -7, 9
+    one = torch.ones(N, device=DEV), torch.ones(M, device=DEV)
+    assert torch.equal(m.w8_linear(x, w, *one, out_dtype=F32), w8_reference(x, w, *one, F32))
+
+
+def test_w8_two_ctas_a_tile_at_once_on_two_streams():
+    g = gen(77)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ins = [w8_inputs(1000, 5003, 2048, g), w8_inputs(700, 6000, 1040, g)]
+    want = [w8_reference(*i, F32) for i in ins]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [m.w8_linear(*i, out_dtype=F32, stream=s) for i, s in zip(ins, sides)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_w8_strides_placement_and_what_is_not_written():
     g = gen(5)
     for M, N, K in ((5, 70, 256), (70, 70, 256), (300, 333, 512)):
