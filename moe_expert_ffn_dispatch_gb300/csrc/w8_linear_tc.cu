@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     };
     // The copy that refills the slot is of the async proxy and can overtake loads that are still on their way to
     // registers (seen as rows whose last chunks were those of two steps on): the slot goes back once the codes have been
-    // converted, so that they have arrived.  (A proxy fence right after the loads costs 200 cycles a step.)
+    // converted, so that they have arrived.  (A proxy fence right after the loads took 100 cycles a step more.)
     auto hand_back = [&]() {
       __syncwarp();
       if (lane == 0) moe::mbar_arrive(&bar.a8_empty[s8]);
