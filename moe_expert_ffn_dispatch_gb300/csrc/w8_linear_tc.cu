@@ -483,14 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     const int tok_to = (tch >> 2) * L::kAtomBytes + tok0 * 128;
     const int j0 = (((tch & 3) * 2) ^ (tok0 & 7)) << 4, j1 = (((tch & 3) * 2 + 1) ^ (tok0 & 7)) << 4;
     uint4 x[4];
-    bool free = true;  // the slot of the next step is known to be
-    auto load = [&](int64_t k) {
-      // two looks whose latencies overlap
-      const bool here = moe::mbar_test_wait(&bar.a8_full[s8], p8);
-      const int sn = s + kGroups < L::kSteps ? s + kGroups : s + kGroups - L::kSteps;
-      const uint32_t pn = s + kGroups < L::kSteps ? ph : ph ^ 1u;
-      free = k < L::kSteps || __all_sync(0xffffffffu, moe::mbar_test_wait(&bar.empty[sn], pn ^ 1u));
-      if (!__all_sync(0xffffffffu, here) && !wait(&bar.a8_full[s8], p8, 9)) return false;
+    auto load = [&]() {
+      if (!wait(&bar.a8_full[s8], p8, 9)) return false;
       const uint8_t* stage = smem + L::kOffA8 + s8 * L::kStageBytes;
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(stage + row * kStage + ((j ^ (row & 7)) << 4));
@@ -510,9 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       s8 += kGroups;
       if (s8 >= L::kA8) s8 -= L::kA8, p8 ^= 1u;
     };
-    bool ok = group < n_stages && load(0);
+    bool ok = group < n_stages && load();
     for (int64_t k = group; ok && k < n_stages; k += kGroups) {
-      if (!free && !wait(&bar.empty[s], ph ^ 1u, 10)) break;
+      if (k >= L::kSteps && !wait(&bar.empty[s], ph ^ 1u, 10)) break;
       moe::tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -535,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         moe::fence_proxy_async_smem();
       }
       hand_back();
-      if (k + kGroups < n_stages) ok = load(k + kGroups);
+      if (k + kGroups < n_stages) ok = load();
       moe::tmem_st_wait();  // also on the way out after a wait that gave up: no store left in flight
       moe::tc_fence_before();
       __syncwarp();

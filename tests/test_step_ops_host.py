@@ -162,3 +162,17 @@ def test_waits_of_the_w8_kernel_have_one_answer_for_a_warp():
     assert len(voted) == 1 and len(voted) + len(after) == len(calls), calls
     # and each answer is taken: no call of the voted wait stands by itself
     assert not re.search(r"[;{}]\s*wait\(", src)
+
+
+def test_waits_of_a_pair_of_ctas_in_the_w8_kernel():
+    """What both CTAs of a pair complete is waited for over the cluster, by the voted wait of that kind, whose answer is
+    taken; and nothing of the pair ends before the cluster's last barrier."""
+    import re
+    src = open(os.path.join(ROOT, "moe_expert_ffn_dispatch_gb300", "csrc", "w8_linear_tc.cu")).read()
+    src = re.sub(r"//[^\n]*", "", src)
+    over = [src[src.rfind("\n", 0, c.start()):src.index(";", c.start())] for c in re.finditer(r"mbar_wait_bounded<", src)]
+    assert len(over) == 1 and "__all_sync(0xffffffffu," in over[0]
+    assert not re.search(r"[;{}]\s*wait_both\(", src)
+    takers = re.findall(r"ok = ok && wait_both\(&bar\.(\w+)", src)
+    assert sorted(takers) == ["acc_empty", "full"] == sorted(re.findall(r"wait_both\(&bar\.(\w+)", src))
+    assert src.index("pair_dealloc(tmem") > src.rindex("if constexpr (FORM == kTwo) cluster_sync();") > src.rindex("wait(&bar")
