@@ -11,7 +11,8 @@
 // 8 x 4096: 2.5 us, latency.  Five CTAs of 256 threads an SM, for which the compiler has 48
 // registers a thread (three CTAs took 31.6 us); two elements an instruction (28.6 without).
 // Past 4096 wide it spills: 2000 x 8192 32 us, 1000 x 16384 31.  Rows that are not 16-byte
-// aligned go through shared memory and take twice the time (4093 x 4097 70 us, 2000 x 8191 59).
+// aligned go through shared memory and take twice the time (4093 x 4097 64 us, 2000 x 8191 53;
+// issue 69 %, 61 instructions an element).
 #include "norm_rows.cuh"
 
 namespace moe_layer {

@@ -9,10 +9,10 @@
 // element.  4093 x 4096 with residual and y: 23.8 us, 6.3 TB/s of 6.8; 8 x 4096:
 // 2.2 us, latency.  Rows that are not 16-byte aligned take about twice the
 // instructions and four barriers: 4093 x 4097 48 us (element by element it was
-// 84), 16000 x 1001 44, 16000 x 513 34 (54).  A weight in fp32 costs little up to
+// 84), 16000 x 1001 39, 16000 x 513 34 (54).  A weight in fp32 costs little up to
 // 4096 wide (4093 x 4096 24.9 us for 23.9); beyond, its 32 values a thread do not fit
 // the registers beside the row, and the spills show: 2000 x 8192 31 us for 24, 1000 x
-// 16384 35 for 26, 2000 x 8191 74 for 51.
+// 16384 35 for 26, 2000 x 8191 57 for 47.
 #include "norm_rows.cuh"
 
 namespace moe_layer {

@@ -41,15 +41,11 @@ struct RowIn {
       if ((e0 >= 0 || before) && (e0 + 8 <= h || after)) {
         b[c] = *reinterpret_cast<const uint4*>(p + e0);
       } else {
-        uint64_t lo = 0, hi = 0;
-#pragma unroll 1
-        for (int j = max(-e0, 0); j < min(h - e0, 8); ++j) {
-          const uint64_t v = static_cast<uint64_t>(p[e0 + j]) << (16 * (j & 3));
-          if (j < 4) lo |= v;
-          else hi |= v;
-        }
-        b[c] = make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
-                          static_cast<uint32_t>(hi >> 32));
+        // (all on their way at once: a loop over them, 1000 x 16383 59.5 us for 54.4)
+        uint32_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = e0 + j >= 0 && e0 + j < h ? p[e0 + j] : 0;
+        b[c] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
       }
     }
   }
@@ -60,15 +56,34 @@ struct RowIn {
   }
 };
 
+// The 8 elements that begin `at` elements (0..7) into slot n, from two wide accesses, which no banks
+// conflict in (word by word four neighbours meet in each), and selects by what is one number a row.
+__device__ __forceinline__ uint4 elements_at(const uint4* buf, int n, int at) {
+  const uint4 a = buf[n], b = buf[n + 1];
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) w[j] = at & 4 ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = at & 2 ? w[j + 1] : w[j];
+  const int bits = (at & 1) * 16;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+
 // chunk n of a staged row
 template <typename E>
 __device__ __forceinline__ void take_row(const uint4* buf, int n, int off, int h, float (&v)[8]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(buf) + n * 4 + (off >> 1);
+  const uint4 u = elements_at(buf, n, off);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = unpack2<E>(__funnelshift_r(w[j], w[j + 1], (off & 1) * 16));
-    v[2 * j] = n * 8 + 2 * j < h ? f.x : 0.0f;
-    v[2 * j + 1] = n * 8 + 2 * j + 1 < h ? f.y : 0.0f;
+    const float2 f = unpack2<E>(w[j]);
+    v[2 * j] = f.x, v[2 * j + 1] = f.y;
+  }
+  if (n * 8 + 8 > h) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n * 8 + j >= h) v[j] = 0.0f;
   }
 }
 
@@ -79,11 +94,7 @@ __device__ __forceinline__ void store_row(void* row, const uint4* buf, int tid, 
   for (int n = tid; n < blocks; n += nt) {
     const int e0 = n * 8 - off;
     if (e0 >= 0 && e0 + 8 <= h) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(buf) + (e0 >> 1);
-      uint32_t c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = __funnelshift_r(w[j], w[j + 1], (off & 1) * 16);
-      *reinterpret_cast<uint4*>(p + e0) = make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint4*>(p + e0) = elements_at(buf, off ? n - 1 : n, off ? 8 - off : 0);
     } else {
 #pragma unroll 1
       for (int e = max(e0, 0); e < min(e0 + 8, h); ++e) p[e] = reinterpret_cast<const uint16_t*>(buf)[e];
