@@ -56,7 +56,7 @@ constexpr int kAtom = 64;           // k of one 128-byte row of f16
 constexpr int kChunk = 1024 / kStage;  // stages that a sum stays exact for
 constexpr int kA16Cols = kStage / 2;  // of a converted weight stage in tensor memory
 constexpr int kTmemCols = 512;
-constexpr int kThreads = 512;
+constexpr int kThreads = 512, kWidenThreads = 256;
 // Registers a thread where a tile has two halves: 128 at launch, and what the drain warps have more the others give.
 // (With one half nobody needs more, and the sums over a cluster are every warp's.)
 constexpr int kRoleRegs = 64, kConvRegs = 96, kDrainRegs = 176;
@@ -122,21 +122,32 @@ __device__ __forceinline__ void widen16(const uint4& c, uint32_t* o) {
   half_pairs(c.w, o[6], o[7]);
 }
 
-// the tokens as f16, dense; and the status words of the call
-__global__ void __launch_bounds__(256) w8_widen_kernel(const moe_layer_w8_args_t a, __half* x16, int32_t* status) {
+// The tokens as f16, dense; and the status words of the call.  2^shift threads a row, 8 codes at a time, so that loads and
+// stores of a warp are whole lines.
+__global__ void __launch_bounds__(kWidenThreads) w8_widen_kernel(const moe_layer_w8_args_t a, __half* x16, int32_t* status,
+                                                                 int shift) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < 8) status[threadIdx.x] = 0;
-  const int chunks = a.k / 16;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.m) * chunks) return;
-  const int64_t row = i / chunks;
-  const int c = static_cast<int>(i - row * chunks);
-  uint32_t o[8];
-  widen16(*reinterpret_cast<const uint4*>(a.x + row * a.x_stride + c * 16), o);
-  uint4* to = reinterpret_cast<uint4*>(x16 + i * 16);
-  to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kWidenThreads >> shift) + (threadIdx.x >> shift);
+  if (row >= a.m) return;
+  const int pieces = a.k / 8, step = 1 << shift;
+  const uint2* from = reinterpret_cast<const uint2*>(a.x + row * a.x_stride);
+  uint4* to = reinterpret_cast<uint4*>(x16 + row * a.k);
+  for (int c = threadIdx.x & (step - 1); c < pieces; c += 4 * step) {
+    uint2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i * step < pieces) v[i] = from[c + i * step];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + i * step >= pieces) continue;
+      uint32_t o[4];
+      half_pairs(v[i].x, o[0], o[1]);
+      half_pairs(v[i].y, o[2], o[3]);
+      to[c + i * step] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 // Every copy that a producer issued has landed when this returns: the last phase
@@ -813,10 +824,12 @@ cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cu
                                             CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   moe_layer_w8_args_t arg = a;
-  void* args[] = {&arg, &x16, &p.status};
-  const int64_t chunks = static_cast<int64_t>(a.m) * (a.k / 16);
-  const cudaError_t e = launch_after((const void*)w8_widen_kernel, dim3(static_cast<unsigned>((chunks + 255) / 256)), dim3(256),
-                                     args, 0, s);
+  int shift = 0;  // a thread has one to four pieces of a row where it can
+  while (shift < 8 && (8 << (shift + 2)) < a.k) ++shift;
+  void* args[] = {&arg, &x16, &p.status, &shift};
+  const int rows = kWidenThreads >> shift;
+  const cudaError_t e = launch_after((const void*)w8_widen_kernel, dim3(static_cast<unsigned>((a.m + rows - 1) / rows)),
+                                     dim3(kWidenThreads), args, 0, s);
   if (e != cudaSuccess) return e;
   return shape.form == kTwo ? launch_tiles<kTwo>(maps, p, num_sms, s) : launch_tiles<kOne>(maps, p, num_sms, s);
 }
