@@ -264,7 +264,8 @@ __device__ __forceinline__ void drain_steps(uint64_t* full, int n, int s, uint32
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-template <int FORM>
+// EARLY: slots of codes go back before the codes are converted
+template <int FORM, bool EARLY>
 __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
   using L = Layout<FORM>;
   constexpr int HALVES = L::kHalves, kAccCols = L::kAccCols;
@@ -494,6 +495,17 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     const int tok_to = (tch >> 2) * L::kAtomBytes + tok0 * 128;
     const int j0 = (((tch & 3) * 2) ^ (tok0 & 7)) << 4, j1 = (((tch & 3) * 2 + 1) ^ (tok0 & 7)) << 4;
     uint4 x[4];
+    // The copy that refills the slot is of the async proxy and can overtake loads that are still on their way to
+    // registers (seen as rows whose last chunks were those of two steps on): the slot goes back once the codes have been
+    // converted, so that they have arrived, or (EARLY) behind a proxy fence right after the loads.  The fence takes 100 cycles
+    // a step (64 x 4096 x 4096 10.6 us for 10.2), but where CTAs of few tokens stream through tiles, the bytes that are on
+    // their way sooner are worth more (16 x 130001 x 4096 88.3 us for 90.5).
+    auto hand_back = [&]() {
+      __syncwarp();
+      if (lane == 0) moe::mbar_arrive(&bar.a8_empty[s8]);
+      s8 += kGroups;
+      if (s8 >= L::kA8) s8 -= L::kA8, p8 ^= 1u;
+    };
     auto load = [&]() {
       if (!wait(&bar.a8_full[s8], p8, 9)) return false;
       const uint8_t* stage = smem + L::kOffA8 + s8 * L::kStageBytes;
@@ -504,16 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i)
           if (tok0 + 16 * i < p.half) x[i] = *reinterpret_cast<const uint4*>(stage + tok_from + i * 16 * kStage);
       }
+      if constexpr (EARLY) {
+        moe::fence_proxy_async_smem();
+        hand_back();
+      }
       return true;
-    };
-    // The copy that refills the slot is of the async proxy and can overtake loads that are still on their way to
-    // registers (seen as rows whose last chunks were those of two steps on): the slot goes back once the codes have been
-    // converted, so that they have arrived.  (A proxy fence right after the loads took 100 cycles a step more.)
-    auto hand_back = [&]() {
-      __syncwarp();
-      if (lane == 0) moe::mbar_arrive(&bar.a8_empty[s8]);
-      s8 += kGroups;
-      if (s8 >= L::kA8) s8 -= L::kA8, p8 ^= 1u;
     };
     bool ok = group < n_stages && load();
     for (int64_t k = group; ok && k < n_stages; k += kGroups) {
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         }
         moe::fence_proxy_async_smem();
       }
-      hand_back();
+      if constexpr (!EARLY) hand_back();
       if (k + kGroups < n_stages) ok = load();
       moe::tmem_st_wait();  // also on the way out after a wait that gave up: no store left in flight
       moe::tc_fence_before();
@@ -750,7 +757,7 @@ Shape shape_of(int m, int n, int k, int num_sms) {
 }
 
 // How many clusters of `parts` CTAs the current device runs at once; asked once a device and size.
-template <int FORM>
+template <int FORM, bool EARLY>
 int clusters_at_once(int parts) {
   static std::atomic<int> known[64][9];
   int dev = 0, n = 0;
@@ -766,7 +773,7 @@ int clusters_at_once(int parts) {
   cfg.dynamicSmemBytes = Layout<FORM>::kBytes + 1024;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, w8_tc_kernel<FORM>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, w8_tc_kernel<FORM, EARLY>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -774,23 +781,23 @@ int clusters_at_once(int parts) {
   return n;
 }
 
-template <int FORM>
+template <int FORM, bool EARLY = false>
 cudaError_t launch_tiles(const Maps& maps, const Params& p, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  const void* k = (const void*)w8_tc_kernel<FORM>;
+  const void* k = (const void*)w8_tc_kernel<FORM, EARLY>;
   if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
   int parts = 1;
   if constexpr (FORM != kTwo) {
     // clusters that share k out, as large as all of them run at once and have two steps a CTA
     const int steps = (p.a.k + kStage - 1) / kStage;
     for (int c = kMostParts; c > 1 && parts == 1; --c)
-      if (p.tiles * c <= num_sms && steps >= 2 * c && clusters_at_once<FORM>(c) >= p.tiles) parts = c;
+      if (p.tiles * c <= num_sms && steps >= 2 * c && clusters_at_once<FORM, EARLY>(c) >= p.tiles) parts = c;
   }
   Maps m = maps;
   Params arg = p;
   void* args[] = {&m, &arg};
   if constexpr (FORM == kTwo) {
-    int64_t pairs = clusters_at_once<FORM>(2);
+    int64_t pairs = clusters_at_once<FORM, EARLY>(2);
     if (pairs < 1) pairs = num_sms / 2;
     if (p.tiles < pairs) pairs = p.tiles;
     return launch_after(k, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), args, Layout<FORM>::kBytes + 1024, s, 2);
@@ -813,7 +820,7 @@ cudaError_t launch_w8_tc(const moe_layer_w8_args_t& a, void* ws, int num_sms, cu
     if (!moe::encode_2d(&maps.x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.m, a.k, kStage, shape.half,
                         CU_TENSOR_MAP_SWIZZLE_128B, a.x_stride))
       return cudaErrorInvalidValue;
-    return launch_tiles<kFew>(maps, p, num_sms, s);
+    return p.tiles > num_sms ? launch_tiles<kFew, true>(maps, p, num_sms, s) : launch_tiles<kFew>(maps, p, num_sms, s);
   }
   p.status = static_cast<int32_t*>(ws);
   __half* x16 = reinterpret_cast<__half*>(static_cast<char*>(ws) + 256);
