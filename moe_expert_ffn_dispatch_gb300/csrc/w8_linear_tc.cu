@@ -15,9 +15,9 @@
 // operand, so that they cross memory and L2 as bytes.  Tokens are the B operand, f16 in
 // shared memory: up to 64 of them arrive as int8 too and are converted by every CTA;
 // more are converted once, by a kernel before this one into the workspace, and arrive
-// as f16.  One CTA with 256 tokens of its own moves 146 KB a step of 128 k through
-// shared memory, all that it can in the step's time (4093 x 6144 x 4096 131 us); of a
-// pair each moves 98.
+// as f16.  One CTA with 224 tokens of its own moves 147 KB a step of 128 k through
+// shared memory, all that it can in the step's time (4093 x 6144 x 4096 131 us for 121,
+// with the tokens' conversion of then); of a pair each moves 90.
 // A pair's tile has an accumulator for each half of the tokens, side by side, and takes
 // two steps of one half, then of the other: at the end of 1024 k one accumulator is
 // drained while two steps' products run into the other (a step of each in turn 137 us
@@ -34,10 +34,10 @@
 // Where there are fewer tiles than SMs a cluster shares k out, and adds its int32
 // sums up over distributed shared memory, a share of the tile's columns each.
 //
-// Bound by: many tokens, the products (4093 x 6144 x 4096 121 us, 1.70 PFLOP/s; 11 us of
+// Bound by: many tokens, the products (4093 x 6144 x 4096 116 us, 1.77 PFLOP/s; 7 us of
 // it is the tokens' conversion before, the tensor pipe is busy for 172 of the 205
 // thousand cycles after, the rest is the ends of 1024 k and of tiles); 16 tokens x 130001
-// x 4096, memory (91 us, 5.9 TB/s); up to 128 tokens on ordinary sizes, latency (64 x 4096
+// x 4096, memory (88 us, 6.1 TB/s); up to 128 tokens on ordinary sizes, latency (64 x 4096
 // x 4096 10.3 us: 3 until the first weights, 3 for the steps, 2 for the sums over the
 // cluster, launch).
 #include "w8_linear.cuh"
@@ -123,7 +123,7 @@ __device__ __forceinline__ void widen16(const uint4& c, uint32_t* o) {
 }
 
 // The tokens as f16, dense; and the status words of the call.  2^shift threads a row, 8 codes at a time, so that loads and
-// stores of a warp are whole lines.
+// stores of a warp are whole lines (16 codes a thread of one long row, which takes a division, 4093 x 4096 4 us more).
 __global__ void __launch_bounds__(kWidenThreads) w8_widen_kernel(const moe_layer_w8_args_t a, __half* x16, int32_t* status,
                                                                  int shift) {
   grid_dependency_wait();
