@@ -1,0 +1,48 @@
+"""Order of reads and refills of shared memory that asynchronous copies write, as the sources have it.
+
+A copy by TMA or cp.async.bulk belongs to another proxy than a thread's loads.  A slot that is handed back right behind
+loads can be refilled while they are still on their way to registers, at full speed and now and then, so no run shows
+that it cannot happen: the order has to be there in the source.  It is there where a proxy fence stands between the loads
+and the arrival, or an instruction that cannot start before the loaded values are there."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "moe_expert_ffn_dispatch_gb300", "csrc")
+FENCE = r"fence_proxy_async_smem\(\);"
+
+
+def source(name):
+    return re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+
+
+def last(patterns, text):
+    """Which of the patterns has the last match in the text."""
+    at = {p: max([m.start() for m in re.finditer(p, text)], default=-1) for p in patterns}
+    best = max(at, key=at.get)
+    assert at[best] >= 0, patterns
+    return best
+
+
+def test_the_dp4a_ring_hands_slots_and_token_rows_back_behind_a_proxy_fence():
+    src = source("moe_gemm.cu")
+    loads = r"stage_dot_m<\w+>\(m, Ws"
+    for arrival in (r"mbar_arrive\(&empty\[s\]\)", r"mbar_arrive\(tok_empty\)"):
+        found = list(re.finditer(arrival, src))
+        assert found
+        for m in found:
+            assert last((loads, FENCE), src[:m.start()]) == FENCE, arrival
+
+
+def test_converted_codes_are_in_registers_before_their_slot_goes_back():
+    """In the two kernels that widen codes into tensor memory: the stores of the converted codes come first, or a fence."""
+    loads, stores = r"c\[j\] = \*reinterpret_cast", r"tmem_st32\("
+    src = source("tc_gemm.cu")
+    found = list(re.finditer(r"mbar_arrive\(&a8_empty", src))
+    assert len(found) == 2
+    for m in found:
+        assert last((loads, FENCE, stores), src[:m.start()]) != loads
+    src = source("w8_linear_tc.cu")
+    found = list(re.finditer(r"[^=] hand_back\(\);", src))
+    assert len(found) == 2
+    for m in found:
+        assert last((loads, FENCE, stores), src[:m.start()]) != loads
