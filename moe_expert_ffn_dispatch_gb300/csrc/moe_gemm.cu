@@ -362,6 +362,7 @@ __device__ void run(const FwdParams& p, int32_t* raw, char* smem, SmallState& ss
       if (ready == nullptr || ss.ready_seen) return true;
       if (!mbar_wait_bounded(ready, 0, abort_flag, status, site + 6, false)) return false;
       ss.ready_seen = true;
+      fence_proxy_async_smem();  // the token rows' area was the dispatch's scratch; bulk copies into it follow
       return *abort_flag == 0;
     };
     // slots beyond the cache are read from the workspace's slot table

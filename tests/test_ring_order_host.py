@@ -46,3 +46,13 @@ def test_converted_codes_are_in_registers_before_their_slot_goes_back():
     assert len(found) == 2
     for m in found:
         assert last((loads, FENCE, stores), src[:m.start()]) != loads
+
+
+def test_the_one_launch_scratch_is_done_with_before_token_rows_are_copied_over_it():
+    """The dispatch's scratch is written and read by threads, in the area that bulk copies of token rows take after the
+    `ready` barrier: the producer, past that barrier, fences before its first copy."""
+    src = source("moe_gemm.cu")
+    wait = src[src.index("auto wait_ready = [&]"):]
+    wait = wait[:wait.index("};")]
+    seen = wait.index("ss.ready_seen = true;")
+    assert wait.index("mbar_wait_bounded(ready") < seen and re.search(FENCE, wait[seen:])
