@@ -27,10 +27,10 @@
 // What bounds a step is how fast one warp can wait, issue and commit (about 100 cycles
 // a wait, 40 a product) and the conversion's chain of waits, loads and stores (830
 // cycles): weights and tokens of a step complete one barrier, and its products one other.
-// Roles: warp 0 copies weights, warp 2 copies tokens, warp 1 issues products (of a
-// pair's second CTA: tells the first that its tokens have landed), warps 4..7 convert
-// weights (a row a thread), warps 8..15 drain and write.  Up to 64 tokens warps 4..7 and
-// 8..11 convert weights and tokens of every other step, and warps 12..15 drain.
+// Roles: warp 0 copies weights, warp 2 copies tokens, warp 1 issues products (the first
+// CTA's of a pair), warps 4..7 convert weights (a row a thread), warps 8..15 drain and
+// write.  Up to 64 tokens warps 4..7 and 8..11 convert weights and tokens of every other
+// step, and warps 12..15 drain.
 // Where there are fewer tiles than SMs a cluster shares k out, and adds its int32
 // sums up over distributed shared memory, a share of the tile's columns each.
 //
@@ -87,13 +87,13 @@ struct Layout {
   static_assert(kBytes + 1024 <= kMaxSmem, "shared memory");
   static_assert(kAccCols + kSteps * kA16Cols <= kTmemCols, "tensor memory");
   static_assert(kOffBar >= kHalf * kRows * 4, "the sums of a tile of one half fit the rings");
-  // arrivals of a step: the converting warps, the tokens' copy, and in a pair the other CTA's of both
-  static constexpr int kFull = FORM == kFew ? 4 : FORM == kOne ? 5 : 10;
+  // arrivals of a step: the converting warps (a pair's: of both CTAs), and the tokens' copy
+  static constexpr int kConvArrivals = FORM == kTwo ? 8 : 4, kFull = kConvArrivals + (FORM == kFew ? 0 : 1);
   static constexpr int kDrained = kDrainWarps * kHalves;
 };
 
 struct Barriers {
-  uint64_t a8_full[6], a8_empty[6], full[4], empty[4], tokens[4], acc_full[2], acc_empty[2], drain;
+  uint64_t a8_full[6], a8_empty[6], full[4], empty[4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort, broken;
 };
@@ -243,13 +243,25 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// Arrive on `bar` of CTA `rank` of the cluster.  What the arrival tells of is tensor memory whose stores (or loads) have
-// been waited for and copies that a barrier of their own has completed, nothing that this thread wrote to memory: a
-// release over the cluster, which waits for all that it did, took 1200 cycles a step more.
-__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+// `bar` of CTA `rank`, as an address in the cluster's shared memory
+__device__ __forceinline__ uint32_t remote_of(uint64_t* bar, uint32_t rank) {
   uint32_t remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(moe::smem_u32(bar)), "r"(rank));
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+  return remote;
+}
+// Arrive on `bar` of CTA `rank`.  What the arrival tells of is tensor memory whose stores (or loads) have been waited for:
+// the tcgen05 fences on either side order it, and ask for an arrival of the cluster's scope, relaxed (a release, which
+// waits for all that the thread did, took 1200 cycles a step more).
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_of(bar, rank)) : "memory");
+}
+// moe::tma_load_2d into this CTA's shared memory, completing bytes on a barrier of either CTA of the pair
+__device__ __forceinline__ void pair_tma_load_2d(void* dst, const void* tmap, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(moe::smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
 }
 
 // The same for the steps, whose barriers the converters complete too: where they have given up, a phase never completes
@@ -295,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
     }
     if (lane < L::kSteps) {
       moe::mbar_init(&bar.full[lane], L::kFull);
-      moe::mbar_init(&bar.tokens[lane], 1);
       moe::mbar_init(&bar.empty[lane], 1);
     }
     if (lane < 2) {
@@ -372,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
       uint32_t ph = 0;
       bool wrapped = false, ok = true;
       // One half's tokens; or, of a pair, half of each half's, so that the columns of a product (the first CTA's tokens,
-      // then the second's) are neighbours.  The second CTA's copies complete a barrier of its own, which warp 1 hands on.
-      uint64_t* landed = side_of_pair ? bar.tokens : bar.full;
+      // then the second's) are neighbours.  Both CTAs' copies complete the first's barrier.
       const int box = p.half / HALVES, box1 = p.half1 / 2;
+      const uint32_t bytes = 2 * tokens * kAtom * 2;  // of both CTAs
       for (int64_t it = first; ok && it < p.tiles; it += step) {
         const int m0 = static_cast<int>(it % p.blocks) * tokens;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -383,14 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
             break;
           }
           if (moe::elect_one()) {
-            moe::mbar_arrive_expect_tx(&landed[s], 2 * tokens / HALVES * kAtom * 2);
+            if (!side_of_pair) moe::mbar_arrive_expect_tx(&bar.full[s], bytes);
+            const uint32_t landed = FORM == kTwo ? remote_of(&bar.full[s], 0) : 0;
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
               uint8_t* to = smem + (2 * s + a) * L::kAtomBytes;
               const int k = kb * kStage + a * kAtom;
-              moe::tma_load_2d(to, &maps.x, k, m0 + side_of_pair * box, &landed[s]);
-              if (HALVES == 2)
-                moe::tma_load_2d(to + box * kAtom * 2, &maps.y, k, m0 + p.half + side_of_pair * box1, &landed[s]);
+              if constexpr (FORM == kTwo) {
+                pair_tma_load_2d(to, &maps.x, k, m0 + side_of_pair * box, landed);
+                pair_tma_load_2d(to + box * kAtom * 2, &maps.y, k, m0 + p.half + side_of_pair * box1, landed);
+              } else {
+                moe::tma_load_2d(to, &maps.x, k, m0, &bar.full[s]);
+              }
             }
           }
           __syncwarp();
@@ -398,21 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
         }
       }
       // what it armed has landed, or (the converters having given up) is past where a barrier could tell
-      drain_steps(landed, L::kSteps, s, ph, wrapped, abort, p.status, kSite + 4);
+      if (!side_of_pair) drain_steps(bar.full, L::kSteps, s, ph, wrapped, abort, p.status, kSite + 4);
     } else if (warp == 1 && side_of_pair) {
-      // ---------------------------------------------------- the second CTA's tokens have landed
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int64_t it = first; ok && it < p.tiles; it += step) {
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = wait(&bar.tokens[s], ph, 13);
-          if (!ok) break;
-          if (lane == 0) arrive(&bar.full[s]);
-          __syncwarp();
-          if (++s == L::kSteps) s = 0, ph ^= 1u;
-        }
-      }
       // the first CTA's products, which are of this one's memory too, are done
       moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 8);
     } else if (warp == 1) {

@@ -56,3 +56,21 @@ def test_the_one_launch_scratch_is_done_with_before_token_rows_are_copied_over_i
     wait = wait[:wait.index("};")]
     seen = wait.index("ss.ready_seen = true;")
     assert wait.index("mbar_wait_bounded(ready") < seen and re.search(FENCE, wait[seen:])
+
+
+def test_what_the_ctas_of_a_pair_tell_each_other_has_the_clusters_scope():
+    """An arrival at the other CTA's barrier, or a wait for one, whose scope is not named has the CTA's own and orders
+    nothing between the two."""
+    src = source("w8_linear_tc.cu") + source("device_prims.cuh")
+    arrivals = re.findall(r'"mbarrier\.arrive[\w.:]*\.shared::cluster[^"]*"', src)
+    assert arrivals and all(re.match(r'"mbarrier\.arrive\.(relaxed|release)\.cluster\.', a) for a in arrivals), arrivals
+    assert "mbarrier.try_wait.parity.acquire.cluster" in src
+
+
+def test_both_ctas_token_copies_complete_the_barrier_that_the_products_wait_for():
+    """Handed on by a thread of the second CTA, they would need its release over the cluster."""
+    src = source("w8_linear_tc.cu")
+    landed = re.search(r"landed = FORM == kTwo \? remote_of\(&bar\.full\[s\], 0\)", src)
+    copies = re.findall(r"\bpair_tma_load_2d\(to[^;]*;", src)
+    assert landed and len(copies) == 2 and all(c.endswith("landed);") for c in copies)
+    assert re.search(r"if \(!side_of_pair\) moe::mbar_arrive_expect_tx\(&bar\.full\[s\], bytes\)", src)
