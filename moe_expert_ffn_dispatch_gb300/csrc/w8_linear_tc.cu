@@ -264,16 +264,10 @@ __device__ __forceinline__ void pair_tma_load_2d(void* dst, const void* tmap, in
       : "memory");
 }
 
-// The same for the steps, whose barriers the converters complete too: where they have given up, a phase never completes
-// and the copies get a while to land.
-__device__ __forceinline__ void drain_steps(uint64_t* full, int n, int s, uint32_t ph, bool wrapped, volatile int* abort,
-                                            int32_t* status, int site) {
-  for (int i = 0; i < n; ++i) {
-    const uint32_t parity = i < s ? ph : ph ^ 1u;
-    if (i < s || wrapped) moe::mbar_wait_bounded(&full[i], parity, abort, status, site);
-  }
-  if (*abort)
-    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+// A wait's budget, for copies whose landing no barrier can show any more
+__device__ __forceinline__ void wait_out_budget() {
+  const uint64_t t0 = moe::global_timer_ns();
+  while (moe::global_timer_ns() - t0 <= moe::kWaitBudgetNs) __nanosleep(100000);
 }
 
 // EARLY: slots of codes go back before the codes are converted
@@ -412,8 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
           if (++s == L::kSteps) s = 0, ph ^= 1u, wrapped = true;
         }
       }
-      // what it armed has landed, or (the converters having given up) is past where a barrier could tell
-      if (!side_of_pair) drain_steps(bar.full, L::kSteps, s, ph, wrapped, abort, p.status, kSite + 4);
+      // (every step's products are done where nothing gave up: the tokens have landed; else: after the roles)
     } else if (warp == 1 && side_of_pair) {
       // the first CTA's products, which are of this one's memory too, are done
       moe::mbar_wait_bounded(&bar.drain, 0, nullptr, p.status, kSite + 8);
@@ -667,6 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) w8_tc_kernel(const __grid_constan
   // (of a pair: no CTA ends, or gives its tensor memory back, while the other's products or arrivals may be under way)
   if constexpr (FORM == kTwo) cluster_sync();
   else __syncthreads();
+  // Tokens on their way into a CTA in which a wait gave up: converters that stopped never complete their steps' barriers,
+  // so the CTA stays for as long as any other wait takes at most.  A CTA in which none did has drained all of its products,
+  // which read every copy that there was.
+  if (FORM != kFew && warp == 2 && *abort) wait_out_budget();
   if (warp == 1) {
     moe::tc_fence_after();
     if constexpr (FORM == kTwo) pair_dealloc(tmem, kTmemCols);
