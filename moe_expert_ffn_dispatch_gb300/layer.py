@@ -322,6 +322,8 @@ def w8_linear_workspace(m: int, n: int, k: int, device="cuda") -> Optional[torch
 
 @functools.lru_cache(maxsize=1024)
 def _w8_workspace_bytes(m: int, n: int, k: int, index: int) -> int:
+    if max(m, n, k) > _I32_MAX or min(m, n, k) < -_I32_MAX:
+        _too_large("w8_linear_workspace", max(m, n, k, key=abs))
     nb = ctypes.c_size_t(0)
     rc = _entry("moe_layer_w8_linear_workspace_size")(m, n, k, ctypes.byref(nb))
     if rc:
@@ -428,6 +430,8 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
             raise TypeError("tokens: dtype %s, expected int32 or int64" % tdtype)
         if not 1 <= len(tshape) <= 2 or tshape[0] != rows:
             raise ValueError("tokens: shape %s, expected [%d] or [%d, n]" % (tuple(tshape), rows, rows))
+        if tokens.numel() > rows * _I32_MAX:
+            _too_large("tokens", tshape[1])
         a.num_tokens = tshape[1] if len(tshape) == 2 else 1
         if a.num_tokens:
             a.tokens = _dense(tokens, "tokens", tdtype, tshape, index)
@@ -480,8 +484,8 @@ def page_plan(page_table: torch.Tensor, held: torch.Tensor, new_tokens: torch.Te
             return page_plan(page_table, held, new_tokens, free_pages, page_size, num_pages, tokens, taken, taken_out)
     table_at, batch, pages, stride = _page_table(page_table, index)
     num_free = free_pages.numel()
-    if page_size > _I32_MAX or num_pages > _I32_MAX or tokens > _I32_MAX or num_free > _I32_MAX:
-        _too_large("page_plan", max(page_size, num_pages, tokens, num_free))
+    if max(page_size, num_pages, tokens, num_free) > _I32_MAX or min(page_size, num_pages) < -_I32_MAX:
+        _too_large("page_plan", max(page_size, num_pages, tokens, num_free, key=abs))
     if tokens < 0:
         raise ValueError("tokens: %d" % tokens)
     i32 = torch.int32

@@ -228,3 +228,25 @@ def test_pair_gate_of_one_row_that_is_expanded(h):
     for gate in (gt.expand(6, h), gt.repeat(6, 1)):
         for a, b in zip(m.norm_add_rmsnorm_quant(x, r, pw, w, gate=gate, want_y=True), want):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ numbers that do not fit the C structures
+def test_numbers_past_32_bits_are_not_cut():
+    one = i32([1])
+    table = i32([[0, 1, 2, 3]])
+    for size, pages, tokens in ((2 ** 32 + 16, 4, 1), (-2 ** 32 + 16, 4, 1), (16, 2 ** 32 + 4, 1), (16, -2 ** 32 + 4, 1), (16, 4, 2 ** 32 + 1),
+                                (16, 4, -2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            m.page_plan(table, one, one, one, size, pages, tokens)
+    for size, pages in ((-16, 4), (16, -4)):
+        with pytest.raises(m.MoeError):
+            m.page_plan(table, one, one, one, size, pages, 1)
+    assert table.tolist() == [[0, 1, 2, 3]]
+    logits = torch.zeros(2, 5, device=DEV)
+    for n in (2 ** 32, 2 ** 32 + 1, 2 ** 31):
+        with pytest.raises(ValueError):
+            m.token_logprobs(logits, i32([[1], [2]]).expand(2, n))
+    with pytest.raises(ValueError):
+        m.token_logprobs(logits[:1].expand(2 ** 32 + 1, 5))
+    with pytest.raises(ValueError):
+        m.w8_linear_workspace(2 ** 32 + 100, 64, 64)
