@@ -369,7 +369,8 @@ int moe_layer_page_plan(const moe_layer_page_plan_args_t* args, void* stream);
  * tokens_64 is 1; NULL with num_tokens 0.  logprob: [rows, num_tokens] fp32.
  * entropy: [rows] fp32 or NULL.  top_logprob fp32, top_id int32: [rows, top], NULL
  * with top 0.  1 <= vocab < 2^31, 0 <= top <= min(32, vocab), rows >= 0.
- * Sums are fp32, exponentials good to about 2^-22.  The order of the sums goes by
+ * Sums are fp32.  An exponential is good to about 2^-22 + 1.2 |l_i - M| 2^-23, its
+ * argument being a difference and a product in fp32.  The order of the sums goes by
  * rows, vocab and the row's alignment: the same row's logprob, top_logprob and
  * entropy can differ in rounding between calls with other rows beside it (its
  * top_id does not).  The same call gives the same bits. */

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
   T* res_out = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
   T* y_out = a.y_out ? static_cast<T*>(a.y_out) + row * h : nullptr;
   const W *post = static_cast<const W*>(a.post_weight), *w = static_cast<const W*>(a.weight);
+  // rows that are not VEC: x, then the new residual; the residual, then y; the gate, then the codes
   uint4 *buf_x = s_rows + (ROW_WARP ? warp * 3 * row_slots(C, 32) : 0), *buf_r = buf_x + row_slots(C, nt),
         *buf_g = buf_r + row_slots(C, nt);
   auto root = [&](float sum) { return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(h)), a.eps)); };

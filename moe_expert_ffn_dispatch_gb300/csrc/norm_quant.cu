@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(ROW_WARP ? kRowWarps * 32 : C * 128, ROW_WARP 
   T* y_out = a.y_out ? static_cast<T*>(a.y_out) + row * h : nullptr;
   int8_t* q = a.q + row * h;
   const W* w = static_cast<const W*>(a.weight);
+  // rows that are not VEC: x, then y; the residual; the new residual, then the codes
   uint4 *buf_x = s_rows + (ROW_WARP ? warp * 3 * row_slots(C, 32) : 0), *buf_r = buf_x + row_slots(C, nt),
         *buf_o = buf_r + row_slots(C, nt);
   auto sync_row = [] {

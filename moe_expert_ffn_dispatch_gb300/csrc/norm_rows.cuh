@@ -156,7 +156,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3]), pack2<E>(v[4], v[5]), pack2<E>(v[6], v[7]));
 }
 
-// shared memory of a row that is not VEC: x (then y), the residual, and the new residual (then the codes)
+// slots of one of the three buffers that a row that is not VEC has in shared memory
 __host__ __device__ constexpr int row_slots(int c, int nt) { return c * nt + 2; }
 
 }  // namespace

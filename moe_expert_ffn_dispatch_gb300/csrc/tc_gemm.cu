@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(kBigThreads, 1)
     // Two loop orders, chosen per launch from the big blocks' mean row count:
     //  * short blocks (<= 64 rows: the MMA of a stage is cheap, conversion
     //    bounds the kernel): software-pipelined over the CTA's stages.  Stage
-    //    k's tensor-memory stores are issued, then stage k + 1's codes are
-    //    loaded (and their staging slot released), and only then does the
+    //    k's tensor-memory stores are issued and its staging slot released,
+    //    then stage k + 1's codes are loaded, and only then does the
     //    warp wait for stage k's stores and hand the slot to the MMA, so the
     //    store latency overlaps the next stage's loads;
     //  * full blocks (the tensor pipe bounds the kernel): stage by stage, each
