@@ -42,8 +42,8 @@ constexpr int kThreads = (kSoftWarps + kConvWarps + 4) * 32;  // warps in fours,
 // weights' warps take 120 once the others have gone down to 80 (256 x 120 + 256
 // x 80 + 128 x 80 = 61440).  With 96 for all the weights' warps spill: 835 us in
 // place of 632 (8 chunks of 512 tokens at 8192 keys, 32 heads on 8).
-constexpr int kSoftRegs = 120, kConvRegs = 80, kMmaRegs = 80;
-static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * 96, "the split fits what the launch has");
+constexpr int kLaunchRegs = 96, kSoftRegs = 120, kConvRegs = 80, kMmaRegs = 80;
+static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs, "the split fits what the launch has");
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kSite = 1 << 8;  // of the waits, in the status
 
@@ -688,7 +688,7 @@ cudaError_t launch_chunk(const AttnParams& p, int num_sms, cudaStream_t s) {
   const moe_layer_kv_attention_args_t& a = p.a;
   static std::atomic<uint64_t> allowed{0};
   const void* k = (const void*)kv_attention_chunk_kernel<T, D>;
-  cudaError_t e = allow_smem(k, kMaxSmem, allowed);
+  cudaError_t e = allow_smem(k, kMaxSmem, allowed, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.cache.page_size + kTile - 1) / kTile;
   const int64_t rows = static_cast<int64_t>(a.max_q) * a.group_size;

@@ -29,12 +29,20 @@ cudaError_t launch_logprobs(const moe_layer_logprobs_args_t& a, int num_sms, cud
 
 // Lets `kernel` have `most` bytes of dynamic shared memory on the current
 // device, asking the runtime once a device and kernel (`done`: one bit a device).
-inline cudaError_t allow_smem(const void* kernel, int most, std::atomic<uint64_t>& done) {
+// A kernel whose warps hand registers on to others has to start with `regs` a thread:
+// built with fewer, those that take them would wait for ever, so it is not launched.
+inline cudaError_t allow_smem(const void* kernel, int most, std::atomic<uint64_t>& done, int regs = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  if (regs) {
+    cudaFuncAttributes is;
+    e = cudaFuncGetAttributes(&is, kernel);
+    if (e != cudaSuccess) return e;
+    if (is.numRegs < regs) return cudaErrorInvalidConfiguration;
+  }
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return e;

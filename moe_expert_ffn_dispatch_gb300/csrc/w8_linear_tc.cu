@@ -59,8 +59,8 @@ constexpr int kTmemCols = 512;
 constexpr int kThreads = 512, kWidenThreads = 256;
 // Registers a thread where a tile has two halves: 128 at launch, and what the drain warps have more the others give.
 // (With one half nobody needs more, and the sums over a cluster are every warp's.)
-constexpr int kRoleRegs = 64, kConvRegs = 96, kDrainRegs = 176;
-static_assert(128 * kRoleRegs + 128 * kConvRegs + 256 * kDrainRegs <= kThreads * 128, "the split fits what the launch has");
+constexpr int kLaunchRegs = 128, kRoleRegs = 64, kConvRegs = 96, kDrainRegs = 176;
+static_assert(128 * kRoleRegs + 128 * kConvRegs + 256 * kDrainRegs <= kThreads * kLaunchRegs, "the split fits what the launch has");
 constexpr int kA8Bytes = kRows * kStage;
 constexpr int kSite = 2 << 8;       // of the waits, in the status
 constexpr float kNan = NAN;
@@ -784,7 +784,7 @@ template <int FORM, bool EARLY = false>
 cudaError_t launch_tiles(const Maps& maps, const Params& p, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   const void* k = (const void*)w8_tc_kernel<FORM, EARLY>;
-  if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem(k, kMaxSmem, allowed, FORM == kTwo ? kLaunchRegs : 0); e != cudaSuccess) return e;
   int parts = 1;
   if constexpr (FORM != kTwo) {
     // clusters that share k out, as large as all of them run at once and have two steps a CTA

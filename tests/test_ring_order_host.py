@@ -74,3 +74,16 @@ def test_both_ctas_token_copies_complete_the_barrier_that_the_products_wait_for(
     copies = re.findall(r"\bpair_tma_load_2d\(to[^;]*;", src)
     assert landed and len(copies) == 2 and all(c.endswith("landed);") for c in copies)
     assert re.search(r"if \(!side_of_pair\) moe::mbar_arrive_expect_tx\(&bar\.full\[s\], bytes\)", src)
+
+
+def test_kernels_that_hand_registers_on_are_launched_only_with_what_the_split_needs():
+    """setmaxnreg.inc waits until the block has the registers: built with fewer a thread than the split adds up to, it would
+    wait for ever.  Each such kernel's launch names the number that its static_assert counts with."""
+    users = [f for f in sorted(os.listdir(CSRC)) if "setmaxnreg.inc" in source(f)]
+    assert users == ["kv_attention_chunk.cu", "w8_linear_tc.cu"]
+    for f in users:
+        src = source(f)
+        assert re.search(r"static_assert\([^;]*<= kThreads \* kLaunchRegs", src)
+        assert re.search(r"allow_smem\(k, kMaxSmem, allowed, [^;]*kLaunchRegs", src)
+    ops = source("layer_ops.cuh")
+    assert re.search(r"if \(is\.numRegs < regs\) return", ops)
